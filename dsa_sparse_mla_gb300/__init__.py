@@ -16,14 +16,16 @@ import torch
 __all__ = ["HSError", "lib_path", "load", "hs_abi_version", "hs_check_flag", "hs_indexer_scores", "hs_topk",
            "hs_indexer_topk",
            "hs_sparse_mla_fwd", "hs_sparse_mla_workspace_size", "hs_sparse_mla_fwd_static", "hs_hisparse_resolve",
-           "hs_hisparse_touch_host", "hs_kv_append", "hs_kv_offload", "FLAGS"]
+           "hs_hisparse_touch_host", "hs_kv_append", "hs_kv_offload", "hs_rope", "hs_rope_inv_freq", "hs_paged_mla_fwd",
+           "hs_paged_mla_workspace_size", "hs_kv_copy_pages", "hs_kv_fork", "hs_kv_free", "hs_kv_compact",
+           "hs_kv_compact_workspace_size", "FLAGS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libhs.so")
 _lib = None
 
 FLAGS = {"BAD_INDEX": 0x01, "BAD_LENGTH": 0x02, "BAD_BLOCK": 0x04, "NOT_ASCENDING": 0x08, "BAD_STATE": 0x10,
-         "TIMEOUT": 0x20}
+         "TIMEOUT": 0x20, "RANGE": 0x40, "NO_PAGES": 0x80}
 _STATUS = {0: "HS_OK", 1: "HS_ERR_INVALID", 2: "HS_ERR_UNSUPPORTED", 3: "HS_ERR_CUDA", 4: "HS_ERR_DEVICE_FLAG",
            5: "HS_ERR_TIMEOUT"}
 
@@ -35,7 +37,7 @@ class HSError(RuntimeError):
 
 
 _P = ctypes.c_void_p
-_i32, _i64, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+_i32, _i64, _f32, _f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double
 
 
 class _IndexerArgs(ctypes.Structure):
@@ -85,6 +87,18 @@ def load():
         lib.hs_hisparse_touch_host.argtypes = [_i32, _P, _P, _P, _P, _P]
         lib.hs_kv_append.argtypes = [ctypes.POINTER(_AppendArgs), _P]
         lib.hs_kv_offload.argtypes = [ctypes.POINTER(_OffloadArgs), _P]
+        lib.hs_rope.argtypes = [ctypes.POINTER(_RopeArgs), _P]
+        lib.hs_rope_inv_freq.argtypes = [_i32, _f64, _i32, _f64, _i32, _f64, _f64, _P, _P]
+        lib.hs_paged_mla_fwd.argtypes = [ctypes.POINTER(_PagedMlaArgs), _P]
+        lib.hs_paged_mla_workspace_size.argtypes = [_i32, _i32, _i32, _i64, ctypes.POINTER(ctypes.c_uint64)]
+        lib.hs_kv_copy_pages.argtypes = [ctypes.POINTER(_CopyArgs), _P]
+        lib.hs_kv_fork.argtypes = [ctypes.POINTER(_ForkArgs), _P]
+        lib.hs_kv_free.argtypes = [ctypes.POINTER(_FreeArgs), _P]
+        lib.hs_kv_compact.argtypes = [ctypes.POINTER(_CompactArgs), _P]
+        lib.hs_kv_compact_workspace_size.argtypes = [_i64, ctypes.POINTER(ctypes.c_uint64)]
+        for f in ("hs_rope", "hs_rope_inv_freq", "hs_paged_mla_fwd", "hs_paged_mla_workspace_size", "hs_kv_copy_pages", "hs_kv_fork",
+                  "hs_kv_free", "hs_kv_compact", "hs_kv_compact_workspace_size"):
+            getattr(lib, f).restype = ctypes.c_int
         for f in ("hs_check_flag", "hs_indexer_scores", "hs_topk", "hs_indexer_topk", "hs_sparse_mla_fwd", "hs_sparse_mla_workspace_size",
                   "hs_sparse_mla_fwd_static", "hs_hisparse_resolve", "hs_hisparse_touch_host", "hs_kv_append", "hs_kv_offload"):
             getattr(lib, f).restype = ctypes.c_int
@@ -307,3 +321,200 @@ def hs_kv_offload(pools, host_rows, layer, req, page, block_table, seq_len, err_
     a.layer, a.req, a.page = _ptr(layer), _ptr(req), _ptr(page)
     a.block_table, a.bt_stride, a.seq_len, a.err_flag = _ptr(block_table), block_table.shape[1], _ptr(seq_len), _ptr(err_flag)
     _check(load().hs_kv_offload(ctypes.byref(a), _stream(stream)))
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("H2", _i32), ("rot", _i32), ("dtype", _i32), ("interleaved", _i32),
+                ("inverse", _i32), ("scale", _f32), ("positions", _P), ("inv_freq", _P), ("x", _P), ("x_stride_t", _i64),
+                ("x_stride_h", _i64), ("out", _P), ("out_stride_t", _i64), ("out_stride_h", _i64), ("y", _P),
+                ("y_stride_t", _i64), ("y_stride_h", _i64), ("y_out", _P), ("y_out_stride_t", _i64),
+                ("y_out_stride_h", _i64)]
+
+
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ROPE_KINDS = {"plain": 0, "linear": 1, "yarn": 2}
+
+
+def hs_rope_inv_freq(rot: int, base: float = 10000.0, kind: str = "plain", factor: float = 1.0, original: int = 4096,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Angles per position of each pair (float64 CPU tensor [rot / 2]) and the scale hs_rope takes; ``kind`` is
+    "plain", "linear" or "yarn" (contexts ``factor`` times ``original``). Host only."""
+    if kind not in _ROPE_KINDS:
+        raise HSError(1, "kind must be one of %s" % ", ".join(_ROPE_KINDS))
+    f, s = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64), ctypes.c_float(1.0)
+    _check(load().hs_rope_inv_freq(int(rot), float(base), _ROPE_KINDS[kind], float(factor), int(original), float(beta_fast),
+                                   float(beta_slow), f.data_ptr(), ctypes.addressof(s)))
+    return f, float(s.value)
+
+
+def _rope_tensor(t, name, T, rot, dtype):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise HSError(1, "%s must be a CUDA tensor" % name)
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != rot or t.dtype != dtype or t.stride(2) != 1:
+        raise HSError(1, "%s must be %s [T, heads, rot] with consecutive values in a head" % (name, dtype))
+
+
+def hs_rope(x, positions, inv_freq, out=None, y=None, y_out=None, interleaved: bool = False, scale: float = 1.0,
+            inverse: bool = False, stream=None):
+    """Rotary positions of ``x`` ([T, H, rot], bf16, fp16 or fp32: a slice of wider heads may be given) into ``out``
+    (``x`` itself when None), and in the same launch of ``y`` ([T, H2, rot]) into ``y_out``. ``positions`` is int32 [T],
+    ``inv_freq`` float64 [rot / 2] on the GPU (see hs_rope_inv_freq)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.dtype not in _ROPE_DTYPES:
+        raise HSError(1, "x must be a bf16, fp16 or fp32 CUDA tensor [T, H, rot]")
+    T, H, rot = x.shape
+    out = x if out is None else out
+    _rope_tensor(x, "x", T, rot, x.dtype), _rope_tensor(out, "out", T, rot, x.dtype)
+    _dev(positions, "positions", torch.int32), _dev(inv_freq, "inv_freq", torch.float64)
+    if out.shape[1] != H or positions.shape != (T,) or inv_freq.shape != (rot // 2,):
+        raise HSError(1, "shape mismatch: out [T, H, rot], positions [T], inv_freq [rot / 2]")
+    a = _RopeArgs(T, H, 0, rot, _ROPE_DTYPES[x.dtype], int(bool(interleaved)), int(bool(inverse)), float(scale), _ptr(positions),
+                  _ptr(inv_freq), _ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0), out.stride(1))
+    if y is not None:
+        y_out = y if y_out is None else y_out
+        _rope_tensor(y, "y", T, rot, x.dtype), _rope_tensor(y_out, "y_out", T, rot, x.dtype)
+        if y_out.shape[1] != y.shape[1]:
+            raise HSError(1, "shape mismatch: y_out has other heads than y")
+        a.H2, a.y, a.y_stride_t, a.y_stride_h = y.shape[1], _ptr(y), y.stride(0), y.stride(1)
+        a.y_out, a.y_out_stride_t, a.y_out_stride_h = _ptr(y_out), y_out.stride(0), y_out.stride(1)
+    _check(load().hs_rope(ctypes.byref(a), _stream(stream)))
+
+
+class _PagedMlaArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("B", _i32), ("H", _i32), ("causal", _i32), ("q", _P), ("kv_pool", _P), ("R", _i64),
+                ("block_table", _P), ("bt_stride", _i32), ("req_start", _P), ("seq_len", _P), ("kv_tokens", _i64),
+                ("softmax_scale", _f32), ("out", _P), ("lse", _P), ("err_flag", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+def hs_paged_mla_workspace_size(T: int, B: int, H: int, kv_tokens: int) -> int:
+    """Bytes of workspace hs_paged_mla_fwd needs for at most these sizes on the current device."""
+    n = ctypes.c_uint64(0)
+    _check(load().hs_paged_mla_workspace_size(int(T), int(B), int(H), int(kv_tokens), ctypes.byref(n)))
+    return int(n.value)
+
+
+def hs_paged_mla_fwd(q, kv_pool, block_table, req_start, seq_len, kv_tokens: int, softmax_scale: float, out, err_flag,
+                     workspace, lse=None, causal: bool = True, stream=None):
+    """Dense attention of each request's new tokens over its paged rows: ``out`` bf16 [T, H, 512] (and ``lse`` float32
+    [T, H] if given). Request r's tokens are ``req_start[r] .. req_start[r + 1] - 1`` (int32 [B + 1]); its cache holds
+    ``seq_len[r]`` rows (int32 [B]), theirs last; ``kv_tokens`` bounds the sum of seq_len. See include/hs.h."""
+    _dev(q, "q", torch.bfloat16), _dev(kv_pool, "kv_pool", torch.uint8), _dev(block_table, "block_table", torch.int32)
+    _dev(req_start, "req_start", torch.int32), _dev(seq_len, "seq_len", torch.int32), _dev(out, "out", torch.bfloat16)
+    _dev(err_flag, "err_flag", torch.int32), _dev(workspace, "workspace", torch.uint8), _dev(lse, "lse", torch.float32)
+    T, H, D = q.shape
+    B = block_table.shape[0]
+    if D != 576 or kv_pool.shape[-1] != 656 or out.shape != (T, H, 512) or req_start.shape != (B + 1,) or seq_len.shape != (B,) \
+            or (lse is not None and lse.shape != (T, H)):
+        raise HSError(1, "shape mismatch: q [T,H,576], kv_pool [R,656], block_table [B,pages], req_start [B+1], seq_len [B], "
+                         "out [T,H,512], lse [T,H]")
+    a = _PagedMlaArgs(T, B, H, int(bool(causal)), _ptr(q), _ptr(kv_pool), kv_pool.shape[0], _ptr(block_table),
+                      block_table.shape[1], _ptr(req_start), _ptr(seq_len), int(kv_tokens), float(softmax_scale), _ptr(out),
+                      _ptr(lse), _ptr(err_flag), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    _check(load().hs_paged_mla_fwd(ctypes.byref(a), _stream(stream)))
+
+
+class _CopyArgs(ctypes.Structure):
+    _fields_ = [("n", _i32), ("L", _i32), ("Li", _i32), ("Di", _i32), ("src", _P), ("dst", _P), ("rows", _P), ("nblk", _i64),
+                ("pools", _P), ("k_caches", _P), ("k_scales", _P), ("err_flag", _P)]
+
+
+class _ForkArgs(ctypes.Structure):
+    _fields_ = [("n", _i32), ("B", _i32), ("bt_stride", _i32), ("L", _i32), ("Li", _i32), ("Di", _i32), ("parent", _P),
+                ("child", _P), ("block_table", _P), ("seq_len", _P), ("refcount", _P), ("nblk", _i64), ("src", _P), ("dst", _P),
+                ("pools", _P), ("k_caches", _P), ("k_scales", _P), ("err_flag", _P)]
+
+
+class _FreeArgs(ctypes.Structure):
+    _fields_ = [("n", _i32), ("B", _i32), ("bt_stride", _i32), ("req", _P), ("block_table", _P), ("seq_len", _P),
+                ("refcount", _P), ("nblk", _i64), ("err_flag", _P)]
+
+
+class _CompactArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("bt_stride", _i32), ("L", _i32), ("Li", _i32), ("Di", _i32), ("block_table", _P),
+                ("refcount", _P), ("nblk", _i64), ("table_out", _P), ("refcount_out", _P), ("src", _P), ("dst", _P),
+                ("counts", _P), ("pools", _P), ("k_caches", _P), ("k_scales", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_uint64), ("err_flag", _P)]
+
+
+def _layers(a, pools, k_caches, k_scales, Di):
+    for t, n in ((pools, "pools"), (k_caches, "k_caches"), (k_scales, "k_scales")):
+        _dev(t, n, torch.int64)
+    a.L = 0 if pools is None else pools.shape[0]
+    a.Li = 0 if k_caches is None else k_caches.shape[0]
+    if a.Li != (0 if k_scales is None else k_scales.shape[0]):
+        raise HSError(1, "k_caches and k_scales must have the same length")
+    a.Di, a.pools, a.k_caches, a.k_scales = int(Di), _ptr(pools), _ptr(k_caches), _ptr(k_scales)
+
+
+def _ints(pairs):
+    for t, n in pairs:
+        _dev(t, n, torch.int32)
+
+
+def hs_kv_copy_pages(src, dst, nblk: int, err_flag, rows=None, pools=None, k_caches=None, k_scales=None, Di: int = 128,
+                     stream=None):
+    """Rows 0 .. rows[i] - 1 (all 64 when ``rows`` is None) of page ``src[i]`` to page ``dst[i]`` in every layer.
+    ``pools`` is an int64 CUDA tensor [L] of device pointers to the latent pools, ``k_caches`` / ``k_scales`` [Li] to the
+    indexer caches and their scales."""
+    _ints(((src, "src"), (dst, "dst"), (rows, "rows"), (err_flag, "err_flag")))
+    a = _CopyArgs()
+    a.n, a.src, a.dst, a.rows, a.nblk, a.err_flag = src.shape[0], _ptr(src), _ptr(dst), _ptr(rows), int(nblk), _ptr(err_flag)
+    if dst.shape[0] != a.n or (rows is not None and rows.shape[0] != a.n):
+        raise HSError(1, "src, dst and rows must have the same length")
+    _layers(a, pools, k_caches, k_scales, Di)
+    _check(load().hs_kv_copy_pages(ctypes.byref(a), _stream(stream)))
+
+
+def hs_kv_fork(parent, child, block_table, seq_len, refcount, src, dst, err_flag, pools=None, k_caches=None, k_scales=None,
+               Di: int = 128, stream=None):
+    """Requests ``child[i]`` become copies of ``parent[i]``: complete pages are shared, the last, partial one is copied
+    to the lowest free page in every layer. ``block_table`` [B, pages], ``seq_len`` [B] and ``refcount`` [nblk] are updated
+    in place; ``src`` / ``dst`` (int32 [n]) receive the pages copied and taken. See include/hs.h."""
+    _ints(((parent, "parent"), (child, "child"), (block_table, "block_table"), (seq_len, "seq_len"), (refcount, "refcount"),
+           (src, "src"), (dst, "dst"), (err_flag, "err_flag")))
+    a = _ForkArgs()
+    a.n, a.B, a.bt_stride, a.nblk = parent.shape[0], block_table.shape[0], block_table.shape[1], refcount.shape[0]
+    if not (child.shape[0] == src.shape[0] == dst.shape[0] == a.n) or seq_len.shape[0] != a.B:
+        raise HSError(1, "parent, child, src and dst must have the same length, and seq_len one entry per request")
+    a.parent, a.child, a.block_table, a.seq_len, a.refcount = _ptr(parent), _ptr(child), _ptr(block_table), _ptr(seq_len), \
+        _ptr(refcount)
+    a.src, a.dst, a.err_flag = _ptr(src), _ptr(dst), _ptr(err_flag)
+    _layers(a, pools, k_caches, k_scales, Di)
+    _check(load().hs_kv_fork(ctypes.byref(a), _stream(stream)))
+
+
+def hs_kv_free(req, block_table, seq_len, refcount, err_flag, stream=None):
+    """Requests ``req[i]`` give their pages back (``refcount`` - 1 each) and become empty, in place."""
+    _ints(((req, "req"), (block_table, "block_table"), (seq_len, "seq_len"), (refcount, "refcount"), (err_flag, "err_flag")))
+    if seq_len.shape[0] != block_table.shape[0]:
+        raise HSError(1, "seq_len must have one entry per request")
+    a = _FreeArgs(req.shape[0], block_table.shape[0], block_table.shape[1], _ptr(req), _ptr(block_table), _ptr(seq_len),
+                  _ptr(refcount), refcount.shape[0], _ptr(err_flag))
+    _check(load().hs_kv_free(ctypes.byref(a), _stream(stream)))
+
+
+def hs_kv_compact_workspace_size(nblk: int) -> int:
+    """Bytes of workspace hs_kv_compact needs for a cache of nblk pages."""
+    n = ctypes.c_uint64(0)
+    _check(load().hs_kv_compact_workspace_size(int(nblk), ctypes.byref(n)))
+    return int(n.value)
+
+
+def hs_kv_compact(block_table, refcount, table_out, refcount_out, src, dst, counts, err_flag, workspace, pools=None,
+                  k_caches=None, k_scales=None, Di: int = 128, stream=None):
+    """Move the pages in use into the lowest ids, in every layer; ``table_out`` and ``refcount_out`` (the inputs
+    themselves are allowed) receive the new state, ``src`` / ``dst`` (int32 [nblk]) the moves, ``counts`` (int32 [2])
+    {pages in use, moves}. See include/hs.h."""
+    _ints(((block_table, "block_table"), (refcount, "refcount"), (table_out, "table_out"), (refcount_out, "refcount_out"),
+           (src, "src"), (dst, "dst"), (counts, "counts"), (err_flag, "err_flag")))
+    _dev(workspace, "workspace", torch.uint8)
+    a = _CompactArgs()
+    a.B, a.bt_stride, a.nblk = block_table.shape[0], block_table.shape[1], refcount.shape[0]
+    if table_out.shape != block_table.shape or counts.shape != (2,) or \
+            not (refcount_out.shape[0] == src.shape[0] == dst.shape[0] == a.nblk):
+        raise HSError(1, "table_out must have block_table's shape, refcount_out, src and dst one entry per page, counts two")
+    a.block_table, a.refcount, a.table_out, a.refcount_out = _ptr(block_table), _ptr(refcount), _ptr(table_out), _ptr(refcount_out)
+    a.src, a.dst, a.counts, a.workspace, a.workspace_bytes = _ptr(src), _ptr(dst), _ptr(counts), _ptr(workspace), workspace.numel()
+    a.err_flag = _ptr(err_flag)
+    _layers(a, pools, k_caches, k_scales, Di)
+    _check(load().hs_kv_compact(ctypes.byref(a), _stream(stream)))

@@ -1,6 +1,7 @@
 // hs_api.cu — the C ABI declared in include/hs.h: host-side argument checks, then launches.
 // Nothing here allocates device memory, synchronises the stream (hs_check_flag aside) or keeps
 // state between calls except the calling thread's last error text.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <unistd.h>
@@ -19,6 +20,14 @@ cudaError_t launch_append(const hs_kv_append_args* a, int sms, cudaStream_t stre
 cudaError_t launch_offload(const hs_kv_offload_args* a, int sms, cudaStream_t stream);
 cudaError_t launch_touch_host(int32_t B, const uint8_t* const* host_rows, const int32_t* seq_len,
                               const int32_t* resident_start, int64_t page, int32_t* err, cudaStream_t stream);
+cudaError_t launch_rope(const hs_rope_args* a, int sms, cudaStream_t stream);
+cudaError_t launch_paged_mla(const hs_paged_mla_args* a, int sms, cudaStream_t stream, const char** why);
+uint64_t paged_mla_workspace_bytes(int sms);
+cudaError_t launch_copy_pages(const hs_kv_copy_args* a, int sms, cudaStream_t stream);
+cudaError_t launch_fork(const hs_kv_fork_args* a, cudaStream_t stream);
+cudaError_t launch_free(const hs_kv_free_args* a, cudaStream_t stream);
+cudaError_t launch_compact(const hs_kv_compact_args* a, int sms, cudaStream_t stream);
+uint64_t compact_workspace_bytes(int64_t nblk);
 }  // namespace hs
 
 namespace {
@@ -279,6 +288,163 @@ hs_status hs_hisparse_touch_host(int32_t B, const uint8_t* const* host_rows, con
   return launched(hs::launch_touch_host(B, host_rows, seq_len, resident_start, page > 0 ? page : 4096, err_flag,
                                         (cudaStream_t)stream),
                   "hs_hisparse_touch_host", nullptr);
+}
+
+hs_status hs_rope(const hs_rope_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->T >= 0 && a->H >= 1, "need T >= 0 and H >= 1 (T=%d, H=%d)", a->T, a->H);
+  REQUIRE(a->rot >= 2 && a->rot <= 512 && a->rot % 2 == 0, "rot must be even, in [2, 512] (got %d)", a->rot);
+  REQUIRE(a->dtype == HS_BF16 || a->dtype == HS_FP16 || a->dtype == HS_FP32, "dtype must be HS_BF16, HS_FP16 or HS_FP32 (got %d)",
+          a->dtype);
+  REQUIRE(isfinite(a->scale), "scale is not finite");
+  if (a->T == 0) return ok();
+  REQUIRE(a->positions && a->inv_freq && a->x && a->out, "a required pointer is NULL");
+  REQUIRE(a->x_stride_t >= 0 && a->x_stride_h >= 0 && a->out_stride_t >= 0 && a->out_stride_h >= 0, "strides must be >= 0");
+  const uintptr_t mask = a->dtype == HS_FP32 ? 3 : 1;
+  REQUIRE((((uintptr_t)a->x | (uintptr_t)a->out | (uintptr_t)a->y | (uintptr_t)a->y_out) & mask) == 0,
+          "x, out, y and y_out must be aligned to their type");
+  int64_t heads = a->H;
+  if (a->y) {
+    REQUIRE(a->y_out && a->H2 >= 1, "y needs y_out and H2 >= 1");
+    REQUIRE(a->y_stride_t >= 0 && a->y_stride_h >= 0 && a->y_out_stride_t >= 0 && a->y_out_stride_h >= 0, "strides must be >= 0");
+    heads += a->H2;
+  }
+  REQUIRE(heads * a->rot <= (1 << 26), "too many values per token");
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  return launched(hs::launch_rope(a, sms, (cudaStream_t)stream), "hs_rope", nullptr);
+}
+
+hs_status hs_rope_inv_freq(int32_t rot, double base, int32_t kind, double factor, int32_t original, double beta_fast,
+                           double beta_slow, double* inv_freq, float* scale) {
+  REQUIRE(rot >= 2 && rot <= 512 && rot % 2 == 0, "rot must be even, in [2, 512] (got %d)", rot);
+  REQUIRE(base > 1.0 && isfinite(base), "base must be finite and > 1");
+  REQUIRE(kind == HS_ROPE_PLAIN || kind == HS_ROPE_LINEAR || kind == HS_ROPE_YARN, "unknown kind %d", kind);
+  REQUIRE(kind == HS_ROPE_PLAIN || (factor >= 1.0 && isfinite(factor)), "factor must be finite and >= 1");
+  REQUIRE(kind != HS_ROPE_YARN || (original >= 1 && beta_fast > beta_slow && beta_slow > 0.0 && isfinite(beta_fast)),
+          "need original >= 1 and beta_fast > beta_slow > 0");
+  REQUIRE(inv_freq && scale, "a required pointer is NULL");
+  double lo = 0.0, hi = 0.0;
+  if (kind == HS_ROPE_YARN) {
+    // the (real-valued) index of the pair that turns beta times within `original` positions
+    const double per = rot / (2.0 * log(base)), turn = 6.283185307179586476925;
+    lo = fmax(floor(per * log(original / (beta_fast * turn))), 0.0);
+    hi = fmin(ceil(per * log(original / (beta_slow * turn))), rot - 1.0);
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = pow(base, -2.0 * i / rot);
+    double slow = kind == HS_ROPE_LINEAR ? 1.0 : 0.0;  // share of the stretched angle
+    if (kind == HS_ROPE_YARN) slow = fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
+    inv_freq[i] = slow == 0.0 ? f : f / factor * slow + f * (1.0 - slow);
+  }
+  *scale = kind == HS_ROPE_YARN && factor > 1.0 ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  return ok();
+}
+
+hs_status hs_paged_mla_workspace_size(int32_t T, int32_t B, int32_t H, int64_t kv_tokens, uint64_t* bytes) {
+  REQUIRE(bytes, "bytes is NULL");
+  REQUIRE(T >= 0 && B >= 1 && B <= 4096, "need T >= 0 and B in [1, 4096] (T=%d, B=%d)", T, B);
+  REQUIRE(H >= 1 && H <= 128, "H must be in [1, 128] (got %d)", H);
+  REQUIRE(kv_tokens >= 0 && kv_tokens <= INT32_MAX, "kv_tokens must be in [0, 2^31 - 1]");
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  *bytes = hs::paged_mla_workspace_bytes(sms);
+  return ok();
+}
+
+hs_status hs_paged_mla_fwd(const hs_paged_mla_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->T >= 0 && a->B >= 1 && a->B <= 4096, "need T >= 0 and B in [1, 4096] (T=%d, B=%d)", a->T, a->B);
+  REQUIRE(a->H >= 1 && a->H <= 128, "H must be in [1, 128] (got %d)", a->H);
+  REQUIRE(a->kv_tokens >= 0 && a->kv_tokens <= INT32_MAX, "kv_tokens must be in [0, 2^31 - 1]");
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->T == 0) return ok();
+  REQUIRE(a->q && a->kv_pool && a->block_table && a->req_start && a->seq_len && a->out && a->workspace, "a required pointer is NULL");
+  REQUIRE(aligned16(a->q) && aligned16(a->kv_pool) && aligned16(a->out) && aligned16(a->workspace),
+          "q, kv_pool, out and workspace must be 16-byte aligned");
+  REQUIRE(a->R >= 1 && a->R <= INT32_MAX, "R must be in [1, 2^31 - 1]");
+  REQUIRE(a->bt_stride >= 1 && (int64_t)a->bt_stride * 64 <= INT32_MAX, "bt_stride out of range (%d)", a->bt_stride);
+  REQUIRE((int64_t)a->T * a->H <= INT32_MAX - 128, "T * H too large");
+  REQUIRE(isfinite(a->softmax_scale), "softmax_scale is not finite");
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  const uint64_t need = hs::paged_mla_workspace_bytes(sms);
+  REQUIRE(a->workspace_bytes >= need, "workspace holds %llu bytes; these sizes need %llu on this device",
+          (unsigned long long)a->workspace_bytes, (unsigned long long)need);
+  const char* why = nullptr;
+  return launched(hs::launch_paged_mla(a, sms, (cudaStream_t)stream, &why), "hs_paged_mla_fwd", why);
+}
+
+// The layers of a page operation: L latent pools, Li indexer caches.
+#define REQUIRE_LAYERS(a)                                                                                          \
+  REQUIRE((a)->L >= 0 && (a)->Li >= 0 && (a)->L + (a)->Li <= 4096, "need L, Li >= 0 and L + Li <= 4096");           \
+  REQUIRE((a)->L == 0 || (a)->pools, "pools is NULL");                                                             \
+  REQUIRE((a)->Li == 0 || ((a)->k_caches && (a)->k_scales), "k_caches or k_scales is NULL");                       \
+  REQUIRE((a)->Li == 0 || (a)->Di == 64 || (a)->Di == 128, "Di must be 64 or 128 (got %d)", (a)->Di);              \
+  REQUIRE((a)->nblk >= 1 && (a)->nblk * 64 <= INT32_MAX, "nblk out of range (%lld)", (long long)(a)->nblk)
+
+hs_status hs_kv_copy_pages(const hs_kv_copy_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->n >= 0, "n must be >= 0");
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->n == 0) return ok();
+  REQUIRE(a->src && a->dst, "a required pointer is NULL");
+  REQUIRE_LAYERS(a);
+  if (a->L + a->Li == 0) return ok();
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  return launched(hs::launch_copy_pages(a, sms, (cudaStream_t)stream), "hs_kv_copy_pages", nullptr);
+}
+
+hs_status hs_kv_fork(const hs_kv_fork_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->n >= 0 && a->n <= 8192, "n must be in [0, 8192] (got %d)", a->n);
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->n == 0) return ok();
+  REQUIRE(a->parent && a->child && a->block_table && a->seq_len && a->refcount && a->src && a->dst, "a required pointer is NULL");
+  REQUIRE(a->B >= 1 && a->bt_stride >= 1, "B and bt_stride must be >= 1");
+  REQUIRE_LAYERS(a);
+  hs_status st = check_device(nullptr);
+  if (st != HS_OK) return st;
+  return launched(hs::launch_fork(a, (cudaStream_t)stream), "hs_kv_fork", nullptr);
+}
+
+hs_status hs_kv_free(const hs_kv_free_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->n >= 0, "n must be >= 0");
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->n == 0) return ok();
+  REQUIRE(a->req && a->block_table && a->seq_len && a->refcount, "a required pointer is NULL");
+  REQUIRE(a->B >= 1 && a->bt_stride >= 1 && a->nblk >= 1, "B, bt_stride and nblk must be >= 1");
+  hs_status st = check_device(nullptr);
+  if (st != HS_OK) return st;
+  return launched(hs::launch_free(a, (cudaStream_t)stream), "hs_kv_free", nullptr);
+}
+
+hs_status hs_kv_compact_workspace_size(int64_t nblk, uint64_t* bytes) {
+  REQUIRE(bytes, "bytes is NULL");
+  REQUIRE(nblk >= 1 && nblk * 64 <= INT32_MAX, "nblk out of range (%lld)", (long long)nblk);
+  *bytes = hs::compact_workspace_bytes(nblk);
+  return ok();
+}
+
+hs_status hs_kv_compact(const hs_kv_compact_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->B >= 0 && a->bt_stride >= 1, "need B >= 0 and bt_stride >= 1");
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  REQUIRE_LAYERS(a);
+  REQUIRE(a->refcount && a->refcount_out && a->src && a->dst && a->counts && a->workspace, "a required pointer is NULL");
+  REQUIRE(a->B == 0 || (a->block_table && a->table_out), "block_table or table_out is NULL");
+  REQUIRE(((uintptr_t)a->workspace & 3) == 0 && a->workspace_bytes >= hs::compact_workspace_bytes(a->nblk),
+          "workspace must be 4-byte aligned and hold hs_kv_compact_workspace_size() bytes");
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  return launched(hs::launch_compact(a, sms, (cudaStream_t)stream), "hs_kv_compact", nullptr);
 }
 
 }  // extern "C"

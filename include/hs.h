@@ -18,6 +18,11 @@
  *   hs_hisparse_touch_host  map the host tier for the GPU once, before the first resolve
  *   hs_kv_append        quantise new tokens into the paged FP8 rows and indexer keys
  *   hs_kv_offload       copy complete KV pages of every layer to the pinned host tier
+ *   hs_rope             rotary positions of queries and keys (any even part of a head)
+ *   hs_paged_mla_fwd    dense attention of each request's new tokens over its paged rows
+ *   hs_kv_copy_pages, hs_kv_fork, hs_kv_free, hs_kv_compact
+ *                       the pages of the cache: copied, shared with a forked request, given back,
+ *                       moved together
  *
  * Sources (web pages describing GLM-5.x serving with DSA in vLLM):
  *   [P1] "vLLM v0.32.0 GLM-5.3 サービング: 16基のH200上でのPCP、DCP、およびハイブリッドHiSparse"
@@ -80,7 +85,8 @@ typedef enum {
 #define HS_FLAG_NOT_ASCENDING  0x08  /* resolve: a request's indices are not strictly ascending */
 #define HS_FLAG_BAD_STATE      0x10  /* resolve: inconsistent LRU state (slot/token maps disagree) */
 #define HS_FLAG_TIMEOUT        0x20  /* a bounded in-kernel wait ran out */
-#define HS_FLAG_RANGE          0x40  /* sparse MLA: a value outside the 16-bit compute range (see below) */
+#define HS_FLAG_RANGE          0x40  /* MLA: a value outside the 16-bit compute range (see below) */
+#define HS_FLAG_NO_PAGES       0x80  /* fork: fewer free pages than forks that need one */
 
 #define HS_PAGE 64               /* tokens per KV page */
 #define HS_KV_ROW_BYTES 656      /* latent-KV row size */
@@ -444,6 +450,224 @@ typedef struct {
 } hs_kv_offload_args;
 
 hs_status hs_kv_offload(const hs_kv_offload_args* a, hs_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * hs_rope — rotary positions.
+ *
+ * The 64 RoPE values of a query and of a cached row ([P1] 「数字がうまくいく理由」) are rotated before
+ * hs_kv_append stores them and the MLA reads them "as given"; so is a part of each indexer query and
+ * key. For token t at position p = positions[t] and pair i < rot / 2, with theta = p * inv_freq[i]:
+ *   (a, b) -> scale * (a cos theta - b sin theta, a sin theta + b cos theta)
+ * (a, b) are values (2i, 2i + 1) of the rotary part (interleaved != 0) or (i, i + rot / 2).
+ * inverse != 0 turns by -theta (undoing a rotation; the gradient's direction). Arithmetic is fp32,
+ * rounded once to the type; the angle is reduced exactly (whole turns dropped in 64-bit fixed point), so
+ * positions up to 2^31 lose nothing. Positions may be negative.
+ *
+ * x and out may be the same tensor (in place). Only the rot values of each head are read and written:
+ * the pointers are to the first value of the rotary part of token 0's head 0, the strides (in elements)
+ * say where the next token and head are, so that "part of a head" is a slice and the result can go
+ * straight into its place in a wider tensor. y is a second tensor of the same type turned by the same
+ * call (the shared key), or NULL.
+ *
+ *   T, H, rot     tokens, heads of x, values turned per head (even, 2 <= rot <= 512)
+ *   H2            heads of y (ignored when y is NULL)
+ *   dtype         HS_BF16, HS_FP16 or HS_FP32
+ *   positions     int32 [T];  inv_freq  fp64 [rot / 2] (hs_rope_inv_freq fills it on the host)
+ *   strides       >= 0; addresses and strides that are all multiples of 16 bytes take wide accesses
+ * ---------------------------------------------------------------------------------------- */
+#define HS_BF16 0
+#define HS_FP16 1
+#define HS_FP32 2
+
+typedef struct {
+  int32_t T, H, H2, rot, dtype, interleaved, inverse;
+  float scale;
+  const int32_t* positions;
+  const double* inv_freq;
+  const void* x;
+  int64_t x_stride_t, x_stride_h;
+  void* out;
+  int64_t out_stride_t, out_stride_h;
+  const void* y;
+  int64_t y_stride_t, y_stride_h;
+  void* y_out;
+  int64_t y_out_stride_t, y_out_stride_h;
+} hs_rope_args;
+
+hs_status hs_rope(const hs_rope_args* a, hs_stream_t stream);
+
+/* Host only: the angle per position of each pair, inv_freq[i] = base^(-2i / rot) (radians, fp64), and the
+ * scale that hs_rope takes, for contexts `factor` times as long as the `original` one it was trained on:
+ *   HS_ROPE_PLAIN   as it is (factor and original ignored), scale 1
+ *   HS_ROPE_LINEAR  every angle divided by factor, scale 1
+ *   HS_ROPE_YARN    pairs that turn more than beta_fast times within `original` positions are kept, those
+ *                   that turn less than beta_slow times are divided by factor, a linear ramp over the pair's
+ *                   index between; scale = 0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023) */
+#define HS_ROPE_PLAIN 0
+#define HS_ROPE_LINEAR 1
+#define HS_ROPE_YARN 2
+hs_status hs_rope_inv_freq(int32_t rot, double base, int32_t kind, double factor, int32_t original, double beta_fast,
+                           double beta_slow, double* inv_freq, float* scale);
+
+/* ------------------------------------------------------------------------------------------
+ * hs_paged_mla_fwd — dense attention of each request's new tokens over its paged latent rows.
+ *
+ * [P1] 「再現方法と必要なフラグ」: prompts no longer than top-k take a dense path, which needs neither
+ * indexer nor top-k. MQA form over the same 656-byte rows as hs_sparse_mla_fwd. Request r's new tokens are
+ * tokens req_start[r] .. req_start[r + 1] - 1; its cache holds seq_len[r] rows, the new tokens' own rows
+ * (hs_kv_append) being the last of them. With m = req_start[r + 1] - req_start[r], its i-th new token sees
+ *   n = seq_len[r] - m + 1 + i  rows (causal != 0; none where that is <= 0)   or   n = seq_len[r] rows,
+ *   logit_j = softmax_scale * <q[t,h,:], [latent_j, rope_j]>,   j < n
+ *   out[t,h,:] = sum_j softmax(logit)_j * latent_j,   lse[t,h] = ln sum_j exp(logit_j)
+ * A token that sees no row gets out = 0, lse = -inf. A request may have no new tokens.
+ *
+ * Compute precision as hs_sparse_mla_fwd: rows dequantised to fp16 (one rounding of code * scale), q
+ * latent part fp16 (a row of q whose largest value fp16 cannot hold well is scaled by a power of two), RoPE
+ * part bf16, P fp16, accumulation, maxima and sums fp32, partial results of a split request fp32. A group
+ * scale outside [2^-14, 146] or a latent q value that is not finite sets HS_FLAG_RANGE; the result is then
+ * not reliable for the tokens that see that row. A latent code that is NaN makes the outputs of the tokens that see
+ * its row NaN; rows that a token does not see never reach its output, whatever they hold.
+ *
+ *   T, B, H       new tokens in all, requests (1 <= B <= 4096), heads (1 <= H <= 128)
+ *   q             bf16 [T, H, 576] (16-byte aligned)
+ *   kv_pool, R    uint8 [R, 656] (16-byte aligned)
+ *   block_table   int32 [B, bt_stride]
+ *   req_start     int32 [B + 1], ascending, req_start[0] = 0, req_start[B] = T
+ *   seq_len       int32 [B], in [0, bt_stride * 64]
+ *   kv_tokens     the caller's bound on the sum of seq_len (its own lengths are known on the host); it sizes the workspace
+ *   out, lse      bf16 [T, H, 512];  fp32 [T, H] or NULL
+ *   err_flag      req_start out of order sets HS_FLAG_BAD_INDEX, a length outside its limits or a sum above
+ *                 kv_tokens HS_FLAG_BAD_LENGTH (such requests see no row); a block outside the pool sets
+ *                 HS_FLAG_BAD_BLOCK and its rows count as not there
+ *   workspace     hs_paged_mla_workspace_size() bytes of 16-byte aligned device memory, scratch; calls that share
+ *                 one must not overlap on the GPU
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, B, H, causal;
+  const uint16_t* q;
+  const uint8_t* kv_pool;
+  int64_t R;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  const int32_t* req_start;
+  const int32_t* seq_len;
+  int64_t kv_tokens;
+  float softmax_scale;
+  uint16_t* out;
+  float* lse;
+  int32_t* err_flag;
+  void* workspace;
+  uint64_t workspace_bytes;
+} hs_paged_mla_args;
+
+hs_status hs_paged_mla_fwd(const hs_paged_mla_args* a, hs_stream_t stream);
+
+/* Bytes of workspace hs_paged_mla_fwd needs for these sizes on the current device. It never shrinks as a
+ * size grows, so the size for a service's limits serves every smaller call. */
+hs_status hs_paged_mla_workspace_size(int32_t T, int32_t B, int32_t H, int64_t kv_tokens, uint64_t* bytes);
+
+/* ------------------------------------------------------------------------------------------
+ * The pages of the cache. [P3] 「主要なアーキテクチャ的詳細」: requests borrow ordinary blocks from one
+ * pool, with one block table for all layers. The caller's state is
+ *   block_table   int32 [B, bt_stride], -1 where there is no page
+ *   seq_len       int32 [B], cached tokens of each request
+ *   refcount      int32 [nblk], requests that hold each page; 0 (or less): free
+ * and a page is 64 rows of each of the L latent pools and 64 keys with their scales of each of the Li indexer
+ * caches, given as device arrays of device pointers (L + Li may be 0: only the tables change):
+ *   pools [L] to uint8 [>= nblk * 64, 656];  k_caches [Li] to uint8 [nblk, 64, Di], k_scales [Li] to fp32 [nblk, 64]
+ *   (16-byte aligned pools and k_caches, 4-byte aligned scales; a misaligned one sets HS_FLAG_BAD_INDEX and is skipped)
+ * Pages are chosen by index (lowest first), so results do not depend on timing. A page id outside
+ * [0, nblk) sets HS_FLAG_BAD_BLOCK.
+ *
+ * hs_kv_copy_pages — for each entry i < n: rows 0 .. rows[i] - 1 (all 64 when rows is NULL) of page src[i] go to
+ *   page dst[i] in every layer. An entry with a negative page is skipped. Two entries with one dst, or a
+ *   dst that is another entry's src, race (caller error).
+ *
+ * hs_kv_fork — for each i < n, request child[i] becomes a copy of request parent[i]: it shares the
+ *   complete pages (refcount + 1) and gets a page of its own for the last, partial one, the lowest free page not
+ *   taken by a fork before it, with that page's rows in use copied in every layer. src[i] / dst[i]
+ *   (int32 [n], outputs) are the page copied and the page taken, -1 without one. The child's row and length
+ *   are overwritten (free it first). A fork for which no page is free sets HS_FLAG_NO_PAGES, one whose
+ *   request is out of range (or parent == child) HS_FLAG_BAD_INDEX, one whose parent's length is outside the
+ *   table HS_FLAG_BAD_LENGTH; such a child is left with no tokens (a child out of range: nothing is written). No child may be
+ *   listed twice or be a parent in the same call (caller error). 0 <= n <= 8192.
+ *
+ * hs_kv_free — for each i < n, request req[i] (negative: skipped) gives its pages back: refcount - 1 for each page
+ *   of its seq_len tokens, its row -1, its length 0. A page whose count is not positive sets
+ *   HS_FLAG_BAD_STATE and keeps its count. No request may be listed twice.
+ *
+ * hs_kv_compact — with U pages in use (refcount > 0), the i-th page in use with an id >= U moves to
+ *   the i-th free page with an id < U, so that afterwards the pages 0 .. U - 1 are in use and the rest is
+ *   free. Rows and keys are copied in every layer; table_out and refcount_out (which may be block_table and
+ *   refcount themselves) receive the new state; src / dst (int32 [nblk], outputs) list the moves, -1 after the
+ *   last; counts (int32 [2], output) = {U, moves}. The contents of pages that were moved away stay. A table
+ *   entry that names a page past U nobody uses sets HS_FLAG_BAD_STATE and stays. workspace:
+ *   hs_kv_compact_workspace_size() bytes, 4-byte aligned, scratch.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t n, L, Li, Di;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* rows;
+  int64_t nblk;
+  uint8_t* const* pools;
+  uint8_t* const* k_caches;
+  float* const* k_scales;
+  int32_t* err_flag;
+} hs_kv_copy_args;
+
+hs_status hs_kv_copy_pages(const hs_kv_copy_args* a, hs_stream_t stream);
+
+typedef struct {
+  int32_t n, B, bt_stride, L, Li, Di;
+  const int32_t* parent;
+  const int32_t* child;
+  int32_t* block_table;
+  int32_t* seq_len;
+  int32_t* refcount;
+  int64_t nblk;
+  int32_t* src;
+  int32_t* dst;
+  uint8_t* const* pools;
+  uint8_t* const* k_caches;
+  float* const* k_scales;
+  int32_t* err_flag;
+} hs_kv_fork_args;
+
+hs_status hs_kv_fork(const hs_kv_fork_args* a, hs_stream_t stream);
+
+typedef struct {
+  int32_t n, B, bt_stride;
+  const int32_t* req;
+  int32_t* block_table;
+  int32_t* seq_len;
+  int32_t* refcount;
+  int64_t nblk;
+  int32_t* err_flag;
+} hs_kv_free_args;
+
+hs_status hs_kv_free(const hs_kv_free_args* a, hs_stream_t stream);
+
+typedef struct {
+  int32_t B, bt_stride, L, Li, Di;
+  const int32_t* block_table;
+  const int32_t* refcount;
+  int64_t nblk;
+  int32_t* table_out;
+  int32_t* refcount_out;
+  int32_t* src;
+  int32_t* dst;
+  int32_t* counts;
+  uint8_t* const* pools;
+  uint8_t* const* k_caches;
+  float* const* k_scales;
+  void* workspace;
+  uint64_t workspace_bytes;
+  int32_t* err_flag;
+} hs_kv_compact_args;
+
+hs_status hs_kv_compact(const hs_kv_compact_args* a, hs_stream_t stream);
+hs_status hs_kv_compact_workspace_size(int64_t nblk, uint64_t* bytes);
 
 #ifdef __cplusplus
 }
