@@ -1,0 +1,287 @@
+// paged.cuh — what the two kernels of the paged attention share: the batch's work as units (block of
+// (token, head) rows, 128 cached rows), the dequantisation of a row, and the join of split blocks.
+#pragma once
+
+#include "cluster.cuh"
+
+namespace hs {
+namespace paged {
+
+constexpr int kKeys = 128;                     // cached rows per tile: two pages
+constexpr float kThreshold = 8.0f;             // log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kScaleMax = 65504.f / 448.f;   // |code * scale| stays finite in fp16
+constexpr float kScaleMin = 6.103515625e-05f;  // 2^-14: scales stay fp16 normals
+constexpr int kMaxReq = 4096;
+
+struct Desc {  // a block that starts in a cluster and goes on in the next ones
+  int32_t row0, nrows, nparts, pad;
+};
+
+struct Params {
+  int32_t T, B, H, causal, bt_stride, clusters;
+  const uint8_t* q;
+  const uint8_t* kv;
+  int64_t R;
+  const int32_t* bt;
+  const int32_t* req_start;
+  const int32_t* seq_len;
+  float scale_log2;  // |softmax_scale| * log2(e)
+  uint32_t flip;     // 0x80008000 when softmax_scale < 0: Q changes sign instead
+  __nv_bfloat16* out;
+  float* lse;
+  int32_t* err;
+  float* part_out;   // [2 clusters][128][512]: slot 2c: the part that ends or passes through cluster c, 2c + 1: one that starts there
+  float* part_lse;   // [2 clusters][128]
+  Desc* desc;        // [clusters]
+  const uint16_t* rows16;  // chunks: the dequantised rows [cap][576]
+  int64_t kv_tokens;
+};
+
+struct Req {
+  int32_t start, m, seq, nb;  // first token, new tokens, cached rows, row blocks
+};
+
+template <int kRows>
+__device__ __forceinline__ Req load_req(const Params& p, int r) {
+  Req q;
+  const int a = p.req_start[r], b = p.req_start[r + 1], s = p.seq_len[r];
+  const bool ok = a >= 0 && a <= b && b <= p.T;
+  q.start = ok ? a : 0;
+  q.m = ok ? b - a : 0;
+  q.seq = s >= 0 && s <= (int64_t)p.bt_stride * HS_PAGE ? s : 0;
+  q.nb = (int)(((int64_t)q.m * p.H + kRows - 1) / kRows);
+  return q;
+}
+// cached rows that row g (of the request's (token, head) rows) sees
+__device__ __forceinline__ int sees(const Params& p, const Req& q, int64_t g) {
+  if (!p.causal) return q.seq;
+  const int n = q.seq - q.m + 1 + (int)(g / p.H);
+  return n < 0 ? 0 : n;
+}
+template <int kRows>
+__device__ __forceinline__ int block_rows(const Params& p, const Req& q, int b) {
+  const int64_t left = (int64_t)q.m * p.H - (int64_t)b * kRows;
+  return left < kRows ? (int)left : kRows;
+}
+template <int kRows>
+__device__ __forceinline__ int block_tiles(const Params& p, const Req& q, int b) {
+  const int n = sees(p, q, (int64_t)b * kRows + block_rows<kRows>(p, q, b) - 1);
+  return n > 0 ? (n + kKeys - 1) / kKeys : 1;  // a block that sees nothing still writes its zeros
+}
+
+__host__ __device__ __forceinline__ int64_t unit_begin(int64_t c, int64_t U, int64_t C) { return c * U / C; }
+__device__ __forceinline__ int64_t unit_cta(int64_t u, int64_t U, int64_t C) { return ((u + 1) * C - 1) / U; }
+
+// Where a cluster's units begin: found by every CTA of it at its start, in shared memory.
+struct Start {
+  int64_t u0, u1, U;  // the cluster's units, all units
+  int64_t base;       // rows before request r in the dequantised copy
+  int32_t r, b, ta;   // request, block and tile of u0
+};
+
+// Rows that a request takes in the dequantised copy: whole tiles, one at least (zeros), none without new tokens.
+__device__ __forceinline__ int64_t copy_rows(const Req& q) {
+  return q.m == 0 ? 0 : q.seq == 0 ? kKeys : (int64_t)(q.seq + kKeys - 1) / kKeys * kKeys;
+}
+
+// A cluster's units as segments: consecutive tiles [ta, tb) of one block.
+struct Seg {
+  Req q;
+  int r, b, ta, tb, tiles, nrows;
+  int64_t base;  // the request's first row in the dequantised copy
+};
+template <int kRows>
+struct Walk {
+  Req q;
+  int r, b, ta;
+  int64_t left, base;
+  __device__ __forceinline__ Walk(const Params& p, const Start& s) : r(s.r), b(s.b), ta(s.ta), left(s.u1 - s.u0), base(s.base) {
+    q = load_req<kRows>(p, r);
+  }
+  __device__ __forceinline__ bool next(const Params& p, Seg& s) {
+    if (left <= 0) return false;
+    while (b >= q.nb) {
+      base += copy_rows(q);
+      q = load_req<kRows>(p, ++r);
+      b = 0;
+    }
+    s.q = q;
+    s.r = r;
+    s.b = b;
+    s.ta = ta;
+    s.base = base;
+    s.tiles = block_tiles<kRows>(p, q, b);
+    s.nrows = block_rows<kRows>(p, q, b);
+    s.tb = (int)(s.tiles < ta + left ? s.tiles : ta + left);
+    left -= s.tb - ta;
+    ta = 0;
+    ++b;
+    return true;
+  }
+};
+
+// Inclusive prefix sum over the lanes of a warp.
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// All threads of the CTA; `pre` is scratch for B + 1 sums. Prefix sums over the requests' units, then the
+// request, block and tile of this cluster's first unit. A batch whose lengths pass kv_tokens has no units.
+template <int kRows>
+__device__ __forceinline__ void find_units(const Params& p, int64_t* pre, Start* st, int c, int threads) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int r = warp; r < p.B; r += threads / 32) {
+    const Req q = load_req<kRows>(p, r);
+    int64_t sum = 0;
+    for (int b = lane; b < q.nb; b += 32) sum += block_tiles<kRows>(p, q, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) pre[r + 1] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t run = 0, cached = 0;
+    if (lane == 0) pre[0] = 0;
+    for (int at = 0; at < p.B; at += 32) {
+      const bool in = at + lane < p.B;
+      const int64_t x = warp_scan(in ? pre[at + lane + 1] : 0, lane);
+      if (in) {
+        pre[at + lane + 1] = run + x;
+        cached += load_req<kRows>(p, at + lane).seq;
+      }
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) cached += __shfl_xor_sync(0xffffffffu, cached, o);
+    __syncwarp();
+    if (cached > p.kv_tokens) {
+      run = 0;
+      if (c == 0 && lane == 0) flag_error(p.err, HS_FLAG_BAD_LENGTH);
+    }
+    const int64_t U = run, C = U < p.clusters ? U : p.clusters;
+    int64_t u0 = 0, u1 = 0, base = 0;
+    int lo = 0, b = 0, ta = 0;
+    if (c < C) {
+      u0 = unit_begin(c, U, C);
+      u1 = unit_begin(c + 1, U, C);
+      int hi = p.B;  // the request with pre[lo] <= u0 < pre[lo + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= u0)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      for (int r = lane; r < lo; r += 32) base += copy_rows(load_req<kRows>(p, r));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+      const Req q = load_req<kRows>(p, lo);
+      int64_t off = u0 - pre[lo];
+      for (int at = 0; at < q.nb; at += 32) {
+        const int t = at + lane < q.nb ? block_tiles<kRows>(p, q, at + lane) : 0;
+        const int64_t x = warp_scan(t, lane);
+        const uint32_t hit = __ballot_sync(0xffffffffu, x > off);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          b = at + l;
+          ta = (int)(off - __shfl_sync(0xffffffffu, x - t, l));
+          break;
+        }
+        off -= __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+    if (lane == 0) {
+      st->u0 = u0;
+      st->u1 = u1;
+      st->U = U;
+      st->base = base;
+      st->r = lo;
+      st->b = b;
+      st->ta = ta;
+    }
+  }
+  if (c == 0) {  // tell of bad lengths and offsets once
+    for (int r = tid; r < p.B; r += threads) {
+      const int a = p.req_start[r], e = p.req_start[r + 1], s = p.seq_len[r];
+      if (a < 0 || a > e || e > p.T || (r == 0 && a != 0) || (r == p.B - 1 && e != p.T)) flag_error(p.err, HS_FLAG_BAD_INDEX);
+      if (s < 0 || s > (int64_t)p.bt_stride * HS_PAGE) flag_error(p.err, HS_FLAG_BAD_LENGTH);
+    }
+  }
+}
+
+// 8 e4m3 codes -> 8 fp16 values code * scale, rounded once: the fp32 scale is split into fp16 hi + lo and
+// t = code * lo corrects fma(code, hi, t).
+__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, uint32_t hi2, uint32_t lo2) {
+  uint4 r;
+  asm("{ .reg .b16 a, b, c, d; .reg .b32 x, y, z, u, tx, ty, tz, tu;\n"
+      " mov.b32 {a, b}, %4; mov.b32 {c, d}, %5;\n"
+      " cvt.rn.f16x2.e4m3x2 x, a; cvt.rn.f16x2.e4m3x2 y, b; cvt.rn.f16x2.e4m3x2 z, c; cvt.rn.f16x2.e4m3x2 u, d;\n"
+      " mul.rn.f16x2 tx, x, %7; mul.rn.f16x2 ty, y, %7; mul.rn.f16x2 tz, z, %7; mul.rn.f16x2 tu, u, %7;\n"
+      " fma.rn.f16x2 %0, x, %6, tx; fma.rn.f16x2 %1, y, %6, ty; fma.rn.f16x2 %2, z, %6, tz; fma.rn.f16x2 %3, u, %6, tu; }"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "r"(w0), "r"(w1), "r"(hi2), "r"(lo2));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// whether one of the eight fp16 values is NaN or infinite (x * 0 is NaN then)
+__device__ __forceinline__ bool unsound(const uint4& a, const uint4& b) {
+  const __half2 z = __float2half2_rn(0.f);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  __half2 acc = z;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc = __hfma2(*reinterpret_cast<const __half2*>(&w[i]), z, acc);
+  return __hisnan(__low2half(acc)) || __hisnan(__high2half(acc));
+}
+
+// Joins the parts of the block that starts in cluster blockIdx.x and goes on in the next ones: each part is
+// normalised by its own sum, so out = sum_s e^(lse_s - lse) O_s. Eight rows per CTA.
+constexpr int kMergeThreads = 256, kMergeRows = 8, kMaxClusters = 128;
+template <int kRows>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Params p) {
+  const int c = blockIdx.x, r0 = blockIdx.y * kMergeRows;
+  const Desc d = p.desc[c];
+  if (d.nparts == 0 || r0 >= d.nrows) return;
+  __shared__ float w[kMaxClusters][kMergeRows];
+  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
+  if (threadIdx.x < kMergeRows) {
+    const int row = r0 + threadIdx.x;
+    float m = -INFINITY, z = 0.f;
+    for (int s = 0; s < d.nparts; ++s) m = fmaxf(m, p.part_lse[slot(s) * kRows + row]);
+    for (int s = 0; s < d.nparts; ++s) {
+      const float l = p.part_lse[slot(s) * kRows + row];
+      const float e = l == -INFINITY ? 0.f : __expf(l - (m == -INFINITY ? 0.f : m));
+      w[s][threadIdx.x] = e;
+      z += e;
+    }
+    for (int s = 0; s < d.nparts; ++s) w[s][threadIdx.x] = z == 0.f ? 0.f : w[s][threadIdx.x] / z;
+    if (p.lse && row < d.nrows) p.lse[(int64_t)d.row0 + row] = z == 0.f ? -INFINITY : m + __logf(z);
+  }
+  __syncthreads();
+  for (int v = threadIdx.x; v < kMergeRows * HS_D_LATENT / 4; v += kMergeThreads) {
+    const int row = v / (HS_D_LATENT / 4), col = 4 * (v % (HS_D_LATENT / 4));
+    if (r0 + row >= d.nrows) break;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < d.nparts; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(p.part_out + ((int64_t)slot(s) * kRows + r0 + row) * HS_D_LATENT + col);
+      const float ws = w[s][row];
+      a[0] += ws * x.x, a[1] += ws * x.y, a[2] += ws * x.z, a[3] += ws * x.w;
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a[0], a[1]), hi = __floats2bfloat162_rn(a[2], a[3]);
+    *reinterpret_cast<uint2*>(p.out + ((int64_t)d.row0 + r0 + row) * HS_D_LATENT + col) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+}  // namespace paged
+}  // namespace hs
