@@ -35,6 +35,13 @@ __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The same without releasing anything: for barriers that pass on no generic-proxy writes of this thread (what
+// they order are tensor-memory accesses, complete by then, and asynchronous copies that count on barriers). A
+// releasing arrival waits for the thread's earlier memory operations, about a thousand cycles.
+__device__ __forceinline__ void remote_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // Orders this thread's generic-proxy accesses of every state space with the async proxy (here: shared

@@ -15,7 +15,8 @@
 // Per tile of 128 cached rows and cluster: QK 36 MMAs of M 256, N 128, K 16 (64 cycles each), PV 16 of N 256 (128
 // cycles each) on the other pair: 2,304 cycles.
 //
-// Roles (384 threads). Softmax CTA: warp 0 loads K by TMA, warp 1 issues QK (CTA 0), warp 2 of CTA 1 tells CTA 0
+// Roles (384 threads). Softmax CTA: warp 0 loads K by TMA, warps 1 and 3 of CTA 0 issue QK, each for every other
+// tile (the tensor core queues too little to stay busy while one warp waits and commits), warp 2 of CTA 1 tells CTA 0
 // that its half of K is there, warps 4-11 are the softmax: thread = row and 64 of the tile's columns; two threads
 // of a row agree on the maximum through shared memory. P goes through shared memory to the CTA that keeps the same
 // rows' O, 4 KB per warp as one bulk copy. Output CTA: warp 0 loads V, warp 1 issues PV (CTA 2), warp 2 of CTA 3
@@ -144,8 +145,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     return;
   }
   uint64_t* bars = (uint64_t*)(smem + kOffBar);
-  uint64_t* full = bars;            // [5] this CTA's half of a stage has landed
-  uint64_t* peer = bars + 5;        // [5] issuing CTA: the other's half has landed
+  uint64_t* full = bars;            // [5] this CTA's half of a stage has landed; in the issuing CTA the other's too
   uint64_t* empty = bars + 10;      // [5] the MMAs have read the stage (both CTAs)
   uint64_t* s_full = bars + 15;     // [2] S complete (both)
   uint64_t* s_empty = bars + 17;    // [2] CTA 0: both CTAs' softmax warps have read S
@@ -157,6 +157,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* q_free = bars + 28;     // the block's QK MMAs have read Q (both)
   uint64_t* o_free = bars + 29;     // CTA 2: both CTAs have read O out
   uint64_t* drain = bars + 30;
+  uint64_t* drain2 = bars + 35;
   uint64_t* swap = bars + 31;       // [4] softmax CTA: the two warps of a lane quarter have written their values
   uint32_t* misc = (uint32_t*)(smem + kOffMisc);
   volatile uint32_t* abort_flag = misc + 1;
@@ -170,8 +171,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < 5; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&peer[s], 1);
+      mbar_init(&full[s], lead ? 2 : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -183,9 +183,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[s], 1);
     }
     mbar_init(q_ready, 16);
-    mbar_init(q_free, 1);
+    mbar_init(q_free, 2);
     mbar_init(o_free, 16);
     mbar_init(drain, 1);
+    mbar_init(drain2, 1);
     for (int q = 0; q < 4; ++q) mbar_init(&swap[q], 2);
     mbar_fence_init();
     misc[1] = 0;
@@ -246,7 +247,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       // every copy has landed before the CTA may leave
       for (int64_t j = issued > slots ? issued - slots : 0; j < issued; ++j) mbar_wait(&full[j % slots], (uint32_t)(j / slots) & 1u, p.err);
     }
-  } else if (warp == 1 && lead) {
+  } else if (lead && (warp == 1 || (warp == 3 && isA))) {
     // ================================================================ MMAs ======================
     if (lane == 0) {
       int slot = 0, i = 0, n = 0;
@@ -254,21 +255,26 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       const int slots = isA ? kStA : kStB;
       auto stage = [&]() -> bool {  // both halves of the next stage
-        const bool r = mbar_wait(&full[slot], par, p.err) && mbar_wait_cluster(&peer[slot], par, p.err);
+        const bool r = mbar_wait(&full[slot], par, p.err);
         tc_fence_after();
         return r;
       };
-      auto pass = [&]() {
-        mma2_commit(&empty[slot], pair_mask);
-        if (++slot == slots) {
-          slot = 0;
+      auto skip = [&](int k) {
+        slot += k;
+        if (slot >= slots) {
+          slot -= slots;
           par ^= 1u;
         }
+      };
+      auto pass = [&]() {
+        mma2_commit(&empty[slot], pair_mask);
+        skip(1);
       };
       if (isA) {
         constexpr uint32_t lat = idesc_f16(kRows, kKeys, 0, 0), rop = idesc_bf16(kRows, kKeys, 0, 0);
         const uint64_t qd = smem_desc(smem_u32(smem + kOffQ), 16, 1024, 2);
         const uint64_t kd = smem_desc(smem_u32(smem + kOffK), 16, 1024, 2);
+        const int mine = warp == 1 ? 0 : 1;  // the parity of the tiles that this warp issues
 #pragma unroll 1
         for (; ok && walk.next(p, s); ++n) {
           if (!mbar_wait_cluster(q_ready, (uint32_t)n & 1u, p.err)) {
@@ -278,8 +284,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_all();
 #pragma unroll 1
           for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
-            const uint32_t d = tmem + kKeys * (i & 1);
-            if (*abort_flag || !mbar_wait_cluster(&s_empty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err)) {
+            if ((i & 1) != mine) {
+              skip(3);
+              continue;
+            }
+            const uint32_t d = tmem + kKeys * mine;
+            if (*abort_flag || !mbar_wait(&s_empty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err)) {
               ok = false;
               break;
             }
@@ -312,13 +322,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t vd = smem_desc(smem_u32(smem + kOffV), kVBlk, 1024, 2);
 #pragma unroll 1
         for (; ok && walk.next(p, s); ++n) {
-          if (n > 0 && !mbar_wait_cluster(o_free, (uint32_t)(n - 1) & 1u, p.err)) {
+          if (n > 0 && !mbar_wait(o_free, (uint32_t)(n - 1) & 1u, p.err)) {
             ok = false;
             break;
           }
 #pragma unroll 1
           for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
-            if (*abort_flag || !mbar_wait_cluster(&corr[i & 1], (uint32_t)(i >> 1) & 1u, p.err)) {
+            if (*abort_flag || !mbar_wait(&corr[i & 1], (uint32_t)(i >> 1) & 1u, p.err)) {
               ok = false;
               break;
             }
@@ -341,13 +351,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) *abort_flag = 1;
-      mma2_commit(drain, (uint16_t)(1u << rank));
-      mbar_wait(drain, 0, p.err);
+      uint64_t* done = warp == 1 ? drain : drain2;
+      mma2_commit(done, (uint16_t)(1u << rank));
+      mbar_wait(done, 0, p.err);
     }
   } else if (warp == 2 && !lead) {
     // ================================================================ the other half is there ===
     if (lane == 0) {
-      const uint32_t to = remote_smem(peer, rank - 1);
+      const uint32_t to = remote_smem(full, rank - 1);
       const int slots = isA ? kStA : kStB;
       const int64_t stages = ntiles * (isA ? 3 : 2);
       int slot = 0;
@@ -358,7 +369,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           *abort_flag = 1;
           break;
         }
-        remote_arrive(to + 8 * (uint32_t)slot);
+        remote_arrive_relaxed(to + 8 * (uint32_t)slot);
         if (++slot == slots) {
           slot = 0;
           par ^= 1u;
@@ -384,7 +395,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&p_full[i & 1], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
-          remote_arrive(back + 8 * (uint32_t)(i & 1));
+          remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));
         }
       }
       if (!ok) *abort_flag = 1;
@@ -493,7 +504,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (idle) {
           __syncwarp();
-          if (lane == 0) remote_arrive(r_sempty + 8 * (uint32_t)b);
+          if (lane == 0) remote_arrive_relaxed(r_sempty + 8 * (uint32_t)b);
           continue;
         }
         uint32_t v[64];
@@ -508,7 +519,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) remote_arrive(r_sempty + 8 * (uint32_t)b);
+        if (lane == 0) remote_arrive_relaxed(r_sempty + 8 * (uint32_t)b);
         const bool there = page < p.bt_stride && k >= 0 && ((int64_t)k + 1) * HS_PAGE <= p.R;
         const int lim = there ? nsee - jt * kKeys - 64 * g : 0;  // columns that this thread's row sees
         if (!__all_sync(0xffffffffu, lim >= 64)) {
@@ -628,7 +639,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) remote_arrive(r_corr + 8 * (uint32_t)b);
+        if (lane == 0) remote_arrive_relaxed(r_corr + 8 * (uint32_t)b);
       }
       if (ok) ok = warp_wait_all(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
       if (!ok) break;
@@ -669,7 +680,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) remote_arrive(r_ofree);
+      if (lane == 0) remote_arrive_relaxed(r_ofree);
     }
     if (!ok) *abort_flag = 1;
     if (rank == 2 && warp == 4 && lane == 0) p.desc[c] = desc;
