@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -87,14 +88,14 @@ def load():
         lib.hs_hisparse_touch_host.argtypes = [_i32, _P, _P, _P, _P, _P]
         lib.hs_kv_append.argtypes = [ctypes.POINTER(_AppendArgs), _P]
         lib.hs_kv_offload.argtypes = [ctypes.POINTER(_OffloadArgs), _P]
-        lib.hs_rope.argtypes = [ctypes.POINTER(_RopeArgs), _P]
+        lib.hs_rope.argtypes = [_P, _P]
         lib.hs_rope_inv_freq.argtypes = [_i32, _f64, _i32, _f64, _i32, _f64, _f64, _P, _P]
-        lib.hs_paged_mla_fwd.argtypes = [ctypes.POINTER(_PagedMlaArgs), _P]
+        lib.hs_paged_mla_fwd.argtypes = [_P, _P]
         lib.hs_paged_mla_workspace_size.argtypes = [_i32, _i32, _i32, _i64, ctypes.POINTER(ctypes.c_uint64)]
-        lib.hs_kv_copy_pages.argtypes = [ctypes.POINTER(_CopyArgs), _P]
-        lib.hs_kv_fork.argtypes = [ctypes.POINTER(_ForkArgs), _P]
-        lib.hs_kv_free.argtypes = [ctypes.POINTER(_FreeArgs), _P]
-        lib.hs_kv_compact.argtypes = [ctypes.POINTER(_CompactArgs), _P]
+        lib.hs_kv_copy_pages.argtypes = [_P, _P]
+        lib.hs_kv_fork.argtypes = [_P, _P]
+        lib.hs_kv_free.argtypes = [_P, _P]
+        lib.hs_kv_compact.argtypes = [_P, _P]
         lib.hs_kv_compact_workspace_size.argtypes = [_i64, ctypes.POINTER(ctypes.c_uint64)]
         for f in ("hs_rope", "hs_rope_inv_freq", "hs_paged_mla_fwd", "hs_paged_mla_workspace_size", "hs_kv_copy_pages", "hs_kv_fork",
                   "hs_kv_free", "hs_kv_compact", "hs_kv_compact_workspace_size"):
@@ -107,7 +108,7 @@ def load():
 
 
 def _check(status: int):
-    if status != 0:
+    if status:
         raise HSError(status, load().hs_last_error().decode(errors="replace"))
 
 
@@ -128,8 +129,29 @@ def _dev(t, name, dtype=None):
 
 
 def _stream(stream) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+_CODES = {_P: "P", _i32: "i", _i64: "q", _f32: "f", _f64: "d", ctypes.c_uint64: "Q"}
+
+
+def _packer(cls):
+    """Packs an args struct's fields (pointers as integers, 0 for none) into bytes of its C layout, which a call reads in
+    place: a few times cheaper than filling the ctypes structure."""
+    return struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0P").pack
+
+
+def _tensor(t, name, dtype):
+    """The address of a contiguous CUDA tensor of this type."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise HSError(1, "%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
+        raise HSError(1, "%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise HSError(1, "%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def hs_abi_version() -> int:
@@ -331,6 +353,7 @@ class _RopeArgs(ctypes.Structure):
                 ("y_out_stride_h", _i64)]
 
 
+_pack_rope = _packer(_RopeArgs)
 _ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _ROPE_KINDS = {"plain": 0, "linear": 1, "yarn": 2}
 
@@ -348,10 +371,13 @@ def hs_rope_inv_freq(rot: int, base: float = 10000.0, kind: str = "plain", facto
 
 
 def _rope_tensor(t, name, T, rot, dtype):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise HSError(1, "%s must be a CUDA tensor" % name)
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != rot or t.dtype != dtype or t.stride(2) != 1:
-        raise HSError(1, "%s must be %s [T, heads, rot] with consecutive values in a head" % (name, dtype))
+    """Address, token and head strides and heads of a [T, heads, rot] tensor whose heads are consecutive values."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != 3:
+        raise HSError(1, "%s must be a %s CUDA tensor [T, heads, rot]" % (name, dtype))
+    (n, heads, r), (a, b, c) = t.shape, t.stride()
+    if n != T or r != rot or c != 1:
+        raise HSError(1, "%s must be [T, heads, rot] with consecutive values in a head" % name)
+    return t.data_ptr(), a, b, heads
 
 
 def hs_rope(x, positions, inv_freq, out=None, y=None, y_out=None, interleaved: bool = False, scale: float = 1.0,
@@ -359,24 +385,23 @@ def hs_rope(x, positions, inv_freq, out=None, y=None, y_out=None, interleaved: b
     """Rotary positions of ``x`` ([T, H, rot], bf16, fp16 or fp32: a slice of wider heads may be given) into ``out``
     (``x`` itself when None), and in the same launch of ``y`` ([T, H2, rot]) into ``y_out``. ``positions`` is int32 [T],
     ``inv_freq`` float64 [rot / 2] on the GPU (see hs_rope_inv_freq)."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.dtype not in _ROPE_DTYPES:
+    dtype = x.dtype if isinstance(x, torch.Tensor) else None
+    if dtype not in _ROPE_DTYPES or x.dim() != 3:
         raise HSError(1, "x must be a bf16, fp16 or fp32 CUDA tensor [T, H, rot]")
-    T, H, rot = x.shape
-    out = x if out is None else out
-    _rope_tensor(x, "x", T, rot, x.dtype), _rope_tensor(out, "out", T, rot, x.dtype)
-    _dev(positions, "positions", torch.int32), _dev(inv_freq, "inv_freq", torch.float64)
-    if out.shape[1] != H or positions.shape != (T,) or inv_freq.shape != (rot // 2,):
+    T, _, rot = x.shape
+    xp, xt, xh, H = _rope_tensor(x, "x", T, rot, dtype)
+    op, ot, oh, H1 = (xp, xt, xh, H) if out is None else _rope_tensor(out, "out", T, rot, dtype)
+    pos, inv = _tensor(positions, "positions", torch.int32), _tensor(inv_freq, "inv_freq", torch.float64)
+    if H1 != H or positions.numel() != T or inv_freq.numel() != rot // 2:
         raise HSError(1, "shape mismatch: out [T, H, rot], positions [T], inv_freq [rot / 2]")
-    a = _RopeArgs(T, H, 0, rot, _ROPE_DTYPES[x.dtype], int(bool(interleaved)), int(bool(inverse)), float(scale), _ptr(positions),
-                  _ptr(inv_freq), _ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0), out.stride(1))
+    yp = yt = yh = H2 = zp = zt = zh = 0
     if y is not None:
-        y_out = y if y_out is None else y_out
-        _rope_tensor(y, "y", T, rot, x.dtype), _rope_tensor(y_out, "y_out", T, rot, x.dtype)
-        if y_out.shape[1] != y.shape[1]:
+        yp, yt, yh, H2 = _rope_tensor(y, "y", T, rot, dtype)
+        zp, zt, zh, H3 = (yp, yt, yh, H2) if y_out is None else _rope_tensor(y_out, "y_out", T, rot, dtype)
+        if H3 != H2:
             raise HSError(1, "shape mismatch: y_out has other heads than y")
-        a.H2, a.y, a.y_stride_t, a.y_stride_h = y.shape[1], _ptr(y), y.stride(0), y.stride(1)
-        a.y_out, a.y_out_stride_t, a.y_out_stride_h = _ptr(y_out), y_out.stride(0), y_out.stride(1)
-    _check(load().hs_rope(ctypes.byref(a), _stream(stream)))
+    _check(load().hs_rope(_pack_rope(T, H, H2, rot, _ROPE_DTYPES[dtype], 1 if interleaved else 0, 1 if inverse else 0, scale, pos,
+                                     inv, xp, xt, xh, op, ot, oh, yp, yt, yh, zp, zt, zh), _stream(stream)))
 
 
 class _PagedMlaArgs(ctypes.Structure):
@@ -384,6 +409,9 @@ class _PagedMlaArgs(ctypes.Structure):
                 ("block_table", _P), ("bt_stride", _i32), ("req_start", _P), ("seq_len", _P), ("kv_tokens", _i64),
                 ("softmax_scale", _f32), ("out", _P), ("lse", _P), ("err_flag", _P), ("workspace", _P),
                 ("workspace_bytes", ctypes.c_uint64)]
+
+
+_pack_paged_mla = _packer(_PagedMlaArgs)
 
 
 def hs_paged_mla_workspace_size(T: int, B: int, H: int, kv_tokens: int) -> int:
@@ -398,19 +426,17 @@ def hs_paged_mla_fwd(q, kv_pool, block_table, req_start, seq_len, kv_tokens: int
     """Dense attention of each request's new tokens over its paged rows: ``out`` bf16 [T, H, 512] (and ``lse`` float32
     [T, H] if given). Request r's tokens are ``req_start[r] .. req_start[r + 1] - 1`` (int32 [B + 1]); its cache holds
     ``seq_len[r]`` rows (int32 [B]), theirs last; ``kv_tokens`` bounds the sum of seq_len. See include/hs.h."""
-    _dev(q, "q", torch.bfloat16), _dev(kv_pool, "kv_pool", torch.uint8), _dev(block_table, "block_table", torch.int32)
-    _dev(req_start, "req_start", torch.int32), _dev(seq_len, "seq_len", torch.int32), _dev(out, "out", torch.bfloat16)
-    _dev(err_flag, "err_flag", torch.int32), _dev(workspace, "workspace", torch.uint8), _dev(lse, "lse", torch.float32)
-    T, H, D = q.shape
-    B = block_table.shape[0]
-    if D != 576 or kv_pool.shape[-1] != 656 or out.shape != (T, H, 512) or req_start.shape != (B + 1,) or seq_len.shape != (B,) \
+    qp, kp, bp = _tensor(q, "q", torch.bfloat16), _tensor(kv_pool, "kv_pool", torch.uint8), _tensor(block_table, "block_table", torch.int32)
+    rp, sp = _tensor(req_start, "req_start", torch.int32), _tensor(seq_len, "seq_len", torch.int32)
+    op, ep, wp = _tensor(out, "out", torch.bfloat16), _tensor(err_flag, "err_flag", torch.int32), _tensor(workspace, "workspace", torch.uint8)
+    lp = 0 if lse is None else _tensor(lse, "lse", torch.float32)
+    (T, H, D), (B, pages), (R, row) = q.shape, block_table.shape, kv_pool.shape
+    if D != 576 or row != 656 or out.shape != (T, H, 512) or req_start.numel() != B + 1 or seq_len.numel() != B \
             or (lse is not None and lse.shape != (T, H)):
         raise HSError(1, "shape mismatch: q [T,H,576], kv_pool [R,656], block_table [B,pages], req_start [B+1], seq_len [B], "
                          "out [T,H,512], lse [T,H]")
-    a = _PagedMlaArgs(T, B, H, int(bool(causal)), _ptr(q), _ptr(kv_pool), kv_pool.shape[0], _ptr(block_table),
-                      block_table.shape[1], _ptr(req_start), _ptr(seq_len), int(kv_tokens), float(softmax_scale), _ptr(out),
-                      _ptr(lse), _ptr(err_flag), _ptr(workspace), 0 if workspace is None else workspace.numel())
-    _check(load().hs_paged_mla_fwd(ctypes.byref(a), _stream(stream)))
+    _check(load().hs_paged_mla_fwd(_pack_paged_mla(T, B, H, 1 if causal else 0, qp, kp, R, bp, pages, rp, sp, kv_tokens, softmax_scale,
+                                                   op, lp, ep, wp, workspace.numel()), _stream(stream)))
 
 
 class _CopyArgs(ctypes.Structure):
@@ -436,19 +462,21 @@ class _CompactArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_uint64), ("err_flag", _P)]
 
 
-def _layers(a, pools, k_caches, k_scales, Di):
-    for t, n in ((pools, "pools"), (k_caches, "k_caches"), (k_scales, "k_scales")):
-        _dev(t, n, torch.int64)
-    a.L = 0 if pools is None else pools.shape[0]
-    a.Li = 0 if k_caches is None else k_caches.shape[0]
-    if a.Li != (0 if k_scales is None else k_scales.shape[0]):
+_pack_copy, _pack_fork, _pack_free, _pack_compact = (_packer(c) for c in (_CopyArgs, _ForkArgs, _FreeArgs, _CompactArgs))
+
+
+def _layers(pools, k_caches, k_scales):
+    """L, Li and the addresses of the three pointer arrays."""
+    L, pp = (0, 0) if pools is None else (pools.numel(), _tensor(pools, "pools", torch.int64))
+    Li, cp = (0, 0) if k_caches is None else (k_caches.numel(), _tensor(k_caches, "k_caches", torch.int64))
+    Ls, sp = (0, 0) if k_scales is None else (k_scales.numel(), _tensor(k_scales, "k_scales", torch.int64))
+    if Li != Ls:
         raise HSError(1, "k_caches and k_scales must have the same length")
-    a.Di, a.pools, a.k_caches, a.k_scales = int(Di), _ptr(pools), _ptr(k_caches), _ptr(k_scales)
+    return L, Li, pp, cp, sp
 
 
-def _ints(pairs):
-    for t, n in pairs:
-        _dev(t, n, torch.int32)
+def _int(t, name):
+    return _tensor(t, name, torch.int32)
 
 
 def hs_kv_copy_pages(src, dst, nblk: int, err_flag, rows=None, pools=None, k_caches=None, k_scales=None, Di: int = 128,
@@ -456,13 +484,12 @@ def hs_kv_copy_pages(src, dst, nblk: int, err_flag, rows=None, pools=None, k_cac
     """Rows 0 .. rows[i] - 1 (all 64 when ``rows`` is None) of page ``src[i]`` to page ``dst[i]`` in every layer.
     ``pools`` is an int64 CUDA tensor [L] of device pointers to the latent pools, ``k_caches`` / ``k_scales`` [Li] to the
     indexer caches and their scales."""
-    _ints(((src, "src"), (dst, "dst"), (rows, "rows"), (err_flag, "err_flag")))
-    a = _CopyArgs()
-    a.n, a.src, a.dst, a.rows, a.nblk, a.err_flag = src.shape[0], _ptr(src), _ptr(dst), _ptr(rows), int(nblk), _ptr(err_flag)
-    if dst.shape[0] != a.n or (rows is not None and rows.shape[0] != a.n):
+    n = src.numel()
+    if dst.numel() != n or (rows is not None and rows.numel() != n):
         raise HSError(1, "src, dst and rows must have the same length")
-    _layers(a, pools, k_caches, k_scales, Di)
-    _check(load().hs_kv_copy_pages(ctypes.byref(a), _stream(stream)))
+    L, Li, pp, cp, sp = _layers(pools, k_caches, k_scales)
+    _check(load().hs_kv_copy_pages(_pack_copy(n, L, Li, Di, _int(src, "src"), _int(dst, "dst"), 0 if rows is None else _int(rows, "rows"),
+                                              nblk, pp, cp, sp, _int(err_flag, "err_flag")), _stream(stream)))
 
 
 def hs_kv_fork(parent, child, block_table, seq_len, refcount, src, dst, err_flag, pools=None, k_caches=None, k_scales=None,
@@ -470,27 +497,23 @@ def hs_kv_fork(parent, child, block_table, seq_len, refcount, src, dst, err_flag
     """Requests ``child[i]`` become copies of ``parent[i]``: complete pages are shared, the last, partial one is copied
     to the lowest free page in every layer. ``block_table`` [B, pages], ``seq_len`` [B] and ``refcount`` [nblk] are updated
     in place; ``src`` / ``dst`` (int32 [n]) receive the pages copied and taken. See include/hs.h."""
-    _ints(((parent, "parent"), (child, "child"), (block_table, "block_table"), (seq_len, "seq_len"), (refcount, "refcount"),
-           (src, "src"), (dst, "dst"), (err_flag, "err_flag")))
-    a = _ForkArgs()
-    a.n, a.B, a.bt_stride, a.nblk = parent.shape[0], block_table.shape[0], block_table.shape[1], refcount.shape[0]
-    if not (child.shape[0] == src.shape[0] == dst.shape[0] == a.n) or seq_len.shape[0] != a.B:
+    n, (B, pages) = parent.numel(), block_table.shape
+    if child.numel() != n or src.numel() != n or dst.numel() != n or seq_len.numel() != B:
         raise HSError(1, "parent, child, src and dst must have the same length, and seq_len one entry per request")
-    a.parent, a.child, a.block_table, a.seq_len, a.refcount = _ptr(parent), _ptr(child), _ptr(block_table), _ptr(seq_len), \
-        _ptr(refcount)
-    a.src, a.dst, a.err_flag = _ptr(src), _ptr(dst), _ptr(err_flag)
-    _layers(a, pools, k_caches, k_scales, Di)
-    _check(load().hs_kv_fork(ctypes.byref(a), _stream(stream)))
+    L, Li, pp, cp, sp = _layers(pools, k_caches, k_scales)
+    _check(load().hs_kv_fork(_pack_fork(n, B, pages, L, Li, Di, _int(parent, "parent"), _int(child, "child"),
+                                        _int(block_table, "block_table"), _int(seq_len, "seq_len"), _int(refcount, "refcount"),
+                                        refcount.numel(), _int(src, "src"), _int(dst, "dst"), pp, cp, sp,
+                                        _int(err_flag, "err_flag")), _stream(stream)))
 
 
 def hs_kv_free(req, block_table, seq_len, refcount, err_flag, stream=None):
     """Requests ``req[i]`` give their pages back (``refcount`` - 1 each) and become empty, in place."""
-    _ints(((req, "req"), (block_table, "block_table"), (seq_len, "seq_len"), (refcount, "refcount"), (err_flag, "err_flag")))
-    if seq_len.shape[0] != block_table.shape[0]:
+    B, pages = block_table.shape
+    if seq_len.numel() != B:
         raise HSError(1, "seq_len must have one entry per request")
-    a = _FreeArgs(req.shape[0], block_table.shape[0], block_table.shape[1], _ptr(req), _ptr(block_table), _ptr(seq_len),
-                  _ptr(refcount), refcount.shape[0], _ptr(err_flag))
-    _check(load().hs_kv_free(ctypes.byref(a), _stream(stream)))
+    _check(load().hs_kv_free(_pack_free(req.numel(), B, pages, _int(req, "req"), _int(block_table, "block_table"), _int(seq_len, "seq_len"),
+                                        _int(refcount, "refcount"), refcount.numel(), _int(err_flag, "err_flag")), _stream(stream)))
 
 
 def hs_kv_compact_workspace_size(nblk: int) -> int:
@@ -505,16 +528,12 @@ def hs_kv_compact(block_table, refcount, table_out, refcount_out, src, dst, coun
     """Move the pages in use into the lowest ids, in every layer; ``table_out`` and ``refcount_out`` (the inputs
     themselves are allowed) receive the new state, ``src`` / ``dst`` (int32 [nblk]) the moves, ``counts`` (int32 [2])
     {pages in use, moves}. See include/hs.h."""
-    _ints(((block_table, "block_table"), (refcount, "refcount"), (table_out, "table_out"), (refcount_out, "refcount_out"),
-           (src, "src"), (dst, "dst"), (counts, "counts"), (err_flag, "err_flag")))
-    _dev(workspace, "workspace", torch.uint8)
-    a = _CompactArgs()
-    a.B, a.bt_stride, a.nblk = block_table.shape[0], block_table.shape[1], refcount.shape[0]
-    if table_out.shape != block_table.shape or counts.shape != (2,) or \
-            not (refcount_out.shape[0] == src.shape[0] == dst.shape[0] == a.nblk):
+    (B, pages), nblk = block_table.shape, refcount.numel()
+    if table_out.shape != (B, pages) or counts.numel() != 2 or refcount_out.numel() != nblk or src.numel() != nblk or dst.numel() != nblk:
         raise HSError(1, "table_out must have block_table's shape, refcount_out, src and dst one entry per page, counts two")
-    a.block_table, a.refcount, a.table_out, a.refcount_out = _ptr(block_table), _ptr(refcount), _ptr(table_out), _ptr(refcount_out)
-    a.src, a.dst, a.counts, a.workspace, a.workspace_bytes = _ptr(src), _ptr(dst), _ptr(counts), _ptr(workspace), workspace.numel()
-    a.err_flag = _ptr(err_flag)
-    _layers(a, pools, k_caches, k_scales, Di)
-    _check(load().hs_kv_compact(ctypes.byref(a), _stream(stream)))
+    L, Li, pp, cp, sp = _layers(pools, k_caches, k_scales)
+    _check(load().hs_kv_compact(_pack_compact(B, pages, L, Li, Di, _int(block_table, "block_table"), _int(refcount, "refcount"), nblk,
+                                              _int(table_out, "table_out"), _int(refcount_out, "refcount_out"), _int(src, "src"),
+                                              _int(dst, "dst"), _int(counts, "counts"), pp, cp, sp,
+                                              _tensor(workspace, "workspace", torch.uint8), workspace.numel(),
+                                              _int(err_flag, "err_flag")), _stream(stream)))

@@ -32,6 +32,7 @@ struct Tensor {
 
 struct Params {
   int32_t T, H, H2, half, inverse, per_cta;
+  int32_t step_t, step_h, step_g;  // kThreads units as tokens, heads and pair groups
   float scale;
   const int32_t* pos;
   const double* inv_freq;
@@ -63,100 +64,100 @@ union Unit {
   uint4 w[sizeof(E) * V >= 16 ? 2 : 1];
 };
 
+// A unit's place in the CTA's work: token, head (of both tensors) and pair group, stepped by kThreads
+// units without divisions.
+struct Place {
+  int t, h, g;
+  __device__ __forceinline__ void step(const Params& p, int groups, int heads) {
+    g += p.step_g;
+    const bool a = g >= groups;
+    g -= a ? groups : 0;
+    h += p.step_h + (a ? 1 : 0);
+    const bool b = h >= heads;
+    h -= b ? heads : 0;
+    t += p.step_t + (b ? 1 : 0);
+  }
+};
+
 template <typename E, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const Params p) {
   extern __shared__ float2 cs[];  // [per_cta][half]: scale * (cos, sin)
   const int t0 = blockIdx.x * p.per_cta;
   const int nt = min(p.per_cta, p.T - t0);
-  const int groups = p.half / V;           // units of a head
+  const int groups = p.half / V;  // units of a head
   const int heads = p.H + p.H2;
-  const int items = nt * heads * groups;
   constexpr bool kVec = V > 1;
-  constexpr int kAhead = kVec ? 4 : 8;     // units in flight per thread
+  constexpr int kAhead = kVec ? 2 : 8;  // units in flight per thread
   Unit<E, V> u[kAhead];
-
-  auto place = [&](int i, int& t, int& g, const E*& src, E*& dst) {
-    const int th = i / groups;
-    g = i - th * groups;
-    t = th / heads;
-    const int h = th - t * heads;
-    const bool first = h < p.H;
-    const Tensor& a = first ? p.a : p.b;
-    const int64_t tt = t0 + t, hh = first ? h : h - p.H;
-    src = reinterpret_cast<const E*>(a.x + tt * a.xt + hh * a.xh);
-    dst = reinterpret_cast<E*>(a.out + tt * a.ot + hh * a.oh);
-  };
-  auto load = [&](Unit<E, V>& w, const E* src, int g) {
-    const E* s0 = src + (kInterleaved ? 2 * V * g : V * g);
-    const E* s1 = kInterleaved ? s0 + V : s0 + p.half;
-    if constexpr (kVec) {
-      w.w[0] = *reinterpret_cast<const uint4*>(s0);
-      w.w[1] = *reinterpret_cast<const uint4*>(s1);
-    } else {
-      w.v[0] = *s0;
-      w.v[1] = *s1;
-    }
-  };
-  auto turn_store = [&](Unit<E, V>& w, E* dst, int t, int g) {
-    const float2* c = cs + t * p.half + V * g;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int ia = kInterleaved ? 2 * k : k, ib = kInterleaved ? 2 * k + 1 : V + k;
-      const float a = to_f(w.v[ia]), b = to_f(w.v[ib]);
-      const float2 e = c[k];
-      w.v[ia] = from_f<E>(a * e.x - b * e.y);
-      w.v[ib] = from_f<E>(a * e.y + b * e.x);
-    }
-    E* d0 = dst + (kInterleaved ? 2 * V * g : V * g);
-    E* d1 = kInterleaved ? d0 + V : d0 + p.half;
-    if constexpr (kVec) {
-      *reinterpret_cast<uint4*>(d0) = w.w[0];
-      *reinterpret_cast<uint4*>(d1) = w.w[1];
-    } else {
-      *d0 = w.v[0];
-      *d1 = w.v[1];
-    }
-  };
-
-  // the first units' values are on their way while the angles are computed
   E* dst[kAhead];
-  int ts[kAhead], gs[kAhead];
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int i = threadIdx.x + k * kThreads;
-    if (i < items) {
-      const E* src;
-      place(i, ts[k], gs[k], src, dst[k]);
-      load(u[k], src, gs[k]);
-    }
+  int at[kAhead];  // the unit's cosines; -1: no unit
+
+  Place w;
+  {
+    const int th = threadIdx.x / groups;
+    w.g = threadIdx.x - th * groups;
+    w.t = th / heads;
+    w.h = th - w.t * heads;
   }
+  auto load = [&]() {  // this thread's next units
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      at[k] = -1;
+      if (w.t < nt) {
+        const bool first = w.h < p.H;
+        const int64_t tt = t0 + w.t, hh = first ? w.h : w.h - p.H;
+        const int off = kInterleaved ? 2 * V * w.g : V * w.g;
+        const E* s0 = reinterpret_cast<const E*>((first ? p.a.x : p.b.x) + tt * (first ? p.a.xt : p.b.xt) + hh * (first ? p.a.xh : p.b.xh)) + off;
+        dst[k] = reinterpret_cast<E*>((first ? p.a.out : p.b.out) + tt * (first ? p.a.ot : p.b.ot) + hh * (first ? p.a.oh : p.b.oh)) + off;
+        at[k] = w.t * p.half + V * w.g;
+        const E* s1 = kInterleaved ? s0 + V : s0 + p.half;
+        if constexpr (kVec) {
+          u[k].w[0] = *reinterpret_cast<const uint4*>(s0);
+          u[k].w[1] = *reinterpret_cast<const uint4*>(s1);
+        } else {
+          u[k].v[0] = *s0;
+          u[k].v[1] = *s1;
+        }
+      }
+      w.step(p, groups, heads);
+    }
+  };
+
+  load();  // the first units' values are on their way while the angles are computed
   for (int i = threadIdx.x; i < nt * p.half; i += kThreads) {
     const int t = i / p.half, k = i - t * p.half;
     double f = p.inv_freq[k] * 0.15915494309189533577;  // turns per position
     f -= floor(f);
     const uint64_t step = (uint64_t)(f * 18446744073709551616.0);
-    const int64_t at = (int64_t)((uint64_t)(int64_t)p.pos[t0 + t] * step);  // whole turns drop out
+    const int64_t turn = (int64_t)((uint64_t)(int64_t)p.pos[t0 + t] * step);  // whole turns drop out
     float s, c;
-    sincospif((float)at * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+    sincospif((float)turn * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
     cs[i] = make_float2(c * p.scale, (p.inverse ? -s : s) * p.scale);
   }
   __syncthreads();
-#pragma unroll 1
-  for (int base = 0; base < items; base += kAhead * kThreads) {
-    if (base > 0) {
+  while (at[0] >= 0) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = base + threadIdx.x + k * kThreads;
-        if (i < items) {
-          const E* src;
-          place(i, ts[k], gs[k], src, dst[k]);
-          load(u[k], src, gs[k]);
-        }
+    for (int k = 0; k < kAhead; ++k) {
+      if (at[k] < 0) break;
+      const float2* c = cs + at[k];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int ia = kInterleaved ? 2 * j : j, ib = kInterleaved ? 2 * j + 1 : V + j;
+        const float a = to_f(u[k].v[ia]), b = to_f(u[k].v[ib]);
+        const float2 e = c[j];
+        u[k].v[ia] = from_f<E>(a * e.x - b * e.y);
+        u[k].v[ib] = from_f<E>(a * e.y + b * e.x);
+      }
+      E* d1 = kInterleaved ? dst[k] + V : dst[k] + p.half;
+      if constexpr (kVec) {
+        *reinterpret_cast<uint4*>(dst[k]) = u[k].w[0];
+        *reinterpret_cast<uint4*>(d1) = u[k].w[1];
+      } else {
+        dst[k][0] = u[k].v[0];
+        d1[0] = u[k].v[1];
       }
     }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (base + threadIdx.x + k * kThreads < items) turn_store(u[k], dst[k], ts[k], gs[k]);
+    load();
   }
 }
 
@@ -194,10 +195,14 @@ cudaError_t launch_rope(const hs_rope_args* a, int sms, cudaStream_t stream) {
             (uint64_t)t->oh;
   const int V = e == 4 ? 4 : 8;
   const bool vec = (bits & 15) == 0 && p.half % V == 0;
-  // Tokens per CTA: enough work for the loads in flight, while every SM still gets several CTAs.
-  const int64_t units = (int64_t)(p.H + p.H2) * p.half / (vec ? V : 1);
+  const int groups = p.half / (vec ? V : 1), heads = p.H + p.H2;
+  p.step_g = kThreads % groups;
+  p.step_h = kThreads / groups % heads;
+  p.step_t = kThreads / groups / heads;
+  // Tokens per CTA: up to eight, while a thread gets no more than eight units and every SM still gets eight CTAs
+  const int64_t units = (int64_t)heads * groups;
   int per = 1;
-  while (per < 8 && (int64_t)2 * per * units <= 4 * kThreads && (int64_t)a->T >= 2LL * per * 4 * sms) per *= 2;
+  while (per < 8 && 2 * per * units <= 8 * kThreads && (int64_t)a->T >= 16LL * per * sms) per *= 2;
   p.per_cta = per;
   const unsigned grid = (unsigned)((a->T + per - 1) / per);
   const size_t smem = (size_t)per * p.half * sizeof(float2);
