@@ -85,34 +85,50 @@ __device__ __forceinline__ void bulk_s2remote(uint32_t dst, const void* src, uin
                : "memory");
 }
 
-// ---------------------------------------------------------------- two-CTA tensor products --
-// cta_group::2: the CTAs with ranks 2k and 2k + 1 work on one product of twice the rows. Each holds its rows of
-// A and of the accumulator and half of B's columns; the even CTA issues.
-__device__ __forceinline__ void tmem_alloc2(uint32_t* dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+// mbarrier.arrive with its default semantics (release at CTA scope) on another CTA's barrier: for handing on what
+// a barrier of this CTA has just shown complete.
+__device__ __forceinline__ void remote_arrive_cta(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void mma2_f16_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem), "l"(a),
-      "l"(b), "r"(idesc), "r"(accumulate));
-}
-// A from tensor memory: 16-bit values, two to a 32-bit column, row r of a CTA in lane r.
-__device__ __forceinline__ void mma2_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
-}
-// Arrives on the barrier at this offset in every CTA of the mask once this thread's products so far are complete.
-__device__ __forceinline__ void mma2_commit(uint64_t* bar, uint16_t mask) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                   smem_u32(bar)),
-               "h"(mask)
-               : "memory");
-}
+
+// ---------------------------------------------------------------- tensor products ----------
+// G = 1: a CTA's own products. G = 2 (cta_group::2): the CTAs with ranks 2k and 2k + 1 work on one product of twice the
+// rows; each holds its rows of A and of the accumulator and half of B's columns, the even CTA issues. ts takes A from tensor
+// memory: 16-bit values, two to a 32-bit column, row r of a CTA in lane r. commit arrives on the barrier at this
+// offset in every CTA of the mask once this thread's products so far are complete.
+template <int G>
+struct Tc;
+#define HS_TC(G)                                                                                                          \
+  template <>                                                                                                            \
+  struct Tc<G> {                                                                                                         \
+    static __device__ __forceinline__ void alloc(uint32_t* dst, uint32_t ncols) {                                        \
+      asm volatile("tcgen05.alloc.cta_group::" #G ".sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),         \
+                   "r"(ncols)                                                                                            \
+                   : "memory");                                                                                          \
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::" #G ".sync.aligned;" ::: "memory");                       \
+    }                                                                                                                    \
+    static __device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t ncols) {                                     \
+      asm volatile("tcgen05.dealloc.cta_group::" #G ".sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");     \
+    }                                                                                                                    \
+    static __device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) { \
+      asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::" #G ".kind::f16 [%0], %1, %2, %3, p; }" \
+                   ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate));                                               \
+    }                                                                                                                    \
+    static __device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) { \
+      asm volatile(                                                                                                      \
+          "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::" #G ".kind::f16 [%0], [%1], %2, %3, p; }" ::"r"( \
+              d),                                                                                                        \
+          "r"(a), "l"(b), "r"(idesc), "r"(accumulate));                                                                  \
+    }                                                                                                                    \
+    static __device__ __forceinline__ void commit(uint64_t* bar, uint16_t mask) {                                        \
+      asm volatile("tcgen05.commit.cta_group::" #G                                                                        \
+                   ".mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),        \
+                   "h"(mask)                                                                                             \
+                   : "memory");                                                                                          \
+    }                                                                                                                    \
+  };
+HS_TC(1)
+HS_TC(2)
+#undef HS_TC
 
 }  // namespace hs

@@ -22,9 +22,7 @@ cudaError_t launch_touch_host(int32_t B, const uint8_t* const* host_rows, const 
                               const int32_t* resident_start, int64_t page, int32_t* err, cudaStream_t stream);
 cudaError_t launch_rope(const hs_rope_args* a, int sms, cudaStream_t stream);
 cudaError_t launch_paged_mla(const hs_paged_mla_args* a, int sms, cudaStream_t stream, const char** why);
-uint64_t paged_mla_workspace_bytes(int sms);
-cudaError_t launch_paged_chunk(const hs_paged_mla_args* a, int sms, cudaStream_t stream, const char** why);
-uint64_t paged_chunk_workspace_bytes(int B, int64_t kv_tokens, int sms);
+uint64_t paged_mla_workspace_bytes(int T, int B, int H, int64_t kv_tokens, int sms);
 cudaError_t launch_copy_pages(const hs_kv_copy_args* a, int sms, cudaStream_t stream);
 cudaError_t launch_fork(const hs_kv_fork_args* a, cudaStream_t stream);
 cudaError_t launch_free(const hs_kv_free_args* a, cudaStream_t stream);
@@ -85,13 +83,6 @@ hs_status set_last_error(hs_status s, const char* fmt, ...) {
   return s;
 }
 }  // namespace hs
-
-// Whether a batch of the paged attention has enough (token, head) rows per request for the kernel that
-// dequantises each row once.
-static bool paged_chunk(int32_t T, int32_t B, int32_t H) { return (int64_t)T * H > 128ll * B; }
-static uint64_t paged_workspace(int32_t B, int64_t kv_tokens, int sms, bool chunk) {
-  return chunk ? hs::paged_chunk_workspace_bytes(B, kv_tokens, sms) : hs::paged_mla_workspace_bytes(sms);
-}
 
 #define REQUIRE(cond, ...) \
   do {                     \
@@ -359,8 +350,7 @@ hs_status hs_paged_mla_workspace_size(int32_t T, int32_t B, int32_t H, int64_t k
   int sms = 0;
   hs_status st = check_device(&sms);
   if (st != HS_OK) return st;
-  const uint64_t a = paged_workspace(B, kv_tokens, sms, false), b = paged_workspace(B, kv_tokens, sms, true);
-  *bytes = paged_chunk(T, B, H) && b > a ? b : a;
+  *bytes = hs::paged_mla_workspace_bytes(T, B, H, kv_tokens, sms);
   return ok();
 }
 
@@ -381,14 +371,11 @@ hs_status hs_paged_mla_fwd(const hs_paged_mla_args* a, hs_stream_t stream) {
   int sms = 0;
   hs_status st = check_device(&sms);
   if (st != HS_OK) return st;
-  const bool chunk = paged_chunk(a->T, a->B, a->H);
-  const uint64_t need = paged_workspace(a->B, a->kv_tokens, sms, chunk);
+  const uint64_t need = hs::paged_mla_workspace_bytes(a->T, a->B, a->H, a->kv_tokens, sms);
   REQUIRE(a->workspace_bytes >= need, "workspace holds %llu bytes; these sizes need %llu on this device",
           (unsigned long long)a->workspace_bytes, (unsigned long long)need);
   const char* why = nullptr;
-  return launched(chunk ? hs::launch_paged_chunk(a, sms, (cudaStream_t)stream, &why)
-                        : hs::launch_paged_mla(a, sms, (cudaStream_t)stream, &why),
-                  "hs_paged_mla_fwd", why);
+  return launched(hs::launch_paged_mla(a, sms, (cudaStream_t)stream, &why), "hs_paged_mla_fwd", why);
 }
 
 // The layers of a page operation: L latent pools, Li indexer caches.

@@ -1,455 +1,584 @@
 // paged.cu — dense attention of each request's new tokens over its paged FP8 latent rows (MLA in MQA
-// form), on tcgen05, two SMs per block of rows.
+// form), on tcgen05.
 //
 // [P1] "vLLM v0.32.0 GLM-5.3 サービング ...", sections 「再現方法と必要なフラグ」 and 「数字がうまくいく理由」:
 // every cached row serves all heads; QK runs over 576 dims (512 latent + 64 RoPE), PV over the 512
-// latent dims. A request's (token, head) pairs, 128 at a time, are the rows of one softmax attention:
+// latent dims. A request's (token, head) pairs are the rows of one softmax attention:
 //   S = Q K^T,  P = 2^(c S - m),  O = P V,  out = O / sum P,     V = the first 512 dims of K.
 //
-// Why two SMs. O of 128 rows and 512 fp32 dims fills an SM's tensor memory, so S has no place beside
-// it; 64 rows per SM would halve the work per row loaded and pay the fixed cost of small MMAs. A cluster of
-// two CTAs splits the two products instead: CTA A computes S and the softmax, CTA B keeps O and computes PV,
-// each with M = 128 rows at the tensor core's full rate (36 MMAs of N = 128 per 128 keys in A, 32 in B).
-// P (fp16) goes from A's registers straight into B's shared memory. Both CTAs dequantise the rows they
-// need themselves (fp16, code * group scale rounded once).
+// Why the two products run on different SMs. O of 128 rows and 512 fp32 dims fills an SM's tensor memory, so S has no
+// place beside it; 64 rows per SM would halve the work per cached row and pay the fixed cost of small MMAs. Here
+// one half of a cluster computes S and the softmax, the other keeps O and computes PV, each with 128 rows per SM
+// at the tensor core's full rate: per tile of 128 cached rows 2,304 cycles of QK, 2,048 of PV.
 //
-// Work. Units are (block of 128 rows, 128 cached rows); every cluster takes an equal share of all units
-// of the batch, found by prefix sums at the start (no plan on the host, which does not know the lengths). A block whose
-// units span clusters leaves fp32 partial outputs and their log-sum-exps in the workspace;
-// paged_merge_kernel joins them.
+// Three variants of one kernel, G = CTAs that share a product (cluster of 2 G):
+//   G = 1, raw    blocks of 128 rows; for requests with up to 128 rows (decode).
+//   G = 2, raw    blocks of 256 rows, two-SM MMAs (cta_group::2, M = 256): each CTA brings half of every K or V tile, which
+//                 halves what it reads from L2, dequantises, and feeds its tensor core from shared memory.
+//   G = 2, TMA    the same from a dequantised copy of the rows that expand_kernel writes to the workspace first ([512 fp16]
+//                 [64 bf16], 1,152 bytes): pays once several blocks of a request read each row.
+// raw: eight producer warps read the 656-byte rows, dequantise (fp16, code * group scale rounded once) and write
+// 128-byte-swizzled blocks. Q's latent dims sit in tensor memory as the A operand (256 columns beside two S
+// buffers of 128), so that a QK MMA reads only K from shared memory.
 //
-// Roles (512 threads; warp w runs on sub-partition w % 4 and reads tensor-memory lanes 32 (w % 4) .. + 31):
-//   warps 1-3, 5-7, 13, 14   producers: read rows, dequantise, write 128-byte-swizzled [128 keys][64 dims]
-//                            blocks into the ring (A: 5 blocks of 16 KB, nine per tile; B: 5 stages
-//                            of two blocks, four per tile);
-//   warp 0                   issues the MMAs (and in A loads Q by TMA);
-//   warps 8-11               A: Q to fp16, softmax, thread = row; B: rescaling of O and the output, thread = row;
-//   warp 4                   B: tells A when PV has read a P buffer.
-// The issuing warp shares its sub-partition with one softmax warp only: producers there would starve it.
+// Work. Units are (block of rows, 128 cached rows); every cluster takes an equal share of all units of the batch, found by
+// prefix sums at the start (no plan on the host, which does not know the lengths). A block whose units span
+// clusters leaves fp32 partial outputs and their log-sum-exps in the workspace; paged_merge_kernel joins them.
 //
-// Lazy maximum: a row's reference max moves only when a logit exceeds it by more than 2^8 (P stays below
-// 2^8, well inside fp16); then A sends the row's factor with P and B rescales that row of O. Masked
-// columns are selected away before the maximum and the exponential, so what they hold does not matter; V rows
-// that fp16 cannot hold are zeroed in B, so that P = 0 times them is 0.
+// Roles. Softmax CTA: warp 0 loads K by TMA (TMA variant), warps 1 and 3 of the issuing CTA issue QK, each for every other
+// tile (the tensor core queues too little to stay busy while one warp waits and commits), warp 2 of the other tells
+// that its half is there, warps 4-11 are the softmax: thread = row and 64 of the tile's columns; the two threads of a row agree
+// on the maximum through shared memory. P goes through shared memory to the CTA that keeps the same rows' O, 4 KB per
+// warp as one bulk copy. Output CTA: warp 0 loads V, warp 1 issues PV, warp 2 as above, warp 3 arms P's barrier and hands
+// P buffers back, one more warp looks at each tile's factors and wakes warps 4-11, which rescale O and write the result: thread = row and 256 of O's columns. Warps 12-19 (raw) are
+// the producers.
+//
+// Lazy maximum: a row's reference max moves only when a logit exceeds it by more than 2^8 (P stays below 2^8, well
+// inside fp16); then its factor goes along with P and O's row is rescaled. Masked columns are selected away before the
+// maximum and the exponential, so what they hold does not matter; V values that fp16 cannot hold are zeroed, so that P = 0
+// times them is 0, while K keeps them (the copy: a NaN in the rotary part), so that rows that see them are NaN.
+#include <atomic>
+
 #include "paged.cuh"
 
 namespace hs {
 namespace paged {
 
-constexpr int kThreads = 512;
-constexpr int kRows = 128;                     // (token, head) rows per block
-constexpr int kBlk = kKeys * 128;              // one swizzled [128][64 x 16-bit] block
-constexpr int kSlots = 5;                      // A: blocks in the K ring;  B: stages in the V ring
-constexpr int kSmWarp0 = 8;
-constexpr int kProdWarps = 8;
-__host__ __device__ constexpr int producer_index(int w) {
-  return (w % 4 == 0 || (w >= 8 && w < 12) || w == 15) ? -1 : (w < 8 ? w - 1 - w / 4 : w - 7);
-}
-// shared memory, A: Q [9 blocks], K ring; B: P [2][2 blocks], V ring [5][2 blocks]
-constexpr int kOffRingA = 9 * kBlk;
-constexpr int kOffRingB = 4 * kBlk;
-constexpr int kOffSmall = 14 * kBlk;           // 229,376
-constexpr int kOffAlpha = kOffSmall;           // B: float [2][128]
-constexpr int kOffSum = kOffAlpha + 1024;      // B: float [2][128]
-constexpr int kOffMoved = kOffSum + 1024;      // B: u32 [2][4]
-constexpr int kOffBar = kOffMoved + 32;
-constexpr int kNumBars = 32;
-constexpr int kOffMisc = kOffBar + 8 * kNumBars;  // tmem base, abort, Start
-constexpr int kSmem = kOffMisc + 64;
-constexpr int kOffScratch = kOffRingA;         // int64 [B + 1] during the set-up
-static_assert(kOffRingB + 10 * kBlk <= kOffSmall && kOffScratch + 8 * (kMaxReq + 1) <= kOffSmall, "layout");
-static_assert(kSmem <= 232448, "shared memory");
+constexpr int G = 2;                           // CTAs that share a product
+constexpr int kHalf = 128;                     // rows of a CTA
+constexpr int kPBuf = 2 * kHalf * 128;         // P of a tile: 2 x [128 rows][64 keys]
+// Roles by warp; warp w runs on sub-partition w % 4. The issuing warps share theirs with no producer: a sub-partition busy
+// with producers' arithmetic feeds an issuing thread several times slower than the tensor core runs.
+constexpr int kIssue0 = 0, kLoadWarp = 1, kRelayWarp = 2, kBufWarp = 3, kSmWarp0 = 4, kProdWarps = 3;
+// producer of warp w (13-15: the first group of three, 17-19: the second), or -1
+__host__ __device__ constexpr int producer_index(int w) { return w < 13 || w % 4 == 0 ? -1 : w - 13 - (w - 12) / 4; }
+static_assert(producer_index(13) == 0 && producer_index(15) == 2 && producer_index(17) == 3 && producer_index(19) == 5, "roles");
+constexpr int kScaleWarpA = 3, kScaleWarpB = 12;  // warps without another role there
+constexpr int kVBlk = kKeys * 128;             // [128 keys][64 dims]
+constexpr int kVStage = 2 * kVBlk;             // 128 dims
+constexpr int kMaxSlots = 8;
+// Shared memory. Softmax CTA: Q's rotary dims, P staging [2], exchange, then the K ring (and raw: codes, scales);
+// output CTA: P [2], exchange unused, V ring (and codes, scales). Both: factors, sums, barriers.
+constexpr int kOffQ = 0;
+constexpr int kOffStage = kHalf * 128;
+constexpr int kOffMax = kOffStage + 2 * kPBuf; // softmax CTA: float [2][2][128]
+constexpr int kOffK = kOffMax + 2048;
+constexpr int kOffP = 0;
+constexpr int kOffV = 2 * kPBuf;
+constexpr int kOffAlpha = 14 * 16384;          // float [2][128]: staging, and at the same place of the output CTA
+constexpr int kOffSum = kOffAlpha + 1024;      // float [2][128]
+constexpr int kOffBar = kOffSum + 1024;
+constexpr int kNumBars = 56;
+constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+constexpr int kSmem = kOffMisc + 128;
+constexpr int kOffScratch = kOffK;             // int64 [B + 1] during the set-up
+static_assert(kOffScratch + 8 * (kMaxReq + 1) <= kOffAlpha && kSmem <= 232448, "shared memory");
+static_assert(kOffK % 1024 == 0 && kOffStage % 1024 == 0 && kOffV % 1024 == 0, "swizzled blocks");
 
-// A latent group's pieces that a producer lane holds: 16 codes of each of its four rows, and their scales.
-struct Chunk {
-  uint4 v[4];
-  float s[4];
+// What differs between the variants.
+template <bool kRaw>
+struct Shape {
+  static constexpr int kThreads = kRaw ? 640 : 384;
+  static constexpr int kIssue1 = kRaw ? 12 : 3;    // the second issuing warp
+  static constexpr int kRows = kHalf * G;          // rows of a block
+  static constexpr int kMine = kKeys / G;          // keys of a K block in one CTA
+  static constexpr int kKBlk = kMine * 128;        // [kMine keys][64 dims]
+  // K stages of a tile in the ring: raw four latent groups of two blocks (the rotary block has two buffers of its own), TMA
+  // three times three blocks
+  static constexpr int kBlocks = kRaw ? 2 : 3;
+  static constexpr int kStages = kRaw ? 4 : 3;
+  static constexpr int kKStage = kBlocks * kKBlk;
+  static constexpr int kStA = kRaw ? 4 : 5;
+  static constexpr int kVStages = 4 / G;           // per tile; an MMA takes 128 G dims of one
+  static constexpr int kStB = kRaw ? 2 : 5;
+  // raw: rotary blocks [2], rings of undecoded latent groups ([keys][128 codes]), two tiles' scales ([keys][4]) and those
+  // split into fp16 pairs ([4 groups][keys])
+  static constexpr int kCodesA = kMine * 128, kCodesB = kKeys * 128;
+  static constexpr int kCodeSlots = 4;
+  static constexpr int kOffRotary = kOffK + kStA * kKStage;
+  static constexpr int kOffCodesA = kOffRotary + 2 * kKBlk, kOffCodesB = kOffV + kStB * kVStage;
+  static constexpr int kOffScaleA = kOffCodesA + kCodeSlots * kCodesA, kOffScaleB = kOffCodesB + kCodeSlots * kCodesB;
+  static constexpr int kOffSplitA = kOffScaleA + 2 * kMine * 16, kOffSplitB = kOffScaleB + 2 * kKeys * 16;
+  static_assert(!kRaw || (kOffSplitA + 8 * kMine * 8 <= kOffAlpha && kOffSplitB + 8 * kKeys * 8 <= kOffAlpha), "layout");
+  static_assert(kOffK + kStA * kKStage <= kOffAlpha && kOffV + kStB * kVStage <= kOffAlpha, "layout");
+};
+constexpr int kRotaryBar = 6;  // raw: full and empty barriers 6 and 7 belong to the rotary buffers
+
+// ------------------------------------------------------------------ dequantisation ---------
+// One warp per row: lane l turns codes 16 l .. + 15 into fp16, lanes 0-7 copy the rotary values. Rows past a
+// request's length (its last tile) and rows of a bad page are zeros. HBM-bound: 656 bytes read, 1,152 written.
+constexpr int kExpandThreads = 512;
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const Params p, uint16_t* out) {
+  __shared__ int64_t pre[kMaxReq + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 0) {
+    int64_t run = 0, cached = 0;
+    if (lane == 0) pre[0] = 0;
+    for (int at = 0; at < p.B; at += 32) {
+      Req q = {0, 0, 0, 0};
+      if (at + lane < p.B) q = load_req<kHalf>(p, at + lane);
+      const int64_t x = warp_scan(copy_rows(q), lane);
+      if (at + lane < p.B) pre[at + lane + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
+      cached += q.seq;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) cached += __shfl_xor_sync(0xffffffffu, cached, o);
+    if (cached > p.kv_tokens && lane == 0) pre[p.B] = -1;  // nothing is computed
+  }
+  __syncthreads();
+  const int64_t total = pre[p.B];
+  bool range_ok = true;
+  // 16 consecutive rows per warp and turn (a quarter of a page)
+  for (int64_t w = (int64_t)blockIdx.x * (kExpandThreads / 32) + warp; w * 16 < total; w += (int64_t)gridDim.x * (kExpandThreads / 32)) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= w * 16)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int j0 = (int)(w * 16 - pre[lo]);
+    const int seq = load_req<kHalf>(p, lo).seq;
+    const int32_t blk = j0 / HS_PAGE < p.bt_stride ? p.bt[(int64_t)lo * p.bt_stride + j0 / HS_PAGE] : -1;
+    const bool good = blk >= 0 && ((int64_t)blk + 1) * HS_PAGE <= p.R;
+    if (!good && j0 < seq && lane == 0) flag_error(p.err, HS_FLAG_BAD_BLOCK);
+    const int n = good ? min(16, seq - j0) : 0;  // rows that exist
+    const uint8_t* src = p.kv + ((int64_t)(good ? blk : 0) * HS_PAGE + j0 % HS_PAGE) * HS_KV_ROW_BYTES;
+    uint16_t* dst = out + w * 16 * HS_D_QK;
+#pragma unroll 1
+    for (int h = 0; h < 16; h += 4) {
+      uint4 v[4], r[4];
+      float s[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = r[k] = make_uint4(0, 0, 0, 0);
+        s[k] = 0.f;
+        if (h + k < n) {
+          const uint8_t* a = src + (h + k) * HS_KV_ROW_BYTES;
+          v[k] = ldg_nc_v4(a + 16 * lane);
+          s[k] = ldg_nc_f32(a + HS_D_LATENT + 4 * (lane >> 3));
+          if (lane < 8) r[k] = ldg_nc_v4(a + HS_D_LATENT + 16 + 16 * lane);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        range_ok &= s[k] == 0.f || (fabsf(s[k]) >= kScaleMin && fabsf(s[k]) <= kScaleMax);
+        const __half shi = __float2half_rn(s[k]);
+        const __half2 h2 = __half2half2(shi), l2 = __float2half2_rn(s[k] - __half2float(shi));
+        const uint32_t hu = *reinterpret_cast<const uint32_t*>(&h2), lu = *reinterpret_cast<const uint32_t*>(&l2);
+        uint4 d0 = dequant8(v[k].x, v[k].y, hu, lu), d1 = dequant8(v[k].z, v[k].w, hu, lu);
+        const bool bad = unsound(d0, d1);
+        if (bad) d0 = d1 = make_uint4(0, 0, 0, 0);
+        if (__any_sync(0xffffffffu, bad) && lane == 0) r[k].x = 0x7FC07FC0u;  // two bf16 NaN
+        uint4* d = reinterpret_cast<uint4*>(dst + (h + k) * HS_D_QK);
+        d[2 * lane] = d0;
+        d[2 * lane + 1] = d1;
+        if (lane < 8) d[64 + lane] = r[k];
+      }
+    }
+  }
+  if (!range_ok) flag_error(p.err, HS_FLAG_RANGE);
+}
+
+// ------------------------------------------------------------------ attention --------------
+// A position in a ring of barriers: its slot, and the parity to wait for.
+struct Ring {
+  int slot;
+  uint32_t par;
+  __device__ __forceinline__ void next(int slots) {
+    if (++slot >= slots) {
+      slot -= slots;
+      par ^= 1u;
+    }
+  }
 };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    paged_kernel(const __grid_constant__ CUtensorMap map_q, const Params p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* bars = (uint64_t*)(smem + kOffBar);
-  uint64_t* full = bars;                  // [5] producers wrote a slot -> MMA
-  uint64_t* empty = bars + kSlots;        // [5] MMA read it -> producers
-  uint64_t* s_full = bars + 2 * kSlots;   // A [2] S complete -> softmax
-  uint64_t* s_empty = s_full + 2;         // A [2] softmax read S -> MMA
-  uint64_t* p_empty = s_full + 4;         // A [2] B has read P, its factors and sums -> softmax
-  uint64_t* p_full = s_full + 6;          // B [2] P written (by A) -> MMA, correction
-  uint64_t* corr = s_full + 8;            // B [2] O rescaled for this P -> MMA
-  uint64_t* pv_done = s_full + 10;        // B [2] PV complete -> correction, relay
-  uint64_t* q_full = s_full + 12;         // A
-  uint64_t* q_ready = s_full + 13;        // A: Q is fp16
-  uint64_t* q_free = s_full + 14;         // A: the block's QK MMAs have read Q
-  uint64_t* o_free = s_full + 15;         // B: O read out -> MMA
-  uint64_t* drain = s_full + 16;
-  uint32_t* misc = (uint32_t*)(smem + kOffMisc);
-  volatile uint32_t* abort_flag = misc + 1;
-  Start* st = (Start*)(misc + 2);
+// Barriers and small arrays of a CTA.
+struct Bars {
+  uint64_t full[kMaxSlots];       // this CTA's part of a stage is there; in the issuing CTA the other's too
+  uint64_t empty[kMaxSlots];      // the MMAs have read the stage (both CTAs)
+  uint64_t codes_full[4];         // raw: a latent group's codes have landed
+  uint64_t scale_full[2];         // raw: a tile's scales have landed
+  uint64_t codes_empty[4];        // raw: the producers have read them
+  uint64_t split_full[2];         // raw: a tile's scales are split -> producers
+  uint64_t split_empty[2];        // raw: both groups of producers are done with them
+  uint64_t s_full[2];             // S complete (both)
+  uint64_t s_empty[2];            // issuing softmax CTA: all softmax warps have read S
+  uint64_t p_empty[2];            // softmax CTA: its P buffer and staging are free
+  uint64_t p_full[2];             // output CTA: P and the factors have landed
+  uint64_t corr[2];               // issuing output CTA: O is rescaled for this P (both)
+  uint64_t pv_done[2];            // PV complete (both)
+  uint64_t q_ready;               // issuing softmax CTA: Q is in place (both)
+  uint64_t q_free;                // the block's QK MMAs have read Q (both)
+  uint64_t o_free;                // issuing output CTA: O is read out (both)
+  uint64_t drain[2];
+  uint64_t swap[4];               // softmax CTA: the two warps of a lane quarter have written their values
+};
+static_assert(sizeof(Bars) <= 8 * kNumBars, "barriers");
+struct Misc {
+  uint32_t tmem;
+  volatile uint32_t abort;
+  Start start;
+  volatile int32_t seen[2];       // stages that each of the two issuing warps has found there
+  int32_t left[2];                // raw: cached rows from the tile's first key on
+  volatile int32_t todo;          // output CTA: what the output warps are woken for (kRescale, kLast, kStop)
+  int32_t tile;                   // and for which tile
+  volatile int32_t stop[2];       // raw: a group of producers' first warp gave up
+};
+static_assert(sizeof(Misc) <= 128, "misc");
+constexpr int kRescale = 1, kLast = 2, kStop = 4;
+// Named barriers. Warps that need not look at a tile (the output warps while no maximum moves) or that work in step (the
+// producers) sleep in these while one warp polls: every arrival on any barrier of a CTA wakes its polling warps.
+constexpr int kWake = 1, kWoken = 2, kGo = 3, kDone = 5;  // kGo, kDone: and the next one for the second group
+__device__ __forceinline__ void named_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool isA = cluster_ctarank() == 0;
-  const int c = blockIdx.x >> 1;
+// raw: one thread brings a tile's undecoded rows: the scales, in the softmax CTA the rotary block, and latent group by
+// latent group the codes. A page that the table does not name, or that lies outside the pool, is read past the pool's
+// end: zeros.
+template <bool isA>
+__device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& br, Misc& mc, const CUtensorMap* codes,
+                                         const CUtensorMap* scales, const CUtensorMap* rotary, Walk<kHalf * G>& walk, int half) {
+  using Sh = Shape<true>;
+  constexpr int kSlots = Sh::kCodeSlots, kCodes = isA ? Sh::kCodesA : Sh::kCodesB;
+  constexpr int kPages = isA ? 1 : 2, kGroups = isA ? 4 : 4 / G;
+  uint8_t* cring = smem + (isA ? Sh::kOffCodesA : Sh::kOffCodesB);
+  uint8_t* sring = smem + (isA ? Sh::kOffScaleA : Sh::kOffScaleB);
+  prefetch_tensormap(codes);
+  prefetch_tensormap(scales);
+  Ring ring = {0, 1};
+  int64_t issued = 0;
+  int tile = 0;
+  bool ok = true;
+  Seg s;
+  // block-table entries of the next tile, read one tile ahead
+  int jn = 0;
+  bool more = walk.next(p, s);
+  if (more) jn = s.ta;
+  int32_t blk[2] = {0, 0};
+  int left = 0;  // cached rows from this CTA's first key of the tile on
+  bool live = false;
+  auto fetch = [&]() {
+    live = more;
+    if (!more) return;
+    left = s.q.seq - jn * kKeys - (isA ? half * HS_PAGE : 0);
+#pragma unroll
+    for (int h = 0; h < kPages; ++h) {
+      const int page = 2 * jn + (isA ? half : h);
+      blk[h] = page < p.bt_stride ? ldg_nc_s32(p.bt + (int64_t)s.r * p.bt_stride + page) : -1;
+    }
+    if (++jn == s.tb) {
+      more = walk.next(p, s);
+      if (more) jn = s.ta;
+    }
+  };
+  fetch();
+#pragma unroll 1
+  for (; ok && live; ++tile) {
+    const int t = tile & 1;
+    const uint32_t ph = (uint32_t)(tile >> 1) & 1u;
+    int32_t y[2];
+    const int now = left;
+#pragma unroll
+    for (int h = 0; h < kPages; ++h) {
+      const bool good = blk[h] >= 0 && ((int64_t)blk[h] + 1) * HS_PAGE <= p.R;
+      if (!good && now > h * HS_PAGE) flag_error(p.err, HS_FLAG_BAD_BLOCK);
+      y[h] = good ? blk[h] * HS_PAGE : (int32_t)p.R;
+    }
+    fetch();
+    if (isA && live && left > 0 && blk[0] >= 0 && ((int64_t)blk[0] + 1) * HS_PAGE <= p.R)  // the next tile's page towards L2
+      bulk_prefetch_l2(p.kv + (int64_t)blk[0] * HS_PAGE * HS_KV_ROW_BYTES, (left < HS_PAGE ? left : HS_PAGE) * HS_KV_ROW_BYTES);
+    // the scales of the tile before the last are split
+    ok = !mc.abort && (tile < 2 || mbar_wait(&br.split_full[t], ph ^ 1u, p.err));
+    if (!ok) break;
+    mc.left[t] = now;
+    mbar_arrive_expect_tx(&br.scale_full[t], kCodes / 8);
+#pragma unroll
+    for (int h = 0; h < kPages; ++h)
+      tma_load_2d(sring + (t * kPages + h) * HS_PAGE * 16, scales, &br.scale_full[t], HS_D_LATENT, y[h]);
+    if (isA) {
+      ok = mbar_wait(&br.empty[kRotaryBar + t], ph ^ 1u, p.err);
+      if (!ok) {
+        ++tile;
+        break;
+      }
+      mbar_arrive_expect_tx(&br.full[kRotaryBar + t], Sh::kKBlk);
+      tma_load_2d(smem + Sh::kOffRotary + t * Sh::kKBlk, rotary, &br.full[kRotaryBar + t], (HS_D_LATENT + 16) / 2, y[0]);
+    }
+#pragma unroll 1
+    for (int k = 0; k < kGroups; ++k) {
+      if (mc.abort || !mbar_wait(&br.codes_empty[ring.slot], ring.par, p.err)) {
+        ok = false;
+        break;
+      }
+      uint64_t* bar = &br.codes_full[ring.slot];
+      const int g = isA ? k : 2 * k + half;
+      mbar_arrive_expect_tx(bar, kCodes);
+#pragma unroll
+      for (int h = 0; h < kPages; ++h) tma_load_2d(cring + ring.slot * kCodes + h * HS_PAGE * 128, codes, bar, 128 * g, y[h]);
+      ++issued;
+      ring.next(kSlots);
+    }
+  }
+  if (!ok) mc.abort = 1;
+  // every copy has landed before the CTA may leave: slots before the position were used in its round
+  for (int q = 0; q < kSlots; ++q)
+    if (q < issued) mbar_wait(&br.codes_full[q], q < ring.slot ? ring.par ^ 1u : ring.par, p.err);
+  for (int u = tile > 2 ? tile - 2 : 0; u < tile; ++u) mbar_wait(&br.scale_full[u & 1], (uint32_t)(u >> 1) & 1u, p.err);
+}
+
+// raw: one warp splits every scale of a tile into two fp16 parts (see dequant8), each twice in a 32-bit word, for the
+// producers; rows past the request's length get scale 0.
+template <bool isA>
+__device__ __forceinline__ void split_scales(const Params& p, uint8_t* smem, Bars& br, Misc& mc, int64_t ntiles, int lane) {
+  using Sh = Shape<true>;
+  constexpr int kKeysHere = isA ? Sh::kMine : kKeys;
+  const float4* in = reinterpret_cast<const float4*>(smem + (isA ? Sh::kOffScaleA : Sh::kOffScaleB));
+  uint2* out = reinterpret_cast<uint2*>(smem + (isA ? Sh::kOffSplitA : Sh::kOffSplitB));
+  bool range_ok = true;
+#pragma unroll 1
+  for (int64_t i = 0; i < ntiles; ++i) {
+    const int t = (int)(i & 1);
+    const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+    const bool ok = !mc.abort && mbar_wait(&br.scale_full[t], ph, p.err) && mbar_wait(&br.split_empty[t], ph ^ 1u, p.err);
+    if (!__all_sync(0xffffffffu, ok)) {
+      mc.abort = 1;
+      break;
+    }
+    const int left = mc.left[t];
+#pragma unroll
+    for (int j = 0; j < kKeysHere / 32; ++j) {
+      const int row = lane + 32 * j;
+      const float4 f = in[t * kKeysHere + row];
+      const float sc[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float v = row < left ? sc[g] : 0.f;
+        range_ok &= v == 0.f || (fabsf(v) >= kScaleMin && fabsf(v) <= kScaleMax);
+        const __half hi = __float2half_rn(v);
+        const __half2 h2 = __half2half2(hi), l2 = __float2half2_rn(v - __half2float(hi));
+        out[(t * 4 + g) * kKeysHere + row] = make_uint2(*reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&l2));
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&br.split_full[t]);
+  }
+  if (isA && !range_ok) flag_error(p.err, HS_FLAG_RANGE);
+}
+
+// raw: the producers turn a latent group's codes into fp16 blocks of the K or V ring. Two groups of three warps take turns,
+// so that one converts while the other waits and hands over (the rings' slots are even in number: a slot is always the
+// same group's). Warp w of a group works on the quads of rows w, w + 3, ...: lane l reads the codes 16 (l % 8) .. + 15 of row
+// l / 8 of a quad as two 8-byte pieces, which become the 16-byte pieces 2 (l % 4) and + 1 of a row of block (l % 8) / 4.
+// Which of the two a lane takes first alternates with l / 4 and with the row, so that the reads and the stores of a warp hit
+// different banks. Bound by issue slots: about 40 instructions per 512 codes, most of them (cvt, half2 arithmetic) at half
+// rate.
+template <bool isA>
+__device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32_t* err, int64_t ntiles, int half, int pw, int lane) {
+  using Sh = Shape<true>;
+  constexpr int kBlk = isA ? Sh::kKBlk : kVBlk, kStage = 2 * kBlk;
+  constexpr int kSlots = isA ? Sh::kStA : Sh::kStB;
+  constexpr int kCodes = isA ? Sh::kCodesA : Sh::kCodesB;
+  constexpr int kKeysHere = isA ? Sh::kMine : kKeys;
+  constexpr int kQuads = kKeysHere / 4, kPass = (kQuads + kProdWarps - 1) / kProdWarps;
+  constexpr int kGroups = isA ? 4 : 4 / G;
+  static_assert(kSlots % 2 == 0 && Sh::kCodeSlots % 2 == 0 && kGroups % 2 == 0, "a slot belongs to one group");
+  const int e = pw / kProdWarps, w = pw % kProdWarps;
+  const int rl = lane >> 3, c8 = lane & 7;
+  // rows 4 q + rl, q = w + 3 j: bit 2 of the row alternates with j, and with it bit 2 of the swizzled piece
+  const uint32_t odd = (uint32_t)((c8 >> 2) ^ (rl & 1));  // the piece taken first
+  const uint8_t* codes = smem + (isA ? Sh::kOffCodesA : Sh::kOffCodesB) + rl * 128 + 16 * c8;
+  const uint2* split = reinterpret_cast<const uint2*>(smem + (isA ? Sh::kOffSplitA : Sh::kOffSplitB)) + rl;
+  uint8_t* out = smem + (isA ? kOffK : kOffV) + (c8 >> 2) * kBlk;
+  const uint32_t o0 = 32 * (c8 & 3) + 16 * odd;
+  Ring ring = {e, 1}, cr = {e, 0};
+  const bool first = w == 0;
+  bool go = true;
+  // the group's first warp waits for what a stage needs
+  auto take = [&](uint64_t* bar, uint32_t par) { go = go && __all_sync(0xffffffffu, !mc.abort && mbar_wait(bar, par, err)); };
+#pragma unroll 1
+  for (int64_t i = 0; i < ntiles && go; ++i) {
+    const int t = (int)(i & 1);
+#pragma unroll 1
+    for (int k = e; k < kGroups; k += 2) {
+      if (first) {
+        if (k == e) take(&br.split_full[t], (uint32_t)(i >> 1) & 1u);
+        take(&br.codes_full[cr.slot], cr.par);
+        take(&br.empty[ring.slot], ring.par);
+        if (!go) mc.stop[e] = 1;
+        __syncwarp();
+      }
+      named_bar(kGo + e, 32 * kProdWarps);
+      go = mc.stop[e] == 0;  // the same for every warp of the group
+      if (!go) break;
+      const int g = isA ? k : 2 * k + half;
+      uint8_t* blk = out + ring.slot * kStage;
+#pragma unroll
+      for (int p0 = 0; p0 < kPass; p0 += 3) {  // three quads at a time
+        uint2 va[3], vb[3], sc[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int q = w + kProdWarps * (p0 + j);
+          if (q < kQuads) {
+            const uint8_t* c = codes + cr.slot * kCodes + q * 512;
+            va[j] = *reinterpret_cast<const uint2*>(c + 8 * odd);
+            vb[j] = *reinterpret_cast<const uint2*>(c + 8 * (odd ^ 1u));
+            sc[j] = split[(t * 4 + g) * kKeysHere + 4 * q];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int q = w + kProdWarps * (p0 + j);
+          if (q < kQuads) {
+            uint4 d0 = dequant8(va[j].x, va[j].y, sc[j].x, sc[j].y);
+            uint4 d1 = dequant8(vb[j].x, vb[j].y, sc[j].x, sc[j].y);
+            if (!isA && unsound(d0, d1)) d0 = d1 = make_uint4(0, 0, 0, 0);
+            const uint32_t at = sw128_offset(4 * q + rl, o0);
+            *reinterpret_cast<uint4*>(blk + at) = d0;
+            *reinterpret_cast<uint4*>(blk + (at ^ 16u)) = d1;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      if (first) {
+        named_bar(kDone + e, 32 * kProdWarps);
+        if (lane == 0) {
+          mbar_arrive(&br.full[ring.slot]);
+          mbar_arrive(&br.codes_empty[cr.slot]);
+          if (k + 2 >= kGroups) mbar_arrive(&br.split_empty[t]);
+        }
+      } else {
+        named_arrive(kDone + e, 32 * kProdWarps);
+      }
+      ring.next(kSlots);
+      ring.next(kSlots);
+      cr.next(Sh::kCodeSlots);
+      cr.next(Sh::kCodeSlots);
+    }
+  }
+  if (!go) mc.abort = 1;
+}
+
+template <bool kRaw>
+__global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kThreads, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ CUtensorMap map_r, const Params p) {
+  // map_k, map_v: K and V blocks of the copy, or raw: codes and scales; map_r: raw: rotary blocks
+  using Sh = Shape<kRaw>;
+  constexpr int kRows = Sh::kRows, kKBlk = Sh::kKBlk, kKStage = Sh::kKStage, kStA = Sh::kStA, kStB = Sh::kStB;
+  extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzled blocks need it; the same in every CTA
-    if (tid == 0) flag_error(p.err, HS_FLAG_BAD_STATE);
+    if (threadIdx.x == 0) flag_error(p.err, HS_FLAG_BAD_STATE);
     return;
   }
+  Bars& br = *reinterpret_cast<Bars*>(smem + kOffBar);
+  Misc& mc = *reinterpret_cast<Misc*>(smem + kOffMisc);
+  uint64_t *full = br.full, *empty = br.empty, *s_full = br.s_full, *s_empty = br.s_empty, *p_empty = br.p_empty, *p_full = br.p_full,
+           *corr = br.corr, *pv_done = br.pv_done, *q_ready = &br.q_ready, *q_free = &br.q_free, *o_free = &br.o_free, *drain = br.drain,
+           *swap = br.swap;
+  volatile uint32_t* abort_flag = &mc.abort;
+  Start* st = &mc.start;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool isA = rank < G, lead = rank % G == 0;
+  const int half = (int)rank % G;  // which rows of a block, and which part of every K and V tile
+  const uint16_t pair_mask = G == 1 ? (uint16_t)(1u << rank) : isA ? 0x3 : 0xC;
+  const int c = blockIdx.x / (2 * G);
 
   if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], kProdWarps);
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(&full[s], G == 2 && lead ? 2 : 1);
       mbar_init(&empty[s], 1);
     }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&br.codes_full[s], 1);
+      mbar_init(&br.codes_empty[s], 1);
+    }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&br.scale_full[s], 1);
+      mbar_init(&br.split_full[s], 1);
+      mbar_init(&br.split_empty[s], 2);
       mbar_init(&s_full[s], 1);
-      mbar_init(&s_empty[s], 4);
-      mbar_init(&p_empty[s], 5);
-      mbar_init(&p_full[s], 4);
-      mbar_init(&corr[s], 4);
+      mbar_init(&s_empty[s], 8 * G);
+      mbar_init(&p_empty[s], 1);
+      mbar_init(&p_full[s], 1);
+      mbar_init(&corr[s], G);
       mbar_init(&pv_done[s], 1);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_ready, 4);
-    mbar_init(q_free, 1);
-    mbar_init(o_free, 4);
-    mbar_init(drain, 1);
+    mbar_init(q_ready, 8 * G);
+    mbar_init(q_free, 2);
+    mbar_init(o_free, 8 * G);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    for (int q = 0; q < 4; ++q) mbar_init(&swap[q], 2);
     mbar_fence_init();
-    misc[1] = 0;
+    mc.abort = 0;
+    mc.stop[0] = mc.stop[1] = 0;
+    mc.seen[0] = mc.seen[1] = 0;
   }
-  if (warp == 0) tmem_alloc(&misc[0], 512);
-  find_units<kRows>(p, (int64_t*)(smem + kOffScratch), st, c, kThreads);
+  find_units<kRows>(p, (int64_t*)(smem + kOffScratch), st, c, Sh::kThreads);
   fence_proxy_async_all();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist
+  cluster_sync();  // every CTA's barriers exist
+  if (warp == 0) Tc<G>::alloc(&mc.tmem, 512);
+  __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = misc[0];
-  const int64_t u0 = st->u0, u1 = st->u1, U = st->U;
+  const uint32_t tmem = mc.tmem;
+  const int64_t u0 = st->u0, ntiles = st->u1 - st->u0, U = st->U;
+  // raw: 640 threads start with 96 registers each (61,440 in all); the softmax and output warps (256 threads) take 120, the
+  // others (384) keep 80: 61,440
+  const bool rows_warp = warp >= kSmWarp0 && warp < kSmWarp0 + 8;
   Walk<kRows> walk(p, *st);
+  Seg s;
 
-  const int pw = producer_index(warp);
-  if (pw >= 0) {
-    // ================================================================ producers =================
-    // Warp pw owns rows 16 pw .. + 15 of every tile (one page holds them all); in pass ps lane l works on row
-    // 16 pw + 4 ps + l / 8 and on the 16 codes 16 (l % 8) of a latent group, which become 16-byte pieces
-    // 2 (l % 4) and + 1 of a row of block (l % 8) / 4. Lanes with l % 8 >= 4 store their second piece first, so
-    // that the eight lanes of a row hit eight bank groups. Two groups are in registers ahead of the one
-    // written; pages are asked into L2 two tiles ahead.
-    const int rl = lane >> 3, c8 = lane & 7;
-    const bool swp = c8 >= 4;
-    uint8_t* ring = smem + (isA ? kOffRingA : kOffRingB);
-    Seg seg;
-    int jt = 0;
-    bool more = walk.next(p, seg);
-    if (more) jt = seg.ta;
-    struct Ent {
-      int32_t blk;   // block-table entry (loaded, not yet checked)
-      int32_t left;  // cached rows from this warp's first row on
-      bool page;     // there is such a page
-    };
-    auto fetch = [&]() -> Ent {  // the next tile of this cluster
-      Ent e;
-      e.left = 0;
-      int page = 0, r = 0;
-      if (more) {
-        page = 2 * jt + (pw >> 2);
-        r = seg.r;
-        e.left = seg.q.seq - jt * kKeys - pw * 16;
-        if (++jt == seg.tb) {
-          more = walk.next(p, seg);
-          if (more) jt = seg.ta;
-        }
-      }
-      e.page = page < p.bt_stride;
-      e.blk = ldg_nc_s32(p.bt + (int64_t)r * p.bt_stride + (e.page ? page : 0));
-      return e;
-    };
-    struct Src {
-      const uint8_t* row;  // this lane's row of pass 0
-      uint32_t ok;         // bit ps: the row of pass ps exists
-    };
-    auto resolve = [&](const Ent& e) -> Src {
-      Src s;
-      const bool good = e.page && e.blk >= 0 && ((int64_t)e.blk + 1) * HS_PAGE <= p.R;
-      if (e.left > 0 && !good && lane == 0) flag_error(p.err, HS_FLAG_BAD_BLOCK);
-      s.ok = 0u;
-#pragma unroll
-      for (int ps = 0; ps < 4; ++ps) s.ok |= (good && rl + 4 * ps < e.left) ? 1u << ps : 0u;
-      s.row = p.kv + ((int64_t)e.blk * HS_PAGE + (pw & 3) * 16 + rl) * HS_KV_ROW_BYTES;
-      if (isA && good && e.left > 0 && (pw & 3) == 0 && lane == 0)  // the page's rows in use
-        bulk_prefetch_l2(p.kv + (int64_t)e.blk * kKeys / 2 * HS_KV_ROW_BYTES, (e.left < HS_PAGE ? e.left : HS_PAGE) * HS_KV_ROW_BYTES);
-      return s;
-    };
-    auto at = [&](const Src& s, int ps) { return ((s.ok >> ps) & 1u) ? s.row + ps * 4 * HS_KV_ROW_BYTES : p.kv; };
-    auto ld_group = [&](Chunk& ch, const Src& s, int g) {
-#pragma unroll
-      for (int ps = 0; ps < 4; ++ps) {
-        const uint8_t* src = at(s, ps);
-        ch.v[ps] = ldg_nc_v4(src + 128 * g + 16 * c8);
-        ch.s[ps] = ldg_nc_f32(src + HS_D_LATENT + 4 * g);
-      }
-    };
-    int slot = 0;
-    uint32_t par = 1;  // parity to wait for: the first round finds the slots free
-    bool go = true;
-    auto take = [&]() {  // the next slot of the ring, once it is free
-      const bool ok = go && !*abort_flag && mbar_wait(&empty[slot], par, p.err);
-      go = __all_sync(0xffffffffu, ok);
-      return ring + slot * (isA ? kBlk : 2 * kBlk);
-    };
-    auto publish = [&]() {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[slot]);
-      if (++slot == kSlots) {
-        slot = 0;
-        par ^= 1u;
-      }
-    };
-    bool range_ok = true;
-    auto st_group = [&](const Chunk& ch, const Src& s) {
-      uint8_t *b0, *b1;  // blocks of dims 0-63 and 64-127 of the group
-      const int s0 = slot;
-      if (isA) {
-        b0 = take();
-        if (++slot == kSlots) {
-          slot = 0;
-          par ^= 1u;
-        }
-        b1 = take();
-      } else {
-        b0 = take();
-        b1 = b0 + kBlk;
-      }
-      if (!go) return;
-      uint8_t* blk = swp ? b1 : b0;
-      const uint32_t o0 = 32 * (c8 & 3) + (swp ? 16 : 0);
-#pragma unroll
-      for (int ps = 0; ps < 4; ++ps) {
-        const int row = 16 * pw + 4 * ps + rl;
-        const bool live = (s.ok >> ps) & 1u;
-        const float sc = live ? ch.s[ps] : 0.f;
-        range_ok &= !live || (fabsf(sc) >= kScaleMin && fabsf(sc) <= kScaleMax);
-        const __half shi = __float2half_rn(sc);
-        const __half2 h2 = __half2half2(shi), l2 = __float2half2_rn(sc - __half2float(shi));
-        const uint32_t hu = *reinterpret_cast<const uint32_t*>(&h2), lu = *reinterpret_cast<const uint32_t*>(&l2);
-        const uint4 v = live ? ch.v[ps] : make_uint4(0, 0, 0, 0);
-        uint4 d0 = dequant8(swp ? v.z : v.x, swp ? v.w : v.y, hu, lu);
-        uint4 d1 = dequant8(swp ? v.x : v.z, swp ? v.y : v.w, hu, lu);
-        if (!isA && unsound(d0, d1)) d0 = d1 = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(blk + sw128_offset(row, o0)) = d0;
-        *reinterpret_cast<uint4*>(blk + sw128_offset(row, o0 ^ 16u)) = d1;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (isA && lane == 0) mbar_arrive(&full[s0]);
-      publish();
-    };
-    const int64_t ntiles = u1 - u0;
-    Src cur, nxt, after;
-    {
-      const Ent e0 = fetch(), e1 = fetch();
-      cur = resolve(e0);
-      nxt = resolve(e1);
-    }
-    Ent e2 = fetch();
-    Chunk c0, c1;
-    if (ntiles > 0) {
-      ld_group(c0, cur, 0);
-      ld_group(c1, cur, 1);
-    }
-#pragma unroll 1
-    for (int64_t i = 0; i < ntiles && go; ++i) {
-      after = resolve(e2);
-      e2 = fetch();
-      uint4 rope[4];
-      st_group(c0, cur);
-      ld_group(c0, cur, 2);
-      st_group(c1, cur);
-      ld_group(c1, cur, 3);
-      if (isA) {
-#pragma unroll
-        for (int ps = 0; ps < 4; ++ps) rope[ps] = ldg_nc_v4(at(cur, ps) + HS_D_LATENT + 16 + 16 * c8);
-      }
-      st_group(c0, cur);
-      ld_group(c0, nxt, 0);
-      st_group(c1, cur);
-      ld_group(c1, nxt, 1);
-      if (isA) {
-        uint8_t* blk = take();
-        if (go) {
-#pragma unroll
-          for (int ps = 0; ps < 4; ++ps)
-            *reinterpret_cast<uint4*>(blk + sw128_offset(16 * pw + 4 * ps + rl, 16 * c8)) =
-                ((cur.ok >> ps) & 1u) ? rope[ps] : make_uint4(0, 0, 0, 0);
-          publish();
-        }
-      }
-      cur = nxt;
-      nxt = after;
-    }
-    if (!go) *abort_flag = 1;
-    if (isA && !range_ok) flag_error(p.err, HS_FLAG_RANGE);
-  } else if (warp == 0 && isA) {
-    // ================================================================ A: QK =====================
-    if (lane == 0) {
-      constexpr uint32_t lat = idesc_f16(kRows, kKeys, 0, 0), rop = idesc_bf16(kRows, kKeys, 0, 0);
-      prefetch_tensormap(&map_q);
-      const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2);
-      const uint64_t kd = smem_desc(smem_u32(smem + kOffRingA), 16, 1024, 2);
-      Seg s;
-      int slot = 0, n = 0, i = 0;
-      uint32_t par = 0;
-      bool ok = true;
-#pragma unroll 1
-      for (; ok && walk.next(p, s); ++n) {
-        if (n > 0) {  // the previous block's MMAs must have read Q
-          mma_commit(q_free);
-          if (!mbar_wait(q_free, (uint32_t)(n - 1) & 1u, p.err)) {
-            ok = false;
-            break;
-          }
-        }
-        mbar_arrive_expect_tx(q_full, 9 * kBlk);
-        const int32_t y = (int32_t)((int64_t)s.q.start * p.H + (int64_t)s.b * kRows);
-#pragma unroll 1
-        for (int d = 0; d < 9; ++d) tma_load_2d(smem + d * kBlk, &map_q, q_full, 64 * d, y);
-        if (!mbar_wait(q_ready, (uint32_t)n & 1u, p.err)) {
-          ok = false;
-          ++n;
-          break;
-        }
-#pragma unroll 1
-        for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
-          const int sb = i & 1;
-          if (*abort_flag || !mbar_wait(&s_empty[sb], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err)) {
-            ok = false;
-            break;
-          }
-#pragma unroll 1
-          for (int d = 0; d < 9; ++d) {
-            if (!mbar_wait(&full[slot], par, p.err)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ss(tmem + kKeys * sb, qd + (uint64_t)((d * kBlk + kk * 32) >> 4), kd + (uint64_t)((slot * kBlk + kk * 32) >> 4),
-                          d < 8 ? lat : rop, (d | kk) != 0 ? 1u : 0u);
-            mma_commit(&empty[slot]);
-            if (++slot == kSlots) {
-              slot = 0;
-              par ^= 1u;
-            }
-          }
-          if (ok) mma_commit(&s_full[sb]);
-        }
-      }
-      if (!ok) *abort_flag = 1;
-      mma_commit(drain);
-      mbar_wait(drain, 0, p.err);
-      if (n > 0) mbar_wait(q_full, (uint32_t)(n - 1) & 1u, p.err);  // the last Q copy has landed
-    }
-  } else if (warp == 0) {
-    // ================================================================ B: PV =====================
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f16(kRows, 128, 0, 1);
-      const uint64_t pd = smem_desc(smem_u32(smem), 16, 1024, 2);
-      const uint64_t vd = smem_desc(smem_u32(smem + kOffRingB), kBlk, 1024, 2);
-      Seg s;
-      int slot = 0, n = 0, i = 0;
-      uint32_t par = 0;
-      bool ok = true;
-#pragma unroll 1
-      for (; ok && walk.next(p, s); ++n) {
-        if (n > 0 && !mbar_wait(o_free, (uint32_t)(n - 1) & 1u, p.err)) {
-          ok = false;
-          break;
-        }
-#pragma unroll 1
-        for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
-          const int pb = i & 1;
-          const uint32_t ph = (uint32_t)(i >> 1) & 1u;
-          if (*abort_flag || !mbar_wait_cluster(&p_full[pb], ph, p.err) || !mbar_wait(&corr[pb], ph, p.err)) {
-            ok = false;
-            break;
-          }
-          fence_proxy_async_all();
-#pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
-            if (!mbar_wait(&full[slot], par, p.err)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_bf16_ss(tmem + 128 * mt, pd + (uint64_t)(((2 * pb + kk / 4) * kBlk + (kk % 4) * 32) >> 4),
-                          vd + (uint64_t)((2 * slot * kBlk + kk * 2048) >> 4), id, (jt > s.ta || kk > 0) ? 1u : 0u);
-            mma_commit(&empty[slot]);
-            if (++slot == kSlots) {
-              slot = 0;
-              par ^= 1u;
-            }
-          }
-          if (ok) mma_commit(&pv_done[pb]);
-        }
-      }
-      if (!ok) *abort_flag = 1;
-      mma_commit(drain);
-      mbar_wait(drain, 0, p.err);
-    }
-  } else if (warp == 4 && !isA) {
-    // ================================================================ B: P buffers back to A ====
-    if (lane == 0) {
-      const uint32_t back = remote_smem(p_empty, 0);
-      const int64_t ntiles = u1 - u0;
-#pragma unroll 1
-      for (int64_t i = 0; i < ntiles; ++i) {
-        if (*abort_flag || !mbar_wait(&pv_done[i & 1], (uint32_t)(i >> 1) & 1u, p.err)) {
-          *abort_flag = 1;
-          break;
-        }
-        remote_arrive(back + 8 * (uint32_t)(i & 1));
-      }
-    }
-  } else if (warp >= kSmWarp0 && warp < kSmWarp0 + 4 && isA) {
-    // ================================================================ A: softmax ================
-    const int quad = warp & 3, row = 32 * quad + lane;
+  if (rows_warp && isA) {
+    if (kRaw) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    // ================================================================ softmax ===================
+    const int quad = warp & 3, g = (warp - 4) >> 2, row = 32 * quad + lane;  // g: columns 64 g .. + 63
     const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
-    const uint32_t r_p = remote_smem(smem, 1), r_alpha = remote_smem(smem + kOffAlpha, 1), r_sum = remote_smem(smem + kOffSum, 1);
-    const uint32_t r_moved = remote_smem(smem + kOffMoved, 1), r_full = remote_smem(p_full, 1);
-    Seg s;
-    int n = 0, i = 0;
+    const uint32_t to = rank + G;
+    const uint32_t r_p = remote_smem(smem + kOffP, to), r_alpha = remote_smem(smem + kOffAlpha, to), r_sum = remote_smem(smem + kOffSum, to);
+    const uint32_t r_full = remote_smem(p_full, to), r_sempty = remote_smem(s_empty, 0), r_qready = remote_smem(q_ready, 0);
+    float* smax = (float*)(smem + kOffMax);  // [2][2][128]
+    float* salpha = (float*)(smem + kOffAlpha);
+    float* ssum = (float*)(smem + kOffSum);
+    int n = 0, i = 0, x = 0;  // x: exchanges through smax, alternating halves
     bool ok = true;
+    // The row's two threads give each other a value. The wait is bounded like every other (ok turns false).
+    auto other = [&](float v) -> float {
+      float* at = smax + 256 * (x & 1);
+      at[128 * g + row] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&swap[quad]);
+      ok = warp_wait_all(&swap[quad], (uint32_t)x & 1u, p.err);
+      ++x;
+      return at[128 * (g ^ 1) + row];
+    };
 #pragma unroll 1
     for (; ok && walk.next(p, s); ++n) {
-      const bool idle = 32 * quad >= s.nrows;  // no row of this warp exists
-      const bool mine = row < s.nrows;
-      // Q's latent dims bf16 -> fp16 in place, this thread's row (the swizzle spreads the rows over the banks). A row
-      // whose largest value is outside [2^-6, 2^15) is rewritten from global memory times a power of two that
-      // puts it in [2^14, 2^15); its logits are scaled back below.
+      const int64_t grow = (int64_t)s.b * kRows + (int64_t)half * kHalf + row;  // of the request's rows
+      const int have = s.nrows - half * kHalf;                            // rows of this CTA that exist
+      const bool idle = 32 * quad >= have, mine = row < have;
       float coef = p.scale_log2;
-      ok = warp_wait_all(q_full, (uint32_t)n & 1u, p.err);
+      if (n > 0) ok = warp_wait_all(q_free, (uint32_t)(n - 1) & 1u, p.err);
       if (ok && !idle) {
+        // This thread's half of Q's row: latent dims 256 g .. + 255 to fp16 in tensor memory, rotary dims 32 g .. + 31 to
+        // shared memory. A row whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it
+        // in [2^14, 2^15); its logits are scaled back.
+        const uint8_t* src = p.q + ((int64_t)s.q.start * p.H + (mine ? grow : (int64_t)s.b * kRows)) * (HS_D_QK * 2) + 512 * g;
         uint32_t mx = 0u;
-#pragma unroll 1
-        for (int d = 0; d < 8; ++d) {
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            uint4* a = reinterpret_cast<uint4*>(smem + d * kBlk + sw128_offset(row, 16 * h));
-            uint4 v = *a;
-            uint32_t* w = &v.x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
-              w[k] ^= p.flip;
-              w[k] = pack_half2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
-            }
-            *a = v;
-          }
+#pragma unroll 4
+        for (int h = 0; h < 32; ++h) {
+          const uint4 v = ldg_nc_v4(src + 16 * h);
+          mx = __vmaxu2(__vmaxu2(mx, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+          mx = __vmaxu2(__vmaxu2(mx, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
         }
-        const uint32_t amax = max(mx & 0xFFFFu, mx >> 16);
+        uint32_t amax = max(mx & 0xFFFFu, mx >> 16);
+        amax = max(amax, __float_as_uint(other(__uint_as_float(amax))));
         int e = 0;
         if (amax >= 0x7F80u) {
           if (mine) flag_error(p.err, HS_FLAG_RANGE);
@@ -459,154 +588,173 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           e = 126;
         }
         e = e < -126 ? -126 : (e > 126 ? 126 : e);
-        if (!mine) e = 0;
-        if (e != 0) {
-          coef *= __uint_as_float((uint32_t)(127 - e) << 23);
-          const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-          const uint8_t* src = p.q + ((int64_t)s.q.start * p.H + (int64_t)s.b * kRows + row) * (HS_D_QK * 2);
+        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+        // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
+        coef = fmaxf(coef * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
 #pragma unroll 1
-          for (int h = 0; h < 72; ++h) {
-            uint4 v = ldg_nc_v4(src + 16 * h);
-            uint32_t* w = &v.x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              w[k] ^= p.flip;
-              const float lo = __uint_as_float(w[k] << 16) * f, hi = __uint_as_float(w[k] & 0xFFFF0000u) * f;
-              if (h < 64) {
-                w[k] = pack_half2(lo, hi);
-              } else {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
-                w[k] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-            }
-            *reinterpret_cast<uint4*>(smem + (h / 8) * kBlk + sw128_offset(row, 16 * (h % 8))) = v;
-          }
-        } else if (p.flip) {
+        for (int b = 0; b < 4; ++b) {  // 64 dims: 32 columns
+          uint32_t w[32];
 #pragma unroll
           for (int h = 0; h < 8; ++h) {
-            uint4* a = reinterpret_cast<uint4*>(smem + 8 * kBlk + sw128_offset(row, 16 * h));
-            uint4 v = *a;
-            v.x ^= p.flip, v.y ^= p.flip, v.z ^= p.flip, v.w ^= p.flip;
-            *a = v;
+            const uint4 v = ldg_nc_v4(src + 128 * b + 16 * h);
+            w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
           }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t u = w[k] ^ p.flip;
+            w[k] = pack_half2(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f);
+          }
+          tmem_st32(tmem + lane_base + 256 + 128 * g + 32 * b, w);
+        }
+        tmem_wait_st();
+        const uint8_t* rsrc = src + 1024 - 512 * g + 64 * g;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint4 v = ldg_nc_v4(rsrc + 16 * h);
+          uint32_t* w = &v.x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t u = w[k] ^ p.flip;
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f);
+            w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          *reinterpret_cast<uint4*>(smem + kOffQ + sw128_offset(row, 64 * g + 16 * h)) = v;
         }
       }
       fence_proxy_async_smem();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
+      if (lane == 0) remote_arrive(r_qready);
       if (!ok) break;
 
-      const int64_t g = (int64_t)s.b * kRows + row;
-      const int nsee = mine ? sees(p, s.q, g) : 0;
+      const int nsee = mine ? sees(p, s.q, grow) : 0;
       float ref = -INFINITY, l = 0.f;
+      const int32_t* bt = p.bt + (int64_t)s.r * p.bt_stride;
+      int32_t next_k = ldg_nc_s32(bt + (2 * s.ta + g < p.bt_stride ? 2 * s.ta + g : 0));
 #pragma unroll 1
       for (int jt = s.ta; jt < s.tb; ++jt, ++i) {
-        const int sb = i & 1;
+        const int b = i & 1;
         const uint32_t ph = (uint32_t)(i >> 1) & 1u;
-        // the tile's two pages, while S is on its way
-        const int32_t* bt = p.bt + (int64_t)s.r * p.bt_stride;
-        const bool in1 = 2 * jt + 1 < p.bt_stride;
-        const int32_t k0 = ldg_nc_s32(bt + (2 * jt < p.bt_stride ? 2 * jt : 0)), k1 = ldg_nc_s32(bt + (in1 ? 2 * jt + 1 : 0));
-        ok = !*abort_flag && warp_wait_all(&s_full[sb], ph, p.err);
-        ok = ok && warp_wait_all(&p_empty[sb], ph ^ 1u, p.err);
+        const int page = 2 * jt + g;  // this warp's page of the tile, read a tile ahead
+        const int32_t k = next_k;
+        next_k = ldg_nc_s32(bt + (page + 2 < p.bt_stride ? page + 2 : 0));
+        ok = !*abort_flag && warp_wait_all(&s_full[b], ph, p.err);
         if (!ok) break;
         tc_fence_after();
-        fence_acq_rel_cluster();
-        if (!idle) {
-          const bool v0 = k0 >= 0 && ((int64_t)k0 + 1) * HS_PAGE <= p.R;
-          const bool v1 = in1 && k1 >= 0 && ((int64_t)k1 + 1) * HS_PAGE <= p.R;
-          const int lim = nsee - jt * kKeys;  // columns of this tile that the row sees
-          const uint32_t sc = tmem + lane_base + kKeys * sb;
-          const bool all = __all_sync(0xffffffffu, lim >= kKeys && v0 && v1);
-          float mx = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t x[32];
-            tmem_ld32(sc + 32 * h, x);
-            tmem_wait_ld();
-            if (all) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(x[k]));
-            } else if (h < 2 ? v0 : v1) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, 32 * h + k < lim ? __uint_as_float(x[k]) : -INFINITY);
-            }
-          }
-          mx = mx == -INFINITY ? mx : mx * coef;
-          const bool up = mx > ref + kThreshold;
-          const bool moved = __any_sync(0xffffffffu, up);
-          if (moved) {
-            const float to = up ? mx : ref;
-            const float al = up ? fast_exp2(ref - to) : 1.f;
-            l *= al;
-            ref = to;
-            remote_st_f32(r_alpha + 4 * (128 * sb + row), al);
-          }
-          if (lane == 0) remote_st_u32(r_moved + 4 * (4 * sb + quad), moved ? 1u : 0u);
-          const float me = ref == -INFINITY ? 0.f : ref;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t x[32], pk[16];
-            tmem_ld32(sc + 32 * h, x);
-            tmem_wait_ld();
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float a = fast_exp2(fmaf(__uint_as_float(x[2 * k]), coef, -me));
-              float b = fast_exp2(fmaf(__uint_as_float(x[2 * k + 1]), coef, -me));
-              if (!all) {
-                const bool v = h < 2 ? v0 : v1;
-                a = v && 32 * h + 2 * k < lim ? a : 0.f;
-                b = v && 32 * h + 2 * k + 1 < lim ? b : 0.f;
-              }
-              sum += a + b;
-              pk[k] = pack_half2(a, b);
-            }
-            l += sum;
-            const uint32_t blk = r_p + (uint32_t)((2 * sb + h / 2) * kBlk);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              remote_st_v4(blk + sw128_offset(row, 64 * (h & 1) + 16 * k), pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-          }
-          if (jt == s.tb - 1) remote_st_f32(r_sum + 4 * (128 * sb + row), l);
+        if (idle) {
+          __syncwarp();
+          if (lane == 0) remote_arrive_relaxed(r_sempty + 8 * (uint32_t)b);
+          continue;
         }
-        // S has been read; P, the factors and the sums are on their way to B
-        tc_fence_before();
-        fence_proxy_async_all();
-        fence_acq_rel_cluster();
+        const bool there = page < p.bt_stride && k >= 0 && ((int64_t)k + 1) * HS_PAGE <= p.R;
+        const int lim = there ? nsee - jt * kKeys - 64 * g : 0;  // columns that this thread's row sees
+        const bool all = __all_sync(0xffffffffu, lim >= 64);
+        const uint32_t at = tmem + lane_base + kKeys * b + 64 * g;
+        // 32 columns, masked ones -inf
+        auto columns = [&](int h, uint32_t (&x)[32]) {
+          tmem_ld32(at + 32 * h, x);
+          tmem_wait_ld();
+          if (!all) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 32 * h + j < lim ? x[j] : 0xFF800000u;
+          }
+        };
+        auto taken = [&]() {  // S has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) remote_arrive_relaxed(r_sempty + 8 * (uint32_t)b);
+        };
+        auto top = [&](const uint32_t (&x)[32]) {
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) m0 = fmaxf(m0, __uint_as_float(x[j])), m1 = fmaxf(m1, __uint_as_float(x[j + 1]));
+          return fmaxf(m0, m1);
+        };
+        uint32_t v0[32], v1[32];
+        columns(0, v0);
+        float mx = top(v0);
+        columns(1, v1);
+        taken();
+        mx = fmaxf(mx, top(v1));
+        mx = fmaxf(mx, other(mx));
+        if (!ok) break;
+        mx = mx == -INFINITY ? mx : mx * coef;
+        const bool up = mx > ref + kThreshold;
+        const float to_ref = up ? mx : ref;
+        const float al = up ? fast_exp2(ref - to_ref) : 1.f;
+        l *= al;
+        ref = to_ref;
+        const float me = ref == -INFINITY ? 0.f : ref;
+        ok = warp_wait_all(&p_empty[b], ph, p.err);
+        if (!ok) break;
+        uint8_t* blk = smem + kOffStage + b * kPBuf + g * (kPBuf / 2);
+        // P of 32 columns; masked columns are -inf and coef > 0: their P is 0
+        auto weights = [&](int h, uint32_t (&x)[32]) {
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float a = fast_exp2(fmaf(__uint_as_float(x[2 * j]), coef, -me));
+            const float c2 = fast_exp2(fmaf(__uint_as_float(x[2 * j + 1]), coef, -me));
+            s0 += a;
+            s1 += c2;
+            x[j] = pack_half2(a, c2);
+          }
+          l += s0 + s1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(blk + sw128_offset(row, 64 * h + 16 * j)) =
+                make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        };
+        weights(0, v0);
+        weights(1, v1);
+        const bool last = jt == s.tb - 1;
+        float sum = 0.f;
+        if (last) {
+          sum = l + other(l);
+          if (!ok) break;
+          if (g == 0 && mine) {
+            const float z = sum == 0.f ? -INFINITY : (me + log2f(sum)) * kLn2;
+            if (s.ta == 0 && s.tb == s.tiles) {
+              if (p.lse) p.lse[(int64_t)s.q.start * p.H + grow] = z;
+            } else {
+              p.part_lse[(2 * c + (s.ta == 0 ? 1 : 0)) * kRows + half * kHalf + row] = z;
+            }
+          }
+        }
+        if (g == 0) {
+          salpha[128 * b + row] = al;
+          if (last) ssum[128 * b + row] = sum;
+        }
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&s_empty[sb]);
-          remote_arrive(r_full + 8 * (uint32_t)sb);
-        }
-      }
-      if (ok && mine) {
-        const float v = l == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(l)) * kLn2;
-        if (s.ta == 0 && s.tb == s.tiles) {
-          if (p.lse) p.lse[(int64_t)s.q.start * p.H + g] = v;
-        } else {
-          p.part_lse[(2 * c + (s.ta == 0 ? 1 : 0)) * kRows + row] = v;
+          const uint32_t bar = r_full + 8 * (uint32_t)b, off = (uint32_t)(b * kPBuf + g * (kPBuf / 2) + 32 * quad * 128);
+          bulk_s2remote(r_p + off, smem + kOffStage + off, 4096, bar);
+          if (g == 0) {
+            const uint32_t o4 = 4 * (uint32_t)(128 * b + 32 * quad);
+            bulk_s2remote(r_alpha + o4, smem + kOffAlpha + o4, 128, bar);
+            if (last) bulk_s2remote(r_sum + o4, smem + kOffSum + o4, 128, bar);
+          }
         }
       }
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp >= kSmWarp0 && warp < kSmWarp0 + 4) {
-    // ================================================================ B: rescaling, output ======
-    const int quad = warp & 3, row = 32 * quad + lane;
-    const uint32_t lane_base = (uint32_t)(32 * quad) << 16;
-    const uint32_t back = remote_smem(p_empty, 0);
+  } else if (rows_warp) {
+    if (kRaw) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    // ================================================================ rescaling, output =========
+    const int quad = warp & 3, g = (warp - 4) >> 2, row = 32 * quad + lane;  // g: O's columns 256 g .. + 255
+    const uint32_t at = tmem + ((uint32_t)(32 * quad) << 16) + 256 * g;
+    const uint32_t r_ofree = remote_smem(o_free, G);
     const float* alpha = (const float*)(smem + kOffAlpha);
     const float* sums = (const float*)(smem + kOffSum);
-    const uint32_t* moved = (const uint32_t*)(smem + kOffMoved);
     const int64_t C = U < p.clusters ? U : p.clusters;
     Desc desc = {0, 0, 0, 0};
     int64_t u = u0;
-    Seg s;
-    int i = 0;
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(p, s)) {
-      const bool idle = 32 * quad >= s.nrows;
+      const int have = s.nrows - half * kHalf;
+      const bool idle = 32 * quad >= have;
       const int64_t row0 = (int64_t)s.q.start * p.H + (int64_t)s.b * kRows;
       if (s.ta == 0 && s.tb < s.tiles) {
         desc.row0 = (int32_t)row0;
@@ -615,60 +763,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       u += s.tb - s.ta;
       float sum = 0.f;
+      int todo, i;
 #pragma unroll 1
-      for (int jt = s.ta; jt < s.tb; ++jt, ++i) {
-        const int pb = i & 1;
-        const uint32_t ph = (uint32_t)(i >> 1) & 1u;
-        ok = !*abort_flag && __all_sync(0xffffffffu, mbar_wait_cluster(&p_full[pb], ph, p.err));
-        if (!ok) break;
-        if (!idle) {
-          if (jt == s.tb - 1) sum = sums[128 * pb + row];
-          if (moved[4 * pb + quad] && jt > s.ta) {
-            const float al = alpha[128 * pb + row];
-            ok = warp_wait_all(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
-            if (!ok) break;
-            tc_fence_after();
+      do {
+        named_bar(kWake, 288);
+        todo = mc.todo;
+        i = mc.tile;
+        if ((todo & kLast) && !idle) sum = sums[128 * (i & 1) + row];
+        if ((todo & kRescale) && !idle) {
+          const float al = alpha[128 * (i & 1) + row];
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll 1
-            for (int h = 0; h < 16; ++h) {
-              uint32_t x[32];
-              tmem_ld32(tmem + lane_base + 32 * h, x);
+            for (int h = 0; h < 8; ++h) {
+              uint32_t v[32];
+              tmem_ld32(at + 32 * h, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
-              tmem_st32(tmem + lane_base + 32 * h, x);
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+              tmem_st32(at + 32 * h, v);
             }
             tmem_wait_st();
-            tc_fence_before();
           }
+          tc_fence_before();
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&corr[pb]);
-          remote_arrive(back + 8 * (uint32_t)pb);
-        }
+        named_bar(kWoken, 288);
+      } while (!(todo & (kLast | kStop)));
+      ok = !(todo & kStop) && warp_wait_all(&pv_done[i & 1], (uint32_t)(i >> 1) & 1u, p.err);
+      if (!ok) {
+        *abort_flag = 1;
+        if (todo & kStop) break;
+        ok = true;  // the controlling warp sees the flag and stops everyone at the next tile
+        continue;
       }
-      if (ok) ok = warp_wait_all(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
-      if (!ok) break;
       tc_fence_after();
       if (!idle) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const bool whole = s.ta == 0 && s.tb == s.tiles;
-        __nv_bfloat16* o = p.out + (row0 + row) * HS_D_LATENT;
-        float* po = p.part_out + ((int64_t)(2 * c + (s.ta == 0 ? 1 : 0)) * kRows + row) * HS_D_LATENT;
+        const bool whole = s.ta == 0 && s.tb == s.tiles, mine = row < have;
+        const int64_t r = (int64_t)half * kHalf + row;
+        __nv_bfloat16* o = p.out + (row0 + r) * HS_D_LATENT + 256 * g;
+        float* po = p.part_out + ((int64_t)(2 * c + (s.ta == 0 ? 1 : 0)) * kRows + r) * HS_D_LATENT + 256 * g;
 #pragma unroll 1
-        for (int h = 0; h < 16; ++h) {
-          uint32_t x[32];
-          tmem_ld32(tmem + lane_base + 32 * h, x);
+        for (int h = 0; h < 8; ++h) {
+          uint32_t v[32];
+          tmem_ld32(at + 32 * h, v);
           tmem_wait_ld();
-          if (row < s.nrows) {
+          if (mine) {
             if (whole) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t w[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * z]) * inv,
-                                                                  __uint_as_float(x[8 * k + 2 * z + 1]) * inv);
+                  const __nv_bfloat162 b2 =
+                      __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * z]) * inv, __uint_as_float(v[8 * k + 2 * z + 1]) * inv);
                   w[z] = *reinterpret_cast<const uint32_t*>(&b2);
                 }
                 *reinterpret_cast<uint4*>(o + 32 * h + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -677,51 +825,391 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 *reinterpret_cast<float4*>(po + 32 * h + 4 * k) =
-                    make_float4(__uint_as_float(x[4 * k]) * inv, __uint_as_float(x[4 * k + 1]) * inv,
-                                __uint_as_float(x[4 * k + 2]) * inv, __uint_as_float(x[4 * k + 3]) * inv);
+                    make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
+                                __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
             }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) remote_arrive_relaxed(r_ofree);
     }
     if (!ok) *abort_flag = 1;
-    if (warp == kSmWarp0 && lane == 0) p.desc[c] = desc;
+    if (rank == G && warp == 4 && lane == 0) p.desc[c] = desc;
+  } else {
+    if (kRaw) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp == kLoadWarp) {
+    // ================================================================ loads =====================
+    if (kRaw && lane == 0) {
+      if (isA)
+        load_raw<true>(p, smem, br, mc, &map_k, &map_v, &map_r, walk, half);
+      else
+        load_raw<false>(p, smem, br, mc, &map_k, &map_v, &map_r, walk, half);
+    } else if (lane == 0) {
+      const CUtensorMap* map = isA ? &map_k : &map_v;
+      prefetch_tensormap(map);
+      const int slots = isA ? kStA : kStB;
+      Ring ring = {0, 1};
+      int64_t issued = 0;
+      bool ok = true;
+#pragma unroll 1
+      while (ok && walk.next(p, s)) {
+#pragma unroll 1
+        for (int jt = s.ta; jt < s.tb && ok; ++jt) {
+          const int32_t y = (int32_t)(s.base + (int64_t)jt * kKeys);
+#pragma unroll 1
+          for (int k = 0; k < (isA ? Sh::kStages : Sh::kVStages); ++k) {
+            uint64_t* bar = &full[ring.slot];
+            if (*abort_flag || !mbar_wait(&empty[ring.slot], ring.par, p.err)) {
+              ok = false;
+              break;
+            }
+            if (isA) {  // dim blocks 3 k .. + 2, this CTA's keys
+              uint8_t* d = smem + kOffK + ring.slot * kKStage;
+              mbar_arrive_expect_tx(bar, kKStage);
+#pragma unroll
+              for (int b = 0; b < 3; ++b) tma_load_2d(d + b * kKBlk, map, bar, 64 * (3 * k + b), y + Sh::kMine * half);
+            } else {    // dims 128 (G k + half) .. + 127, all keys
+              uint8_t* d = smem + kOffV + ring.slot * kVStage;
+              mbar_arrive_expect_tx(bar, kVStage);
+              tma_load_2d(d, map, bar, 128 * (G * k + half), y);
+              tma_load_2d(d + kVBlk, map, bar, 128 * (G * k + half) + 64, y);
+            }
+            ++issued;
+            ring.next(slots);
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      // every copy has landed before the CTA may leave: slots before the position were used in its round
+      for (int q = 0; q < slots; ++q)
+        if (q < issued) mbar_wait(&full[q], q < ring.slot ? ring.par ^ 1u : ring.par, p.err);
+    }
+  } else if (lead && (warp == kIssue0 || (warp == Sh::kIssue1 && isA))) {
+    // ================================================================ MMAs ======================
+    if (lane == 0) {
+      const int mine = warp == kIssue0 ? 0 : 1;  // QK: the parity of the tiles that this warp issues
+      const int slots = isA ? kStA : kStB;
+      int slot = 0, i = 0, n = 0;
+      uint32_t par = 0;
+      int32_t stages = 0;  // stages of the ring before this one
+      bool ok = true;
+      // The next stage is there (the other CTA's part too). A parity tells two phases apart, so a warp that did not see
+      // the slot's last use (the other warp's tile) makes sure that the other warp has.
+      auto stage = [&]() -> bool {
+        bool r = true;
+        const int32_t last = stages - slots;  // the slot's last use
+        if (isA && last >= 0 && ((last / Sh::kStages) & 1) != mine) {
+          const uint64_t t0 = globaltimer();
+          for (uint32_t it = 0; mc.seen[mine ^ 1] <= last; ++it)
+            if ((it & 63) == 63 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
+              flag_error(p.err, HS_FLAG_TIMEOUT);
+              r = false;
+              break;
+            }
+        }
+        r = r && mbar_wait(&full[slot], par, p.err);
+        if (isA) mc.seen[mine] = stages + 1;
+        tc_fence_after();
+        return r;
+      };
+      auto skip = [&](int k) {
+        stages += k;
+        for (slot += k; slot >= slots; slot -= slots) par ^= 1u;
+      };
+      auto pass = [&]() {
+        Tc<G>::commit(&empty[slot], pair_mask);
+        skip(1);
+      };
+      if (isA) {
+        constexpr uint32_t lat = idesc_f16(kRows, kKeys, 0, 0), rop = idesc_bf16(kRows, kKeys, 0, 0);
+        const uint64_t qd = smem_desc(smem_u32(smem + kOffQ), 16, 1024, 2);
+        const uint64_t kd = smem_desc(smem_u32(smem + kOffK), 16, 1024, 2);
+#pragma unroll 1
+        for (; ok && walk.next(p, s); ++n) {
+          if (!mbar_wait_cluster(q_ready, (uint32_t)n & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_all();
+#pragma unroll 1
+          for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
+            if ((i & 1) != mine) {
+              skip(Sh::kStages);
+              continue;
+            }
+            const uint32_t d = tmem + kKeys * mine;
+            if (*abort_flag || !mbar_wait(&s_empty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err)) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int k = 0; k < Sh::kStages; ++k) {
+              if (!stage()) {
+                ok = false;
+                break;
+              }
+              const uint64_t kb = kd + (uint64_t)((slot * kKStage) >> 4);
+#pragma unroll
+              for (int b = 0; b < Sh::kBlocks && Sh::kBlocks * k + b < 9; ++b)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint64_t bd = kb + (uint64_t)((b * kKBlk + kk * 32) >> 4);
+                  if (Sh::kBlocks * k + b < 8)
+                    Tc<G>::ts(d, tmem + 256 + 32 * (Sh::kBlocks * k + b) + 8 * kk, bd, lat, (k | b | kk) != 0 ? 1u : 0u);
+                  else
+                    Tc<G>::ss(d, qd + (uint64_t)((kk * 32) >> 4), bd, rop, 1u);
+                }
+              pass();
+            }
+            if (kRaw && ok) {
+              const uint32_t rb = kRotaryBar + (uint32_t)mine;
+              ok = mbar_wait(&full[rb], (uint32_t)(i >> 1) & 1u, p.err);
+              tc_fence_after();
+              if (!ok) break;
+              const uint64_t rd = smem_desc(smem_u32(smem + Sh::kOffRotary + mine * kKBlk), 16, 1024, 2);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) Tc<G>::ss(d, qd + (uint64_t)((kk * 32) >> 4), rd + (uint64_t)((kk * 32) >> 4), rop, 1u);
+              Tc<G>::commit(&empty[rb], pair_mask);
+            }
+            if (ok) Tc<G>::commit(&s_full[i & 1], pair_mask);
+          }
+          if (ok) Tc<G>::commit(q_free, pair_mask);
+        }
+      } else {
+        constexpr uint32_t id = idesc_f16(kRows, 128 * G, 0, 1);
+        const uint64_t pd = smem_desc(smem_u32(smem + kOffP), 16, 1024, 2);
+        const uint64_t vd = smem_desc(smem_u32(smem + kOffV), kVBlk, 1024, 2);
+#pragma unroll 1
+        for (; ok && walk.next(p, s); ++n) {
+          if (n > 0 && !mbar_wait(o_free, (uint32_t)(n - 1) & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+#pragma unroll 1
+          for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
+            if (*abort_flag || !mbar_wait(&corr[i & 1], (uint32_t)(i >> 1) & 1u, p.err)) {
+              ok = false;
+              break;
+            }
+            const uint64_t pb = pd + (uint64_t)(((i & 1) * kPBuf) >> 4);
+#pragma unroll
+            for (int k = 0; k < Sh::kVStages; ++k) {
+              if (!stage()) {
+                ok = false;
+                break;
+              }
+              const uint64_t vb = vd + (uint64_t)((slot * kVStage) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                Tc<G>::ss(tmem + 128 * G * k, pb + (uint64_t)(((kk / 4) * (kPBuf / 2) + (kk % 4) * 32) >> 4),
+                            vb + (uint64_t)((kk * 2048) >> 4), id, (jt > s.ta || kk > 0) ? 1u : 0u);
+              pass();
+            }
+            if (ok) Tc<G>::commit(&pv_done[i & 1], pair_mask);
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      uint64_t* done = &drain[mine];
+      Tc<G>::commit(done, (uint16_t)(1u << rank));
+      mbar_wait(done, 0, p.err);
+    }
+  } else if (warp == kRelayWarp && !lead) {
+    // ================================================================ the other half is there ===
+    if (lane == 0) {
+      const uint32_t to = remote_smem(full, rank - 1);
+      const int slots = isA ? kStA : kStB;
+      Ring ring = {0, 0};
+      bool ok = true;
+#pragma unroll 1
+      for (int64_t i = 0; i < ntiles && ok; ++i) {
+#pragma unroll 1
+        for (int k = 0; k < (isA ? Sh::kStages : Sh::kVStages) && ok; ++k) {
+          ok = !*abort_flag && mbar_wait(&full[ring.slot], ring.par, p.err);
+          if (ok) remote_arrive_cta(to + 8 * (uint32_t)ring.slot);
+          ring.next(slots);
+        }
+        if (kRaw && isA && ok) {
+          const uint32_t rb = kRotaryBar + (uint32_t)(i & 1);
+          ok = mbar_wait(&full[rb], (uint32_t)(i >> 1) & 1u, p.err);
+          if (ok) remote_arrive_cta(to + 8 * rb);
+        }
+      }
+      if (!ok) *abort_flag = 1;
+    }
+  } else if (!isA && warp == (lead ? kRelayWarp : kIssue0)) {
+    // ================================================================ output control ============
+    // Waits for every tile's P; wakes the output warps where some row's maximum moved (once PV of the tile before has
+    // completed) or the block ends, and lets PV go on.
+    const uint32_t r_corr = remote_smem(corr, G);
+    const float4* alpha = (const float4*)(smem + kOffAlpha);
+    int i = 0;
+    bool ok = true;
+#pragma unroll 1
+    while (ok && walk.next(p, s)) {
+      const int have = s.nrows - half * kHalf;
+#pragma unroll 1
+      for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
+        const int b = i & 1;
+        ok = !*abort_flag && warp_wait_all(&p_full[b], (uint32_t)(i >> 1) & 1u, p.err);
+        int todo = ok ? 0 : kStop;
+        if (ok && jt > s.ta) {
+          const float4 al = alpha[32 * b + lane];  // rows 4 lane .. + 3
+          if (__any_sync(0xffffffffu, 32 * (lane >> 3) < have && (al.x != 1.f || al.y != 1.f || al.z != 1.f || al.w != 1.f))) {
+            ok = warp_wait_all(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
+            todo = ok ? kRescale : kStop;
+            tc_fence_after();
+            tc_fence_before();
+          }
+        }
+        if (jt == s.tb - 1 && ok) todo |= kLast;
+        if (todo) {
+          if (lane == 0) {
+            mc.todo = todo;
+            mc.tile = i;
+          }
+          __syncwarp();
+          named_bar(kWake, 288);
+          named_bar(kWoken, 288);
+        }
+        if (ok && lane == 0) remote_arrive_relaxed(r_corr + 8 * (uint32_t)b);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  } else if (warp == kBufWarp && !isA) {
+    // ================================================================ P buffers =================
+    // Arms a buffer's barrier with the bytes that its tile brings (4 KB of P and 128 bytes of factors per
+    // 32 rows, at a block's last tile 128 bytes of sums), then hands it to the softmax CTA.
+    if (lane == 0) {
+      const uint32_t back = remote_smem(p_empty, rank - G);
+      int i = 0;
+      bool ok = true;
+#pragma unroll 1
+      while (ok && walk.next(p, s)) {
+        const int left = s.nrows - half * kHalf;
+        const uint32_t quads = left <= 0 ? 0 : left >= kHalf ? 4 : (uint32_t)(left + 31) / 32;
+#pragma unroll 1
+        for (int jt = s.ta; jt < s.tb; ++jt, ++i) {
+          if (i >= 2 && (*abort_flag || !mbar_wait(&pv_done[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err))) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&p_full[i & 1], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
+          remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));
+        }
+      }
+      if (!ok) *abort_flag = 1;
+    }
+  } else if (kRaw && warp == (isA ? kScaleWarpA : kScaleWarpB)) {
+    // ================================================================ scales ====================
+    if (isA)
+      split_scales<true>(p, smem, br, mc, ntiles, lane);
+    else
+      split_scales<false>(p, smem, br, mc, ntiles, lane);
+  } else if (kRaw && producer_index(warp) >= 0) {
+    // ================================================================ producers =================
+    if (isA)
+      produce<true>(smem, br, mc, p.err, ntiles, half, producer_index(warp), lane);
+    else
+      produce<false>(smem, br, mc, p.err, ntiles, half, producer_index(warp), lane);
+  }
   }
   __syncthreads();
-  cluster_sync();  // no CTA leaves while the other may still write to it
+  cluster_sync();  // no CTA leaves while another may still write to it
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    Tc<G>::dealloc(tmem, 512);
   }
 }
 
 }  // namespace paged
 
-uint64_t paged_mla_workspace_bytes(int sms) {
+namespace paged {
+// Rows of the dequantised copy: every request's last tile is whole.
+static int64_t copy_capacity(int B, int64_t kv_tokens) { return kv_tokens + (int64_t)B * kKeys; }
+static uint64_t part_bytes(int sms) {
+  const uint64_t c = (uint64_t)(sms / (2 * G));
+  return 2 * c * (kHalf * G) * (HS_D_LATENT + 1) * 4 + c * sizeof(Desc);
+}
+
+// Whether T tokens of B requests with H heads have rows enough for a dequantised copy to pay.
+static bool copies(int T, int B, int H) { return (int64_t)T * H > 256ll * B; }
+
+template <bool kRaw>
+static cudaError_t launch(const Params& p0, const uint16_t* rows, uint64_t n, int sms, cudaStream_t stream, const char** why) {
+  using Sh = Shape<kRaw>;
+  auto kernel = paged_kernel<kRaw>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  // Clusters that run at once: the SMs of a GPC need not be a multiple of a cluster. Asked once per device.
+  static std::atomic<int> asked[64];
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int C = dev < 64 ? asked[dev].load(std::memory_order_relaxed) : 0;
+  if (C == 0) {
+    C = sms / (2 * G);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * G * C);
+    cfg.blockDim = dim3(Sh::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {2 * G, 1, 1};
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int most = 0;
+    if (cudaOccupancyMaxActiveClusters(&most, kernel, &cfg) == cudaSuccess && most > 0 && most < C) C = most;
+    if (dev < 64) asked[dev].store(C, std::memory_order_relaxed);
+  }
+  Params p = p0;
+  p.clusters = C;
+  CUtensorMap mk = {}, mv = {}, mr = {};
+  if (kRaw) {
+    if (!encode_2d(&mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.kv, HS_KV_ROW_BYTES, (uint64_t)p.R, HS_KV_ROW_BYTES, 128, HS_PAGE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_2d(&mv, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.kv, HS_KV_ROW_BYTES, (uint64_t)p.R, HS_KV_ROW_BYTES, 16, HS_PAGE,
+                   CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_2d(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.kv, HS_KV_ROW_BYTES / 2, (uint64_t)p.R, HS_KV_ROW_BYTES, 64, HS_PAGE,
+                   CU_TENSOR_MAP_SWIZZLE_128B)) {
+      *why = "cuTensorMapEncodeTiled failed for the pool";
+      return cudaErrorInvalidValue;
+    }
+  } else {
+    if (!encode_2d(&mk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rows, HS_D_QK, n, HS_D_QK * 2, 64, Sh::kMine, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&mv, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rows, HS_D_QK, n, HS_D_QK * 2, 64, kKeys, CU_TENSOR_MAP_SWIZZLE_128B)) {
+      *why = "cuTensorMapEncodeTiled failed for the dequantised rows";
+      return cudaErrorInvalidValue;
+    }
+    expand_kernel<<<4 * sms, kExpandThreads, 0, stream>>>(p, const_cast<uint16_t*>(rows));
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<2 * G * C, Sh::kThreads, kSmem, stream>>>(mk, mv, mr, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  paged_merge_kernel<Sh::kRows><<<dim3((unsigned)C, Sh::kRows / kMergeRows), kMergeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+}  // namespace paged
+
+uint64_t paged_mla_workspace_bytes(int T, int B, int H, int64_t kv_tokens, int sms) {
   using namespace paged;
-  const uint64_t c = (uint64_t)(sms / 2);
-  return 2 * c * kRows * (HS_D_LATENT + 1) * 4 + c * sizeof(Desc);
+  const uint64_t base = (part_bytes(sms) + 15) / 16 * 16;
+  return copies(T, B, H) ? base + (uint64_t)copy_capacity(B, kv_tokens) * HS_D_QK * 2 : base;
 }
 
 cudaError_t launch_paged_mla(const hs_paged_mla_args* a, int sms, cudaStream_t stream, const char** why) {
   using namespace paged;
-  CUtensorMap mq;
-  if (!encode_2d(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->q, HS_D_QK, (uint64_t)a->T * a->H, HS_D_QK * 2, 64, kRows,
-                 CU_TENSOR_MAP_SWIZZLE_128B)) {
-    *why = "cuTensorMapEncodeTiled failed for q";
-    return cudaErrorInvalidValue;
-  }
-  const int C = sms / 2;
+  const int most = sms / (2 * G);
   Params p;
   p.T = a->T;
   p.B = a->B;
   p.H = a->H;
   p.causal = a->causal;
   p.bt_stride = a->bt_stride;
-  p.clusters = C;
   p.q = reinterpret_cast<const uint8_t*>(a->q);
   p.kv = a->kv_pool;
   p.R = a->R;
@@ -735,15 +1223,12 @@ cudaError_t launch_paged_mla(const hs_paged_mla_args* a, int sms, cudaStream_t s
   p.lse = a->lse;
   p.err = a->err_flag;
   p.part_out = reinterpret_cast<float*>(a->workspace);
-  p.part_lse = p.part_out + (int64_t)2 * C * kRows * HS_D_LATENT;
-  p.desc = reinterpret_cast<Desc*>(p.part_lse + (int64_t)2 * C * kRows);
-  cudaError_t e = cudaFuncSetAttribute(paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  paged_kernel<<<2 * C, kThreads, kSmem, stream>>>(mq, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  paged_merge_kernel<kRows><<<dim3((unsigned)C, kRows / kMergeRows), kMergeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  p.part_lse = p.part_out + (int64_t)2 * most * (kHalf * G) * HS_D_LATENT;
+  p.desc = reinterpret_cast<Desc*>(p.part_lse + (int64_t)2 * most * (kHalf * G));
+  const uint16_t* rows = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(a->workspace) +
+                                                           paged_mla_workspace_bytes(0, a->B, a->H, a->kv_tokens, sms));
+  const uint64_t n = (uint64_t)copy_capacity(a->B, a->kv_tokens);
+  return copies(a->T, a->B, a->H) ? launch<false>(p, rows, n, sms, stream, why) : launch<true>(p, rows, n, sms, stream, why);
 }
 
 }  // namespace hs

@@ -35,7 +35,6 @@ struct Params {
   float* part_out;   // [2 clusters][128][512]: slot 2c: the part that ends or passes through cluster c, 2c + 1: one that starts there
   float* part_lse;   // [2 clusters][128]
   Desc* desc;        // [clusters]
-  const uint16_t* rows16;  // chunks: the dequantised rows [cap][576]
   int64_t kv_tokens;
 };
 

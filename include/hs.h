@@ -536,9 +536,10 @@ hs_status hs_rope_inv_freq(int32_t rot, double base, int32_t kind, double factor
  *   seq_len       int32 [B], in [0, bt_stride * 64]
  *   kv_tokens     the caller's bound on the sum of seq_len (its own lengths are known on the host); it sizes the workspace
  *   out, lse      bf16 [T, H, 512];  fp32 [T, H] or NULL
- *   err_flag      req_start out of order sets HS_FLAG_BAD_INDEX, a length outside its limits or a sum above
- *                 kv_tokens HS_FLAG_BAD_LENGTH (such requests see no row); a block outside the pool sets
- *                 HS_FLAG_BAD_BLOCK and its rows count as not there
+ *   err_flag      a request's offsets out of order set HS_FLAG_BAD_INDEX (its outputs are not written), a length outside its
+ *                 limits HS_FLAG_BAD_LENGTH (the request sees no row), a sum of lengths above kv_tokens
+ *                 HS_FLAG_BAD_LENGTH (nothing is written); a block outside the pool sets HS_FLAG_BAD_BLOCK and its rows
+ *                 count as not there
  *   workspace     hs_paged_mla_workspace_size() bytes of 16-byte aligned device memory, scratch; calls that share
  *                 one must not overlap on the GPU
  * ---------------------------------------------------------------------------------------- */
@@ -562,8 +563,9 @@ typedef struct {
 
 hs_status hs_paged_mla_fwd(const hs_paged_mla_args* a, hs_stream_t stream);
 
-/* Bytes of workspace hs_paged_mla_fwd needs for these sizes on the current device. It never shrinks as a
- * size grows, so the size for a service's limits serves every smaller call. */
+/* Bytes of workspace hs_paged_mla_fwd needs for these sizes on the current device: 40 MB for partial results, and,
+ * where a request has more than 256 (token, head) rows on average (T * H > 256 * B), 1,152 bytes for each of
+ * kv_tokens + 128 * B dequantised rows. */
 hs_status hs_paged_mla_workspace_size(int32_t T, int32_t B, int32_t H, int64_t kv_tokens, uint64_t* bytes);
 
 /* ------------------------------------------------------------------------------------------
