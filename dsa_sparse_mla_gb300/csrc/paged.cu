@@ -47,13 +47,12 @@ namespace paged {
 constexpr int G = 2;                           // CTAs that share a product
 constexpr int kHalf = 128;                     // rows of a CTA
 constexpr int kPBuf = 2 * kHalf * 128;         // P of a tile: 2 x [128 rows][64 keys]
-// Roles by warp; warp w runs on sub-partition w % 4. The issuing warps share theirs with no producer: a sub-partition busy
-// with producers' arithmetic feeds an issuing thread several times slower than the tensor core runs.
-constexpr int kIssue0 = 0, kLoadWarp = 1, kRelayWarp = 2, kBufWarp = 3, kSmWarp0 = 4, kProdWarps = 3;
-// producer of warp w (13-15: the first group of three, 17-19: the second), or -1
-__host__ __device__ constexpr int producer_index(int w) { return w < 13 || w % 4 == 0 ? -1 : w - 13 - (w - 12) / 4; }
-static_assert(producer_index(13) == 0 && producer_index(15) == 2 && producer_index(17) == 3 && producer_index(19) == 5, "roles");
-constexpr int kScaleWarpA = 3, kScaleWarpB = 12;  // warps without another role there
+// Roles by warp (warp w runs on sub-partition w % 4).
+constexpr int kIssue0 = 0, kIssue1 = 3, kLoadWarp = 1, kRelayWarp = 2, kBufWarp = 3, kSmWarp0 = 4;
+constexpr int kScaleWarpB = 12;  // softmax CTA: the warp that does not relay (issuing CTA) or issue (the other)
+// Producers, two groups of kProd warps: softmax CTA 12-15 and 16-19, output CTA 13-15 and 17-19. Index of warp w, or -1.
+__host__ __device__ constexpr int producer_index(int w, bool isA) { return w < 12 ? -1 : isA ? w - 12 : w % 4 == 0 ? -1 : w - 13 - (w - 12) / 4; }
+static_assert(producer_index(13, false) == 0 && producer_index(15, false) == 2 && producer_index(17, false) == 3 && producer_index(19, false) == 5, "roles");
 constexpr int kVBlk = kKeys * 128;             // [128 keys][64 dims]
 constexpr int kVStage = 2 * kVBlk;             // 128 dims
 constexpr int kMaxSlots = 8;
@@ -79,7 +78,6 @@ static_assert(kOffK % 1024 == 0 && kOffStage % 1024 == 0 && kOffV % 1024 == 0, "
 template <bool kRaw>
 struct Shape {
   static constexpr int kThreads = kRaw ? 640 : 384;
-  static constexpr int kIssue1 = kRaw ? 12 : 3;    // the second issuing warp
   static constexpr int kRows = kHalf * G;          // rows of a block
   static constexpr int kMine = kKeys / G;          // keys of a K block in one CTA
   static constexpr int kKBlk = kMine * 128;        // [kMine keys][64 dims]
@@ -289,8 +287,6 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
       y[h] = good ? blk[h] * HS_PAGE : (int32_t)p.R;
     }
     fetch();
-    if (isA && live && left > 0 && blk[0] >= 0 && ((int64_t)blk[0] + 1) * HS_PAGE <= p.R)  // the next tile's page towards L2
-      bulk_prefetch_l2(p.kv + (int64_t)blk[0] * HS_PAGE * HS_KV_ROW_BYTES, (left < HS_PAGE ? left : HS_PAGE) * HS_KV_ROW_BYTES);
     // the scales of the tile before the last are split
     ok = !mc.abort && (tile < 2 || mbar_wait(&br.split_full[t], ph ^ 1u, p.err));
     if (!ok) break;
@@ -322,6 +318,8 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
       ++issued;
       ring.next(kSlots);
     }
+    if (isA && live && left > 0 && blk[0] >= 0 && ((int64_t)blk[0] + 1) * HS_PAGE <= p.R)  // the next tile's page towards L2
+      bulk_prefetch_l2(p.kv + (int64_t)blk[0] * HS_PAGE * HS_KV_ROW_BYTES, (left < HS_PAGE ? left : HS_PAGE) * HS_KV_ROW_BYTES);
   }
   if (!ok) mc.abort = 1;
   // every copy has landed before the CTA may leave: slots before the position were used in its round
@@ -369,9 +367,9 @@ __device__ __forceinline__ void split_scales(const Params& p, uint8_t* smem, Bar
   if (isA && !range_ok) flag_error(p.err, HS_FLAG_RANGE);
 }
 
-// raw: the producers turn a latent group's codes into fp16 blocks of the K or V ring. Two groups of three warps take turns,
+// raw: the producers turn a latent group's codes into fp16 blocks of the K or V ring. Two groups of warps take turns,
 // so that one converts while the other waits and hands over (the rings' slots are even in number: a slot is always the
-// same group's). Warp w of a group works on the quads of rows w, w + 3, ...: lane l reads the codes 16 (l % 8) .. + 15 of row
+// same group's). Warp w of a group works on the quads of rows w, w + kProd, ...: lane l reads the codes 16 (l % 8) .. + 15 of row
 // l / 8 of a quad as two 8-byte pieces, which become the 16-byte pieces 2 (l % 4) and + 1 of a row of block (l % 8) / 4.
 // Which of the two a lane takes first alternates with l / 4 and with the row, so that the reads and the stores of a warp hit
 // different banks. Bound by issue slots: about 40 instructions per 512 codes, most of them (cvt, half2 arithmetic) at half
@@ -383,12 +381,12 @@ __device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32
   constexpr int kSlots = isA ? Sh::kStA : Sh::kStB;
   constexpr int kCodes = isA ? Sh::kCodesA : Sh::kCodesB;
   constexpr int kKeysHere = isA ? Sh::kMine : kKeys;
-  constexpr int kQuads = kKeysHere / 4, kPass = (kQuads + kProdWarps - 1) / kProdWarps;
+  constexpr int kProd = isA ? 4 : 3, kBatch = isA ? 2 : 3;
+  constexpr int kQuads = kKeysHere / 4, kPass = (kQuads + kProd - 1) / kProd;
   constexpr int kGroups = isA ? 4 : 4 / G;
   static_assert(kSlots % 2 == 0 && Sh::kCodeSlots % 2 == 0 && kGroups % 2 == 0, "a slot belongs to one group");
-  const int e = pw / kProdWarps, w = pw % kProdWarps;
+  const int e = pw / kProd, w = pw % kProd;
   const int rl = lane >> 3, c8 = lane & 7;
-  // rows 4 q + rl, q = w + 3 j: bit 2 of the row alternates with j, and with it bit 2 of the swizzled piece
   const uint32_t odd = (uint32_t)((c8 >> 2) ^ (rl & 1));  // the piece taken first
   const uint8_t* codes = smem + (isA ? Sh::kOffCodesA : Sh::kOffCodesB) + rl * 128 + 16 * c8;
   const uint2* split = reinterpret_cast<const uint2*>(smem + (isA ? Sh::kOffSplitA : Sh::kOffSplitB)) + rl;
@@ -411,17 +409,17 @@ __device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32
         if (!go) mc.stop[e] = 1;
         __syncwarp();
       }
-      named_bar(kGo + e, 32 * kProdWarps);
+      named_bar(kGo + e, 32 * kProd);
       go = mc.stop[e] == 0;  // the same for every warp of the group
       if (!go) break;
       const int g = isA ? k : 2 * k + half;
       uint8_t* blk = out + ring.slot * kStage;
 #pragma unroll
-      for (int p0 = 0; p0 < kPass; p0 += 3) {  // three quads at a time
-        uint2 va[3], vb[3], sc[3];
+      for (int p0 = 0; p0 < kPass; p0 += kBatch) {  // a few quads at a time
+        uint2 va[kBatch], vb[kBatch], sc[kBatch];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const int q = w + kProdWarps * (p0 + j);
+        for (int j = 0; j < kBatch; ++j) {
+          const int q = w + kProd * (p0 + j);
           if (q < kQuads) {
             const uint8_t* c = codes + cr.slot * kCodes + q * 512;
             va[j] = *reinterpret_cast<const uint2*>(c + 8 * odd);
@@ -430,8 +428,8 @@ __device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32
           }
         }
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const int q = w + kProdWarps * (p0 + j);
+        for (int j = 0; j < kBatch; ++j) {
+          const int q = w + kProd * (p0 + j);
           if (q < kQuads) {
             uint4 d0 = dequant8(va[j].x, va[j].y, sc[j].x, sc[j].y);
             uint4 d1 = dequant8(vb[j].x, vb[j].y, sc[j].x, sc[j].y);
@@ -444,14 +442,14 @@ __device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32
       }
       fence_proxy_async_smem();
       if (first) {
-        named_bar(kDone + e, 32 * kProdWarps);
+        named_bar(kDone + e, 32 * kProd);
         if (lane == 0) {
           mbar_arrive(&br.full[ring.slot]);
           mbar_arrive(&br.codes_empty[cr.slot]);
           if (k + 2 >= kGroups) mbar_arrive(&br.split_empty[t]);
         }
       } else {
-        named_arrive(kDone + e, 32 * kProdWarps);
+        named_arrive(kDone + e, 32 * kProd);
       }
       ring.next(kSlots);
       ring.next(kSlots);
@@ -886,7 +884,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       for (int q = 0; q < slots; ++q)
         if (q < issued) mbar_wait(&full[q], q < ring.slot ? ring.par ^ 1u : ring.par, p.err);
     }
-  } else if (lead && (warp == kIssue0 || (warp == Sh::kIssue1 && isA))) {
+  } else if (lead && (warp == kIssue0 || (warp == kIssue1 && isA))) {
     // ================================================================ MMAs ======================
     if (lane == 0) {
       const int mine = warp == kIssue0 ? 0 : 1;  // QK: the parity of the tiles that this warp issues
@@ -1102,18 +1100,18 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       }
       if (!ok) *abort_flag = 1;
     }
-  } else if (kRaw && warp == (isA ? kScaleWarpA : kScaleWarpB)) {
+  } else if (kRaw && warp == (!isA ? kScaleWarpB : lead ? kRelayWarp : kIssue0)) {
     // ================================================================ scales ====================
     if (isA)
       split_scales<true>(p, smem, br, mc, ntiles, lane);
     else
       split_scales<false>(p, smem, br, mc, ntiles, lane);
-  } else if (kRaw && producer_index(warp) >= 0) {
+  } else if (kRaw && producer_index(warp, isA) >= 0) {
     // ================================================================ producers =================
     if (isA)
-      produce<true>(smem, br, mc, p.err, ntiles, half, producer_index(warp), lane);
+      produce<true>(smem, br, mc, p.err, ntiles, half, producer_index(warp, isA), lane);
     else
-      produce<false>(smem, br, mc, p.err, ntiles, half, producer_index(warp), lane);
+      produce<false>(smem, br, mc, p.err, ntiles, half, producer_index(warp, isA), lane);
   }
   }
   __syncthreads();
