@@ -92,10 +92,10 @@ struct Shape {
   // raw: rotary blocks [2], rings of undecoded latent groups ([keys][128 codes]), two tiles' scales ([keys][4]) and those
   // split into fp16 pairs ([4 groups][keys])
   static constexpr int kCodesA = kMine * 128, kCodesB = kKeys * 128;
-  static constexpr int kCodeSlots = 4;
+  static constexpr int kSlotsA = 6, kSlotsB = 4;   // of the rings of codes
   static constexpr int kOffRotary = kOffK + kStA * kKStage;
   static constexpr int kOffCodesA = kOffRotary + 2 * kKBlk, kOffCodesB = kOffV + kStB * kVStage;
-  static constexpr int kOffScaleA = kOffCodesA + kCodeSlots * kCodesA, kOffScaleB = kOffCodesB + kCodeSlots * kCodesB;
+  static constexpr int kOffScaleA = kOffCodesA + kSlotsA * kCodesA, kOffScaleB = kOffCodesB + kSlotsB * kCodesB;
   static constexpr int kOffSplitA = kOffScaleA + 2 * kMine * 16, kOffSplitB = kOffScaleB + 2 * kKeys * 16;
   static_assert(!kRaw || (kOffSplitA + 8 * kMine * 8 <= kOffAlpha && kOffSplitB + 8 * kKeys * 8 <= kOffAlpha), "layout");
   static_assert(kOffK + kStA * kKStage <= kOffAlpha && kOffV + kStB * kVStage <= kOffAlpha, "layout");
@@ -197,9 +197,9 @@ struct Ring {
 struct Bars {
   uint64_t full[kMaxSlots];       // this CTA's part of a stage is there; in the issuing CTA the other's too
   uint64_t empty[kMaxSlots];      // the MMAs have read the stage (both CTAs)
-  uint64_t codes_full[4];         // raw: a latent group's codes have landed
+  uint64_t codes_full[6];         // raw: a latent group's codes have landed
   uint64_t scale_full[2];         // raw: a tile's scales have landed
-  uint64_t codes_empty[4];        // raw: the producers have read them
+  uint64_t codes_empty[6];        // raw: the producers have read them
   uint64_t split_full[2];         // raw: a tile's scales are split -> producers
   uint64_t split_empty[2];        // raw: both groups of producers are done with them
   uint64_t s_full[2];             // S complete (both)
@@ -241,7 +241,7 @@ template <bool isA>
 __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& br, Misc& mc, const CUtensorMap* codes,
                                          const CUtensorMap* scales, const CUtensorMap* rotary, Walk<kHalf * G>& walk, int half) {
   using Sh = Shape<true>;
-  constexpr int kSlots = Sh::kCodeSlots, kCodes = isA ? Sh::kCodesA : Sh::kCodesB;
+  constexpr int kSlots = isA ? Sh::kSlotsA : Sh::kSlotsB, kCodes = isA ? Sh::kCodesA : Sh::kCodesB;
   constexpr int kPages = isA ? 1 : 2, kGroups = isA ? 4 : 4 / G;
   uint8_t* cring = smem + (isA ? Sh::kOffCodesA : Sh::kOffCodesB);
   uint8_t* sring = smem + (isA ? Sh::kOffScaleA : Sh::kOffScaleB);
@@ -295,15 +295,6 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
 #pragma unroll
     for (int h = 0; h < kPages; ++h)
       tma_load_2d(sring + (t * kPages + h) * HS_PAGE * 16, scales, &br.scale_full[t], HS_D_LATENT, y[h]);
-    if (isA) {
-      ok = mbar_wait(&br.empty[kRotaryBar + t], ph ^ 1u, p.err);
-      if (!ok) {
-        ++tile;
-        break;
-      }
-      mbar_arrive_expect_tx(&br.full[kRotaryBar + t], Sh::kKBlk);
-      tma_load_2d(smem + Sh::kOffRotary + t * Sh::kKBlk, rotary, &br.full[kRotaryBar + t], (HS_D_LATENT + 16) / 2, y[0]);
-    }
 #pragma unroll 1
     for (int k = 0; k < kGroups; ++k) {
       if (mc.abort || !mbar_wait(&br.codes_empty[ring.slot], ring.par, p.err)) {
@@ -318,8 +309,13 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
       ++issued;
       ring.next(kSlots);
     }
-    if (isA && live && left > 0 && blk[0] >= 0 && ((int64_t)blk[0] + 1) * HS_PAGE <= p.R)  // the next tile's page towards L2
-      bulk_prefetch_l2(p.kv + (int64_t)blk[0] * HS_PAGE * HS_KV_ROW_BYTES, (left < HS_PAGE ? left : HS_PAGE) * HS_KV_ROW_BYTES);
+    if (isA && ok) {
+      ok = mbar_wait(&br.empty[kRotaryBar + t], ph ^ 1u, p.err);
+      if (ok) {
+        mbar_arrive_expect_tx(&br.full[kRotaryBar + t], Sh::kKBlk);
+        tma_load_2d(smem + Sh::kOffRotary + t * Sh::kKBlk, rotary, &br.full[kRotaryBar + t], (HS_D_LATENT + 16) / 2, y[0]);
+      }
+    }
   }
   if (!ok) mc.abort = 1;
   // every copy has landed before the CTA may leave: slots before the position were used in its round
@@ -379,12 +375,12 @@ __device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32
   using Sh = Shape<true>;
   constexpr int kBlk = isA ? Sh::kKBlk : kVBlk, kStage = 2 * kBlk;
   constexpr int kSlots = isA ? Sh::kStA : Sh::kStB;
-  constexpr int kCodes = isA ? Sh::kCodesA : Sh::kCodesB;
+  constexpr int kCodes = isA ? Sh::kCodesA : Sh::kCodesB, kCodeSlots = isA ? Sh::kSlotsA : Sh::kSlotsB;
   constexpr int kKeysHere = isA ? Sh::kMine : kKeys;
   constexpr int kProd = isA ? 4 : 3, kBatch = isA ? 2 : 3;
   constexpr int kQuads = kKeysHere / 4, kPass = (kQuads + kProd - 1) / kProd;
   constexpr int kGroups = isA ? 4 : 4 / G;
-  static_assert(kSlots % 2 == 0 && Sh::kCodeSlots % 2 == 0 && kGroups % 2 == 0, "a slot belongs to one group");
+  static_assert(kSlots % 2 == 0 && kCodeSlots % 2 == 0 && kGroups % 2 == 0, "a slot belongs to one group");
   const int e = pw / kProd, w = pw % kProd;
   const int rl = lane >> 3, c8 = lane & 7;
   const uint32_t odd = (uint32_t)((c8 >> 2) ^ (rl & 1));  // the piece taken first
@@ -453,8 +449,8 @@ __device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32
       }
       ring.next(kSlots);
       ring.next(kSlots);
-      cr.next(Sh::kCodeSlots);
-      cr.next(Sh::kCodeSlots);
+      cr.next(kCodeSlots);
+      cr.next(kCodeSlots);
     }
   }
   if (!go) mc.abort = 1;
@@ -492,7 +488,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       mbar_init(&full[s], G == 2 && lead ? 2 : 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 6; ++s) {
       mbar_init(&br.codes_full[s], 1);
       mbar_init(&br.codes_empty[s], 1);
     }
