@@ -560,17 +560,50 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       float coef = p.scale_log2;
       if (n > 0) ok = warp_wait_all(q_free, (uint32_t)(n - 1) & 1u, p.err);
       if (ok && !idle) {
-        // This thread's half of Q's row: latent dims 256 g .. + 255 to fp16 in tensor memory, rotary dims 32 g .. + 31 to
-        // shared memory. A row whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it
-        // in [2^14, 2^15); its logits are scaled back.
-        const uint8_t* src = p.q + ((int64_t)s.q.start * p.H + (mine ? grow : (int64_t)s.b * kRows)) * (HS_D_QK * 2) + 512 * g;
-        uint32_t mx = 0u;
-#pragma unroll 4
-        for (int h = 0; h < 32; ++h) {
-          const uint4 v = ldg_nc_v4(src + 16 * h);
-          mx = __vmaxu2(__vmaxu2(mx, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
-          mx = __vmaxu2(__vmaxu2(mx, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+        // Q's rows 32 quad .. + 31 of this CTA: latent dims 256 g .. + 255 to fp16 in tensor memory, rotary dims 32 g .. + 31 to
+        // shared memory. 32 dims at a time: coalesced loads (lane l takes 16 bytes of rows l / 4 + 8 j), through 2 KB of the
+        // rotary block's place (64-byte swizzle) to the thread that owns the row. Rows past the block's are read as its
+        // first row.
+        const uint8_t* base = p.q + ((int64_t)s.q.start * p.H + (int64_t)s.b * kRows) * (HS_D_QK * 2);
+        const int64_t myrow = mine ? (int64_t)half * kHalf + row : 0;
+        uint8_t* scratch = smem + kOffQ + 4096 * quad + 2048 * g;
+        const uint8_t* src[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 32 * quad + 8 * j + (lane >> 2);
+          src[j] = base + (r < have ? (int64_t)half * kHalf + r : 0) * (HS_D_QK * 2) + 512 * g + 16 * (lane & 3);
         }
+        uint32_t mx = 0u;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 8; c0 += 2) {
+          uint4 x[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[u][j] = ldg_nc_v4(src[j] + 64 * (c0 + u));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            __syncwarp();  // the piece before has been read
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(scratch + sw64_offset(8 * j + (lane >> 2), 16 * (lane & 3))) = x[u][j];
+            __syncwarp();
+            uint32_t w[16];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const uint4 v = *reinterpret_cast<const uint4*>(scratch + sw64_offset(lane, 16 * h));
+              w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+              const uint32_t f = w[k] ^ p.flip;
+              w[k] = pack_half2(__uint_as_float(f << 16), __uint_as_float(f & 0xFFFF0000u));
+            }
+            tmem_st16(tmem + lane_base + 256 + 128 * g + 16 * (c0 + u), w);
+          }
+        }
+        // A row whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it in
+        // [2^14, 2^15); its logits are scaled back.
         uint32_t amax = max(mx & 0xFFFFu, mx >> 16);
         amax = max(amax, __float_as_uint(other(__uint_as_float(amax))));
         int e = 0;
@@ -585,26 +618,28 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
         const float f = __uint_as_float((uint32_t)(e + 127) << 23);
         // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
         coef = fmaxf(coef * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
+        const uint8_t* own = base + myrow * (HS_D_QK * 2);
+        if (__any_sync(0xffffffffu, e != 0)) {  // rare: again, each thread its row
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {  // 64 dims: 32 columns
-          uint32_t w[32];
+          for (int b = 0; b < 8; ++b) {
+            uint32_t w[16];
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const uint4 v = ldg_nc_v4(src + 128 * b + 16 * h);
-            w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
-          }
+            for (int h = 0; h < 4; ++h) {
+              const uint4 v = ldg_nc_v4(own + 512 * g + 64 * b + 16 * h);
+              w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+            }
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const uint32_t u = w[k] ^ p.flip;
-            w[k] = pack_half2(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f);
+            for (int k = 0; k < 16; ++k) {
+              const uint32_t q = w[k] ^ p.flip;
+              w[k] = pack_half2(__uint_as_float(q << 16) * f, __uint_as_float(q & 0xFFFF0000u) * f);
+            }
+            tmem_st16(tmem + lane_base + 256 + 128 * g + 16 * b, w);
           }
-          tmem_st32(tmem + lane_base + 256 + 128 * g + 32 * b, w);
         }
         tmem_wait_st();
-        const uint8_t* rsrc = src + 1024 - 512 * g + 64 * g;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          uint4 v = ldg_nc_v4(rsrc + 16 * h);
+          uint4 v = ldg_nc_v4(own + 1024 + 64 * g + 16 * h);
           uint32_t* w = &v.x;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

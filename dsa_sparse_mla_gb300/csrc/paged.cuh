@@ -245,6 +245,7 @@ __device__ __forceinline__ bool unsound(const uint4& a, const uint4& b) {
 // Joins the parts of the block that starts in cluster blockIdx.x and goes on in the next ones: each part is
 // normalised by its own sum, so out = sum_s e^(lse_s - lse) O_s. Eight rows per CTA.
 constexpr int kMergeThreads = 256, kMergeRows = 8, kMaxClusters = 128;
+static_assert(kMergeThreads == 32 * kMergeRows, "a warp per row");
 template <int kRows>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Params p) {
   const int c = blockIdx.x, r0 = blockIdx.y * kMergeRows;
@@ -252,18 +253,26 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Params
   if (d.nparts == 0 || r0 >= d.nrows) return;
   __shared__ float w[kMaxClusters][kMergeRows];
   auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
-  if (threadIdx.x < kMergeRows) {
-    const int row = r0 + threadIdx.x;
+  // weights of the parts: a warp per row, a lane per part (and 32 further on)
+  {
+    const int i = threadIdx.x / 32, lane = threadIdx.x % 32, row = r0 + i;
     float m = -INFINITY, z = 0.f;
-    for (int s = 0; s < d.nparts; ++s) m = fmaxf(m, p.part_lse[slot(s) * kRows + row]);
-    for (int s = 0; s < d.nparts; ++s) {
+    for (int s = lane; s < d.nparts; s += 32) {
       const float l = p.part_lse[slot(s) * kRows + row];
-      const float e = l == -INFINITY ? 0.f : __expf(l - (m == -INFINITY ? 0.f : m));
-      w[s][threadIdx.x] = e;
+      w[s][i] = l;
+      m = fmaxf(m, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int s = lane; s < d.nparts; s += 32) {
+      const float l = w[s][i], e = l == -INFINITY ? 0.f : __expf(l - (m == -INFINITY ? 0.f : m));
+      w[s][i] = e;
       z += e;
     }
-    for (int s = 0; s < d.nparts; ++s) w[s][threadIdx.x] = z == 0.f ? 0.f : w[s][threadIdx.x] / z;
-    if (p.lse && row < d.nrows) p.lse[(int64_t)d.row0 + row] = z == 0.f ? -INFINITY : m + __logf(z);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    for (int s = lane; s < d.nparts; s += 32) w[s][i] = z == 0.f ? 0.f : w[s][i] / z;
+    if (lane == 0 && p.lse && row < d.nrows) p.lse[(int64_t)d.row0 + row] = z == 0.f ? -INFINITY : m + __logf(z);
   }
   __syncthreads();
   for (int v = threadIdx.x; v < kMergeRows * HS_D_LATENT / 4; v += kMergeThreads) {
