@@ -70,8 +70,8 @@ constexpr int kOffBar = kOffSum + 1024;
 constexpr int kNumBars = 56;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 constexpr int kSmem = kOffMisc + 128;
-constexpr int kOffScratch = kOffK;             // int64 [B + 1] during the set-up
-static_assert(kOffScratch + 8 * (kMaxReq + 1) <= kOffAlpha && kSmem <= 232448, "shared memory");
+constexpr int kOffScratch = kOffK;             // int64 [B + 1] and int32 [B + 1] during the set-up
+static_assert(kOffScratch + 12 * (kMaxReq + 1) <= kOffAlpha && kSmem <= 232448, "shared memory");
 static_assert(kOffK % 1024 == 0 && kOffStage % 1024 == 0 && kOffV % 1024 == 0, "swizzled blocks");
 
 // What differs between the variants.
@@ -211,6 +211,7 @@ struct Bars {
   uint64_t q_ready;               // issuing softmax CTA: Q is in place (both)
   uint64_t q_free;                // the block's QK MMAs have read Q (both)
   uint64_t o_free;                // issuing output CTA: O is read out (both)
+  uint64_t out_done;              // output CTA: a block's output has left the P buffer of its last tile
   uint64_t drain[2];
   uint64_t swap[4];               // softmax CTA: the two warps of a lane quarter have written their values
 };
@@ -232,6 +233,14 @@ constexpr int kRescale = 1, kLast = 2, kStop = 4;
 constexpr int kWake = 1, kWoken = 2, kGo = 3, kDone = 5;  // kGo, kDone: and the next one for the second group
 __device__ __forceinline__ void named_arrive(uint32_t id, uint32_t count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// Asks for the queries of a block's rows in this CTA into L2, some tiles before they are read.
+__device__ __forceinline__ void prefetch_q(const Params& p, const Seg& s, int half) {
+  const int have = s.nrows - half * kHalf;
+  if (have > 0)
+    bulk_prefetch_l2(p.q + ((int64_t)s.q.start * p.H + (int64_t)s.b * (kHalf * G) + half * kHalf) * (HS_D_QK * 2),
+                     (have < kHalf ? have : kHalf) * (HS_D_QK * 2));
 }
 
 // raw: one thread brings a tile's undecoded rows: the scales, in the softmax CTA the rotary block, and latent group by
@@ -271,6 +280,7 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
     if (++jn == s.tb) {
       more = walk.next(p, s);
       if (more) jn = s.ta;
+      if (more && isA) prefetch_q(p, s, half);
     }
   };
   fetch();
@@ -327,14 +337,14 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
 // raw: one warp splits every scale of a tile into two fp16 parts (see dequant8), each twice in a 32-bit word, for the
 // producers; rows past the request's length get scale 0.
 template <bool isA>
-__device__ __forceinline__ void split_scales(const Params& p, uint8_t* smem, Bars& br, Misc& mc, int64_t ntiles, int lane) {
+__device__ __forceinline__ void split_scales(const Params& p, uint8_t* smem, Bars& br, Misc& mc, int ntiles, int lane) {
   using Sh = Shape<true>;
   constexpr int kKeysHere = isA ? Sh::kMine : kKeys;
   const float4* in = reinterpret_cast<const float4*>(smem + (isA ? Sh::kOffScaleA : Sh::kOffScaleB));
   uint2* out = reinterpret_cast<uint2*>(smem + (isA ? Sh::kOffSplitA : Sh::kOffSplitB));
   bool range_ok = true;
 #pragma unroll 1
-  for (int64_t i = 0; i < ntiles; ++i) {
+  for (int i = 0; i < ntiles; ++i) {
     const int t = (int)(i & 1);
     const uint32_t ph = (uint32_t)(i >> 1) & 1u;
     const bool ok = !mc.abort && mbar_wait(&br.scale_full[t], ph, p.err) && mbar_wait(&br.split_empty[t], ph ^ 1u, p.err);
@@ -371,7 +381,7 @@ __device__ __forceinline__ void split_scales(const Params& p, uint8_t* smem, Bar
 // different banks. Bound by issue slots: about 40 instructions per 512 codes, most of them (cvt, half2 arithmetic) at half
 // rate.
 template <bool isA>
-__device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32_t* err, int64_t ntiles, int half, int pw, int lane) {
+__device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32_t* err, int ntiles, int half, int pw, int lane) {
   using Sh = Shape<true>;
   constexpr int kBlk = isA ? Sh::kKBlk : kVBlk, kStage = 2 * kBlk;
   constexpr int kSlots = isA ? Sh::kStA : Sh::kStB;
@@ -394,7 +404,7 @@ __device__ __forceinline__ void produce(uint8_t* smem, Bars& br, Misc& mc, int32
   // the group's first warp waits for what a stage needs
   auto take = [&](uint64_t* bar, uint32_t par) { go = go && __all_sync(0xffffffffu, !mc.abort && mbar_wait(bar, par, err)); };
 #pragma unroll 1
-  for (int64_t i = 0; i < ntiles && go; ++i) {
+  for (int i = 0; i < ntiles && go; ++i) {
     const int t = (int)(i & 1);
 #pragma unroll 1
     for (int k = e; k < kGroups; k += 2) {
@@ -506,6 +516,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
     mbar_init(q_ready, 8 * G);
     mbar_init(q_free, 2);
     mbar_init(o_free, 8 * G);
+    mbar_init(&br.out_done, 8);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     for (int q = 0; q < 4; ++q) mbar_init(&swap[q], 2);
@@ -522,7 +533,8 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = mc.tmem;
-  const int64_t u0 = st->u0, ntiles = st->u1 - st->u0, U = st->U;
+  const int64_t U = st->U;
+  const int ntiles = st->ntiles;
   // raw: 640 threads start with 96 registers each (61,440 in all); the softmax and output warps (256 threads) take 120, the
   // others (384) keep 80: 61,440
   const bool rows_warp = warp >= kSmWarp0 && warp < kSmWarp0 + 8;
@@ -778,7 +790,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
     const float* sums = (const float*)(smem + kOffSum);
     const int64_t C = U < p.clusters ? U : p.clusters;
     Desc desc = {0, 0, 0, 0};
-    int64_t u = u0;
+    int64_t cost = st->cost;  // of the blocks before this one
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(p, s)) {
@@ -788,9 +800,9 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       if (s.ta == 0 && s.tb < s.tiles) {
         desc.row0 = (int32_t)row0;
         desc.nrows = s.nrows;
-        desc.nparts = (int32_t)(unit_cta(u + s.tiles - 1, U, C) - c + 1);
+        desc.nparts = (int32_t)(unit_cta(cost + s.tiles + kBlockCost - 1, U, C) - c + 1);
       }
-      u += s.tb - s.ta;
+      if (s.tb == s.tiles) cost += s.tiles + kBlockCost;
       float sum = 0.f;
       int todo, i;
 #pragma unroll 1
@@ -828,38 +840,54 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       tc_fence_after();
       if (!idle) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const bool whole = s.ta == 0 && s.tb == s.tiles, mine = row < have;
-        const int64_t r = (int64_t)half * kHalf + row;
-        __nv_bfloat16* o = p.out + (row0 + r) * HS_D_LATENT + 256 * g;
-        float* po = p.part_out + ((int64_t)(2 * c + (s.ta == 0 ? 1 : 0)) * kRows + r) * HS_D_LATENT + 256 * g;
+        const bool whole = s.ta == 0 && s.tb == s.tiles;
+        // 128 bytes of each of the warp's rows at a time, through 4 KB of the last tile's P buffer (PV has read it), so that a
+        // store covers whole lines of four rows
+        uint8_t* scratch = smem + kOffP + (i & 1) * kPBuf + 4096 * (4 * g + quad);
+        const int pl = lane & 7, rl = lane >> 3;
+        auto rows_out = [&](uint8_t* to, int64_t pitch) {  // scratch to rows 32 quad + 4 j + rl of this CTA
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r4 = 4 * j + rl;
+            const uint4 v = *reinterpret_cast<const uint4*>(scratch + sw128_offset(r4, 16 * pl));
+            if (32 * quad + r4 < have) *reinterpret_cast<uint4*>(to + (32 * quad + r4) * pitch + 16 * pl) = v;
+          }
+          __syncwarp();
+        };
+        const int64_t r = (int64_t)half * kHalf;
+        uint8_t* o = reinterpret_cast<uint8_t*>(p.out + (row0 + r) * HS_D_LATENT + 256 * g);
+        uint8_t* po = reinterpret_cast<uint8_t*>(p.part_out + ((int64_t)(2 * c + (s.ta == 0 ? 1 : 0)) * kRows + r) * HS_D_LATENT + 256 * g);
 #pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
+        for (int h = 0; h < 8; ++h) {  // 32 columns
           uint32_t v[32];
           tmem_ld32(at + 32 * h, v);
           tmem_wait_ld();
-          if (mine) {
-            if (whole) {
+          if (whole) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t w[4];
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  const __nv_bfloat162 b2 =
-                      __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * z]) * inv, __uint_as_float(v[8 * k + 2 * z + 1]) * inv);
-                  w[z] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-                *reinterpret_cast<uint4*>(o + 32 * h + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int z = 0; z < 4; ++z) {
+                const __nv_bfloat162 b2 =
+                    __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * z]) * inv, __uint_as_float(v[8 * k + 2 * z + 1]) * inv);
+                w[z] = *reinterpret_cast<const uint32_t*>(&b2);
               }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<float4*>(po + 32 * h + 4 * k) =
-                    make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
-                                __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
+              *reinterpret_cast<uint4*>(scratch + sw128_offset(lane, 64 * (h & 1) + 16 * k)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            if (h & 1) rows_out(o + 64 * (h - 1), HS_D_LATENT * 2);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(scratch + sw128_offset(lane, 16 * k)) =
+                  make_float4(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv,
+                              __uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv);
+            rows_out(po + 128 * h, HS_D_LATENT * 4);
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br.out_done);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) remote_arrive_relaxed(r_ofree);
@@ -884,6 +912,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       bool ok = true;
 #pragma unroll 1
       while (ok && walk.next(p, s)) {
+        if (isA) prefetch_q(p, s, half);
 #pragma unroll 1
         for (int jt = s.ta; jt < s.tb && ok; ++jt) {
           const int32_t y = (int32_t)(s.base + (int64_t)jt * kKeys);
@@ -1053,7 +1082,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       Ring ring = {0, 0};
       bool ok = true;
 #pragma unroll 1
-      for (int64_t i = 0; i < ntiles && ok; ++i) {
+      for (int i = 0; i < ntiles && ok; ++i) {
 #pragma unroll 1
         for (int k = 0; k < (isA ? Sh::kStages : Sh::kVStages) && ok; ++k) {
           ok = !*abort_flag && mbar_wait(&full[ring.slot], ring.par, p.err);
@@ -1113,7 +1142,8 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
     // 32 rows, at a block's last tile 128 bytes of sums), then hands it to the softmax CTA.
     if (lane == 0) {
       const uint32_t back = remote_smem(p_empty, rank - G);
-      int i = 0;
+      int i = 0, n = 0;   // tiles; blocks whose output has passed through a P buffer
+      uint32_t ends = 0;  // bit j: the tile j before this one ended a block
       bool ok = true;
 #pragma unroll 1
       while (ok && walk.next(p, s)) {
@@ -1121,12 +1151,14 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
         const uint32_t quads = left <= 0 ? 0 : left >= kHalf ? 4 : (uint32_t)(left + 31) / 32;
 #pragma unroll 1
         for (int jt = s.ta; jt < s.tb; ++jt, ++i) {
-          if (i >= 2 && (*abort_flag || !mbar_wait(&pv_done[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err))) {
+          if (i >= 2 && (*abort_flag || !mbar_wait(&pv_done[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err) ||
+                         ((ends & 4u) && !mbar_wait(&br.out_done, (uint32_t)n++ & 1u, p.err)))) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&p_full[i & 1], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
           remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));
+          ends = (ends | (jt == s.tb - 1 ? 1u : 0u)) << 1;
         }
       }
       if (!ok) *abort_flag = 1;

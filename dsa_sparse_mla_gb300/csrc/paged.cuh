@@ -32,8 +32,8 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   int32_t* err;
-  float* part_out;   // [2 clusters][128][512]: slot 2c: the part that ends or passes through cluster c, 2c + 1: one that starts there
-  float* part_lse;   // [2 clusters][128]
+  float* part_out;   // [2 clusters][rows][512]: slot 2c: the part that ends or passes through cluster c, 2c + 1: one that starts there
+  float* part_lse;   // [2 clusters][rows]
   Desc* desc;        // [clusters]
   int64_t kv_tokens;
 };
@@ -73,11 +73,16 @@ __device__ __forceinline__ int block_tiles(const Params& p, const Req& q, int b)
 __host__ __device__ __forceinline__ int64_t unit_begin(int64_t c, int64_t U, int64_t C) { return c * U / C; }
 __device__ __forceinline__ int64_t unit_cta(int64_t u, int64_t U, int64_t C) { return ((u + 1) * C - 1) / U; }
 
-// Where a cluster's units begin: found by every CTA of it at its start, in shared memory.
+// A block costs its tiles and what it takes to begin and end it (its queries, its output), in tiles: about two.
+constexpr int kBlockCost = 2;
+
+// Where a cluster's work begins: found by every CTA of it at its start, in shared memory.
 struct Start {
-  int64_t u0, u1, U;  // the cluster's units, all units
+  int64_t U;          // cost of all blocks
+  int64_t cost;       // cost of the blocks before the first one here
   int64_t base;       // rows before request r in the dequantised copy
-  int32_t r, b, ta;   // request, block and tile of u0
+  int32_t ntiles;     // tiles of this cluster
+  int32_t r, b, ta;   // request, block and tile of the first
 };
 
 // Rows that a request takes in the dequantised copy: whole tiles, one at least (zeros), none without new tokens.
@@ -95,8 +100,9 @@ template <int kRows>
 struct Walk {
   Req q;
   int r, b, ta;
-  int64_t left, base;
-  __device__ __forceinline__ Walk(const Params& p, const Start& s) : r(s.r), b(s.b), ta(s.ta), left(s.u1 - s.u0), base(s.base) {
+  int32_t left;
+  int64_t base;
+  __device__ __forceinline__ Walk(const Params& p, const Start& s) : r(s.r), b(s.b), ta(s.ta), left(s.ntiles), base(s.base) {
     q = load_req<kRows>(p, r);
   }
   __device__ __forceinline__ bool next(const Params& p, Seg& s) {
@@ -113,7 +119,7 @@ struct Walk {
     s.base = base;
     s.tiles = block_tiles<kRows>(p, q, b);
     s.nrows = block_rows<kRows>(p, q, b);
-    s.tb = (int)(s.tiles < ta + left ? s.tiles : ta + left);
+    s.tb = s.tiles < ta + left ? s.tiles : ta + left;
     left -= s.tb - ta;
     ta = 0;
     ++b;
@@ -131,31 +137,38 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
   return x;
 }
 
-// All threads of the CTA; `pre` is scratch for B + 1 sums. Prefix sums over the requests' units, then the
-// request, block and tile of this cluster's first unit. A batch whose lengths pass kv_tokens has no units.
+// All threads of the CTA; `pre` is scratch for 2 (B + 1) sums. Prefix sums over the requests' costs and blocks, then the
+// request, block and tile where this cluster's share begins and how many tiles it has. A batch whose lengths pass
+// kv_tokens has none.
 template <int kRows>
 __device__ __forceinline__ void find_units(const Params& p, int64_t* pre, Start* st, int c, int threads) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t* nblk = reinterpret_cast<int32_t*>(pre + p.B + 1);  // blocks before each request
   for (int r = warp; r < p.B; r += threads / 32) {
     const Req q = load_req<kRows>(p, r);
     int64_t sum = 0;
-    for (int b = lane; b < q.nb; b += 32) sum += block_tiles<kRows>(p, q, b);
+    for (int b = lane; b < q.nb; b += 32) sum += block_tiles<kRows>(p, q, b) + kBlockCost;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) pre[r + 1] = sum;
+    if (lane == 0) {
+      pre[r + 1] = sum;
+      nblk[r + 1] = q.nb;
+    }
   }
   __syncthreads();
   if (warp == 0) {
-    int64_t run = 0, cached = 0;
-    if (lane == 0) pre[0] = 0;
+    int64_t run = 0, cached = 0, blocks = 0;
+    if (lane == 0) pre[0] = 0, nblk[0] = 0;
     for (int at = 0; at < p.B; at += 32) {
       const bool in = at + lane < p.B;
-      const int64_t x = warp_scan(in ? pre[at + lane + 1] : 0, lane);
+      const int64_t x = warp_scan(in ? pre[at + lane + 1] : 0, lane), n = warp_scan(in ? nblk[at + lane + 1] : 0, lane);
       if (in) {
         pre[at + lane + 1] = run + x;
+        nblk[at + lane + 1] = (int32_t)(blocks + n);
         cached += load_req<kRows>(p, at + lane).seq;
       }
       run += __shfl_sync(0xffffffffu, x, 31);
+      blocks += __shfl_sync(0xffffffffu, n, 31);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) cached += __shfl_xor_sync(0xffffffffu, cached, o);
@@ -165,45 +178,57 @@ __device__ __forceinline__ void find_units(const Params& p, int64_t* pre, Start*
       if (c == 0 && lane == 0) flag_error(p.err, HS_FLAG_BAD_LENGTH);
     }
     const int64_t U = run, C = U < p.clusters ? U : p.clusters;
-    int64_t u0 = 0, u1 = 0, base = 0;
-    int lo = 0, b = 0, ta = 0;
+    int64_t tiles_before[2] = {0, 0}, cost = 0, base = 0;
+    int r0 = 0, b0 = 0, ta0 = 0;
     if (c < C) {
-      u0 = unit_begin(c, U, C);
-      u1 = unit_begin(c + 1, U, C);
-      int hi = p.B;  // the request with pre[lo] <= u0 < pre[lo + 1]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= u0)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      for (int r = lane; r < lo; r += 32) base += copy_rows(load_req<kRows>(p, r));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
-      const Req q = load_req<kRows>(p, lo);
-      int64_t off = u0 - pre[lo];
-      for (int at = 0; at < q.nb; at += 32) {
-        const int t = at + lane < q.nb ? block_tiles<kRows>(p, q, at + lane) : 0;
-        const int64_t x = warp_scan(t, lane);
-        const uint32_t hit = __ballot_sync(0xffffffffu, x > off);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          b = at + l;
-          ta = (int)(off - __shfl_sync(0xffffffffu, x - t, l));
-          break;
+      for (int end = 0; end < 2; ++end) {  // the share's beginning and its end
+        const int64_t u = unit_begin(c + end, U, C);
+        int lo = 0, hi = p.B;  // the request with pre[lo] <= u < pre[lo + 1]; the last one with blocks for u = U
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (pre[mid] <= u && pre[mid] < U)
+            lo = mid;
+          else
+            hi = mid;
         }
-        off -= __shfl_sync(0xffffffffu, x, 31);
+        const Req q = load_req<kRows>(p, lo);
+        int64_t off = u - pre[lo];  // cost into the request, then into the block
+        int b = q.nb, ta = 0;
+        for (int at = 0; at < q.nb; at += 32) {
+          const int t = at + lane < q.nb ? block_tiles<kRows>(p, q, at + lane) + kBlockCost : 0;
+          const int64_t x = warp_scan(t, lane);
+          const uint32_t hit = __ballot_sync(0xffffffffu, x > off);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            b = at + l;
+            off -= __shfl_sync(0xffffffffu, x - t, l);
+            ta = off > kBlockCost ? (int)(off - kBlockCost) : 0;
+            break;
+          }
+          off -= __shfl_sync(0xffffffffu, x, 31);
+        }
+        // where the end lies past the last block, off is 0 and b the number of blocks
+        const int64_t at_block = u - off;
+        tiles_before[end] = at_block - (int64_t)kBlockCost * (nblk[lo] + b) + ta;
+        if (end == 0) {
+          r0 = lo;
+          b0 = b;
+          ta0 = ta;
+          cost = at_block;
+          for (int r = lane; r < lo; r += 32) base += copy_rows(load_req<kRows>(p, r));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+        }
       }
     }
     if (lane == 0) {
-      st->u0 = u0;
-      st->u1 = u1;
       st->U = U;
+      st->cost = cost;
       st->base = base;
-      st->r = lo;
-      st->b = b;
-      st->ta = ta;
+      st->ntiles = (int32_t)(tiles_before[1] - tiles_before[0]);
+      st->r = r0;
+      st->b = b0;
+      st->ta = ta0;
     }
   }
   if (c == 0) {  // tell of bad lengths and offsets once
