@@ -1,4 +1,4 @@
-// cluster.cuh — device helpers for thread-block clusters: addresses, stores and barrier arrivals in
+// cluster.cuh — device helpers for thread-block clusters: addresses and barrier arrivals in
 // another CTA's shared memory, waits that acquire at cluster scope (bounded like mbar_wait), and the
 // cluster-wide barrier.
 #pragma once
@@ -20,16 +20,6 @@ __device__ __forceinline__ uint32_t remote_smem(const void* p, uint32_t rank) {
   return a;
 }
 
-__device__ __forceinline__ void remote_st_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void remote_st_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void remote_st_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // Arrives on a barrier of another CTA (address from remote_smem); releases at cluster scope.
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -41,8 +31,6 @@ __device__ __forceinline__ void remote_arrive(uint32_t bar) {
 __device__ __forceinline__ void remote_arrive_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-
-__device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // Orders this thread's generic-proxy accesses of every state space with the async proxy (here: shared
 // memory of another CTA that its tensor core reads).
@@ -91,44 +79,33 @@ __device__ __forceinline__ void remote_arrive_cta(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// ---------------------------------------------------------------- tensor products ----------
-// G = 1: a CTA's own products. G = 2 (cta_group::2): the CTAs with ranks 2k and 2k + 1 work on one product of twice the
-// rows; each holds its rows of A and of the accumulator and half of B's columns, the even CTA issues. ts takes A from tensor
-// memory: 16-bit values, two to a 32-bit column, row r of a CTA in lane r. commit arrives on the barrier at this
-// offset in every CTA of the mask once this thread's products so far are complete.
-template <int G>
-struct Tc;
-#define HS_TC(G)                                                                                                          \
-  template <>                                                                                                            \
-  struct Tc<G> {                                                                                                         \
-    static __device__ __forceinline__ void alloc(uint32_t* dst, uint32_t ncols) {                                        \
-      asm volatile("tcgen05.alloc.cta_group::" #G ".sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),         \
-                   "r"(ncols)                                                                                            \
-                   : "memory");                                                                                          \
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::" #G ".sync.aligned;" ::: "memory");                       \
-    }                                                                                                                    \
-    static __device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t ncols) {                                     \
-      asm volatile("tcgen05.dealloc.cta_group::" #G ".sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");     \
-    }                                                                                                                    \
-    static __device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) { \
-      asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::" #G ".kind::f16 [%0], %1, %2, %3, p; }" \
-                   ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate));                                               \
-    }                                                                                                                    \
-    static __device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) { \
-      asm volatile(                                                                                                      \
-          "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::" #G ".kind::f16 [%0], [%1], %2, %3, p; }" ::"r"( \
-              d),                                                                                                        \
-          "r"(a), "l"(b), "r"(idesc), "r"(accumulate));                                                                  \
-    }                                                                                                                    \
-    static __device__ __forceinline__ void commit(uint64_t* bar, uint16_t mask) {                                        \
-      asm volatile("tcgen05.commit.cta_group::" #G                                                                        \
-                   ".mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),        \
-                   "h"(mask)                                                                                             \
-                   : "memory");                                                                                          \
-    }                                                                                                                    \
-  };
-HS_TC(1)
-HS_TC(2)
-#undef HS_TC
+// ---------------------------------------------------------------- two-SM tensor products ---
+// cta_group::2: the CTAs with ranks 2k and 2k + 1 work on one product of twice the rows; each holds its rows of A and of the
+// accumulator and half of B's columns, the even CTA issues. ts takes A from tensor memory: 16-bit values, two to a 32-bit
+// column, row r of a CTA in lane r. commit arrives on the barrier at this offset in every CTA of the mask once this
+// thread's products so far are complete.
+namespace tc2 {
+__device__ __forceinline__ void alloc(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
+               "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
+               "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint16_t mask) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"(mask)
+               : "memory");
+}
+}  // namespace tc2
 
 }  // namespace hs

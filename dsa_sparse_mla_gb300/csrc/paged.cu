@@ -11,27 +11,37 @@
 // one half of a cluster computes S and the softmax, the other keeps O and computes PV, each with 128 rows per SM
 // at the tensor core's full rate: per tile of 128 cached rows 2,304 cycles of QK, 2,048 of PV.
 //
-// Three variants of one kernel, G = CTAs that share a product (cluster of 2 G):
-//   G = 1, raw    blocks of 128 rows; for requests with up to 128 rows (decode).
-//   G = 2, raw    blocks of 256 rows, two-SM MMAs (cta_group::2, M = 256): each CTA brings half of every K or V tile, which
-//                 halves what it reads from L2, dequantises, and feeds its tensor core from shared memory.
-//   G = 2, TMA    the same from a dequantised copy of the rows that expand_kernel writes to the workspace first ([512 fp16]
-//                 [64 bf16], 1,152 bytes): pays once several blocks of a request read each row.
-// raw: eight producer warps read the 656-byte rows, dequantise (fp16, code * group scale rounded once) and write
-// 128-byte-swizzled blocks. Q's latent dims sit in tensor memory as the A operand (256 columns beside two S
-// buffers of 128), so that a QK MMA reads only K from shared memory.
+// Products are two-SM MMAs (cta_group::2, M = 256): blocks of 256 rows, and each CTA of a pair brings half of every K or V
+// tile, which halves what it reads from L2, dequantises, and feeds its tensor core from shared memory. A cluster is the
+// softmax pair (ranks 0, 1) and the output pair (ranks 2, 3).
+//
+// Two variants, chosen by copies() below:
+//   raw   eight (softmax CTA) or six (output CTA) producer warps dequantise the rows' codes, which TMA brings as they lie in
+//         the pool, to fp16 (code * group scale rounded once) in 128-byte-swizzled blocks.
+//   copy  expand_kernel first writes every row dequantised to the workspace ([512 fp16][64 bf16], 1,152 bytes), and TMA brings
+//         the blocks from there.
+// Q's latent dims sit in tensor memory as the A operand (256 columns beside two S buffers of 128), so that a QK MMA reads
+// only K from shared memory.
 //
 // Work. Units are (block of rows, 128 cached rows); every cluster takes an equal share of all units of the batch, found by
 // prefix sums at the start (no plan on the host, which does not know the lengths). A block whose units span
 // clusters leaves fp32 partial outputs and their log-sum-exps in the workspace; paged_merge_kernel joins them.
 //
-// Roles. Softmax CTA: warp 0 loads K by TMA (TMA variant), warps 1 and 3 of the issuing CTA issue QK, each for every other
-// tile (the tensor core queues too little to stay busy while one warp waits and commits), warp 2 of the other tells
-// that its half is there, warps 4-11 are the softmax: thread = row and 64 of the tile's columns; the two threads of a row agree
-// on the maximum through shared memory. P goes through shared memory to the CTA that keeps the same rows' O, 4 KB per
-// warp as one bulk copy. Output CTA: warp 0 loads V, warp 1 issues PV, warp 2 as above, warp 3 arms P's barrier and hands
-// P buffers back, one more warp looks at each tile's factors and wakes warps 4-11, which rescale O and write the result: thread = row and 256 of O's columns. Warps 12-19 (raw) are
-// the producers.
+// Roles. Softmax CTA: warp 1 loads K (raw: codes, scales, rotary blocks); warps 0 and 3 of the issuing CTA issue QK, each for
+// every other tile (the tensor core queues too little to stay busy while one warp waits and commits); warp 2 of the other CTA
+// tells that its half is there; warps 4-11 are the softmax: thread = row and 64 of the tile's columns, the two threads of a
+// row agree on the maximum through shared memory. P goes through shared memory to the CTA that keeps the same rows' O,
+// 4 KB per warp as one bulk copy. Output CTA: warp 1 loads V, warp 0 of the issuing CTA issues PV, warp 2 of the other as above,
+// warp 3 arms P's barriers and hands P buffers back, one more warp (2 or 0) looks at each tile's factors and wakes warps
+// 4-11, which rescale O and write the result: thread = row and 256 of O's columns. raw adds a warp that splits scales and the
+// producers (warps 12-19).
+//
+// Measured on a GB300 (events, inputs far larger than L2). copy, 2,048 tokens x 64 heads over 32,768 rows: 5.9 ms, 1,530
+// TFLOP/s, 0.80 of a bf16 matrix product's burst rate and 0.90 of its sustained rate; about 3,170 cycles per tile, of which QK's MMAs take
+// 2,304. raw, 64 requests x 4 tokens x 64 heads over 16-65 thousand rows: 1.37 ms, 967 TFLOP/s; about 4,400 cycles per
+// tile, the sum of hand-offs (codes -> producers -> K -> S -> P): no single unit is busy all the time, and
+// more or fewer producer warps, deeper code rings, whole pages as bulk copies and single or double P buffers change it by less
+// than 3 %.
 //
 // Lazy maximum: a row's reference max moves only when a logit exceeds it by more than 2^8 (P stays below 2^8, well
 // inside fp16); then its factor goes along with P and O's row is rescaled. Masked columns are selected away before the
@@ -49,7 +59,7 @@ constexpr int kHalf = 128;                     // rows of a CTA
 constexpr int kPBuf = 2 * kHalf * 128;         // P of a tile: 2 x [128 rows][64 keys]
 // Roles by warp (warp w runs on sub-partition w % 4).
 constexpr int kIssue0 = 0, kIssue1 = 3, kLoadWarp = 1, kRelayWarp = 2, kBufWarp = 3, kSmWarp0 = 4;
-constexpr int kScaleWarpB = 12;  // softmax CTA: the warp that does not relay (issuing CTA) or issue (the other)
+constexpr int kScaleWarpB = 12;  // splits scales in the output CTA; in the softmax CTA warp 2 (issuing) or 0 does
 // Producers, two groups of kProd warps: softmax CTA 12-15 and 16-19, output CTA 13-15 and 17-19. Index of warp w, or -1.
 __host__ __device__ constexpr int producer_index(int w, bool isA) { return w < 12 ? -1 : isA ? w - 12 : w % 4 == 0 ? -1 : w - 13 - (w - 12) / 4; }
 static_assert(producer_index(13, false) == 0 && producer_index(15, false) == 2 && producer_index(17, false) == 3 && producer_index(19, false) == 5, "roles");
@@ -490,12 +500,12 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
   const uint32_t rank = cluster_ctarank();
   const bool isA = rank < G, lead = rank % G == 0;
   const int half = (int)rank % G;  // which rows of a block, and which part of every K and V tile
-  const uint16_t pair_mask = G == 1 ? (uint16_t)(1u << rank) : isA ? 0x3 : 0xC;
+  const uint16_t pair_mask = isA ? 0x3 : 0xC;
   const int c = blockIdx.x / (2 * G);
 
   if (tid == 0) {
     for (int s = 0; s < kMaxSlots; ++s) {
-      mbar_init(&full[s], G == 2 && lead ? 2 : 1);
+      mbar_init(&full[s], lead ? 2 : 1);
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 6; ++s) {
@@ -529,7 +539,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
   fence_proxy_async_all();
   __syncthreads();
   cluster_sync();  // every CTA's barriers exist
-  if (warp == 0) Tc<G>::alloc(&mc.tmem, 512);
+  if (warp == 0) tc2::alloc(&mc.tmem, 512);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = mc.tmem;
@@ -896,292 +906,292 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
     if (rank == G && warp == 4 && lane == 0) p.desc[c] = desc;
   } else {
     if (kRaw) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == kLoadWarp) {
-    // ================================================================ loads =====================
-    if (kRaw && lane == 0) {
-      if (isA)
-        load_raw<true>(p, smem, br, mc, &map_k, &map_v, &map_r, walk, half);
-      else
-        load_raw<false>(p, smem, br, mc, &map_k, &map_v, &map_r, walk, half);
-    } else if (lane == 0) {
-      const CUtensorMap* map = isA ? &map_k : &map_v;
-      prefetch_tensormap(map);
-      const int slots = isA ? kStA : kStB;
-      Ring ring = {0, 1};
-      int64_t issued = 0;
-      bool ok = true;
+    if (warp == kLoadWarp) {
+      // ================================================================ loads =====================
+      if (kRaw && lane == 0) {
+        if (isA)
+          load_raw<true>(p, smem, br, mc, &map_k, &map_v, &map_r, walk, half);
+        else
+          load_raw<false>(p, smem, br, mc, &map_k, &map_v, &map_r, walk, half);
+      } else if (lane == 0) {
+        const CUtensorMap* map = isA ? &map_k : &map_v;
+        prefetch_tensormap(map);
+        const int slots = isA ? kStA : kStB;
+        Ring ring = {0, 1};
+        int64_t issued = 0;
+        bool ok = true;
 #pragma unroll 1
-      while (ok && walk.next(p, s)) {
-        if (isA) prefetch_q(p, s, half);
+        while (ok && walk.next(p, s)) {
+          if (isA) prefetch_q(p, s, half);
 #pragma unroll 1
-        for (int jt = s.ta; jt < s.tb && ok; ++jt) {
-          const int32_t y = (int32_t)(s.base + (int64_t)jt * kKeys);
+          for (int jt = s.ta; jt < s.tb && ok; ++jt) {
+            const int32_t y = (int32_t)(s.base + (int64_t)jt * kKeys);
 #pragma unroll 1
-          for (int k = 0; k < (isA ? Sh::kStages : Sh::kVStages); ++k) {
-            uint64_t* bar = &full[ring.slot];
-            if (*abort_flag || !mbar_wait(&empty[ring.slot], ring.par, p.err)) {
+            for (int k = 0; k < (isA ? Sh::kStages : Sh::kVStages); ++k) {
+              uint64_t* bar = &full[ring.slot];
+              if (*abort_flag || !mbar_wait(&empty[ring.slot], ring.par, p.err)) {
+                ok = false;
+                break;
+              }
+              if (isA) {  // dim blocks 3 k .. + 2, this CTA's keys
+                uint8_t* d = smem + kOffK + ring.slot * kKStage;
+                mbar_arrive_expect_tx(bar, kKStage);
+#pragma unroll
+                for (int b = 0; b < 3; ++b) tma_load_2d(d + b * kKBlk, map, bar, 64 * (3 * k + b), y + Sh::kMine * half);
+              } else {    // dims 128 (G k + half) .. + 127, all keys
+                uint8_t* d = smem + kOffV + ring.slot * kVStage;
+                mbar_arrive_expect_tx(bar, kVStage);
+                tma_load_2d(d, map, bar, 128 * (G * k + half), y);
+                tma_load_2d(d + kVBlk, map, bar, 128 * (G * k + half) + 64, y);
+              }
+              ++issued;
+              ring.next(slots);
+            }
+          }
+        }
+        if (!ok) *abort_flag = 1;
+        // every copy has landed before the CTA may leave: slots before the position were used in its round
+        for (int q = 0; q < slots; ++q)
+          if (q < issued) mbar_wait(&full[q], q < ring.slot ? ring.par ^ 1u : ring.par, p.err);
+      }
+    } else if (lead && (warp == kIssue0 || (warp == kIssue1 && isA))) {
+      // ================================================================ MMAs ======================
+      if (lane == 0) {
+        const int mine = warp == kIssue0 ? 0 : 1;  // QK: the parity of the tiles that this warp issues
+        const int slots = isA ? kStA : kStB;
+        int slot = 0, i = 0, n = 0;
+        uint32_t par = 0;
+        int32_t stages = 0;  // stages of the ring before this one
+        bool ok = true;
+        // The next stage is there (the other CTA's part too). A parity tells two phases apart, so a warp that did not see
+        // the slot's last use (the other warp's tile) makes sure that the other warp has.
+        auto stage = [&]() -> bool {
+          bool r = true;
+          const int32_t last = stages - slots;  // the slot's last use
+          if (isA && last >= 0 && ((last / Sh::kStages) & 1) != mine) {
+            const uint64_t t0 = globaltimer();
+            for (uint32_t it = 0; mc.seen[mine ^ 1] <= last; ++it)
+              if ((it & 63) == 63 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
+                flag_error(p.err, HS_FLAG_TIMEOUT);
+                r = false;
+                break;
+              }
+          }
+          r = r && mbar_wait(&full[slot], par, p.err);
+          if (isA) mc.seen[mine] = stages + 1;
+          tc_fence_after();
+          return r;
+        };
+        auto skip = [&](int k) {
+          stages += k;
+          for (slot += k; slot >= slots; slot -= slots) par ^= 1u;
+        };
+        auto pass = [&]() {
+          tc2::commit(&empty[slot], pair_mask);
+          skip(1);
+        };
+        if (isA) {
+          constexpr uint32_t lat = idesc_f16(kRows, kKeys, 0, 0), rop = idesc_bf16(kRows, kKeys, 0, 0);
+          const uint64_t qd = smem_desc(smem_u32(smem + kOffQ), 16, 1024, 2);
+          const uint64_t kd = smem_desc(smem_u32(smem + kOffK), 16, 1024, 2);
+#pragma unroll 1
+          for (; ok && walk.next(p, s); ++n) {
+            if (!mbar_wait_cluster(q_ready, (uint32_t)n & 1u, p.err)) {
               ok = false;
               break;
             }
-            if (isA) {  // dim blocks 3 k .. + 2, this CTA's keys
-              uint8_t* d = smem + kOffK + ring.slot * kKStage;
-              mbar_arrive_expect_tx(bar, kKStage);
+            fence_proxy_async_all();
+#pragma unroll 1
+            for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
+              if ((i & 1) != mine) {
+                skip(Sh::kStages);
+                continue;
+              }
+              const uint32_t d = tmem + kKeys * mine;
+              if (*abort_flag || !mbar_wait(&s_empty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err)) {
+                ok = false;
+                break;
+              }
 #pragma unroll
-              for (int b = 0; b < 3; ++b) tma_load_2d(d + b * kKBlk, map, bar, 64 * (3 * k + b), y + Sh::kMine * half);
-            } else {    // dims 128 (G k + half) .. + 127, all keys
-              uint8_t* d = smem + kOffV + ring.slot * kVStage;
-              mbar_arrive_expect_tx(bar, kVStage);
-              tma_load_2d(d, map, bar, 128 * (G * k + half), y);
-              tma_load_2d(d + kVBlk, map, bar, 128 * (G * k + half) + 64, y);
+              for (int k = 0; k < Sh::kStages; ++k) {
+                if (!stage()) {
+                  ok = false;
+                  break;
+                }
+                const uint64_t kb = kd + (uint64_t)((slot * kKStage) >> 4);
+#pragma unroll
+                for (int b = 0; b < Sh::kBlocks && Sh::kBlocks * k + b < 9; ++b)
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk) {
+                    const uint64_t bd = kb + (uint64_t)((b * kKBlk + kk * 32) >> 4);
+                    if (Sh::kBlocks * k + b < 8)
+                      tc2::ts(d, tmem + 256 + 32 * (Sh::kBlocks * k + b) + 8 * kk, bd, lat, (k | b | kk) != 0 ? 1u : 0u);
+                    else
+                      tc2::ss(d, qd + (uint64_t)((kk * 32) >> 4), bd, rop, 1u);
+                  }
+                pass();
+              }
+              if (kRaw && ok) {
+                const uint32_t rb = kRotaryBar + (uint32_t)mine;
+                ok = mbar_wait(&full[rb], (uint32_t)(i >> 1) & 1u, p.err);
+                tc_fence_after();
+                if (!ok) break;
+                const uint64_t rd = smem_desc(smem_u32(smem + Sh::kOffRotary + mine * kKBlk), 16, 1024, 2);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) tc2::ss(d, qd + (uint64_t)((kk * 32) >> 4), rd + (uint64_t)((kk * 32) >> 4), rop, 1u);
+                tc2::commit(&empty[rb], pair_mask);
+              }
+              if (ok) tc2::commit(&s_full[i & 1], pair_mask);
             }
-            ++issued;
+            if (ok) tc2::commit(q_free, pair_mask);
+          }
+        } else {
+          constexpr uint32_t id = idesc_f16(kRows, 128 * G, 0, 1);
+          const uint64_t pd = smem_desc(smem_u32(smem + kOffP), 16, 1024, 2);
+          const uint64_t vd = smem_desc(smem_u32(smem + kOffV), kVBlk, 1024, 2);
+#pragma unroll 1
+          for (; ok && walk.next(p, s); ++n) {
+            if (n > 0 && !mbar_wait(o_free, (uint32_t)(n - 1) & 1u, p.err)) {
+              ok = false;
+              break;
+            }
+#pragma unroll 1
+            for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
+              if (*abort_flag || !mbar_wait(&corr[i & 1], (uint32_t)(i >> 1) & 1u, p.err)) {
+                ok = false;
+                break;
+              }
+              const uint64_t pb = pd + (uint64_t)(((i & 1) * kPBuf) >> 4);
+#pragma unroll
+              for (int k = 0; k < Sh::kVStages; ++k) {
+                if (!stage()) {
+                  ok = false;
+                  break;
+                }
+                const uint64_t vb = vd + (uint64_t)((slot * kVStage) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                  tc2::ss(tmem + 128 * G * k, pb + (uint64_t)(((kk / 4) * (kPBuf / 2) + (kk % 4) * 32) >> 4),
+                              vb + (uint64_t)((kk * 2048) >> 4), id, (jt > s.ta || kk > 0) ? 1u : 0u);
+                pass();
+              }
+              if (ok) tc2::commit(&pv_done[i & 1], pair_mask);
+            }
+          }
+        }
+        if (!ok) *abort_flag = 1;
+        uint64_t* done = &drain[mine];
+        tc2::commit(done, (uint16_t)(1u << rank));
+        mbar_wait(done, 0, p.err);
+      }
+    } else if (warp == kRelayWarp && !lead) {
+      // ================================================================ the other half is there ===
+      if (lane == 0) {
+        const uint32_t to = remote_smem(full, rank - 1);
+        const int slots = isA ? kStA : kStB;
+        Ring ring = {0, 0};
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < ntiles && ok; ++i) {
+#pragma unroll 1
+          for (int k = 0; k < (isA ? Sh::kStages : Sh::kVStages) && ok; ++k) {
+            ok = !*abort_flag && mbar_wait(&full[ring.slot], ring.par, p.err);
+            if (ok) remote_arrive_cta(to + 8 * (uint32_t)ring.slot);
             ring.next(slots);
           }
+          if (kRaw && isA && ok) {
+            const uint32_t rb = kRotaryBar + (uint32_t)(i & 1);
+            ok = mbar_wait(&full[rb], (uint32_t)(i >> 1) & 1u, p.err);
+            if (ok) remote_arrive_cta(to + 8 * rb);
+          }
         }
+        if (!ok) *abort_flag = 1;
       }
-      if (!ok) *abort_flag = 1;
-      // every copy has landed before the CTA may leave: slots before the position were used in its round
-      for (int q = 0; q < slots; ++q)
-        if (q < issued) mbar_wait(&full[q], q < ring.slot ? ring.par ^ 1u : ring.par, p.err);
-    }
-  } else if (lead && (warp == kIssue0 || (warp == kIssue1 && isA))) {
-    // ================================================================ MMAs ======================
-    if (lane == 0) {
-      const int mine = warp == kIssue0 ? 0 : 1;  // QK: the parity of the tiles that this warp issues
-      const int slots = isA ? kStA : kStB;
-      int slot = 0, i = 0, n = 0;
-      uint32_t par = 0;
-      int32_t stages = 0;  // stages of the ring before this one
-      bool ok = true;
-      // The next stage is there (the other CTA's part too). A parity tells two phases apart, so a warp that did not see
-      // the slot's last use (the other warp's tile) makes sure that the other warp has.
-      auto stage = [&]() -> bool {
-        bool r = true;
-        const int32_t last = stages - slots;  // the slot's last use
-        if (isA && last >= 0 && ((last / Sh::kStages) & 1) != mine) {
-          const uint64_t t0 = globaltimer();
-          for (uint32_t it = 0; mc.seen[mine ^ 1] <= last; ++it)
-            if ((it & 63) == 63 && (*abort_flag || globaltimer() - t0 > kWaitLimitNs)) {
-              flag_error(p.err, HS_FLAG_TIMEOUT);
-              r = false;
-              break;
-            }
-        }
-        r = r && mbar_wait(&full[slot], par, p.err);
-        if (isA) mc.seen[mine] = stages + 1;
-        tc_fence_after();
-        return r;
-      };
-      auto skip = [&](int k) {
-        stages += k;
-        for (slot += k; slot >= slots; slot -= slots) par ^= 1u;
-      };
-      auto pass = [&]() {
-        Tc<G>::commit(&empty[slot], pair_mask);
-        skip(1);
-      };
-      if (isA) {
-        constexpr uint32_t lat = idesc_f16(kRows, kKeys, 0, 0), rop = idesc_bf16(kRows, kKeys, 0, 0);
-        const uint64_t qd = smem_desc(smem_u32(smem + kOffQ), 16, 1024, 2);
-        const uint64_t kd = smem_desc(smem_u32(smem + kOffK), 16, 1024, 2);
-#pragma unroll 1
-        for (; ok && walk.next(p, s); ++n) {
-          if (!mbar_wait_cluster(q_ready, (uint32_t)n & 1u, p.err)) {
-            ok = false;
-            break;
-          }
-          fence_proxy_async_all();
-#pragma unroll 1
-          for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
-            if ((i & 1) != mine) {
-              skip(Sh::kStages);
-              continue;
-            }
-            const uint32_t d = tmem + kKeys * mine;
-            if (*abort_flag || !mbar_wait(&s_empty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err)) {
-              ok = false;
-              break;
-            }
-#pragma unroll
-            for (int k = 0; k < Sh::kStages; ++k) {
-              if (!stage()) {
-                ok = false;
-                break;
-              }
-              const uint64_t kb = kd + (uint64_t)((slot * kKStage) >> 4);
-#pragma unroll
-              for (int b = 0; b < Sh::kBlocks && Sh::kBlocks * k + b < 9; ++b)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const uint64_t bd = kb + (uint64_t)((b * kKBlk + kk * 32) >> 4);
-                  if (Sh::kBlocks * k + b < 8)
-                    Tc<G>::ts(d, tmem + 256 + 32 * (Sh::kBlocks * k + b) + 8 * kk, bd, lat, (k | b | kk) != 0 ? 1u : 0u);
-                  else
-                    Tc<G>::ss(d, qd + (uint64_t)((kk * 32) >> 4), bd, rop, 1u);
-                }
-              pass();
-            }
-            if (kRaw && ok) {
-              const uint32_t rb = kRotaryBar + (uint32_t)mine;
-              ok = mbar_wait(&full[rb], (uint32_t)(i >> 1) & 1u, p.err);
-              tc_fence_after();
-              if (!ok) break;
-              const uint64_t rd = smem_desc(smem_u32(smem + Sh::kOffRotary + mine * kKBlk), 16, 1024, 2);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) Tc<G>::ss(d, qd + (uint64_t)((kk * 32) >> 4), rd + (uint64_t)((kk * 32) >> 4), rop, 1u);
-              Tc<G>::commit(&empty[rb], pair_mask);
-            }
-            if (ok) Tc<G>::commit(&s_full[i & 1], pair_mask);
-          }
-          if (ok) Tc<G>::commit(q_free, pair_mask);
-        }
-      } else {
-        constexpr uint32_t id = idesc_f16(kRows, 128 * G, 0, 1);
-        const uint64_t pd = smem_desc(smem_u32(smem + kOffP), 16, 1024, 2);
-        const uint64_t vd = smem_desc(smem_u32(smem + kOffV), kVBlk, 1024, 2);
-#pragma unroll 1
-        for (; ok && walk.next(p, s); ++n) {
-          if (n > 0 && !mbar_wait(o_free, (uint32_t)(n - 1) & 1u, p.err)) {
-            ok = false;
-            break;
-          }
-#pragma unroll 1
-          for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
-            if (*abort_flag || !mbar_wait(&corr[i & 1], (uint32_t)(i >> 1) & 1u, p.err)) {
-              ok = false;
-              break;
-            }
-            const uint64_t pb = pd + (uint64_t)(((i & 1) * kPBuf) >> 4);
-#pragma unroll
-            for (int k = 0; k < Sh::kVStages; ++k) {
-              if (!stage()) {
-                ok = false;
-                break;
-              }
-              const uint64_t vb = vd + (uint64_t)((slot * kVStage) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                Tc<G>::ss(tmem + 128 * G * k, pb + (uint64_t)(((kk / 4) * (kPBuf / 2) + (kk % 4) * 32) >> 4),
-                            vb + (uint64_t)((kk * 2048) >> 4), id, (jt > s.ta || kk > 0) ? 1u : 0u);
-              pass();
-            }
-            if (ok) Tc<G>::commit(&pv_done[i & 1], pair_mask);
-          }
-        }
-      }
-      if (!ok) *abort_flag = 1;
-      uint64_t* done = &drain[mine];
-      Tc<G>::commit(done, (uint16_t)(1u << rank));
-      mbar_wait(done, 0, p.err);
-    }
-  } else if (warp == kRelayWarp && !lead) {
-    // ================================================================ the other half is there ===
-    if (lane == 0) {
-      const uint32_t to = remote_smem(full, rank - 1);
-      const int slots = isA ? kStA : kStB;
-      Ring ring = {0, 0};
-      bool ok = true;
-#pragma unroll 1
-      for (int i = 0; i < ntiles && ok; ++i) {
-#pragma unroll 1
-        for (int k = 0; k < (isA ? Sh::kStages : Sh::kVStages) && ok; ++k) {
-          ok = !*abort_flag && mbar_wait(&full[ring.slot], ring.par, p.err);
-          if (ok) remote_arrive_cta(to + 8 * (uint32_t)ring.slot);
-          ring.next(slots);
-        }
-        if (kRaw && isA && ok) {
-          const uint32_t rb = kRotaryBar + (uint32_t)(i & 1);
-          ok = mbar_wait(&full[rb], (uint32_t)(i >> 1) & 1u, p.err);
-          if (ok) remote_arrive_cta(to + 8 * rb);
-        }
-      }
-      if (!ok) *abort_flag = 1;
-    }
-  } else if (!isA && warp == (lead ? kRelayWarp : kIssue0)) {
-    // ================================================================ output control ============
-    // Waits for every tile's P; wakes the output warps where some row's maximum moved (once PV of the tile before has
-    // completed) or the block ends, and lets PV go on.
-    const uint32_t r_corr = remote_smem(corr, G);
-    const float4* alpha = (const float4*)(smem + kOffAlpha);
-    int i = 0;
-    bool ok = true;
-#pragma unroll 1
-    while (ok && walk.next(p, s)) {
-      const int have = s.nrows - half * kHalf;
-#pragma unroll 1
-      for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
-        const int b = i & 1;
-        ok = !*abort_flag && warp_wait_all(&p_full[b], (uint32_t)(i >> 1) & 1u, p.err);
-        int todo = ok ? 0 : kStop;
-        if (ok && jt > s.ta) {
-          const float4 al = alpha[32 * b + lane];  // rows 4 lane .. + 3
-          if (__any_sync(0xffffffffu, 32 * (lane >> 3) < have && (al.x != 1.f || al.y != 1.f || al.z != 1.f || al.w != 1.f))) {
-            ok = warp_wait_all(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
-            todo = ok ? kRescale : kStop;
-            tc_fence_after();
-            tc_fence_before();
-          }
-        }
-        if (jt == s.tb - 1 && ok) todo |= kLast;
-        if (todo) {
-          if (lane == 0) {
-            mc.todo = todo;
-            mc.tile = i;
-          }
-          __syncwarp();
-          named_bar(kWake, 288);
-          named_bar(kWoken, 288);
-        }
-        if (ok && lane == 0) remote_arrive_relaxed(r_corr + 8 * (uint32_t)b);
-      }
-    }
-    if (!ok) *abort_flag = 1;
-  } else if (warp == kBufWarp && !isA) {
-    // ================================================================ P buffers =================
-    // Arms a buffer's barrier with the bytes that its tile brings (4 KB of P and 128 bytes of factors per
-    // 32 rows, at a block's last tile 128 bytes of sums), then hands it to the softmax CTA.
-    if (lane == 0) {
-      const uint32_t back = remote_smem(p_empty, rank - G);
-      int i = 0, n = 0;   // tiles; blocks whose output has passed through a P buffer
-      uint32_t ends = 0;  // bit j: the tile j before this one ended a block
+    } else if (!isA && warp == (lead ? kRelayWarp : kIssue0)) {
+      // ================================================================ output control ============
+      // Waits for every tile's P; wakes the output warps where some row's maximum moved (once PV of the tile before has
+      // completed) or the block ends, and lets PV go on.
+      const uint32_t r_corr = remote_smem(corr, G);
+      const float4* alpha = (const float4*)(smem + kOffAlpha);
+      int i = 0;
       bool ok = true;
 #pragma unroll 1
       while (ok && walk.next(p, s)) {
-        const int left = s.nrows - half * kHalf;
-        const uint32_t quads = left <= 0 ? 0 : left >= kHalf ? 4 : (uint32_t)(left + 31) / 32;
+        const int have = s.nrows - half * kHalf;
 #pragma unroll 1
-        for (int jt = s.ta; jt < s.tb; ++jt, ++i) {
-          if (i >= 2 && (*abort_flag || !mbar_wait(&pv_done[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err) ||
-                         ((ends & 4u) && !mbar_wait(&br.out_done, (uint32_t)n++ & 1u, p.err)))) {
-            ok = false;
-            break;
+        for (int jt = s.ta; jt < s.tb && ok; ++jt, ++i) {
+          const int b = i & 1;
+          ok = !*abort_flag && warp_wait_all(&p_full[b], (uint32_t)(i >> 1) & 1u, p.err);
+          int todo = ok ? 0 : kStop;
+          if (ok && jt > s.ta) {
+            const float4 al = alpha[32 * b + lane];  // rows 4 lane .. + 3
+            if (__any_sync(0xffffffffu, 32 * (lane >> 3) < have && (al.x != 1.f || al.y != 1.f || al.z != 1.f || al.w != 1.f))) {
+              ok = warp_wait_all(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
+              todo = ok ? kRescale : kStop;
+              tc_fence_after();
+              tc_fence_before();
+            }
           }
-          mbar_arrive_expect_tx(&p_full[i & 1], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
-          remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));
-          ends = (ends | (jt == s.tb - 1 ? 1u : 0u)) << 1;
+          if (jt == s.tb - 1 && ok) todo |= kLast;
+          if (todo) {
+            if (lane == 0) {
+              mc.todo = todo;
+              mc.tile = i;
+            }
+            __syncwarp();
+            named_bar(kWake, 288);
+            named_bar(kWoken, 288);
+          }
+          if (ok && lane == 0) remote_arrive_relaxed(r_corr + 8 * (uint32_t)b);
         }
       }
       if (!ok) *abort_flag = 1;
+    } else if (warp == kBufWarp && !isA) {
+      // ================================================================ P buffers =================
+      // Arms a buffer's barrier with the bytes that its tile brings (4 KB of P and 128 bytes of factors per
+      // 32 rows, at a block's last tile 128 bytes of sums), then hands it to the softmax CTA.
+      if (lane == 0) {
+        const uint32_t back = remote_smem(p_empty, rank - G);
+        int i = 0, n = 0;   // tiles; blocks whose output has passed through a P buffer
+        uint32_t ends = 0;  // bit j: the tile j before this one ended a block
+        bool ok = true;
+#pragma unroll 1
+        while (ok && walk.next(p, s)) {
+          const int left = s.nrows - half * kHalf;
+          const uint32_t quads = left <= 0 ? 0 : left >= kHalf ? 4 : (uint32_t)(left + 31) / 32;
+#pragma unroll 1
+          for (int jt = s.ta; jt < s.tb; ++jt, ++i) {
+            if (i >= 2 && (*abort_flag || !mbar_wait(&pv_done[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err) ||
+                           ((ends & 4u) && !mbar_wait(&br.out_done, (uint32_t)n++ & 1u, p.err)))) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&p_full[i & 1], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
+            remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));
+            ends = (ends | (jt == s.tb - 1 ? 1u : 0u)) << 1;
+          }
+        }
+        if (!ok) *abort_flag = 1;
+      }
+    } else if (kRaw && warp == (!isA ? kScaleWarpB : lead ? kRelayWarp : kIssue0)) {
+      // ================================================================ scales ====================
+      if (isA)
+        split_scales<true>(p, smem, br, mc, ntiles, lane);
+      else
+        split_scales<false>(p, smem, br, mc, ntiles, lane);
+    } else if (kRaw && producer_index(warp, isA) >= 0) {
+      // ================================================================ producers =================
+      if (isA)
+        produce<true>(smem, br, mc, p.err, ntiles, half, producer_index(warp, isA), lane);
+      else
+        produce<false>(smem, br, mc, p.err, ntiles, half, producer_index(warp, isA), lane);
     }
-  } else if (kRaw && warp == (!isA ? kScaleWarpB : lead ? kRelayWarp : kIssue0)) {
-    // ================================================================ scales ====================
-    if (isA)
-      split_scales<true>(p, smem, br, mc, ntiles, lane);
-    else
-      split_scales<false>(p, smem, br, mc, ntiles, lane);
-  } else if (kRaw && producer_index(warp, isA) >= 0) {
-    // ================================================================ producers =================
-    if (isA)
-      produce<true>(smem, br, mc, p.err, ntiles, half, producer_index(warp, isA), lane);
-    else
-      produce<false>(smem, br, mc, p.err, ntiles, half, producer_index(warp, isA), lane);
-  }
   }
   __syncthreads();
   cluster_sync();  // no CTA leaves while another may still write to it
   if (warp == 0) {
     tc_fence_after();
-    Tc<G>::dealloc(tmem, 512);
+    tc2::dealloc(tmem, 512);
   }
 }
 
@@ -1192,10 +1202,14 @@ namespace paged {
 static int64_t copy_capacity(int B, int64_t kv_tokens) { return kv_tokens + (int64_t)B * kKeys; }
 static uint64_t part_bytes(int sms) {
   const uint64_t c = (uint64_t)(sms / (2 * G));
-  return 2 * c * (kHalf * G) * (HS_D_LATENT + 1) * 4 + c * sizeof(Desc);
+  return (2 * c * (kHalf * G) * (HS_D_LATENT + 1) * 4 + c * sizeof(Desc) + 15) / 16 * 16;
 }
 
-// Whether T tokens of B requests with H heads have rows enough for a dequantised copy to pay.
+// Whether T tokens of B requests with H heads have rows enough for a dequantised copy to pay: when a request's rows make more
+// than one block on average, so that its cached rows are read more than once. Measured (raw / copy, us, 30,000 cached rows per
+// request): 64 requests x 256 rows 1,114 / 1,347; x 320 2,160 / 1,981; x 512 2,184 / 2,072; 32 x 1,024 2,184 / 1,794; 16 x 2,048
+// 2,181 / 1,663. With short caches the copy's extra launch and pass show longer: 8 x 512 rows over 2,000 53 / 64; 8 x 4,096
+// 199 / 177.
 static bool copies(int T, int B, int H) { return (int64_t)T * H > 256ll * B; }
 
 template <bool kRaw>
@@ -1258,8 +1272,7 @@ static cudaError_t launch(const Params& p0, const uint16_t* rows, uint64_t n, in
 
 uint64_t paged_mla_workspace_bytes(int T, int B, int H, int64_t kv_tokens, int sms) {
   using namespace paged;
-  const uint64_t base = (part_bytes(sms) + 15) / 16 * 16;
-  return copies(T, B, H) ? base + (uint64_t)copy_capacity(B, kv_tokens) * HS_D_QK * 2 : base;
+  return part_bytes(sms) + (copies(T, B, H) ? (uint64_t)copy_capacity(B, kv_tokens) * HS_D_QK * 2 : 0);
 }
 
 cudaError_t launch_paged_mla(const hs_paged_mla_args* a, int sms, cudaStream_t stream, const char** why) {
@@ -1286,8 +1299,7 @@ cudaError_t launch_paged_mla(const hs_paged_mla_args* a, int sms, cudaStream_t s
   p.part_out = reinterpret_cast<float*>(a->workspace);
   p.part_lse = p.part_out + (int64_t)2 * most * (kHalf * G) * HS_D_LATENT;
   p.desc = reinterpret_cast<Desc*>(p.part_lse + (int64_t)2 * most * (kHalf * G));
-  const uint16_t* rows = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(a->workspace) +
-                                                           paged_mla_workspace_bytes(0, a->B, a->H, a->kv_tokens, sms));
+  const uint16_t* rows = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(a->workspace) + part_bytes(sms));
   const uint64_t n = (uint64_t)copy_capacity(a->B, a->kv_tokens);
   return copies(a->T, a->B, a->H) ? launch<false>(p, rows, n, sms, stream, why) : launch<true>(p, rows, n, sms, stream, why);
 }

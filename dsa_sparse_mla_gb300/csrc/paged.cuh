@@ -1,4 +1,4 @@
-// paged.cuh — what the two kernels of the paged attention share: the batch's work as units (block of
+// paged.cuh — what the kernels of the paged attention share: the batch's work as units (block of
 // (token, head) rows, 128 cached rows), the dequantisation of a row, and the join of split blocks.
 #pragma once
 
