@@ -8,7 +8,8 @@ indexer and top-k for each request's final query token only and lets the request
 tokens reuse that set in hs_sparse_mla_fwd (shared index sets); ``LongPrefillPass`` runs every
 chunk of a long prefill through the same three calls. ``DeviceHiSparse`` does the
 same for the mixed-residency decode (hs_hisparse_resolve -> hs_sparse_mla_fwd on physical rows),
-with the older rows in pinned host memory.
+with the older rows in pinned host memory. ``DenseSession`` runs requests that attend densely and may branch
+(hs_rope -> hs_kv_append -> hs_paged_mla_fwd; hs_kv_fork, hs_kv_free and hs_kv_compact between steps).
 
 Only buffer management lives here; all arithmetic runs in libhs.so.
 """
@@ -19,8 +20,9 @@ import dataclasses
 import numpy as np
 import torch
 
-from . import (hs_hisparse_resolve, hs_hisparse_touch_host, hs_indexer_scores, hs_indexer_topk, hs_sparse_mla_fwd,
-               hs_sparse_mla_workspace_size, hs_topk)
+from . import (hs_hisparse_resolve, hs_hisparse_touch_host, hs_indexer_scores, hs_indexer_topk, hs_kv_append, hs_kv_compact,
+               hs_kv_compact_workspace_size, hs_kv_fork, hs_kv_free, hs_paged_mla_fwd, hs_paged_mla_workspace_size, hs_rope,
+               hs_rope_inv_freq, hs_sparse_mla_fwd, hs_sparse_mla_workspace_size, hs_topk)
 from .inputs import HiSparseWorkload, Workload
 
 
@@ -265,3 +267,70 @@ class DeviceHiSparse:
     def step(self, step: int, stream=None):
         self.resolve(step, stream)
         self.mla(step, stream)
+
+
+class DenseSession:
+    """Requests that attend densely over the paged latent cache and may branch (several samples of one prompt, beams):
+    device state for ``B`` request slots and ``L`` layers, and the calls of a step in their order. ``extend`` gives the new
+    tokens their positions and pages, then ``attend`` runs once per layer (hs_rope of queries and keys -> hs_kv_append ->
+    hs_paged_mla_fwd). Between steps ``fork`` makes slots copies of others (pages shared, the partial one copied), ``free``
+    empties slots, and ``compact`` moves the pages in use to the front. Everything runs on the current stream."""
+
+    def __init__(self, B: int, H: int, nblk: int, pages: int, L: int = 1, max_tokens: int = 4096, base: float = 10000.0,
+                 kind: str = "plain", factor: float = 1.0, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.B, self.H, self.nblk, self.L, self.device = B, H, nblk, L, device
+        self.pool = torch.zeros((L, nblk * 64, 656), dtype=torch.uint8, device=device)
+        self.pools = torch.tensor([p.data_ptr() for p in self.pool], dtype=torch.int64, device=device)
+        self.table = torch.full((B, pages), -1, **i32)
+        self.seq_len = torch.zeros(B, **i32)
+        self.refcount = torch.zeros(nblk, **i32)
+        self.src, self.dst = torch.empty(nblk, **i32), torch.empty(nblk, **i32)
+        self.counts, self.err = torch.zeros(2, **i32), torch.zeros(1, **i32)
+        inv, self.rope_scale = hs_rope_inv_freq(64, base, kind, factor)
+        self.inv_freq = inv.to(device)
+        self.softmax_scale = 1.0 / 24.0
+        self.kv_tokens = min(B * pages, 2 ** 25 - 1) * 64  # shared pages count once per request
+        # a batch of fewer tokens may need the room of a longer one: the dequantised rows are used from some size on
+        self.workspace = torch.empty(hs_paged_mla_workspace_size(max_tokens, B, H, self.kv_tokens), dtype=torch.uint8, device=device)
+        self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
+
+    def extend(self, new) -> int:
+        """``new[r]`` more tokens for slot r: takes free pages where they need some; returns the number of tokens. Tokens are
+        ordered by slot. A partial page is a slot's own (fork copied it), so it may be written."""
+        new = torch.as_tensor(new, dtype=torch.int32, device=self.device)
+        after = self.seq_len + new
+        page = torch.arange(self.table.shape[1], device=self.device)[None]
+        take = (page >= ((self.seq_len + 63) // 64)[:, None]) & (page < ((after + 63) // 64)[:, None])
+        free = (self.refcount <= 0).nonzero()[:, 0][:int(take.sum())].int()
+        if int(take.sum()) > free.numel() or int(after.max()) > 64 * self.table.shape[1]:
+            raise RuntimeError("the cache has too few pages")
+        self.table[take] = free
+        self.refcount[free.long()] = 1
+        self.token_req = torch.repeat_interleave(torch.arange(self.B, dtype=torch.int32, device=self.device), new)
+        self.req_start = torch.cat([new.new_zeros(1), new.cumsum(0).int()])
+        T = self.token_req.numel()
+        self.positions = (torch.arange(T, dtype=torch.int32, device=self.device)
+                          + torch.repeat_interleave(self.seq_len - self.req_start[:-1], new))
+        self.seq_len = after
+        return T
+
+    def attend(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, out: torch.Tensor, lse=None):
+        """Layer ``layer`` of the tokens of the last extend: ``q`` bf16 [T, H, 576] and ``rope`` bf16 [T, 64] are rotated in
+        place, ``latent`` bf16 [T, 512] and ``rope`` become cache rows, ``out`` bf16 [T, H, 512] receives the attention."""
+        hs_rope(q[..., 512:], self.positions, self.inv_freq, y=rope[:, None], scale=self.rope_scale)
+        hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=self.pool[layer])
+        hs_paged_mla_fwd(q, self.pool[layer], self.table, self.req_start, self.seq_len, self.kv_tokens, self.softmax_scale, out,
+                         self.err, self.workspace, lse=lse)
+
+    def fork(self, parent, child):
+        parent, child = (torch.as_tensor(x, dtype=torch.int32, device=self.device) for x in (parent, child))
+        n = parent.numel()
+        hs_kv_fork(parent, child, self.table, self.seq_len, self.refcount, self.src[:n], self.dst[:n], self.err, pools=self.pools)
+
+    def free(self, req):
+        hs_kv_free(torch.as_tensor(req, dtype=torch.int32, device=self.device), self.table, self.seq_len, self.refcount, self.err)
+
+    def compact(self):
+        hs_kv_compact(self.table, self.refcount, self.table, self.refcount, self.src, self.dst, self.counts, self.err,
+                      self.compact_workspace, pools=self.pools)

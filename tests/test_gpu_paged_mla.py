@@ -190,3 +190,102 @@ def test_far_rows_pass_32_bits():
     b["table"] = torch.where(b["table"] >= 0, b["table"] + (nblk - have), -1)
     out, _, flag = run(b)
     assert flag == 0 and torch.equal(out, want)
+
+
+# Batches by rows per request: few (at most 64), some (at most 256), many (the cached rows are dequantised first).
+SIZES = {"few": [2, 3], "some": [9, 12], "many": [60, 40]}
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("causal", [True, False])
+def test_sizes(size, causal):
+    for kv in ([700, 90], [64, 128], [129, 5000]):
+        check(plain.make_batch(SIZES[size], kv, 16, seed=20 + sum(kv)), causal)
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+def test_sizes_masked_values_never_reach_a_row(size):
+    """What only a request's last token sees: a NaN code, an infinite scale, infinite and NaN rotary values."""
+    m = SIZES[size]
+    b = plain.make_batch(m, [200, 300], 16, seed=21)
+    clean, last = run(b)[0], m[0] - 1
+    row = int(b["table"][0, 199 // 64]) * 64 + 199 % 64
+    keep = b["pool"][row].clone()
+    for at, value, flag in ((slice(17, 18), torch.tensor([0x7F], dtype=torch.uint8), 0),
+                            (slice(512, 516), torch.tensor([math.inf]).view(torch.uint8), hs.FLAGS["RANGE"]),
+                            (slice(528, 530), torch.tensor([math.inf], dtype=torch.bfloat16).view(torch.uint8), 0),
+                            (slice(528, 530), torch.tensor([math.nan], dtype=torch.bfloat16).view(torch.uint8), 0)):
+        b["pool"][row] = keep
+        b["pool"][row, at] = value.cuda()
+        out, _, got = run(b)
+        others = torch.arange(sum(m), device="cuda") != last
+        assert got == flag and torch.equal(out[others], clean[others])
+        if at.start == 17 or bool(torch.isnan(b["pool"][row, 528:530].view(torch.bfloat16)).any()):
+            assert bool(out[last].isnan().all())
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+def test_sizes_bad_pages_and_lengths(size):
+    m = SIZES[size]
+    b = plain.make_batch(m, [200, 300], 16, seed=22)
+    clean, table = run(b)[0], b["table"].clone()
+    for bad in (-1, b["pool"].shape[0] // 64, 2 ** 31 - 1):
+        b["table"][0, 1] = bad
+        out, lse, flag = run(b)
+        assert flag == hs.FLAGS["BAD_BLOCK"] and torch.equal(out[m[0]:], clean[m[0]:])
+        assert bool(out.isfinite().all()) and bool(lse.isfinite().all())
+    b["table"] = table
+    b["seq_len"][0] = -1
+    out, lse, flag = run(b)
+    assert flag & hs.FLAGS["BAD_LENGTH"] and not out[:m[0]].any() and bool((lse[:m[0]] == -math.inf).all())
+    assert torch.equal(out[m[0]:], clean[m[0]:])
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+def test_sizes_more_cached_rows_than_told(size):
+    """kv_tokens bounds the sum of the lengths (the workspace is sized by it): a batch beyond it is flagged, nothing is computed."""
+    b = plain.make_batch(SIZES[size], [200, 300], 16, seed=23)
+    b["kv_tokens"] = 499
+    out, lse, flag = run(b)
+    assert flag == hs.FLAGS["BAD_LENGTH"] and bool((out == 7.0).all()) and bool((lse == 7.0).all())
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+def test_sizes_workspace_too_small(size):
+    b = plain.make_batch(SIZES[size], [200, 300], 16, seed=24)
+    T, H, _ = b["q"].shape
+    out, err = torch.empty((T, H, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(hs.hs_paged_mla_workspace_size(T, 2, H, b["kv_tokens"]) - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(hs.HSError, match="workspace"):
+        hs.hs_paged_mla_fwd(b["q"], b["pool"], b["table"], b["req_start"], b["seq_len"], b["kv_tokens"], b["scale"], out, err, ws)
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("scale", [0.0, -1.0 / 24.0])
+def test_sizes_scales_and_queries(size, scale):
+    b = plain.make_batch(SIZES[size], [300, 65], 16, seed=25, sigma_q=0.5)
+    b["scale"] = scale
+    check(b)
+    b = plain.make_batch(SIZES[size], [300, 65], 16, seed=26, sigma_q=3e4)
+    b["scale"] = 1.0 / 24.0 / 3e4
+    b["q"][1, 3] *= 2.0 ** -20
+    check(b)
+    clean = run(b)[0]
+    b["q"][1, 5, 100] = math.inf
+    out, _, flag = run(b)
+    assert flag == hs.FLAGS["RANGE"]
+    out[1, 5] = clean[1, 5]
+    assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+def test_sizes_same_bits_each_time(size):
+    """One request over many tiles: every share of the work is a part, and the parts are joined in their order."""
+    m = SIZES[size]
+    b = plain.make_batch([m[0], 0, m[1]], [20_000, 0, 5000], 16, seed=27)
+    want, lse, _ = run(b)
+    for _ in range(3):
+        out, l, flag = run(b)
+        assert flag == 0 and torch.equal(out, want) and torch.equal(l, lse)
+    assert torch.equal(run(b, lse=False)[0], want)
+    check(b)
