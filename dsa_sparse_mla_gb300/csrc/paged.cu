@@ -1201,8 +1201,8 @@ namespace paged {
 // Rows of the dequantised copy: every request's last tile is whole.
 static int64_t copy_capacity(int B, int64_t kv_tokens) { return kv_tokens + (int64_t)B * kKeys; }
 static uint64_t part_bytes(int sms) {
-  const uint64_t c = (uint64_t)(sms / (2 * G));
-  return (2 * c * (kHalf * G) * (HS_D_LATENT + 1) * 4 + c * sizeof(Desc) + 15) / 16 * 16;
+  const uint64_t c = (uint64_t)(sms / (2 * G)), n = 2 * c * (kHalf * G) * (HS_D_LATENT + 1) * 4 + c * sizeof(Desc), f = few_bytes(sms);
+  return ((n > f ? n : f) + 15) / 16 * 16;
 }
 
 // Whether T tokens of B requests with H heads have rows enough for a dequantised copy to pay: when a request's rows make more
@@ -1211,6 +1211,8 @@ static uint64_t part_bytes(int sms) {
 // 2,181 / 1,663. With short caches the copy's extra launch and pass show longer: 8 x 512 rows over 2,000 53 / 64; 8 x 4,096
 // 199 / 177.
 static bool copies(int T, int B, int H) { return (int64_t)T * H > 256ll * B; }
+// Whether they have few enough for paged_few.cu.
+static bool few_rows(int T, int B, int H) { return (int64_t)T * H <= 64ll * B; }
 
 template <bool kRaw>
 static cudaError_t launch(const Params& p0, const uint16_t* rows, uint64_t n, int sms, cudaStream_t stream, const char** why) {
@@ -1297,6 +1299,7 @@ cudaError_t launch_paged_mla(const hs_paged_mla_args* a, int sms, cudaStream_t s
   p.lse = a->lse;
   p.err = a->err_flag;
   p.part_out = reinterpret_cast<float*>(a->workspace);
+  if (few_rows(a->T, a->B, a->H)) return launch_few(p, sms, stream);
   p.part_lse = p.part_out + (int64_t)2 * most * (kHalf * G) * HS_D_LATENT;
   p.desc = reinterpret_cast<Desc*>(p.part_lse + (int64_t)2 * most * (kHalf * G));
   const uint16_t* rows = reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(a->workspace) + part_bytes(sms));

@@ -267,9 +267,13 @@ __device__ __forceinline__ bool unsound(const uint4& a, const uint4& b) {
   return __hisnan(__low2half(acc)) || __hisnan(__high2half(acc));
 }
 
+// paged_few.cu: its workspace for partial results (p.part_out is its start), and the launch.
+uint64_t few_bytes(int sms);
+cudaError_t launch_few(const Params& p, int sms, cudaStream_t stream);
+
 // Joins the parts of the block that starts in cluster blockIdx.x and goes on in the next ones: each part is
 // normalised by its own sum, so out = sum_s e^(lse_s - lse) O_s. Eight rows per CTA.
-constexpr int kMergeThreads = 256, kMergeRows = 8, kMaxClusters = 128;
+constexpr int kMergeThreads = 256, kMergeRows = 8, kMaxClusters = 160;
 static_assert(kMergeThreads == 32 * kMergeRows, "a warp per row");
 template <int kRows>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Params p) {
