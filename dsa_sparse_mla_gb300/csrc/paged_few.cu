@@ -24,8 +24,9 @@ namespace paged {
 namespace few {
 
 constexpr int kRows = 64, kPageKeys = HS_PAGE;
-constexpr int kThreads = 512;
-constexpr int kPvWarp = 4, kSmWarp0 = 8, kProducers = 8;
+constexpr int kThreads = 768;
+constexpr int kPvWarp = 4, kSmWarp0 = 8, kProducers = 16;
+constexpr int kQuads = kPageKeys / (4 * kProducers);  // fours of rows per producer
 constexpr int kBlk = kPageKeys * 128;          // [64][64 dims] of 16 bits
 constexpr int kTile = 9 * kBlk;
 constexpr int kOffQ = 0, kOffTile = kTile;
@@ -53,7 +54,7 @@ constexpr int kColS = 256;                     // S buffers; O^T is columns 0 ..
 
 // Index of warp w among the producers, or -1.
 __host__ __device__ constexpr int producer_index(int w) {
-  return w >= 1 && w <= 3 ? w - 1 : w >= 5 && w <= 7 ? w - 2 : w == 13 || w == 14 ? w - 7 : -1;
+  return w == 12 ? 15 : w % 4 == 0 || (w >= 8 && w < 12) ? -1 : (w < 8 ? w / 4 : w / 4 - 1) * 3 + w % 4 - 1;
 }
 
 // Pages [first, end) of a segment: the last tile of a block may need only its first page.
@@ -93,7 +94,7 @@ struct Pages {
 // A producer lane's part of a page: of two rows (8 w + l / 8, and 4 further) 16 codes of every group, the four scales
 // and 16 bytes of the rotary values.
 struct Raw {
-  uint4 code[4][2], rope[2], scale[2];
+  uint4 code[4][kQuads], rope[kQuads], scale[kQuads];
 };
 
 // Whether one of 16 codes is NaN (0x7F, 0xFF).
@@ -138,157 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
   const Start& st = mc.start;
   const int pw = producer_index(warp);
 
-  if (pw >= 0) {
-    // ================================================================ producers =================
-    const int rl = lane >> 3, c8 = lane & 7;
-    const uint32_t odd = (uint32_t)((c8 >> 2) ^ (rl & 1));  // which half of its codes a lane stores first: spreads the banks
-    Pages pages(p, st);
-    Raw raw;
-    auto rows_of = [&](const Page& g) -> const uint8_t* {
-      const bool good = g.blk >= 0 && ((int64_t)g.blk + 1) * HS_PAGE <= p.R;
-      if (g.live && !good && g.left > 0 && lane == 0) flag_error(p.err, HS_FLAG_BAD_BLOCK);
-      return good ? p.kv + ((int64_t)g.blk * HS_PAGE + 8 * pw + rl) * HS_KV_ROW_BYTES : nullptr;
-    };
-    auto load = [&](const uint8_t* from, int off) { return from ? ldg_nc_v4(from + off) : make_uint4(0, 0, 0, 0); };
-    auto load_group = [&](const uint8_t* from, int g) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) raw.code[g][h] = load(from, h * 4 * HS_KV_ROW_BYTES + 128 * g + 16 * c8);
-    };
-    auto load_rest = [&](const uint8_t* from) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        raw.scale[h] = load(from, h * 4 * HS_KV_ROW_BYTES + HS_D_LATENT);
-        raw.rope[h] = load(from, h * 4 * HS_KV_ROW_BYTES + HS_D_LATENT + 16 + 16 * c8);
-      }
-    };
-    Page now = pages.next(p);
-    const uint8_t* from = rows_of(now);
-    load_rest(from);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) load_group(from, g);
-    Page then = pages.next(p), after = pages.next(p);  // table entries are read two pages ahead, rows one
-    bool range_ok = true, ok = true;
-#pragma unroll 1
-    for (int i = 0; ok && now.live; ++i) {
-      const int s = i & 1;
-      uint8_t* tile = smem + kOffTile + s * kTile;
-      const uint8_t* ahead = rows_of(then);
-      bool bad[2] = {false, false};
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        ok = ok && !mc.abort && warp_wait_all(&br.free[s][g], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err);
-        if (!ok) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 8 * pw + 4 * h + rl;
-          const uint32_t* sc = &raw.scale[h].x;
-          const float f = row < now.left ? __uint_as_float(sc[g]) : 0.f;
-          const bool fits = f == 0.f || (fabsf(f) >= kScaleMin && fabsf(f) <= kScaleMax);
-          range_ok &= fits;
-          const __half hi = __float2half_rn(f);
-          const __half2 h2 = __half2half2(hi), l2 = __float2half2_rn(f - __half2float(hi));
-          const uint32_t hu = *reinterpret_cast<const uint32_t*>(&h2), lu = *reinterpret_cast<const uint32_t*>(&l2);
-          const uint4 v = raw.code[g][h];
-          uint4 d0 = dequant8(odd ? v.z : v.x, odd ? v.w : v.y, hu, lu);
-          uint4 d1 = dequant8(odd ? v.x : v.z, odd ? v.y : v.w, hu, lu);
-          if (has_nan(v) || !(fabsf(f) <= kScaleMax)) {
-            d0 = d1 = make_uint4(0, 0, 0, 0);
-            bad[h] = true;
-          }
-          uint8_t* blk = tile + (2 * g + (c8 >> 2)) * kBlk;
-          const uint32_t at = sw128_offset(row, 32 * (c8 & 3) + 16 * odd);
-          *reinterpret_cast<uint4*>(blk + at) = d0;
-          *reinterpret_cast<uint4*>(blk + (at ^ 16u)) = d1;
-          if (g == 3) {
-            uint4 r = raw.rope[h];
-            if ((__ballot_sync(0xffffffffu, bad[h]) >> (8 * rl)) & 0xFFu) r.x = 0x7FC07FC0u;  // two bf16 NaN
-            *reinterpret_cast<uint4*>(tile + 8 * kBlk + sw128_offset(row, 16 * c8)) = r;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&br.full[s][g]);
-        load_group(ahead, g);
-      }
-      load_rest(ahead);
-      now = then;
-      then = after;
-      after = pages.next(p);
-    }
-    if (!ok) mc.abort = 1;
-    if (!range_ok) flag_error(p.err, HS_FLAG_RANGE);
-  } else if (warp == 0) {
-    // ================================================================ QK ========================
-    if (lane == 0) {
-      constexpr uint32_t lat = idesc_f16(kRows, kPageKeys, 0, 0), rop = idesc_bf16(kRows, kPageKeys, 0, 0);
-      const uint64_t qd = smem_desc(smem_u32(smem + kOffQ), 16, 1024, 2);
-      Walk<kRows> walk(p, st);
-      Seg s;
-      int i = 0;
-      bool ok = true;
-#pragma unroll 1
-      for (int n = 0; ok && walk.next(p, s); ++n) {
-        ok = !mc.abort && mbar_wait(&br.q_ready, (uint32_t)n & 1u, p.err);
-        const int end = end_page(p, s);
-#pragma unroll 1
-        for (int j = first_page(s); ok && j < end; ++j, ++i) {
-          const int b = i & 1;
-          const uint32_t ph = (uint32_t)(i >> 1) & 1u;
-          ok = !mc.abort && mbar_wait(&br.s_empty[b], ph ^ 1u, p.err);
-          const uint64_t kd = smem_desc(smem_u32(smem + kOffTile + b * kTile), 16, 1024, 2);
-          const uint32_t d = tmem + kColS + 64 * b;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            ok = ok && mbar_wait(&br.full[b][g], ph, p.err);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < (g < 3 ? 8 : 12); ++k) {  // 16 dims each
-              const uint64_t at = (uint64_t)(((2 * g + k / 4) * kBlk + (k % 4) * 32) >> 4);
-              mma_bf16_ss(d, qd + at, kd + at, k < 8 ? lat : rop, (g | k) != 0 ? 1u : 0u);
-            }
-          }
-          if (ok) mma_commit(&br.s_full[b]);
-        }
-      }
-      if (!ok) mc.abort = 1;
-      mma_commit(&br.drain[0]);
-      mbar_wait(&br.drain[0], 0, p.err);
-    }
-  } else if (warp == kPvWarp) {
-    // ================================================================ PV ========================
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f16(128, kRows, 1, 0);
-      Walk<kRows> walk(p, st);
-      Seg s;
-      int i = 0;
-      bool ok = true;
-#pragma unroll 1
-      while (ok && walk.next(p, s)) {
-        const int first = first_page(s), end = end_page(p, s);
-#pragma unroll 1
-        for (int j = first; ok && j < end; ++j, ++i) {
-          const int b = i & 1;
-          ok = !mc.abort && mbar_wait(&br.p_full[b], (uint32_t)(i >> 1) & 1u, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t at = smem_u32(smem + kOffTile + b * kTile);
-          const uint64_t vd = smem_desc(at, kBlk, 1024, 2), pd = smem_desc(at + 8 * kBlk, 16, 1024, 2);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16_ss(tmem + 64 * g, vd + (uint64_t)((2 * g * kBlk + k * 2048) >> 4), pd + (uint64_t)((k * 32) >> 4), id,
-                          j > first || k > 0 ? 1u : 0u);
-            mma_commit(&br.free[b][g]);
-          }
-        }
-      }
-      if (!ok) mc.abort = 1;
-      mma_commit(&br.drain[1]);
-      mbar_wait(&br.drain[1], 0, p.err);
-    }
-  } else if (warp >= kSmWarp0 && warp < kSmWarp0 + 4) {
+  // 768 threads start with 80 registers each (61,440 in all); the softmax warps (128 threads) take 120, the others keep 72:
+  // 61,440
+  if (warp >= kSmWarp0 && warp < kSmWarp0 + 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ================================================================ softmax, output ===========
     const int quad = warp & 3, half = lane >> 4, row = 16 * quad + (lane & 15);  // half: columns 32 half .. + 31
     const uint32_t quarter = tmem + ((uint32_t)(32 * quad) << 16);
@@ -504,6 +358,159 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
     }
     if (!ok) mc.abort = 1;
     if (warp == kSmWarp0 && lane == 0) p.desc[c] = desc;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (pw >= 0) {
+      // ================================================================ producers =================
+      const int rl = lane >> 3, c8 = lane & 7;
+      const uint32_t odd = (uint32_t)((c8 >> 2) ^ (rl & 1));  // which half of its codes a lane stores first: spreads the banks
+      Pages pages(p, st);
+      Raw raw;
+      auto rows_of = [&](const Page& g) -> const uint8_t* {
+        const bool good = g.blk >= 0 && ((int64_t)g.blk + 1) * HS_PAGE <= p.R;
+        if (g.live && !good && g.left > 0 && lane == 0) flag_error(p.err, HS_FLAG_BAD_BLOCK);
+        return good ? p.kv + ((int64_t)g.blk * HS_PAGE + 4 * kQuads * pw + rl) * HS_KV_ROW_BYTES : nullptr;
+      };
+      auto load = [&](const uint8_t* from, int off) { return from ? ldg_nc_v4(from + off) : make_uint4(0, 0, 0, 0); };
+      auto load_group = [&](const uint8_t* from, int g) {
+#pragma unroll
+        for (int h = 0; h < kQuads; ++h) raw.code[g][h] = load(from, h * 4 * HS_KV_ROW_BYTES + 128 * g + 16 * c8);
+      };
+      auto load_rest = [&](const uint8_t* from) {
+#pragma unroll
+        for (int h = 0; h < kQuads; ++h) {
+          raw.scale[h] = load(from, h * 4 * HS_KV_ROW_BYTES + HS_D_LATENT);
+          raw.rope[h] = load(from, h * 4 * HS_KV_ROW_BYTES + HS_D_LATENT + 16 + 16 * c8);
+        }
+      };
+      Page now = pages.next(p);
+      const uint8_t* from = rows_of(now);
+      load_rest(from);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) load_group(from, g);
+      Page then = pages.next(p), after = pages.next(p);  // table entries are read two pages ahead, rows one
+      bool range_ok = true, ok = true;
+#pragma unroll 1
+      for (int i = 0; ok && now.live; ++i) {
+        const int s = i & 1;
+        uint8_t* tile = smem + kOffTile + s * kTile;
+        const uint8_t* ahead = rows_of(then);
+        bool bad[kQuads] = {};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          ok = ok && !mc.abort && warp_wait_all(&br.free[s][g], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err);
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < kQuads; ++h) {
+            const int row = 4 * kQuads * pw + 4 * h + rl;
+            const uint32_t* sc = &raw.scale[h].x;
+            const float f = row < now.left ? __uint_as_float(sc[g]) : 0.f;
+            const bool fits = f == 0.f || (fabsf(f) >= kScaleMin && fabsf(f) <= kScaleMax);
+            range_ok &= fits;
+            const __half hi = __float2half_rn(f);
+            const __half2 h2 = __half2half2(hi), l2 = __float2half2_rn(f - __half2float(hi));
+            const uint32_t hu = *reinterpret_cast<const uint32_t*>(&h2), lu = *reinterpret_cast<const uint32_t*>(&l2);
+            const uint4 v = raw.code[g][h];
+            uint4 d0 = dequant8(odd ? v.z : v.x, odd ? v.w : v.y, hu, lu);
+            uint4 d1 = dequant8(odd ? v.x : v.z, odd ? v.y : v.w, hu, lu);
+            if (has_nan(v) || !(fabsf(f) <= kScaleMax)) {
+              d0 = d1 = make_uint4(0, 0, 0, 0);
+              bad[h] = true;
+            }
+            uint8_t* blk = tile + (2 * g + (c8 >> 2)) * kBlk;
+            const uint32_t at = sw128_offset(row, 32 * (c8 & 3) + 16 * odd);
+            *reinterpret_cast<uint4*>(blk + at) = d0;
+            *reinterpret_cast<uint4*>(blk + (at ^ 16u)) = d1;
+            if (g == 3) {
+              uint4 r = raw.rope[h];
+              if ((__ballot_sync(0xffffffffu, bad[h]) >> (8 * rl)) & 0xFFu) r.x = 0x7FC07FC0u;  // two bf16 NaN
+              *reinterpret_cast<uint4*>(tile + 8 * kBlk + sw128_offset(row, 16 * c8)) = r;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&br.full[s][g]);
+          load_group(ahead, g);
+        }
+        load_rest(ahead);
+        now = then;
+        then = after;
+        after = pages.next(p);
+      }
+      if (!ok) mc.abort = 1;
+      if (!range_ok) flag_error(p.err, HS_FLAG_RANGE);
+    } else if (warp == 0) {
+      // ================================================================ QK ========================
+      if (lane == 0) {
+        constexpr uint32_t lat = idesc_f16(kRows, kPageKeys, 0, 0), rop = idesc_bf16(kRows, kPageKeys, 0, 0);
+        const uint64_t qd = smem_desc(smem_u32(smem + kOffQ), 16, 1024, 2);
+        Walk<kRows> walk(p, st);
+        Seg s;
+        int i = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int n = 0; ok && walk.next(p, s); ++n) {
+          ok = !mc.abort && mbar_wait(&br.q_ready, (uint32_t)n & 1u, p.err);
+          const int end = end_page(p, s);
+#pragma unroll 1
+          for (int j = first_page(s); ok && j < end; ++j, ++i) {
+            const int b = i & 1;
+            const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+            ok = !mc.abort && mbar_wait(&br.s_empty[b], ph ^ 1u, p.err);
+            const uint64_t kd = smem_desc(smem_u32(smem + kOffTile + b * kTile), 16, 1024, 2);
+            const uint32_t d = tmem + kColS + 64 * b;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              ok = ok && mbar_wait(&br.full[b][g], ph, p.err);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < (g < 3 ? 8 : 12); ++k) {  // 16 dims each
+                const uint64_t at = (uint64_t)(((2 * g + k / 4) * kBlk + (k % 4) * 32) >> 4);
+                mma_bf16_ss(d, qd + at, kd + at, k < 8 ? lat : rop, (g | k) != 0 ? 1u : 0u);
+              }
+            }
+            if (ok) mma_commit(&br.s_full[b]);
+          }
+        }
+        if (!ok) mc.abort = 1;
+        mma_commit(&br.drain[0]);
+        mbar_wait(&br.drain[0], 0, p.err);
+      }
+    } else if (warp == kPvWarp) {
+      // ================================================================ PV ========================
+      if (lane == 0) {
+        constexpr uint32_t id = idesc_f16(128, kRows, 1, 0);
+        Walk<kRows> walk(p, st);
+        Seg s;
+        int i = 0;
+        bool ok = true;
+#pragma unroll 1
+        while (ok && walk.next(p, s)) {
+          const int first = first_page(s), end = end_page(p, s);
+#pragma unroll 1
+          for (int j = first; ok && j < end; ++j, ++i) {
+            const int b = i & 1;
+            ok = !mc.abort && mbar_wait(&br.p_full[b], (uint32_t)(i >> 1) & 1u, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t at = smem_u32(smem + kOffTile + b * kTile);
+            const uint64_t vd = smem_desc(at, kBlk, 1024, 2), pd = smem_desc(at + 8 * kBlk, 16, 1024, 2);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16_ss(tmem + 64 * g, vd + (uint64_t)((2 * g * kBlk + k * 2048) >> 4), pd + (uint64_t)((k * 32) >> 4), id,
+                            j > first || k > 0 ? 1u : 0u);
+              mma_commit(&br.free[b][g]);
+            }
+          }
+        }
+        if (!ok) mc.abort = 1;
+        mma_commit(&br.drain[1]);
+        mbar_wait(&br.drain[1], 0, p.err);
+      }
+    }
   }
   __syncthreads();
   if (warp == 0) {
