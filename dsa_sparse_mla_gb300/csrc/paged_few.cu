@@ -25,32 +25,40 @@ namespace few {
 
 constexpr int kRows = 64, kPageKeys = HS_PAGE;
 constexpr int kThreads = 768;
-constexpr int kPvWarp = 4, kSmWarp0 = 8, kProducers = 16;
-constexpr int kQuads = kPageKeys / (4 * kProducers);  // fours of rows per producer
+constexpr int kPvWarp = 4, kLoadWarp = 16, kSmWarp0 = 8, kProducers = 16;
 constexpr int kBlk = kPageKeys * 128;          // [64][64 dims] of 16 bits
 constexpr int kTile = 9 * kBlk;
-constexpr int kOffQ = 0, kOffTile = kTile;
+constexpr int kOffQ = 0;                       // Q's dims 256 .. 575: five blocks
+constexpr int kOffTile = 5 * kBlk;
 constexpr int kOffScratch = kOffTile;          // int64 [B + 1] and int32 [B + 1] during the set-up
-constexpr int kOffRow = 3 * kTile;             // float [64] each: factors, 1 / sums, logit coefficients
-constexpr int kOffBar = kOffRow + 3 * 256;
+constexpr int kOffRaw = kOffTile + 2 * kTile;  // a page as it lies in the pool: four rows per producer
+constexpr int kRawRows = 4 * HS_KV_ROW_BYTES;
+constexpr int kOffRow = kOffRaw + kProducers * kRawRows;  // float [64] each: factors, 1 / sums, logit coefficients, Q's scales
+constexpr int kOffBar = kOffRow + 4 * 256;
 struct Bars {
-  uint64_t full[2][4];   // producers have written a group of a page -> QK
-  uint64_t free[2][4];   // PV has read it (group 3: and P) -> producers, softmax
+  uint64_t full[2][2];   // producers have written a half of a page's dims -> QK
+  uint64_t free[2];      // PV has read the page and P -> producers, softmax
   uint64_t s_full[2];    // S complete -> softmax
   uint64_t s_empty[2];   // S read -> QK
   uint64_t p_full[2];    // P written, O^T rescaled -> PV
   uint64_t q_ready;      // a block's Q is in place -> QK
   uint64_t drain[2];
+  uint64_t raw_full;     // a page's codes have landed -> producers
+  uint64_t raw_free;     // they have read them
 };
+constexpr int32_t kEnd = -1;
 struct Misc {
   uint32_t tmem;
   volatile uint32_t abort;
+  int32_t left;          // rows in use of the page that has landed; kEnd after the last one
   Start start;
 };
 constexpr int kOffMisc = kOffBar + (int)sizeof(Bars);
 constexpr int kSmem = kOffMisc + (int)sizeof(Misc);
 static_assert(kSmem <= 232448 && 12 * (kMaxReq + 1) <= 2 * kTile && kOffBar % 8 == 0 && kOffMisc % 8 == 0, "shared memory");
-constexpr int kColS = 256;                     // S buffers; O^T is columns 0 .. 255
+// Tensor memory columns: O^T 0 .. 255, S buffers, Q's dims 0 .. 255 as pairs. Row r of Q and S is in lane
+// 32 (r / 16) + r % 16, where a 64-row product has it; the other lanes belong to no row.
+constexpr int kColS = 256, kColQ = 384;
 
 // Index of warp w among the producers, or -1.
 __host__ __device__ constexpr int producer_index(int w) {
@@ -91,16 +99,36 @@ struct Pages {
   }
 };
 
-// A producer lane's part of a page: of two rows (8 w + l / 8, and 4 further) 16 codes of every group, the four scales
-// and 16 bytes of the rotary values.
+// A producer lane's part of a page: of row 4 w + l / 8, of every group the codes 8 (l % 8) .. + 7 and 64 further (so that the
+// eight lanes of a row store its eight 16-byte pieces of a block at once, in different banks), the four scales and 16
+// bytes of the rotary values.
 struct Raw {
-  uint4 code[4][kQuads], rope[kQuads], scale[kQuads];
+  uint2 code[4][2];
+  uint4 rope, scale;
 };
 
 // Whether one of 16 codes is NaN (0x7F, 0xFF).
-__device__ __forceinline__ bool has_nan(const uint4& v) {
+__device__ __forceinline__ bool has_nan(const uint2& a, const uint2& b) {
   const uint32_t m = 0x7F7F7F7Fu, o = 0x01010101u;
-  return ((((v.x & m) + o) | ((v.y & m) + o) | ((v.z & m) + o) | ((v.w & m) + o)) & 0x80808080u) != 0u;
+  return ((((a.x & m) + o) | ((a.y & m) + o) | ((b.x & m) + o) | ((b.y & m) + o)) & 0x80808080u) != 0u;
+}
+
+// The store that mirrors tmem_ld16x2_32.
+__device__ __forceinline__ void tmem_st16x2_32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], 32, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// A from tensor memory (two 16-bit values to a column, row = lane).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
+               "l"(b), "r"(idesc), "r"(accumulate));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
@@ -114,19 +142,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
   float* alpha = reinterpret_cast<float*>(smem + kOffRow);
   float* inverse = alpha + 64;
   float* coefs = alpha + 128;
+  float* scales = alpha + 192;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      for (int g = 0; g < 4; ++g) {
-        mbar_init(&br.full[s][g], kProducers);
-        mbar_init(&br.free[s][g], 1);
-      }
+      for (int g = 0; g < 2; ++g) mbar_init(&br.full[s][g], kProducers);
+      mbar_init(&br.free[s], 1);
       mbar_init(&br.s_full[s], 1);
       mbar_init(&br.s_empty[s], 4);
       mbar_init(&br.p_full[s], 4);
       mbar_init(&br.drain[s], 1);
     }
     mbar_init(&br.q_ready, 4);
+    mbar_init(&br.raw_full, 1);
+    mbar_init(&br.raw_free, kProducers);
     mbar_fence_init();
     mc.abort = 0;
   }
@@ -163,17 +192,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       }
       if (s.tb == s.tiles) cost += s.tiles + kBlockCost;
       const bool idle = 16 * quad >= s.nrows, mine = row < s.nrows;
-      // Q: four rows of 64 dims per load; the block before has been read (its last S is complete). Rows past the block's are
-      // read as its first row.
+      // Q: the block before has been read (its last S is complete). Rows past the block's are read as its first row.
       if (!idle) {
-        const uint8_t* q0 = p.q + row0 * (HS_D_QK * 2) + 16 * (lane & 7);
+        const uint8_t* q0 = p.q + row0 * (HS_D_QK * 2);
+        auto row_at = [&](int r) { return q0 + (int64_t)(r < s.nrows ? r : 0) * (HS_D_QK * 2); };
+        // A row whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it in
+        // [2^14, 2^15); its logits are scaled back.
 #pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           const int r = 16 * quad + 4 * h + (lane >> 3);
-          const uint8_t* src = q0 + (int64_t)(r < s.nrows ? r : 0) * (HS_D_QK * 2);
-          uint4 v[9];
+          const uint8_t* src = row_at(r) + 16 * (lane & 7);
+          uint4 v[8];
 #pragma unroll
-          for (int k = 0; k < 9; ++k) v[k] = ldg_nc_v4(src + 128 * k);
+          for (int k = 0; k < 8; ++k) v[k] = ldg_nc_v4(src + 128 * k);
           uint32_t mx = 0u;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -182,8 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           uint32_t amax = max(mx & 0xFFFFu, mx >> 16);
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // A row whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it in
-          // [2^14, 2^15); its logits are scaled back.
           int e = 0;
           if (amax >= 0x7F80u) {
             if (r < s.nrows) flag_error(p.err, HS_FLAG_RANGE);
@@ -193,26 +222,51 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
             e = 126;
           }
           e = e < -126 ? -126 : (e > 126 ? 126 : e);
-          const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-          // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
-          if ((lane & 7) == 0) coefs[r] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
-#pragma unroll
-          for (int k = 0; k < 9; ++k) {
-            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const uint32_t u = w[z] ^ p.flip;
-              const float a = __uint_as_float(u << 16) * f, b = __uint_as_float(u & 0xFFFF0000u) * f;
-              if (k < 8) {
-                w[z] = pack_half2(a, b);
-              } else {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, b);
-                w[z] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-            }
-            *reinterpret_cast<uint4*>(smem + kOffQ + k * kBlk + sw128_offset(r, 16 * (lane & 7))) = make_uint4(w[0], w[1], w[2], w[3]);
+          if ((lane & 7) == 0) {
+            scales[r] = __uint_as_float((uint32_t)(e + 127) << 23);
+            // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
+            coefs[r] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
           }
         }
+        __syncwarp();
+        auto scaled = [&](uint32_t w, float f, bool half16) -> uint32_t {
+          const uint32_t u = w ^ p.flip;
+          const float a = __uint_as_float(u << 16) * f, b = __uint_as_float(u & 0xFFFF0000u) * f;
+          if (half16) return pack_half2(a, b);
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, b);
+          return *reinterpret_cast<const uint32_t*>(&b2);
+        };
+        // dims 128 h + 64 half .. + 63 of this thread's row to tensor memory
+        const uint8_t* own = row_at(row) + 128 * half;
+        const float own_scale = scales[row];
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint4 v = ldg_nc_v4(own + 256 * h + 16 * k);
+            w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) w[k] = scaled(w[k], own_scale, true);
+          tmem_st16x2_32(quarter + kColQ + 64 * h, w);
+        }
+        // the rest to shared memory, four rows of 64 dims per load
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          const int r = 16 * quad + 4 * h + (lane >> 3);
+          const uint8_t* src = row_at(r) + 512 + 16 * (lane & 7);
+          const float f = scales[r];
+          uint4 v[5];
+#pragma unroll
+          for (int k = 0; k < 5; ++k) v[k] = ldg_nc_v4(src + 128 * k);
+#pragma unroll
+          for (int k = 0; k < 5; ++k)
+            *reinterpret_cast<uint4*>(smem + kOffQ + k * kBlk + sw128_offset(r, 16 * (lane & 7))) =
+                make_uint4(scaled(v[k].x, f, k < 4), scaled(v[k].y, f, k < 4), scaled(v[k].z, f, k < 4), scaled(v[k].w, f, k < 4));
+        }
+        tmem_wait_st();
+        tc_fence_before();
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -260,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           ref = to;
           if (j > first) {
             if (half == 0) alpha[row] = al;
-            here = here && warp_wait_all(&br.free[b ^ 1][3], (uint32_t)((i - 1) >> 1) & 1u, p.err);  // PV so far is complete
+            here = here && warp_wait_all(&br.free[b ^ 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);  // PV so far is complete
             if (!here) mc.abort = 1;
             named_bar(2, 128);
             tc_fence_after();
@@ -321,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
             p.lse[row0 + row] = z;
         }
       }
-      const bool done = ok && !mc.abort && warp_wait_all(&br.free[(i - 1) & 1][3], (uint32_t)((i - 1) >> 1) & 1u, p.err);
+      const bool done = ok && !mc.abort && warp_wait_all(&br.free[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
       if (!done) mc.abort = 1;
       named_bar(2, 128);
       tc_fence_after();
@@ -363,86 +417,104 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
     if (pw >= 0) {
       // ================================================================ producers =================
       const int rl = lane >> 3, c8 = lane & 7;
-      const uint32_t odd = (uint32_t)((c8 >> 2) ^ (rl & 1));  // which half of its codes a lane stores first: spreads the banks
-      Pages pages(p, st);
+      const int row = 4 * pw + rl;
+      const uint32_t at = sw128_offset(row, 16 * c8);
+      const uint8_t* mine = smem + kOffRaw + row * HS_KV_ROW_BYTES;
       Raw raw;
-      auto rows_of = [&](const Page& g) -> const uint8_t* {
-        const bool good = g.blk >= 0 && ((int64_t)g.blk + 1) * HS_PAGE <= p.R;
-        if (g.live && !good && g.left > 0 && lane == 0) flag_error(p.err, HS_FLAG_BAD_BLOCK);
-        return good ? p.kv + ((int64_t)g.blk * HS_PAGE + 4 * kQuads * pw + rl) * HS_KV_ROW_BYTES : nullptr;
-      };
-      auto load = [&](const uint8_t* from, int off) { return from ? ldg_nc_v4(from + off) : make_uint4(0, 0, 0, 0); };
-      auto load_group = [&](const uint8_t* from, int g) {
-#pragma unroll
-        for (int h = 0; h < kQuads; ++h) raw.code[g][h] = load(from, h * 4 * HS_KV_ROW_BYTES + 128 * g + 16 * c8);
-      };
-      auto load_rest = [&](const uint8_t* from) {
-#pragma unroll
-        for (int h = 0; h < kQuads; ++h) {
-          raw.scale[h] = load(from, h * 4 * HS_KV_ROW_BYTES + HS_D_LATENT);
-          raw.rope[h] = load(from, h * 4 * HS_KV_ROW_BYTES + HS_D_LATENT + 16 + 16 * c8);
-        }
-      };
-      Page now = pages.next(p);
-      const uint8_t* from = rows_of(now);
-      load_rest(from);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) load_group(from, g);
-      Page then = pages.next(p), after = pages.next(p);  // table entries are read two pages ahead, rows one
+      int left = kEnd;
       bool range_ok = true, ok = true;
+      // this warp's rows of the next page into registers; the place is handed back at once
+      auto take = [&](int i) {
+        ok = ok && !mc.abort && warp_wait_all(&br.raw_full, (uint32_t)i & 1u, p.err);
+        if (!ok) return;
+        left = mc.left;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) raw.code[g][h] = *reinterpret_cast<const uint2*>(mine + 128 * g + 64 * h + 8 * c8);
+        raw.scale = *reinterpret_cast<const uint4*>(mine + HS_D_LATENT);
+        raw.rope = *reinterpret_cast<const uint4*>(mine + HS_D_LATENT + 16 + 16 * c8);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br.raw_free);
+      };
+      take(0);
 #pragma unroll 1
-      for (int i = 0; ok && now.live; ++i) {
+      for (int i = 0; ok && left != kEnd; ++i) {
         const int s = i & 1;
-        uint8_t* tile = smem + kOffTile + s * kTile;
-        const uint8_t* ahead = rows_of(then);
-        bool bad[kQuads] = {};
+        uint8_t* tile = smem + kOffTile + s * kTile + at;
+        bool bad = false;
+        ok = warp_wait_all(&br.free[s], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err);
+        if (!ok) break;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          ok = ok && !mc.abort && warp_wait_all(&br.free[s][g], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err);
-          if (!ok) break;
-#pragma unroll
-          for (int h = 0; h < kQuads; ++h) {
-            const int row = 4 * kQuads * pw + 4 * h + rl;
-            const uint32_t* sc = &raw.scale[h].x;
-            const float f = row < now.left ? __uint_as_float(sc[g]) : 0.f;
-            const bool fits = f == 0.f || (fabsf(f) >= kScaleMin && fabsf(f) <= kScaleMax);
-            range_ok &= fits;
-            const __half hi = __float2half_rn(f);
-            const __half2 h2 = __half2half2(hi), l2 = __float2half2_rn(f - __half2float(hi));
-            const uint32_t hu = *reinterpret_cast<const uint32_t*>(&h2), lu = *reinterpret_cast<const uint32_t*>(&l2);
-            const uint4 v = raw.code[g][h];
-            uint4 d0 = dequant8(odd ? v.z : v.x, odd ? v.w : v.y, hu, lu);
-            uint4 d1 = dequant8(odd ? v.x : v.z, odd ? v.y : v.w, hu, lu);
-            if (has_nan(v) || !(fabsf(f) <= kScaleMax)) {
-              d0 = d1 = make_uint4(0, 0, 0, 0);
-              bad[h] = true;
-            }
-            uint8_t* blk = tile + (2 * g + (c8 >> 2)) * kBlk;
-            const uint32_t at = sw128_offset(row, 32 * (c8 & 3) + 16 * odd);
-            *reinterpret_cast<uint4*>(blk + at) = d0;
-            *reinterpret_cast<uint4*>(blk + (at ^ 16u)) = d1;
-            if (g == 3) {
-              uint4 r = raw.rope[h];
-              if ((__ballot_sync(0xffffffffu, bad[h]) >> (8 * rl)) & 0xFFu) r.x = 0x7FC07FC0u;  // two bf16 NaN
-              *reinterpret_cast<uint4*>(tile + 8 * kBlk + sw128_offset(row, 16 * c8)) = r;
-            }
+          float f = row < left ? __uint_as_float((&raw.scale.x)[g]) : 0.f;
+          range_ok &= f == 0.f || (fabsf(f) >= kScaleMin && fabsf(f) <= kScaleMax);
+          const bool wild = !(fabsf(f) <= kScaleMax);
+          f = wild ? 0.f : f;
+          const __half2 h2 = __floats2half2_rn(f, f);
+          const float lo = f - __low2float(h2);
+          const __half2 l2 = __floats2half2_rn(lo, lo);
+          const uint32_t hu = *reinterpret_cast<const uint32_t*>(&h2), lu = *reinterpret_cast<const uint32_t*>(&l2);
+          uint2 v = raw.code[g][0], w = raw.code[g][1];
+          if (has_nan(v, w) || wild) {
+            v = w = make_uint2(0, 0);
+            bad = true;
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&br.full[s][g]);
-          load_group(ahead, g);
+          *reinterpret_cast<uint4*>(tile + 2 * g * kBlk) = dequant8(v.x, v.y, hu, lu);
+          *reinterpret_cast<uint4*>(tile + (2 * g + 1) * kBlk) = dequant8(w.x, w.y, hu, lu);
+          if (g == 3) {
+            if ((__ballot_sync(0xffffffffu, bad) >> (8 * rl)) & 0xFFu) raw.rope.x = 0x7FC07FC0u;  // two bf16 NaN
+            *reinterpret_cast<uint4*>(tile + 8 * kBlk) = raw.rope;
+          }
+          if (g & 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&br.full[s][g >> 1]);
+          }
         }
-        load_rest(ahead);
-        now = then;
-        then = after;
-        after = pages.next(p);
+        take(i + 1);
       }
       if (!ok) mc.abort = 1;
       if (!range_ok) flag_error(p.err, HS_FLAG_RANGE);
+    } else if (warp == kLoadWarp) {
+      // ================================================================ codes =====================
+      // One page at a time, the next as soon as the producers have taken it into registers. Table entries are read three pages
+      // ahead, pages asked into L2 two ahead.
+      if (lane == 0) {
+        Pages pages(p, st);
+        auto good = [&](const Page& g) { return g.blk >= 0 && ((int64_t)g.blk + 1) * HS_PAGE <= p.R; };
+        constexpr uint32_t kPageBytes = HS_PAGE * HS_KV_ROW_BYTES;
+        Page now = pages.next(p), then = pages.next(p), after = pages.next(p);
+        bool ok = true;
+        int i = 0;
+#pragma unroll 1
+        for (;; ++i) {
+          ok = !mc.abort && mbar_wait(&br.raw_free, ((uint32_t)i & 1u) ^ 1u, p.err);
+          if (!ok) break;
+          const bool have = now.live && good(now) && now.left > 0;
+          if (now.live && now.left > 0 && !have) flag_error(p.err, HS_FLAG_BAD_BLOCK);
+          mc.left = !now.live ? kEnd : have ? now.left : 0;
+          if (have) {  // also rows past the length: the page is there
+            mbar_arrive_expect_tx(&br.raw_full, kPageBytes);
+            bulk_g2s(smem + kOffRaw, p.kv + (int64_t)now.blk * kPageBytes, kPageBytes, &br.raw_full);
+          } else {
+            mbar_arrive(&br.raw_full);
+          }
+          if (!now.live) break;
+          now = then;
+          then = after;
+          after = pages.next(p);
+          if (then.live && good(then)) bulk_prefetch_l2(p.kv + (int64_t)then.blk * kPageBytes, kPageBytes);
+        }
+        if (!ok) {
+          mc.abort = 1;
+          if (i > 0) mbar_wait(&br.raw_full, (uint32_t)(i - 1) & 1u, p.err);  // no copy is under way at the end
+        }
+      }
     } else if (warp == 0) {
       // ================================================================ QK ========================
       if (lane == 0) {
-        constexpr uint32_t lat = idesc_f16(kRows, kPageKeys, 0, 0), rop = idesc_bf16(kRows, kPageKeys, 0, 0);
+        constexpr uint32_t wide = idesc_f16(128, kPageKeys, 0, 0), lat = idesc_f16(kRows, kPageKeys, 0, 0), rop = idesc_bf16(kRows, kPageKeys, 0, 0);
         const uint64_t qd = smem_desc(smem_u32(smem + kOffQ), 16, 1024, 2);
         Walk<kRows> walk(p, st);
         Seg s;
@@ -451,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
 #pragma unroll 1
         for (int n = 0; ok && walk.next(p, s); ++n) {
           ok = !mc.abort && mbar_wait(&br.q_ready, (uint32_t)n & 1u, p.err);
+          tc_fence_after();
           const int end = end_page(p, s);
 #pragma unroll 1
           for (int j = first_page(s); ok && j < end; ++j, ++i) {
@@ -461,13 +534,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
             const uint32_t d = tmem + kColS + 64 * b;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              ok = ok && mbar_wait(&br.full[b][g], ph, p.err);
-              if (!ok) break;
-              tc_fence_after();
+              if ((g & 1) == 0) {
+                ok = ok && mbar_wait(&br.full[b][g >> 1], ph, p.err);
+                if (!ok) break;
+                tc_fence_after();
+              }
 #pragma unroll
               for (int k = 0; k < (g < 3 ? 8 : 12); ++k) {  // 16 dims each
-                const uint64_t at = (uint64_t)(((2 * g + k / 4) * kBlk + (k % 4) * 32) >> 4);
-                mma_bf16_ss(d, qd + at, kd + at, k < 8 ? lat : rop, (g | k) != 0 ? 1u : 0u);
+                const int blk = 2 * g + k / 4;
+                const uint64_t b16 = kd + (uint64_t)((blk * kBlk + (k % 4) * 32) >> 4);
+                if (g < 2)  // Q from tensor memory: 128 lanes, of which 64 are rows
+                  mma_f16_ts(d, tmem + kColQ + 64 * g + 8 * k, b16, wide, (g | k) != 0 ? 1u : 0u);
+                else
+                  mma_bf16_ss(d, qd + (uint64_t)(((blk - 4) * kBlk + (k % 4) * 32) >> 4), b16, k < 8 ? lat : rop, 1u);
               }
             }
             if (ok) mma_commit(&br.s_full[b]);
@@ -502,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
               for (int k = 0; k < 4; ++k)
                 mma_bf16_ss(tmem + 64 * g, vd + (uint64_t)((2 * g * kBlk + k * 2048) >> 4), pd + (uint64_t)((k * 32) >> 4), id,
                             j > first || k > 0 ? 1u : 0u);
-              mma_commit(&br.free[b][g]);
             }
+            mma_commit(&br.free[b]);
           }
         }
         if (!ok) mc.abort = 1;
