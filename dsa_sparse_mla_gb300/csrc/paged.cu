@@ -15,7 +15,7 @@
 // tile, which halves what it reads from L2, dequantises, and feeds its tensor core from shared memory. A cluster is the
 // softmax pair (ranks 0, 1) and the output pair (ranks 2, 3).
 //
-// Two variants, chosen by copies() below:
+// Two variants, chosen by copies() below (requests with few rows go to paged_few.cu):
 //   raw   eight (softmax CTA) or six (output CTA) producer warps dequantise the rows' codes, which TMA brings as they lie in
 //         the pool, to fp16 (code * group scale rounded once) in 128-byte-swizzled blocks.
 //   copy  expand_kernel first writes every row dequantised to the workspace ([512 fp16][64 bf16], 1,152 bytes), and TMA brings
@@ -1211,8 +1211,10 @@ static uint64_t part_bytes(int sms) {
 // 2,181 / 1,663. With short caches the copy's extra launch and pass show longer: 8 x 512 rows over 2,000 53 / 64; 8 x 4,096
 // 199 / 177.
 static bool copies(int T, int B, int H) { return (int64_t)T * H > 256ll * B; }
-// Whether they have few enough for paged_few.cu.
-static bool few_rows(int T, int B, int H) { return (int64_t)T * H <= 64ll * B; }
+// Whether they have few enough for paged_few.cu: two of its blocks of 64 per request on average. Measured (us, this file's raw
+// variant / paged_few.cu): 64 requests x 64 rows over 30,000 cached rows 1,089 / 414; x 128 rows 1,093 / 794; x 144 (three
+// blocks) 1,125 / 1,143; 8 x 128 over 1,000 40 / 40; 64 x 128 over 200 47 / 54.
+static bool few_rows(int T, int B, int H) { return (int64_t)T * H <= 128ll * B; }
 
 template <bool kRaw>
 static cudaError_t launch(const Params& p0, const uint16_t* rows, uint64_t n, int sms, cudaStream_t stream, const char** why) {
@@ -1267,7 +1269,7 @@ static cudaError_t launch(const Params& p0, const uint16_t* rows, uint64_t n, in
   kernel<<<2 * G * C, Sh::kThreads, kSmem, stream>>>(mk, mv, mr, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<Sh::kRows><<<dim3((unsigned)C, Sh::kRows / kMergeRows), kMergeThreads, 0, stream>>>(p);
+  paged_merge_kernel<Sh::kRows><<<Merge<Sh::kRows>::grid(C), kMergeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 }  // namespace paged

@@ -1,22 +1,36 @@
 // paged_few.cu — dense attention over paged FP8 latent rows for requests with few (token, head) rows (decode): the formulas of
 // paged.cu on one SM per block of 64 rows.
 //
-//   S = Q K^T (M = 64 rows, N = 64 cached rows, 36 MMAs of 45 cycles),  P = 2^(c S - m),
-//   O^T += V^T P^T (M = 128 dims x 4, N = 64 rows, 16 MMAs): O^T takes 256 of the SM's tensor memory columns, two S buffers 128.
+//   S = Q K^T (M = 64 rows, N = 64 cached rows, 36 MMAs),  P = 2^(c S - m),
+//   O^T += V^T P^T (M = 128 dims x 4, N = 64 rows, 16 MMAs)
+//
+// Why not 128 or 256 rows as in paged.cu: a request has only 64, and each SM pays for dequantising every cached row that it
+// visits; with O transposed, O^T of 64 rows takes 256 of the tensor memory's columns, so S (two buffers of 64 columns) and
+// half of Q (128 columns) fit beside it and nothing crosses SMs.
 //
 // Work. Persistent, one CTA per SM; units as in paged.cu (block of rows, 128 cached rows), shared out evenly, split blocks joined
-// by paged_merge_kernel. Inside a unit the step is one page (64 rows).
+// by paged_merge_kernel. Inside a unit the step is one page (64 cached rows).
 //
-// Roles (warp w runs on sub-partition w % 4, so the two issuing warps share theirs with one softmax warp only). Warp 0 issues QK,
-// warp 4 PV. Warps 1-3, 5-7, 13, 14 are the producers: each turns 8 rows of a page from codes into fp16 (code * group scale,
-// rounded once) in 128-byte-swizzled blocks [64 rows][64 dims], from registers that it loaded a page ahead. Two pages fit beside
-// Q; a 128-dim group of a page is handed to QK when all producers have written it and comes back when PV has read it. Warps 8-11
-// are the softmax, 16 rows each, two threads per row with 32 columns each (what a 64-row product leaves in tensor memory).
-// P goes into the page's rotary block, which QK has read by then.
+// Shared memory: Q's other half (five blocks of [64 rows][64 dims], 128-byte swizzle), two pages dequantised (nine blocks
+// each), one page as it lies in the pool.
+//
+// Roles (768 threads; warp w runs on sub-partition w % 4). Warp 16 brings a page by one bulk copy, with the next one asked into
+// L2. Warps 1-3, 5-7, 12-15, 17-19 and 21-23 are the producers: each takes four rows into registers, so that the next
+// page can land, and writes them as fp16 (code * group scale, rounded once), in two halves of the dims that QK starts on as
+// soon as every producer has written one; PV gives them back in halves too. Warp 0 issues QK (Q's first 256 dims from
+// tensor memory as a 128-row A of which 64 lanes are rows, the rest from shared memory), warp 4 PV. Warps 8-11 are the
+// softmax, 16 rows each, two threads per row with 32 columns each (what a 64-row product leaves in tensor memory);
+// they also load Q, rescale and write O^T. P goes into the page's rotary block, which QK has read by then.
 //
 // Lazy maximum and masks as in paged.cu: a row's reference moves only when a logit passes it by more than 2^8; one OR-barrier
 // per page tells the softmax warps, which then rescale O^T's columns. A latent value that is NaN or cannot be fp16 is zeroed
 // and its row's rotary values become NaN: rows that see it are NaN, P = 0 times it stays 0.
+//
+// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 575 us, 3,180 GB/s
+// of cache, 0.47 of a plain copy's rate; about 4,000 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
+// that pace (about 8,000 cycles for two slots): without the MMAs 3,150, without the producers' arithmetic 3,800. On
+// the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (the loads share too few
+// scoreboards and wait for each other); four hand-overs per page 4,750.
 #include "paged.cuh"
 
 namespace hs {
@@ -37,7 +51,7 @@ constexpr int kOffRow = kOffRaw + kProducers * kRawRows;  // float [64] each: fa
 constexpr int kOffBar = kOffRow + 4 * 256;
 struct Bars {
   uint64_t full[2][2];   // producers have written a half of a page's dims -> QK
-  uint64_t free[2];      // PV has read the page and P -> producers, softmax
+  uint64_t free[2][2];   // PV has read a half (the second: and P) -> producers, softmax
   uint64_t s_full[2];    // S complete -> softmax
   uint64_t s_empty[2];   // S read -> QK
   uint64_t p_full[2];    // P written, O^T rescaled -> PV
@@ -147,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       for (int g = 0; g < 2; ++g) mbar_init(&br.full[s][g], kProducers);
-      mbar_init(&br.free[s], 1);
+      for (int g = 0; g < 2; ++g) mbar_init(&br.free[s][g], 1);
       mbar_init(&br.s_full[s], 1);
       mbar_init(&br.s_empty[s], 4);
       mbar_init(&br.p_full[s], 4);
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           ref = to;
           if (j > first) {
             if (half == 0) alpha[row] = al;
-            here = here && warp_wait_all(&br.free[b ^ 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);  // PV so far is complete
+            here = here && warp_wait_all(&br.free[b ^ 1][1], (uint32_t)((i - 1) >> 1) & 1u, p.err);  // PV so far is complete
             if (!here) mc.abort = 1;
             named_bar(2, 128);
             tc_fence_after();
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
             p.lse[row0 + row] = z;
         }
       }
-      const bool done = ok && !mc.abort && warp_wait_all(&br.free[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
+      const bool done = ok && !mc.abort && warp_wait_all(&br.free[(i - 1) & 1][1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
       if (!done) mc.abort = 1;
       named_bar(2, 128);
       tc_fence_after();
@@ -443,10 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
         const int s = i & 1;
         uint8_t* tile = smem + kOffTile + s * kTile + at;
         bool bad = false;
-        ok = warp_wait_all(&br.free[s], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err);
-        if (!ok) break;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          if ((g & 1) == 0) {
+            ok = ok && warp_wait_all(&br.free[s][g >> 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err);
+            if (!ok) break;
+          }
           float f = row < left ? __uint_as_float((&raw.scale.x)[g]) : 0.f;
           range_ok &= f == 0.f || (fabsf(f) >= kScaleMin && fabsf(f) <= kScaleMax);
           const bool wild = !(fabsf(f) <= kScaleMax);
@@ -581,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
               for (int k = 0; k < 4; ++k)
                 mma_bf16_ss(tmem + 64 * g, vd + (uint64_t)((2 * g * kBlk + k * 2048) >> 4), pd + (uint64_t)((k * 32) >> 4), id,
                             j > first || k > 0 ? 1u : 0u);
+              if (g & 1) mma_commit(&br.free[b][g >> 1]);
             }
-            mma_commit(&br.free[b]);
           }
         }
         if (!ok) mc.abort = 1;
@@ -613,7 +629,7 @@ cudaError_t launch_few(const Params& p0, int sms, cudaStream_t stream) {
   few_kernel<<<p.clusters, kThreads, kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<kRows><<<dim3((unsigned)p.clusters, kRows / kMergeRows), kMergeThreads, 0, stream>>>(p);
+  paged_merge_kernel<kRows><<<Merge<kRows>::grid(p.clusters), kMergeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
