@@ -1,6 +1,7 @@
 // hs_api.cu — the C ABI declared in include/hs.h: host-side argument checks, then launches.
 // Nothing here allocates device memory, synchronises the stream (hs_check_flag aside) or keeps
 // state between calls except the calling thread's last error text.
+#include <atomic>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -51,15 +52,21 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // The kernels use sm_103a instructions (tcgen05, TMA); other devices are refused up front.
 hs_status check_device(int* num_sms) {
-  int dev = 0, major = 0, minor = 0;
+  static std::atomic<int> known[64];  // per device: its SMs, once it was found to be the right kind
+  int dev = 0, major = 0, minor = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (e == cudaSuccess && num_sms) e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return fail(HS_ERR_CUDA, "device query failed: %s", cudaGetErrorString(e));
-  if (major != 10 || minor != 3)
-    return fail(HS_ERR_UNSUPPORTED, "device %d has compute capability %d.%d; this library needs 10.3 (sm_103a)", dev,
-                major, minor);
+  if (e == cudaSuccess && dev < 64) sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return fail(HS_ERR_CUDA, "device query failed: %s", cudaGetErrorString(e));
+    if (major != 10 || minor != 3)
+      return fail(HS_ERR_UNSUPPORTED, "device %d has compute capability %d.%d; this library needs 10.3 (sm_103a)", dev,
+                  major, minor);
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  }
+  if (num_sms) *num_sms = sms;
   return HS_OK;
 }
 

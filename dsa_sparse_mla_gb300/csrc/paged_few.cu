@@ -26,11 +26,12 @@
 // per page tells the softmax warps, which then rescale O^T's columns. A latent value that is NaN or cannot be fp16 is zeroed
 // and its row's rotary values become NaN: rows that see it are NaN, P = 0 times it stays 0.
 //
-// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 575 us, 3,180 GB/s
-// of cache, 0.47 of a plain copy's rate; about 4,000 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
+// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 569 us, 3,220 GB/s
+// of cache, 0.48 of a plain copy's rate; about 4,000 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
 // that pace (about 8,000 cycles for two slots): without the MMAs 3,150, without the producers' arithmetic 3,800. On
 // the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (the loads share too few
-// scoreboards and wait for each other); four hand-overs per page 4,750.
+// scoreboards and wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 31 us: about 3 us until
+// the shares are known, 7 for Q, 3 per page, 4 for the partial results (7 with 4-byte stores), the rest launches and the join.
 #include "paged.cuh"
 
 namespace hs {
@@ -127,15 +128,14 @@ __device__ __forceinline__ bool has_nan(const uint2& a, const uint2& b) {
   return ((((a.x & m) + o) | ((a.y & m) + o) | ((b.x & m) + o) | ((b.y & m) + o)) & 0x80808080u) != 0u;
 }
 
-// The store that mirrors tmem_ld16x2_32.
-__device__ __forceinline__ void tmem_st16x2_32(uint32_t taddr, const uint32_t (&r)[32]) {
+// Stores what tmem_ld16x2_32 reads, 16 columns to a half: thread i < 16 lane (base + i), columns [c, c + 16), thread i >= 16
+// lane (base + i - 16), columns [c + 16, c + 32).
+__device__ __forceinline__ void tmem_st16x2_16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], 32, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], 16, {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
@@ -210,6 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       if (!idle) {
         const uint8_t* q0 = p.q + row0 * (HS_D_QK * 2);
         auto row_at = [&](int r) { return q0 + (int64_t)(r < s.nrows ? r : 0) * (HS_D_QK * 2); };
+        // everything this warp reads, asked for at once (nine lines a row); the loops below stay small, since code that runs
+        // once per block costs its fetch from memory
+#pragma unroll 1
+        for (int k = lane; k < 16 * 9; k += 32) prefetch_l2(row_at(16 * quad + k / 9) + 128 * (k % 9));
         // A row whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it in
         // [2^14, 2^15); its logits are scaled back.
 #pragma unroll 1
@@ -250,20 +254,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, b);
           return *reinterpret_cast<const uint32_t*>(&b2);
         };
-        // dims 128 h + 64 half .. + 63 of this thread's row to tensor memory
-        const uint8_t* own = row_at(row) + 128 * half;
+        // dims 64 h + 32 half .. + 31 of this thread's row to tensor memory
+        const uint8_t* own = row_at(row) + 64 * half;
         const float own_scale = scales[row];
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint4 v = ldg_nc_v4(own + 256 * h + 16 * k);
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = ldg_nc_v4(own + 128 * h + 16 * k);
             w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
           }
 #pragma unroll
-          for (int k = 0; k < 32; ++k) w[k] = scaled(w[k], own_scale, true);
-          tmem_st16x2_32(quarter + kColQ + 64 * h, w);
+          for (int k = 0; k < 16; ++k) w[k] = scaled(w[k], own_scale, true);
+          tmem_st16x2_16(quarter + kColQ + 32 * h, w);
         }
         // the rest to shared memory, four rows of 64 dims per load
 #pragma unroll 1
@@ -394,28 +398,39 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       named_bar(2, 128);
       tc_fence_after();
       if (done) {
-        // O^T: lane = dim 128 g + 32 quad + lane, column = row
-#pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
-          const int g = h >> 1, r0 = 32 * (h & 1), d = 128 * g + 32 * quad + lane;
-          if (r0 >= s.nrows) continue;
-          uint32_t o[32];
-          tmem_ld32(quarter + 32 * h, o);
+        // O^T: lane = dim 128 g + 32 quad + lane, column = row. 16 rows of 32 dims at a time, turned in Q's place (the block's
+        // QK is done; rows of 36 floats: both sides hit all banks), so that stores are 16 bytes wide.
+        // Unrolled by four: with a smaller loop here the whole kernel came out 8 % slower on long caches.
+        float* turn = reinterpret_cast<float*>(smem + kOffQ) + quad * 16 * 36;
+#pragma unroll 4
+        for (int h = 0; h < 16; ++h) {
+          const int r0 = 16 * (h & 3), n = s.nrows - r0, d = 128 * (h >> 2) + 32 * quad;
+          if (n <= 0) continue;
+          uint32_t o[16];
+          tmem_ld16(quarter + 16 * h, o);
           tmem_wait_ld();
-          const int n = s.nrows - r0;
+          __syncwarp();  // the rows before have been read
 #pragma unroll
-          for (int z = 0; z < 32; z += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(inverse + r0 + z);
-            const float a = __uint_as_float(o[z]) * f.x, e = __uint_as_float(o[z + 1]) * f.y;
-            if (whole) {  // lanes swap, so that each stores two dims: the even one of row z, the odd one of row z + 1
-              const float y = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : e, 1);
-              const __nv_bfloat162 b2 = lane & 1 ? __floats2bfloat162_rn(y, e) : __floats2bfloat162_rn(a, y);
-              const int r = z + (lane & 1);
-              if (r < n) *reinterpret_cast<__nv_bfloat162*>(p.out + (row0 + r0 + r) * HS_D_LATENT + (d & ~1)) = b2;
-            } else {
-              float* to = p.part_out + (part * kRows + r0 + z) * HS_D_LATENT + d;
-              if (z < n) to[0] = a;
-              if (z + 1 < n) to[HS_D_LATENT] = e;
+          for (int z = 0; z < 16; ++z) turn[36 * z + lane] = __uint_as_float(o[z]) * inverse[r0 + z];
+          __syncwarp();
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int r = 8 * j + (lane >> 2);
+              const float4 x = *reinterpret_cast<const float4*>(turn + 36 * r + 8 * (lane & 3));
+              const float4 y = *reinterpret_cast<const float4*>(turn + 36 * r + 8 * (lane & 3) + 4);
+              alignas(16) const __nv_bfloat162 b2[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                                            __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+              if (r < n)
+                *reinterpret_cast<uint4*>(p.out + (row0 + r0 + r) * HS_D_LATENT + d + 8 * (lane & 3)) = *reinterpret_cast<const uint4*>(b2);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = 4 * j + (lane >> 3);
+              if (r < n)
+                *reinterpret_cast<float4*>(p.part_out + (part * kRows + r0 + r) * HS_D_LATENT + d + 4 * (lane & 7)) =
+                    *reinterpret_cast<const float4*>(turn + 36 * r + 4 * (lane & 7));
             }
           }
         }
