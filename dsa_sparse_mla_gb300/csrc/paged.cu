@@ -118,6 +118,7 @@ constexpr int kRotaryBar = 6;  // raw: full and empty barriers 6 and 7 belong to
 // requests of 30,000 rows, 3.47 GB, take 577 us, 6,010 GB/s.
 constexpr int kExpandThreads = 512;
 __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const Params p, uint16_t* out) {
+  let_next();
   __shared__ int64_t pre[kMaxReq + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
@@ -498,6 +499,8 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
   Start* st = &mc.start;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  let_next();
+  if (!kRaw) after_previous();
   const uint32_t rank = cluster_ctarank();
   const bool isA = rank < G, lead = rank % G == 0;
   const int half = (int)rank % G;  // which rows of a block, and which part of every K and V tile
@@ -1267,11 +1270,14 @@ static cudaError_t launch(const Params& p0, const uint16_t* rows, uint64_t n, in
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  kernel<<<2 * G * C, Sh::kThreads, kSmem, stream>>>(mk, mv, mr, p);
-  e = cudaGetLastError();
+  if (kRaw) {
+    kernel<<<2 * G * C, Sh::kThreads, kSmem, stream>>>(mk, mv, mr, p);
+    e = cudaGetLastError();
+  } else {
+    e = launch_next(kernel, dim3(2 * G * C), Sh::kThreads, kSmem, stream, mk, mv, mr, p);
+  }
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<Sh::kRows><<<Merge<Sh::kRows>::grid(C), kMergeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_next(paged_merge_kernel<Sh::kRows>, Merge<Sh::kRows>::grid(C), kMergeThreads, 0, stream, p);
 }
 }  // namespace paged
 

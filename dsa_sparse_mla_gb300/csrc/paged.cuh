@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const Params
   __shared__ float w[kMaxClusters][kTake];
   __shared__ float4 other[256];
   const int tid = threadIdx.x, r0 = blockIdx.y * kTake;
+  after_previous();
   Desc desc[kStarts];
 #pragma unroll
   for (int k = 0; k < kStarts; ++k) {

@@ -30,7 +30,7 @@
 // of cache, 0.48 of a plain copy's rate; about 4,000 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
 // that pace (about 8,000 cycles for two slots): without the MMAs 3,150, without the producers' arithmetic 3,800. On
 // the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (the loads share too few
-// scoreboards and wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 31 us: about 3 us until
+// scoreboards and wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 29 us: about 3 us until
 // the shares are known, 7 for Q, 3 per page, 4 for the partial results (7 with 4-byte stores), the rest launches and the join.
 #include "paged.cuh"
 
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
   float* coefs = alpha + 128;
   float* scales = alpha + 192;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  let_next();
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       for (int g = 0; g < 2; ++g) mbar_init(&br.full[s][g], kProducers);
@@ -644,8 +645,7 @@ cudaError_t launch_few(const Params& p0, int sms, cudaStream_t stream) {
   few_kernel<<<p.clusters, kThreads, kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<kRows><<<Merge<kRows>::grid(p.clusters), kMergeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_next(paged_merge_kernel<kRows>, Merge<kRows>::grid(p.clusters), kMergeThreads, 0, stream, p);
 }
 
 }  // namespace paged

@@ -15,7 +15,8 @@
 // use counts once, 16 bytes per thread. Measured on a GB300: compaction that moves 2,100 pages of 24 + 6 layers (4.4 GB)
 // 687 us, 6,470 GB/s, 0.97 of a plain copy's rate; 256 forks of requests with 24 + 6 layers (255 MB) and their release
 // 63 us, of which the copies 34 us, the forks' plan 7.5 us, the release 6 us, and the rest between launches; a compaction of
-// 133 pages 15 us (count 2.5, plan 4.5, moves 8.5).
+// 133 pages 13 us (count 2.5, plan 4.5, moves 8.5 one after the other; 15.6 without launching each before the one before it
+// ends, which costs the host 1.5 us per launch: small forks, bound by the host, are slower with it, 44 against 41 us).
 #include "common.cuh"
 
 namespace hs {
@@ -309,6 +310,7 @@ struct CompactParams {
 };
 
 __global__ void __launch_bounds__(kChunk) compact_count_kernel(const CompactParams p) {
+  let_next();
   const int i = blockIdx.x * kChunk + threadIdx.x;
   const int n = __syncthreads_count(i < p.N && p.ref[i] > 0);
   if (threadIdx.x == 0) p.chunk_used[blockIdx.x] = n;
@@ -319,8 +321,10 @@ __global__ void __launch_bounds__(kChunk) compact_plan_kernel(const CompactParam
   __shared__ int s[33];
   __shared__ int sums[3];  // in use: in all, before this chunk, before the chunk that holds U
   const int tid = threadIdx.x;
+  let_next();
   if (tid < 3) sums[tid] = 0;
   __syncthreads();
+  after_previous();
   int all = 0, before = 0;
   for (int c = tid; c < p.chunks; c += kChunk) {
     const int u = p.chunk_used[c];
@@ -364,6 +368,7 @@ __global__ void __launch_bounds__(kChunk) compact_plan_kernel(const CompactParam
 
 // Copies every move in every layer, and rewrites the table and the use counts.
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const CompactParams p) {
+  after_previous();
   const int moved = p.counts[1], U = p.counts[0];
   const int64_t stride = (int64_t)gridDim.x * kCopyThreads, t0 = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
   for (int64_t i = t0; i < (int64_t)p.B * p.bt_stride; i += stride) {
@@ -447,11 +452,9 @@ cudaError_t launch_compact(const hs_kv_compact_args* a, int sms, cudaStream_t st
   compact_count_kernel<<<(unsigned)p.chunks, kChunk, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  compact_plan_kernel<<<(unsigned)p.chunks, kChunk, 0, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_next(compact_plan_kernel, dim3((unsigned)p.chunks), kChunk, 0, stream, p);
   if (e != cudaSuccess) return e;
-  compact_move_kernel<<<(unsigned)(8 * sms), kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_next(compact_move_kernel, dim3((unsigned)(8 * sms)), kCopyThreads, 0, stream, p);
 }
 
 }  // namespace hs
