@@ -73,8 +73,17 @@ __device__ __forceinline__ int block_tiles(const Params& p, const Req& q, int b)
 __host__ __device__ __forceinline__ int64_t unit_begin(int64_t c, int64_t U, int64_t C) { return c * U / C; }
 __device__ __forceinline__ int64_t unit_cta(int64_t u, int64_t U, int64_t C) { return ((u + 1) * C - 1) / U; }
 
-// A block costs its tiles and what it takes to begin and end it (its queries, its output), in tiles: about two.
-constexpr int kBlockCost = 2;
+// A block costs its tiles and what it takes to begin and end it (its queries, its output), in tiles: about four. Measured with
+// 1 / 2 / 3 / 4 / 5 / 7 / 10 tiles: 9 ragged requests of up to 400 tokens 331 / 277 / 241 / 217 / 216 / 220 / 230 us; 32 long
+// requests of one token 571 / 566 / 561 / 562 / 562 / 565 / 568 us.
+constexpr int kBlockCost = 4;
+
+// Splitting costs this many tiles: partial results and their join. A batch of at most one block per cluster is split only where
+// its longest block takes longer than an equal share and the join. Measured (us, split / whole): 30 requests x 4 tokens x 64
+// heads over 500 / 760 / 1,500 rows 48 / 33, 51 / 38, 66 / 50; 8 x 16 x 16 over 760 / 1,000 38 / 35, 39 / 40; 64 x 1 x 64 over
+// 380 / 700 42 / 35, 50 / 46; 16 x 1 x 64 over 700 33 / 44.
+template <int kRows>
+constexpr int kJoinCost = kRows <= 64 ? 6 : 8;
 
 // Where a cluster's work begins: found by every CTA of it at its start, in shared memory.
 struct Start {
@@ -158,6 +167,7 @@ __device__ __forceinline__ void find_units(const Params& p, int64_t* pre, Start*
   __syncthreads();
   if (warp == 0) {
     int64_t run = 0, cached = 0, blocks = 0;
+    int most = 0;  // tiles of a block: a request's last one has the most
     if (lane == 0) pre[0] = 0, nblk[0] = 0;
     for (int at = 0; at < p.B; at += 32) {
       const bool in = at + lane < p.B;
@@ -165,22 +175,49 @@ __device__ __forceinline__ void find_units(const Params& p, int64_t* pre, Start*
       if (in) {
         pre[at + lane + 1] = run + x;
         nblk[at + lane + 1] = (int32_t)(blocks + n);
-        cached += load_req<kRows>(p, at + lane).seq;
+        const Req q = load_req<kRows>(p, at + lane);
+        cached += q.seq;
+        if (q.nb > 0) most = max(most, block_tiles<kRows>(p, q, q.nb - 1));
       }
       run += __shfl_sync(0xffffffffu, x, 31);
       blocks += __shfl_sync(0xffffffffu, n, 31);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) cached += __shfl_xor_sync(0xffffffffu, cached, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      cached += __shfl_xor_sync(0xffffffffu, cached, o);
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
     __syncwarp();
     if (cached > p.kv_tokens) {
       run = 0;
       if (c == 0 && lane == 0) flag_error(p.err, HS_FLAG_BAD_LENGTH);
     }
     const int64_t U = run, C = U < p.clusters ? U : p.clusters;
+    auto rows_before = [&](int request) {
+      int64_t n = 0;
+      for (int r = lane; r < request; r += 32) n += copy_rows(load_req<kRows>(p, r));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      return n;
+    };
     int64_t tiles_before[2] = {0, 0}, cost = 0, base = 0;
     int r0 = 0, b0 = 0, ta0 = 0;
-    if (c < C) {
+    if (U > 0 && blocks <= p.clusters && (int64_t)(most + kBlockCost - kJoinCost<kRows>) * p.clusters <= U) {
+      if (c < blocks) {  // block c
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (nblk[mid] <= c)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        r0 = lo;
+        b0 = c - nblk[lo];
+        tiles_before[1] = block_tiles<kRows>(p, load_req<kRows>(p, lo), b0);
+        base = rows_before(lo);
+      }
+    } else if (c < C) {
       for (int end = 0; end < 2; ++end) {  // the share's beginning and its end
         const int64_t u = unit_begin(c + end, U, C);
         int lo = 0, hi = p.B;  // the request with pre[lo] <= u < pre[lo + 1]; the last one with blocks for u = U
@@ -215,9 +252,7 @@ __device__ __forceinline__ void find_units(const Params& p, int64_t* pre, Start*
           b0 = b;
           ta0 = ta;
           cost = at_block;
-          for (int r = lane; r < lo; r += 32) base += copy_rows(load_req<kRows>(p, r));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+          base = rows_before(lo);
         }
       }
     }
