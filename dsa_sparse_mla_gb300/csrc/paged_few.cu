@@ -48,7 +48,7 @@ constexpr int kOffTile = 5 * kBlk;
 constexpr int kOffScratch = kOffTile;          // int64 [B + 1] and int32 [B + 1] during the set-up
 constexpr int kOffRaw = kOffTile + 2 * kTile;  // a page as it lies in the pool: four rows per producer
 constexpr int kRawRows = 4 * HS_KV_ROW_BYTES;
-constexpr int kOffRow = kOffRaw + kProducers * kRawRows;  // float [64] each: factors, 1 / sums, logit coefficients, Q's scales
+constexpr int kOffRow = kOffRaw + kProducers * kRawRows;  // [64] each: factors, 1 / sums, Q's largest values and scales
 constexpr int kOffBar = kOffRow + 4 * 256;
 struct Bars {
   uint64_t full[2][2];   // producers have written a half of a page's dims -> QK
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
   Misc& mc = *reinterpret_cast<Misc*>(smem + kOffMisc);
   float* alpha = reinterpret_cast<float*>(smem + kOffRow);
   float* inverse = alpha + 64;
-  float* coefs = alpha + 128;
+  uint32_t* largest = reinterpret_cast<uint32_t*>(alpha + 128);
   float* scales = alpha + 192;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
   let_next();
@@ -207,47 +207,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       }
       if (s.tb == s.tiles) cost += s.tiles + kBlockCost;
       const bool idle = 16 * quad >= s.nrows, mine = row < s.nrows;
-      // Q: the block before has been read (its last S is complete). Rows past the block's are read as its first row.
+      // Q: the block before has been read (its last S is complete). Rows past the block's are read as its first row. A row
+      // whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it in [2^14, 2^15) and its
+      // logits are scaled back: rare, so the values are converted as they are first, and again if need be.
+      float coef = 1.f;
       if (!idle) {
         const uint8_t* q0 = p.q + row0 * (HS_D_QK * 2);
         auto row_at = [&](int r) { return q0 + (int64_t)(r < s.nrows ? r : 0) * (HS_D_QK * 2); };
-        // everything this warp reads, asked for at once (nine lines a row); the loops below stay small, since code that runs
-        // once per block costs its fetch from memory
+        // everything this warp reads, asked for at once (nine lines a row)
 #pragma unroll 1
         for (int k = lane; k < 16 * 9; k += 32) prefetch_l2(row_at(16 * quad + k / 9) + 128 * (k % 9));
-        // A row whose largest latent value is outside [2^-6, 2^15) is scaled by a power of two that puts it in
-        // [2^14, 2^15); its logits are scaled back.
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          const int r = 16 * quad + 4 * h + (lane >> 3);
-          const uint8_t* src = row_at(r) + 16 * (lane & 7);
-          uint4 v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = ldg_nc_v4(src + 128 * k);
-          uint32_t mx = 0u;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu),
-                                       __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu)));
-          uint32_t amax = max(mx & 0xFFFFu, mx >> 16);
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          int e = 0;
-          if (amax >= 0x7F80u) {
-            if (r < s.nrows) flag_error(p.err, HS_FLAG_RANGE);
-          } else if (amax >= 0x4700u || (amax >= 0x0080u && amax < 0x3C80u)) {
-            e = 14 - ((int)(amax >> 7) - 127);
-          } else if (amax > 0u && amax < 0x0080u) {
-            e = 126;
-          }
-          e = e < -126 ? -126 : (e > 126 ? 126 : e);
-          if ((lane & 7) == 0) {
-            scales[r] = __uint_as_float((uint32_t)(e + 127) << 23);
-            // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
-            coefs[r] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
-          }
-        }
-        __syncwarp();
         auto scaled = [&](uint32_t w, float f, bool half16) -> uint32_t {
           const uint32_t u = w ^ p.flip;
           const float a = __uint_as_float(u << 16) * f, b = __uint_as_float(u & 0xFFFF0000u) * f;
@@ -255,34 +224,73 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, b);
           return *reinterpret_cast<const uint32_t*>(&b2);
         };
-        // dims 64 h + 32 half .. + 31 of this thread's row to tensor memory
         const uint8_t* own = row_at(row) + 64 * half;
-        const float own_scale = scales[row];
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          uint32_t w[16];
+        for (int pass = 0;; ++pass) {
+          // dims 64 h + 32 half .. + 31 of this thread's row to tensor memory
+          const float own_scale = pass ? scales[row] : 1.f;
+          uint32_t mx = 0u;
+#pragma unroll 1
+          for (int h = 0; h < 4; h += 2) {
+            uint4 v[2][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 v = ldg_nc_v4(own + 128 * h + 16 * k);
-            w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[e][k] = ldg_nc_v4(own + 128 * (h + e) + 16 * k);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[4 * k] = v[e][k].x, w[4 * k + 1] = v[e][k].y, w[4 * k + 2] = v[e][k].z, w[4 * k + 3] = v[e][k].w;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                mx = __vmaxu2(mx, w[k] & 0x7FFF7FFFu);
+                w[k] = scaled(w[k], own_scale, true);
+              }
+              tmem_st16x2_16(quarter + kColQ + 32 * (h + e), w);
+            }
           }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = scaled(w[k], own_scale, true);
-          tmem_st16x2_16(quarter + kColQ + 32 * h, w);
-        }
-        // the rest to shared memory, four rows of 64 dims per load
+          // the rest to shared memory, four rows of 64 dims per load
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          const int r = 16 * quad + 4 * h + (lane >> 3);
-          const uint8_t* src = row_at(r) + 512 + 16 * (lane & 7);
-          const float f = scales[r];
-          uint4 v[5];
+          for (int h = 0; h < 4; ++h) {
+            const int r = 16 * quad + 4 * h + (lane >> 3);
+            const uint8_t* src = row_at(r) + 512 + 16 * (lane & 7);
+            const float f = pass ? scales[r] : 1.f;
+            uint4 v[5];
 #pragma unroll
-          for (int k = 0; k < 5; ++k) v[k] = ldg_nc_v4(src + 128 * k);
+            for (int k = 0; k < 5; ++k) v[k] = ldg_nc_v4(src + 128 * k);
+            uint32_t m = 0u;
 #pragma unroll
-          for (int k = 0; k < 5; ++k)
-            *reinterpret_cast<uint4*>(smem + kOffQ + k * kBlk + sw128_offset(r, 16 * (lane & 7))) =
-                make_uint4(scaled(v[k].x, f, k < 4), scaled(v[k].y, f, k < 4), scaled(v[k].z, f, k < 4), scaled(v[k].w, f, k < 4));
+            for (int k = 0; k < 5; ++k) {
+              if (k < 4)
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu)));
+              *reinterpret_cast<uint4*>(smem + kOffQ + k * kBlk + sw128_offset(r, 16 * (lane & 7))) =
+                  make_uint4(scaled(v[k].x, f, k < 4), scaled(v[k].y, f, k < 4), scaled(v[k].z, f, k < 4), scaled(v[k].w, f, k < 4));
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if ((lane & 7) == 0) largest[r] = m;
+          }
+          if (pass) break;
+          __syncwarp();
+          mx = __vmaxu2(__vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 16)), largest[row]);
+          const uint32_t amax = max(mx & 0xFFFFu, mx >> 16);
+          int e = 0;
+          if (amax >= 0x7F80u) {
+            if (mine) flag_error(p.err, HS_FLAG_RANGE);
+          } else if (amax >= 0x4700u || (amax >= 0x0080u && amax < 0x3C80u)) {
+            e = 14 - ((int)(amax >> 7) - 127);
+          } else if (amax > 0u && amax < 0x0080u) {
+            e = 126;
+          }
+          e = e < -126 ? -126 : (e > 126 ? 126 : e);
+          // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
+          coef = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
+          if (!__any_sync(0xffffffffu, e != 0)) break;
+          if (half == 0) scales[row] = __uint_as_float((uint32_t)(e + 127) << 23);
+          tmem_wait_st();
+          __syncwarp();
         }
         tmem_wait_st();
         tc_fence_before();
@@ -290,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&br.q_ready);
-      const float coef = idle ? 1.f : coefs[row];
 
       const int nsee = mine ? sees(p, s.q, (int64_t)s.b * kRows + row) : 0;
       const int first = first_page(s), end = end_page(p, s);
