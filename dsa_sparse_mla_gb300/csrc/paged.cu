@@ -682,7 +682,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       if (lane == 0) remote_arrive(r_qready);
       if (!ok) break;
 
-      const int nsee = mine ? sees(p, s.q, grow) : 0;
+      const int nsee = mine ? sees<kRows>(p, s.q, grow) : 0;
       float ref = -INFINITY, l = 0.f;
       const int32_t* bt = p.bt + (int64_t)s.r * p.bt_stride;
       int32_t next_k = ldg_nc_s32(bt + (2 * s.ta + g < p.bt_stride ? 2 * s.ta + g : 0));

@@ -26,12 +26,12 @@
 // per page tells the softmax warps, which then rescale O^T's columns. A latent value that is NaN or cannot be fp16 is zeroed
 // and its row's rotary values become NaN: rows that see it are NaN, P = 0 times it stays 0.
 //
-// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 569 us, 3,220 GB/s
-// of cache, 0.48 of a plain copy's rate; about 4,000 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
-// that pace (about 8,000 cycles for two slots): without the MMAs 3,150, without the producers' arithmetic 3,800. On
+// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 515 us, 3,560 GB/s
+// of cache, 0.53 of a plain copy's rate; about 3,630 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
+// that pace (two slots); at 4,170 cycles it took 3,150 without the MMAs and 3,800 without the producers' arithmetic. On
 // the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (the loads share too few
-// scoreboards and wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 29 us: about 3 us until
-// the shares are known, 7 for Q, 3 per page, 4 for the partial results (7 with 4-byte stores), the rest launches and the join.
+// scoreboards and wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 27 us: about 2 us until
+// the shares are known, 5 for Q, 2 to 3 per page, 4 for the partial results (7 with 4-byte stores), the rest launches and the join.
 #include "paged.cuh"
 
 namespace hs {
@@ -83,7 +83,7 @@ __host__ __device__ constexpr int producer_index(int w) {
 // Pages [first, end) of a segment: the last tile of a block may need only its first page.
 __device__ __forceinline__ int first_page(const Seg& s) { return 2 * s.ta; }
 __device__ __forceinline__ int end_page(const Params& p, const Seg& s) {
-  const int n = sees(p, s.q, (int64_t)s.b * kRows + s.nrows - 1);
+  const int n = sees<kRows>(p, s.q, (int64_t)s.b * kRows + s.nrows - 1);
   const int pages = n > 0 ? (n + kPageKeys - 1) / kPageKeys : 1;
   return 2 * s.tb < pages ? 2 * s.tb : pages;
 }
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&br.q_ready);
 
-      const int nsee = mine ? sees(p, s.q, (int64_t)s.b * kRows + row) : 0;
+      const int nsee = mine ? sees<kRows>(p, s.q, (int64_t)s.b * kRows + row) : 0;
       const int first = first_page(s), end = end_page(p, s);
       const int32_t* bt = p.bt + (int64_t)s.r * p.bt_stride;
       int32_t next_k = ldg_nc_s32(bt + (first < p.bt_stride ? first : 0));
