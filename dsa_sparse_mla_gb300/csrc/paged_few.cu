@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           for (int h = 0; h < 2; ++h) raw.code[g][h] = *reinterpret_cast<const uint2*>(mine + 128 * g + 64 * h + 8 * c8);
         raw.scale = *reinterpret_cast<const uint4*>(mine + HS_D_LATENT);
         raw.rope = *reinterpret_cast<const uint4*>(mine + HS_D_LATENT + 16 + 16 * c8);
+        fence_proxy_async_smem();  // these reads come before the next page's copy
         __syncwarp();
         if (lane == 0) mbar_arrive(&br.raw_free);
       };

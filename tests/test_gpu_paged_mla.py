@@ -289,3 +289,13 @@ def test_sizes_same_bits_each_time(size):
         assert flag == 0 and torch.equal(out, want) and torch.equal(l, lse)
     assert torch.equal(run(b, lse=False)[0], want)
     check(b)
+
+
+@pytest.mark.parametrize("H", [8, 64])
+def test_many_short_requests_again_and_again(H):
+    """Several blocks of one to four pages per SM, many times over: what is not ordered shows as bits that change."""
+    b = plain.make_batch([1 + (i % 3) for i in range(230)], [3 + (i * 37) % 200 for i in range(230)], H, seed=4)
+    want, lse = check(b)
+    for _ in range(150):
+        out, l, flag = run(b)
+        assert flag == 0 and torch.equal(out, want) and torch.equal(l, lse)
