@@ -53,6 +53,7 @@ constexpr int kOffBar = kOffRow + 4 * 256;
 struct Bars {
   uint64_t full[2][2];   // producers have written a half of a page's dims -> QK
   uint64_t free[2][2];   // PV has read a half (the second: and P) -> producers, softmax
+  uint64_t wide_done;    // a page's 128-row products of QK are complete (its issuer's own)
   uint64_t s_full[2];    // S complete -> softmax
   uint64_t s_empty[2];   // S read -> QK
   uint64_t p_full[2];    // P written, O^T rescaled -> PV
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       mbar_init(&br.drain[s], 1);
     }
     mbar_init(&br.q_ready, 4);
+    mbar_init(&br.wide_done, 1);
     mbar_init(&br.raw_full, 1);
     mbar_init(&br.raw_free, kProducers);
     mbar_fence_init();
@@ -576,6 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
             for (int g = 0; g < 4; ++g) {
               if ((g & 1) == 0) {
                 ok = ok && mbar_wait(&br.full[b][g >> 1], ph, p.err);
+                // products of different shapes on one accumulator are not kept in order by themselves
+                if (g == 2) ok = ok && mbar_wait(&br.wide_done, (uint32_t)i & 1u, p.err);
                 if (!ok) break;
                 tc_fence_after();
               }
@@ -588,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
                 else
                   mma_bf16_ss(d, qd + (uint64_t)(((blk - 4) * kBlk + (k % 4) * 32) >> 4), b16, k < 8 ? lat : rop, 1u);
               }
+              if (g == 1) mma_commit(&br.wide_done);
             }
             if (ok) mma_commit(&br.s_full[b]);
           }
