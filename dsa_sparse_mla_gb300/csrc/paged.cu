@@ -38,7 +38,7 @@
 //
 // Measured on a GB300 (events, inputs far larger than L2). copy, 2,048 tokens x 64 heads over 32,768 rows: 5.9 ms, 1,530
 // TFLOP/s, 0.80 of a bf16 matrix product's burst rate and 0.90 of its sustained rate; about 3,170 cycles per tile, of which QK's MMAs take
-// 2,304. raw, 64 requests x 4 tokens x 64 heads over 16-65 thousand rows: 1.37 ms, 967 TFLOP/s; about 4,400 cycles per
+// 2,304. raw, 64 requests x 4 tokens x 64 heads over 16-65 thousand rows: 1.10 ms, 1,210 TFLOP/s; about 3,500 cycles per
 // tile, the sum of hand-offs (codes -> producers -> K -> S -> P): no single unit is busy all the time, and
 // more or fewer producer warps, deeper code rings, whole pages as bulk copies and single or double P buffers change it by less
 // than 3 %.
@@ -900,6 +900,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
           }
         }
       }
+      fence_proxy_async_smem();  // the buffer's reads come before the next P's copy into it
       __syncwarp();
       if (lane == 0) mbar_arrive(&br.out_done);
       tc_fence_before();
@@ -960,6 +961,9 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       }
     } else if (lead && (warp == kIssue0 || (warp == kIssue1 && isA))) {
       // ================================================================ MMAs ======================
+      // The raw variant's loops over stages and steps are not unrolled: its roles' code shares the instruction caches, and 28 MMAs
+      // less of it make the whole kernel 19 % faster (64 requests x 4 tokens 1,350 -> 1,097 us). The copy variant, with fewer
+      // roles, is 20 % slower without unrolling (chunk 5.95 -> 7.2 ms).
       if (lane == 0) {
         const int mine = warp == kIssue0 ? 0 : 1;  // QK: the parity of the tiles that this warp issues
         const int slots = isA ? kStA : kStB;
@@ -1016,7 +1020,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
                 ok = false;
                 break;
               }
-#pragma unroll
+#pragma unroll (kRaw ? 1 : Sh::kStages)
               for (int k = 0; k < Sh::kStages; ++k) {
                 if (!stage()) {
                   ok = false;
@@ -1066,14 +1070,14 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
                 break;
               }
               const uint64_t pb = pd + (uint64_t)(((i & 1) * kPBuf) >> 4);
-#pragma unroll
+#pragma unroll (kRaw ? 1 : Sh::kVStages)
               for (int k = 0; k < Sh::kVStages; ++k) {
                 if (!stage()) {
                   ok = false;
                   break;
                 }
                 const uint64_t vb = vd + (uint64_t)((slot * kVStage) >> 4);
-#pragma unroll
+#pragma unroll (kRaw ? 4 : kKeys / 16)
                 for (int kk = 0; kk < kKeys / 16; ++kk)
                   tc2::ss(tmem + 128 * G * k, pb + (uint64_t)(((kk / 4) * (kPBuf / 2) + (kk % 4) * 32) >> 4),
                               vb + (uint64_t)((kk * 2048) >> 4), id, (jt > s.ta || kk > 0) ? 1u : 0u);
@@ -1209,15 +1213,14 @@ static uint64_t part_bytes(int sms) {
   return ((n > f ? n : f) + 15) / 16 * 16;
 }
 
-// Whether T tokens of B requests with H heads have rows enough for a dequantised copy to pay: when a request's rows make more
-// than one block on average, so that its cached rows are read more than once. Measured (raw / copy, us, 30,000 cached rows per
-// request): 64 requests x 256 rows 1,114 / 1,347; x 320 2,160 / 1,981; x 512 2,184 / 2,072; 32 x 1,024 2,184 / 1,794; 16 x 2,048
-// 2,181 / 1,663. With short caches the copy's extra launch and pass show longer: 8 x 512 rows over 2,000 53 / 64; 8 x 4,096
-// 199 / 177.
-static bool copies(int T, int B, int H) { return (int64_t)T * H > 256ll * B; }
+// Whether T tokens of B requests with H heads have rows enough for a dequantised copy to pay: when its cost, a pass over the cached
+// rows, is shared by more than three blocks of a request. Measured (raw / copy, us, 30,000 cached rows per request): 64
+// requests x 256 rows 893 / 1,346; x 512 1,806 / 2,097; 32 x 768 1,365 / 1,447; 32 x 1,024 1,816 / 1,813; 16 x 2,048 1,806 / 1,687. With
+// 2,000 cached rows: 8 x 512 58 / 67; x 1,024 62 / 60-68; x 2,048 107 / 110; x 4,096 181 / 174.
+static bool copies(int T, int B, int H) { return (int64_t)T * H > 768ll * B; }
 // Whether they have few enough for paged_few.cu: two of its blocks of 64 per request on average. Measured (us, this file's raw
-// variant / paged_few.cu): 64 requests x 64 rows over 30,000 cached rows 1,089 / 414; x 128 rows 1,093 / 794; x 144 (three
-// blocks) 1,125 / 1,143; 8 x 128 over 1,000 40 / 40; 64 x 128 over 200 47 / 54.
+// variant / paged_few.cu): 64 requests x 64 rows over 30,000 cached rows 860 / 380; x 128 rows 871 / 710; x 144 (three
+// blocks) 883 / 1,042; 8 x 128 over 1,000 42 / 34; 64 x 128 over 200 46 / 29.
 static bool few_rows(int T, int B, int H) { return (int64_t)T * H <= 128ll * B; }
 
 template <bool kRaw>

@@ -26,8 +26,8 @@
 // per page tells the softmax warps, which then rescale O^T's columns. A latent value that is NaN or cannot be fp16 is zeroed
 // and its row's rotary values become NaN: rows that see it are NaN, P = 0 times it stays 0.
 //
-// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 515 us, 3,560 GB/s
-// of cache, 0.53 of a plain copy's rate; about 3,630 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
+// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 527 us, 3,480 GB/s
+// of cache, 0.52 of a plain copy's rate; about 3,700 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
 // that pace (two slots); at 4,170 cycles it took 3,150 without the MMAs and 3,800 without the producers' arithmetic. On
 // the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (the loads share too few
 // scoreboards and wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 27 us: about 2 us until

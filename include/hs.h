@@ -564,7 +564,7 @@ typedef struct {
 hs_status hs_paged_mla_fwd(const hs_paged_mla_args* a, hs_stream_t stream);
 
 /* Bytes of workspace hs_paged_mla_fwd needs for these sizes on the current device: 40 MB for partial results, and,
- * where a request has more than 256 (token, head) rows on average (T * H > 256 * B), 1,152 bytes for each of
+ * where a request has more than 768 (token, head) rows on average (T * H > 768 * B), 1,152 bytes for each of
  * kv_tokens + 128 * B dequantised rows. */
 hs_status hs_paged_mla_workspace_size(int32_t T, int32_t B, int32_t H, int64_t kv_tokens, uint64_t* bytes);
 
