@@ -29,8 +29,8 @@
 // Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 527 us, 3,480 GB/s
 // of cache, 0.52 of a plain copy's rate; about 3,700 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
 // that pace (two slots); at 4,170 cycles it took 3,150 without the MMAs and 3,800 without the producers' arithmetic. On
-// the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (the loads share too few
-// scoreboards and wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 27 us: about 2 us until
+// the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (4,430 in one batch per
+// page: the loads seem to wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 27 us: about 2 us until
 // the shares are known, 5 for Q, 2 to 3 per page, 4 for the partial results (7 with 4-byte stores), the rest launches and the join.
 #include "paged.cuh"
 
