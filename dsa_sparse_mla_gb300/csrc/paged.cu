@@ -379,6 +379,7 @@ __device__ __forceinline__ void split_scales(const Params& p, uint8_t* smem, Bar
         out[(t * 4 + g) * kKeysHere + row] = make_uint2(*reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&l2));
       }
     }
+    fence_proxy_async_smem();  // the scales' reads come before the next copy over them
     __syncwarp();
     if (lane == 0) mbar_arrive(&br.split_full[t]);
   }
