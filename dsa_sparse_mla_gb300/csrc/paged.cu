@@ -642,10 +642,20 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
           e = 126;
         }
         e = e < -126 ? -126 : (e > 126 ? 126 : e);
-        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-        // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
-        coef = fmaxf(coef * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
         const uint8_t* own = base + myrow * (HS_D_QK * 2);
+        if (__any_sync(0xffffffffu, e > 0)) {  // rare: the rotary values go along
+          uint32_t m = 0u;
+#pragma unroll 1
+          for (int h = 0; h < 8; ++h) {
+            const uint4 v = ldg_nc_v4(own + 1024 + 16 * h);
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+          }
+          e = query_exponent(e, max(m & 0xFFFFu, m >> 16));
+        }
+        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+        // not 0, so that a masked column stays -inf (softmax scales next to 0, or rows that are tiny in both parts: their logits
+        // stay below 2^-60 and do not show)
+        coef = fmaxf(coef * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
         if (__any_sync(0xffffffffu, e != 0)) {  // rare: again, each thread its row
 #pragma unroll 1
           for (int b = 0; b < 8; ++b) {

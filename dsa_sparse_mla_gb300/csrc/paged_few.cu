@@ -287,7 +287,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
             e = 126;
           }
           e = e < -126 ? -126 : (e > 126 ? 126 : e);
-          // not 0, so that a masked column stays -inf; logits below 2^-60 or so do not show anyway
+          if (__any_sync(0xffffffffu, e > 0)) {  // rare: the rotary values go along
+            uint32_t m = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 v = ldg_nc_v4(own + 1024 + 16 * k);
+              m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            }
+            m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            e = query_exponent(e, max(m & 0xFFFFu, m >> 16));
+          }
+          // not 0, so that a masked column stays -inf (softmax scales next to 0, or rows that are tiny in both parts: their
+          // logits stay below 2^-60 and do not show)
           coef = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 7.5e-37f);
           if (!__any_sync(0xffffffffu, e != 0)) break;
           if (half == 0) scales[row] = __uint_as_float((uint32_t)(e + 127) << 23);
