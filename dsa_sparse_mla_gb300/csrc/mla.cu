@@ -673,6 +673,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             else if (amax > 0u && amax < 0x0080u) e = 126;  // bf16 subnormals only
             if (qrow >= p.H) e = 0;  // rows of the next query (or beyond the tensor): not computed here
             e = e < -126 ? -126 : (e > 126 ? 126 : e);
+            if (__any_sync(0xffffffffu, e > 0)) {  // rare: the rotary values go along (see query_exponent)
+              uint32_t m = 0u;
+              if (e > 0) {
+                const uint4 v = ldg_nc_v4(reinterpret_cast<const uint8_t*>(p.q) + (q * p.H + qrow) * HS_D_QK * 2 + 1024 + 16 * (sm_tid & 7));
+                m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+              }
+#pragma unroll
+              for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+              e = query_exponent(e, max(m & 0xFFFFu, m >> 16));
+            }
             if ((sm_tid & 7) == 0) {
               sQe[qrow] = e;
               sC[qrow] = p.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
