@@ -287,9 +287,11 @@ class DenseSession:
         self.refcount = torch.zeros(nblk, **i32)
         self.src, self.dst = torch.empty(nblk, **i32), torch.empty(nblk, **i32)
         self.counts, self.err = torch.zeros(2, **i32), torch.zeros(1, **i32)
-        inv, self.rope_scale = hs_rope_inv_freq(64, base, kind, factor)
+        inv, temperature = hs_rope_inv_freq(64, base, kind, factor)
         self.inv_freq = inv.to(device)
-        self.softmax_scale = 1.0 / 24.0
+        # YaRN's factor is one of the whole query and key; only 64 of their 576 values are turned, so its square goes with the
+        # softmax scale and the rotation takes none
+        self.rope_scale, self.softmax_scale = 1.0, temperature ** 2 / 24.0
         self.kv_tokens = min(B * pages, 2 ** 25 - 1) * 64  # shared pages count once per request
         # a batch of fewer tokens may need the room of a longer one: the dequantised rows are used from some size on
         self.workspace = torch.empty(hs_paged_mla_workspace_size(max_tokens, B, H, self.kv_tokens), dtype=torch.uint8, device=device)

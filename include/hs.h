@@ -504,7 +504,9 @@ hs_status hs_rope(const hs_rope_args* a, hs_stream_t stream);
  *   HS_ROPE_LINEAR  every angle divided by factor, scale 1
  *   HS_ROPE_YARN    pairs that turn more than beta_fast times within `original` positions are kept, those
  *                   that turn less than beta_slow times are divided by factor, a linear ramp over the pair's
- *                   index between; scale = 0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023) */
+ *                   index between; scale = 0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023). It is meant for every
+ *                   value of query and key: where only a part of a head is turned, turn it with scale 1 and multiply
+ *                   the softmax scale by its square instead */
 #define HS_ROPE_PLAIN 0
 #define HS_ROPE_LINEAR 1
 #define HS_ROPE_YARN 2
