@@ -274,7 +274,8 @@ class DenseSession:
     device state for ``B`` request slots and ``L`` layers, and the calls of a step in their order. ``extend`` gives the new
     tokens their positions and pages, then ``attend`` runs once per layer (hs_rope of queries and keys -> hs_kv_append ->
     hs_paged_mla_fwd). Between steps ``fork`` makes slots copies of others (pages shared, the partial one copied), ``free``
-    empties slots, and ``compact`` moves the pages in use to the front. Everything runs on the current stream."""
+    empties slots, and ``compact`` moves the pages in use to the front. Everything runs on the current stream. The attention's
+    workspace is made for steps of ``max_tokens`` and grows with the cached rows, or where a step has more tokens."""
 
     def __init__(self, B: int, H: int, nblk: int, pages: int, L: int = 1, max_tokens: int = 4096, base: float = 10000.0,
                  kind: str = "plain", factor: float = 1.0, device="cuda"):
@@ -292,10 +293,18 @@ class DenseSession:
         # YaRN's factor is one of the whole query and key; only 64 of their 576 values are turned, so its square goes with the
         # softmax scale and the rotation takes none
         self.rope_scale, self.softmax_scale = 1.0, temperature ** 2 / 24.0
-        self.kv_tokens = min(B * pages, 2 ** 25 - 1) * 64  # shared pages count once per request
-        # a batch of fewer tokens may need the room of a longer one: the dequantised rows are used from some size on
-        self.workspace = torch.empty(hs_paged_mla_workspace_size(max_tokens, B, H, self.kv_tokens), dtype=torch.uint8, device=device)
+        self.kv_tokens = 0  # cached rows: shared pages count once per request
+        self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
+        self._make_room(max_tokens, 0)
         self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
+
+    def _make_room(self, tokens: int, cached: int):
+        """A workspace for a step of this many tokens over this many rows. A larger one is made with a quarter to spare, so that a
+        growing cache does not make one at every step."""
+        need = hs_paged_mla_workspace_size(tokens, self.B, self.H, cached)
+        if self.workspace.numel() < need:
+            self.workspace = torch.empty(0, dtype=torch.uint8, device=self.device)  # its memory may serve the larger one
+            self.workspace = torch.empty(need + need // 4, dtype=torch.uint8, device=self.device)
 
     def extend(self, new) -> int:
         """``new[r]`` more tokens for slot r: takes free pages where they need some; returns the number of tokens. Tokens are
@@ -307,6 +316,9 @@ class DenseSession:
         free = (self.refcount <= 0).nonzero()[:, 0][:int(take.sum())].int()
         if int(take.sum()) > free.numel() or int(after.max()) > 64 * self.table.shape[1]:
             raise RuntimeError("the cache has too few pages")
+        cached = int(after.sum())
+        self._make_room(int(new.sum()), cached)
+        self.kv_tokens = cached
         self.table[take] = free
         self.refcount[free.long()] = 1
         self.token_req = torch.repeat_interleave(torch.arange(self.B, dtype=torch.int32, device=self.device), new)
