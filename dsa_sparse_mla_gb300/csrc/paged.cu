@@ -216,7 +216,7 @@ struct Bars {
   uint64_t split_empty[2];        // raw: both groups of producers are done with them
   uint64_t s_full[2];             // S complete (both)
   uint64_t s_empty[2];            // issuing softmax CTA: all softmax warps have read S
-  uint64_t p_empty[2];            // softmax CTA: its P buffer and staging are free
+  uint64_t p_empty[2];            // softmax CTA: its P buffer and staging are free (a phase per tile of a block in which it has rows)
   uint64_t p_full[2];             // output CTA: P and the factors have landed
   uint64_t corr[2];               // issuing output CTA: O is rescaled for this P (both)
   uint64_t pv_done[2];            // PV complete (both)
@@ -568,6 +568,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
     float* salpha = (float*)(smem + kOffAlpha);
     float* ssum = (float*)(smem + kOffSum);
     int n = 0, i = 0, x = 0;  // x: exchanges through smax, alternating halves
+    uint32_t skipped = 0;     // bit b: whether the tiles in buffer b that had no phase of p_empty[b] are odd in number
     bool ok = true;
     // The row's two threads give each other a value. The wait is bounded like every other (ok turns false).
     auto other = [&](float v) -> float {
@@ -710,6 +711,9 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
         if (idle) {
           __syncwarp();
           if (lane == 0) remote_arrive_relaxed(r_sempty + 8 * (uint32_t)b);
+          // Where this CTA has rows, its other warps wait for p_empty's phase, and all of them before the next block's first S;
+          // where it has none, there is no phase that a later wait could take for its own.
+          if (have <= 0) skipped ^= 1u << b;
           continue;
         }
         const bool there = page < p.bt_stride && k >= 0 && ((int64_t)k + 1) * HS_PAGE <= p.R;
@@ -751,7 +755,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
         l *= al;
         ref = to_ref;
         const float me = ref == -INFINITY ? 0.f : ref;
-        ok = warp_wait_all(&p_empty[b], ph, p.err);
+        ok = warp_wait_all(&p_empty[b], ph ^ ((skipped >> b) & 1u), p.err);
         if (!ok) break;
         uint8_t* blk = smem + kOffStage + b * kPBuf + g * (kPBuf / 2);
         // P of 32 columns; masked columns are -inf and coef > 0: their P is 0
@@ -1186,7 +1190,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
               break;
             }
             mbar_arrive_expect_tx(&p_full[i & 1], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
-            remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));
+            if (quads) remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));  // without rows nobody would see the phase
             ends = (ends | (jt == s.tb - 1 ? 1u : 0u)) << 1;
           }
         }
