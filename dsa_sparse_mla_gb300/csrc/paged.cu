@@ -77,7 +77,7 @@ constexpr int kOffV = 2 * kPBuf;
 constexpr int kOffAlpha = 14 * 16384;          // float [2][128]: staging, and at the same place of the output CTA
 constexpr int kOffSum = kOffAlpha + 1024;      // float [2][128]
 constexpr int kOffBar = kOffSum + 1024;
-constexpr int kNumBars = 56;
+constexpr int kNumBars = 58;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 constexpr int kSmem = kOffMisc + 128;
 constexpr int kOffScratch = kOffK;             // int64 [B + 1] and int32 [B + 1] during the set-up
@@ -223,7 +223,7 @@ struct Bars {
   uint64_t q_ready;               // issuing softmax CTA: Q is in place (both)
   uint64_t q_free;                // the block's QK MMAs have read Q (both)
   uint64_t o_free;                // issuing output CTA: O is read out (both)
-  uint64_t out_done;              // output CTA: a block's output has left the P buffer of its last tile
+  uint64_t out_done[2];           // output CTA: a block's output has left the P buffer of its last tile
   uint64_t drain[2];
   uint64_t swap[4];               // softmax CTA: the two warps of a lane quarter have written their values
 };
@@ -527,11 +527,11 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       mbar_init(&p_full[s], 1);
       mbar_init(&corr[s], G);
       mbar_init(&pv_done[s], 1);
+      mbar_init(&br.out_done[s], 8);
     }
     mbar_init(q_ready, 8 * G);
     mbar_init(q_free, 2);
     mbar_init(o_free, 8 * G);
-    mbar_init(&br.out_done, 8);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     for (int q = 0; q < 4; ++q) mbar_init(&swap[q], 2);
@@ -917,7 +917,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       }
       fence_proxy_async_smem();  // the buffer's reads come before the next P's copy into it
       __syncwarp();
-      if (lane == 0) mbar_arrive(&br.out_done);
+      if (lane == 0) mbar_arrive(&br.out_done[i & 1]);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) remote_arrive_relaxed(r_ofree);
@@ -1175,8 +1175,11 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
       // 32 rows, at a block's last tile 128 bytes of sums), then hands it to the softmax CTA.
       if (lane == 0) {
         const uint32_t back = remote_smem(p_empty, rank - G);
-        int i = 0, n = 0;   // tiles; blocks whose output has passed through a P buffer
+        int i = 0;          // tiles
         uint32_t ends = 0;  // bit j: the tile j before this one ended a block
+        // bit b: parity of the next block whose output passes through buffer b. A barrier per buffer: the next phase needs a tile
+        // that is armed after this wait, so it cannot be over before the wait has seen the one before.
+        uint32_t outs = 0;
         bool ok = true;
 #pragma unroll 1
         while (ok && walk.next(p, s)) {
@@ -1184,13 +1187,15 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
           const uint32_t quads = left <= 0 ? 0 : left >= kHalf ? 4 : (uint32_t)(left + 31) / 32;
 #pragma unroll 1
           for (int jt = s.ta; jt < s.tb; ++jt, ++i) {
-            if (i >= 2 && (*abort_flag || !mbar_wait(&pv_done[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err) ||
-                           ((ends & 4u) && !mbar_wait(&br.out_done, (uint32_t)n++ & 1u, p.err)))) {
+            const int b = i & 1;
+            if (i >= 2 && (*abort_flag || !mbar_wait(&pv_done[b], ((uint32_t)(i >> 1) & 1u) ^ 1u, p.err) ||
+                           ((ends & 4u) && !mbar_wait(&br.out_done[b], (outs >> b) & 1u, p.err)))) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&p_full[i & 1], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
-            if (quads) remote_arrive_relaxed(back + 8 * (uint32_t)(i & 1));  // without rows nobody would see the phase
+            if (ends & 4u) outs ^= 1u << b;
+            mbar_arrive_expect_tx(&p_full[b], quads * (8192u + 128u + (jt == s.tb - 1 ? 128u : 0u)));
+            if (quads) remote_arrive_relaxed(back + 8 * (uint32_t)b);  // without rows nobody would see the phase
             ends = (ends | (jt == s.tb - 1 ? 1u : 0u)) << 1;
           }
         }

@@ -26,3 +26,10 @@ def test_blocks_without_rows_in_one_half(name, low, high, tokens, requests):
     q = [tokens[i % len(tokens)] for i in range(requests)]
     kv = [max(m, 3 + (i * 37) % 300) for i, m in enumerate(q)]
     again_and_again(plain.make_batch(q, kv, 16, seed=41), low, high)
+
+
+@pytest.mark.parametrize("name,low,high,tokens,requests", [("some", 128, 768, [16, 32, 48, 20], 230), ("many", 768, 1 << 30, [64, 48, 120], 96)])
+def test_blocks_of_one_tile(name, low, high, tokens, requests):
+    """Blocks that end with the tile they begin with, one after the other: every tile's P buffer also passes an output on."""
+    q = [tokens[i % len(tokens)] for i in range(requests)]
+    again_and_again(plain.make_batch(q, [max(m, 5 + (i * 29) % 124) for i, m in enumerate(q)], 16, seed=42), low, high)
