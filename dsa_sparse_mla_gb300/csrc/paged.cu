@@ -270,7 +270,7 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
   prefetch_tensormap(scales);
   Ring ring = {0, 1};
   int64_t issued = 0;
-  int tile = 0;
+  int tile = 0, rotaries = 0;
   bool ok = true;
   Seg s;
   // block-table entries of the next tile, read one tile ahead
@@ -336,6 +336,7 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
       if (ok) {
         mbar_arrive_expect_tx(&br.full[kRotaryBar + t], Sh::kKBlk);
         tma_load_2d(smem + Sh::kOffRotary + t * Sh::kKBlk, rotary, &br.full[kRotaryBar + t], (HS_D_LATENT + 16) / 2, y[0]);
+        ++rotaries;
       }
     }
   }
@@ -344,6 +345,9 @@ __device__ __forceinline__ void load_raw(const Params& p, uint8_t* smem, Bars& b
   for (int q = 0; q < kSlots; ++q)
     if (q < issued) mbar_wait(&br.codes_full[q], q < ring.slot ? ring.par ^ 1u : ring.par, p.err);
   for (int u = tile > 2 ? tile - 2 : 0; u < tile; ++u) mbar_wait(&br.scale_full[u & 1], (uint32_t)(u >> 1) & 1u, p.err);
+  // (full also counts the other CTA's word, which an abort may leave out: the wait's limit then gives the copy its time)
+  for (int u = rotaries > 2 ? rotaries - 2 : 0; u < rotaries; ++u)
+    mbar_wait(&br.full[kRotaryBar + (u & 1)], (uint32_t)(u >> 1) & 1u, p.err);
 }
 
 // raw: one warp splits every scale of a tile into two fp16 parts (see dequant8), each twice in a 32-bit word, for the
@@ -1200,6 +1204,9 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
           }
         }
         if (!ok) *abort_flag = 1;
+        // every P and factor that was sent has landed before the CTA may leave: an armed buffer is sent to once, and those before
+        // the last two have been used (after an abort a part may never be sent: the wait's limit then gives the rest its time)
+        for (int u = i > 2 ? i - 2 : 0; u < i; ++u) mbar_wait(&p_full[u & 1], (uint32_t)(u >> 1) & 1u, p.err);
       }
     } else if (kRaw && warp == (!isA ? kScaleWarpB : lead ? kRelayWarp : kIssue0)) {
       // ================================================================ scales ====================
