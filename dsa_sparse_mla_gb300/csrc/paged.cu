@@ -43,8 +43,8 @@
 // more or fewer producer warps, deeper code rings, whole pages as bulk copies and single or double P buffers change it by less
 // than 3 %.
 //
-// Lazy maximum: a row's reference max moves only when a logit exceeds it by more than 2^8 (P stays below 2^8, well
-// inside fp16); then its factor goes along with P and O's row is rescaled. Masked columns are selected away before the
+// Lazy maximum: a row's reference max moves only when a logit exceeds it by more than 2^8 (P, held 2^7 times as large, stays
+// below 2^15, inside fp16); then its factor goes along with P and O's row is rescaled. Masked columns are selected away before the
 // maximum and the exponential, so what they hold does not matter; V values that fp16 cannot hold are zeroed, so that P = 0
 // times them is 0, while K keeps them (the copy: a NaN in the rotary part), so that rows that see them are NaN.
 #include <atomic>
@@ -758,7 +758,7 @@ __global__ void __cluster_dims__(2 * G, 1, 1) __launch_bounds__(Shape<kRaw>::kTh
         const float al = up ? fast_exp2(ref - to_ref) : 1.f;
         l *= al;
         ref = to_ref;
-        const float me = ref == -INFINITY ? 0.f : ref;
+        const float me = ref == -INFINITY ? 0.f : ref - kLift;
         ok = warp_wait_all(&p_empty[b], ph ^ ((skipped >> b) & 1u), p.err);
         if (!ok) break;
         uint8_t* blk = smem + kOffStage + b * kPBuf + g * (kPBuf / 2);

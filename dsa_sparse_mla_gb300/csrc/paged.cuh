@@ -9,6 +9,10 @@ namespace paged {
 
 constexpr int kKeys = 128;                     // cached rows per tile: two pages
 constexpr float kThreshold = 8.0f;             // log2 units
+// P is held 2^7 times as large, and so are its sums: up to 2^15 with a reference that lags by the threshold. fp16's smallest step,
+// 2^-24, is then 2^-31 of the reference. Without it weights below 2^-25 were lost from P but not from the sum: 262,144 weights
+// of 2^-25.25 beside one large one, 0.65 % together, left nothing in the output.
+constexpr float kLift = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kScaleMax = 65504.f / 448.f;   // |code * scale| stays finite in fp16

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
           }
         }
         if (!idle) {
-          const float me = ref == -INFINITY ? 0.f : ref;
+          const float me = ref == -INFINITY ? 0.f : ref - kLift;
           float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int z = 0; z < 16; ++z) {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const Params p) {
       if (half == 0) {
         inverse[row] = sum == 0.f ? 0.f : 1.f / sum;
         if (mine) {
-          const float z = sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref) + log2f(sum)) * kLn2;
+          const float z = sum == 0.f ? -INFINITY : ((ref == -INFINITY ? 0.f : ref - kLift) + log2f(sum)) * kLn2;
           if (!whole)
             p.part_lse[part * kRows + row] = z;
           else if (p.lse)

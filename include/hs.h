@@ -527,7 +527,8 @@ hs_status hs_rope_inv_freq(int32_t rot, double base, int32_t kind, double factor
  *
  * Compute precision as hs_sparse_mla_fwd: rows dequantised to fp16 (one rounding of code * scale), q
  * latent part fp16 (a row of q whose largest value fp16 cannot hold well is scaled by a power of two), RoPE
- * part bf16, P fp16, accumulation, maxima and sums fp32, partial results of a split request fp32. A group
+ * part bf16, P fp16 (steps of 2^-31 of the largest weight at most for the smallest ones), accumulation, maxima and
+ * sums fp32, partial results of a split request fp32. A group
  * scale outside [2^-14, 146] or a latent q value that is not finite sets HS_FLAG_RANGE; the result is then
  * not reliable for the tokens that see that row. A latent code that is NaN makes the outputs of the tokens that see
  * its row NaN; rows that a token does not see never reach its output, whatever they hold.

@@ -1,8 +1,12 @@
-"""hs_paged_mla_fwd where 16-bit operands run out of range: queries whose latent part is far below their rotary part. Every test
-runs in all three variants (by rows per request)."""
+"""hs_paged_mla_fwd where 16-bit operands run out of range: queries whose latent part is far below their rotary part, and caches
+so long that many small weights count together. Every test runs in all three variants (by rows per request)."""
+import math
+
 import pytest
+import torch
+
 import plain_ops as plain
-from test_gpu_paged_mla import check
+from test_gpu_paged_mla import check, run
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +41,31 @@ def test_small_parts_under_a_large_scale(size):
     b["q"][..., 512:] = (b["q"][..., 512:].double() * 2.0 ** -97).bfloat16()
     b["scale"] = 2.0 ** 96
     check(b)
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+def test_many_small_weights(size):
+    """The first row has nearly all the weight and a latent part of zeros; each of the others has 2^-25.25 of it, together 0.65 %,
+    and ones. Enough requests that a block's rows are not spread over all SMs. All pages after the first are one page."""
+    H, n = 16, 1 << 18
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    m, B = {"few": (4, sms), "some": (16, sms // 4), "many": (64, sms // 16)}[size]
+    assert in_size(size, m * B, B, H)
+    rows = torch.zeros((128, 656), dtype=torch.uint8)
+    rows[1:, :512] = 0x38                                                                  # 1.0
+    rows[:, 512:528] = torch.ones((128, 4)).view(torch.uint8)
+    rows[0, 528:530] = torch.tensor([25.25], dtype=torch.bfloat16).view(torch.uint8)
+    table = torch.ones((B, n // 64), dtype=torch.int32)
+    table[:, 0] = 0
+    q = torch.zeros((m * B, H, 576), dtype=torch.bfloat16)
+    q[..., 512] = 1.0
+    b = dict(q=q.cuda(), pool=rows.cuda(), table=table.cuda(), kv_tokens=B * n, scale=math.log(2.0),
+             req_start=(torch.arange(B + 1, dtype=torch.int32) * m).cuda(), seq_len=torch.full((B,), n, dtype=torch.int32).cuda())
+    out, lse, flag = run(b, causal=False)
+    assert flag == 0
+    tail = (n - 1) * 2.0 ** -25.25
+    want = tail / (1.0 + tail)
+    # a weight is off by half of fp16's smallest step, 2^-25, of a reference held 2^7 above one; sums over 2^12 pages
+    # and the result's rounding: 2^-12 and 2^-8 of the value
+    assert float((out.double() - want).abs().max()) <= want * (2.0 ** -8 + 2.0 ** -12) + n * 2.0 ** -32
+    assert float((lse.double() - math.log(2.0 ** 25.25 + n - 1)).abs().max()) <= 2.0 ** -12 + 2.0 ** -20 * 17.5
