@@ -75,7 +75,7 @@ __device__ __forceinline__ int block_rows(const Params& p, const Req& q, int b) 
 template <int kRows>
 __device__ __forceinline__ int block_tiles(const Params& p, const Req& q, int b) {
   const int n = sees<kRows>(p, q, (int64_t)b * kRows + block_rows<kRows>(p, q, b) - 1);
-  return n > 0 ? (n + kKeys - 1) / kKeys : 1;  // a block that sees nothing still writes its zeros
+  return n > 0 ? (int)(((uint32_t)n + kKeys - 1) / kKeys) : 1;  // a block that sees nothing still writes its zeros
 }
 
 __host__ __device__ __forceinline__ int64_t unit_begin(int64_t c, int64_t U, int64_t C) { return c * U / C; }
@@ -104,7 +104,7 @@ struct Start {
 
 // Rows that a request takes in the dequantised copy: whole tiles, one at least (zeros), none without new tokens.
 __device__ __forceinline__ int64_t copy_rows(const Req& q) {
-  return q.m == 0 ? 0 : q.seq == 0 ? kKeys : (int64_t)(q.seq + kKeys - 1) / kKeys * kKeys;
+  return q.m == 0 ? 0 : q.seq == 0 ? kKeys : (int64_t)(((uint32_t)q.seq + kKeys - 1) / kKeys) * kKeys;
 }
 
 // A cluster's units as segments: consecutive tiles [ta, tb) of one block.

@@ -85,7 +85,7 @@ __host__ __device__ constexpr int producer_index(int w) {
 __device__ __forceinline__ int first_page(const Seg& s) { return 2 * s.ta; }
 __device__ __forceinline__ int end_page(const Params& p, const Seg& s) {
   const int n = sees<kRows>(p, s.q, (int64_t)s.b * kRows + s.nrows - 1);
-  const int pages = n > 0 ? (n + kPageKeys - 1) / kPageKeys : 1;
+  const int pages = n > 0 ? (int)(((uint32_t)n + kPageKeys - 1) / kPageKeys) : 1;
   return 2 * s.tb < pages ? 2 * s.tb : pages;
 }
 

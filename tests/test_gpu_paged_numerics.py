@@ -69,3 +69,27 @@ def test_many_small_weights(size):
     # and the result's rounding: 2^-12 and 2^-8 of the value
     assert float((out.double() - want).abs().max()) <= want * (2.0 ** -8 + 2.0 ** -12) + n * 2.0 ** -32
     assert float((lse.double() - math.log(2.0 ** 25.25 + n - 1)).abs().max()) <= 2.0 ** -12 + 2.0 ** -20 * 17.5
+
+
+@pytest.mark.parametrize("m", [1, 16])
+def test_longest_length(m):
+    """2^31 - 64 cached rows, the most that a table of 2^25 - 1 pages holds (here one page, over and over): tiles count up to the
+    last row. All rows are alike, and their values powers of two, so that sums stay exact."""
+    H, n = 16, 2 ** 31 - 64
+    g = torch.Generator().manual_seed(33)
+    row = torch.zeros(656, dtype=torch.uint8)
+    value = torch.randint(-3, 4, (512,), generator=g)
+    latent = torch.ldexp(torch.where(torch.rand(512, generator=g) < 0.5, -1.0, 1.0), value)
+    row[:512] = latent.to(torch.float8_e4m3fn).view(torch.uint8)
+    row[512:528] = torch.ones(4).view(torch.uint8)
+    row[528:] = torch.full((64,), 0.5, dtype=torch.bfloat16).view(torch.uint8)
+    b = dict(q=torch.randn((m, H, 576), generator=g).bfloat16().cuda(), pool=row.expand(64, 656).contiguous().cuda(),
+             table=torch.zeros((1, n // 64), dtype=torch.int32, device="cuda"), kv_tokens=n, scale=1.0 / 24.0,
+             req_start=torch.tensor([0, m], dtype=torch.int32, device="cuda"),
+             seq_len=torch.tensor([n], dtype=torch.int32, device="cuda"))
+    out, lse, flag = run(b, causal=False)
+    assert flag == 0
+    want = latent.double().cuda()
+    assert bool(((out.double() - want).abs() <= want.abs() * 2.0 ** -8).all())
+    logit = (b["q"].double() @ torch.cat([want, torch.full((64,), 0.5, device="cuda", dtype=torch.float64)])) / 24.0
+    assert float((lse.double() - logit - math.log(n)).abs().max()) <= 2.0 ** -11
