@@ -209,7 +209,7 @@ cudaError_t launch_rope(const hs_rope_args* a, int sms, cudaStream_t stream) {
   int per = 1;
   while (per < 8 && 2 * per * units <= 8 * kThreads && (int64_t)a->T >= 16LL * per * sms) per *= 2;
   p.per_cta = per;
-  const unsigned grid = (unsigned)((a->T + per - 1) / per);
+  const unsigned grid = ((unsigned)a->T + per - 1) / per;
   const size_t smem = (size_t)per * p.half * sizeof(float2);
   const bool il = a->interleaved != 0;
   switch (a->dtype) {
