@@ -364,37 +364,6 @@ __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t
   return row * 128u + ((((byte_in_row >> 4) ^ (row & 7u)) << 4) | (byte_in_row & 15u));
 }
 
-// The exponent e by which a query's row is scaled (2^e) so that its latent values fit fp16, given the largest of its rotary
-// values (|bf16| bits), which are scaled along. Where e would carry that value past 2^21, it is cut to what does not, though
-// not below 0: the logits stay finite, and their scale back (2^-e) a normal number. Latent values that e then leaves
-// below fp16's smallest step, 2^-25, are 2^-45 of the rotary ones: next to them they do not show in an fp32 sum.
-__device__ __forceinline__ int query_exponent(int e, uint32_t rotary) {
-  const int room = 20 - ((int)(rotary >> 7) - 127);
-  return e <= 0 || e <= room ? e : (room > 0 ? room : 0);
-}
-
-// ---------------------------------------------------------------- launches in a row -------
-// A call's second kernel may be launched while its first still runs (launch_next), so that its blocks stand ready when the first
-// ends: the first lets it (let_next), the second waits for the first's end and its writes before it reads or writes
-// anything (after_previous). The first kernel of a call, and whatever the caller enqueues next, start as usual.
-__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... P, typename... A>
-inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // ---------------------------------------------------------------- host: tensor maps -------
 // cuTensorMapEncodeTiled is a driver-API entry point. It is looked up through the runtime on
 // first use, so the library itself does not link libcuda and loads on machines without a driver.

@@ -54,6 +54,7 @@
 // A query split between CTAs leaves, from each, a normalised partial and its LSE in the workspace;
 // mla_merge_kernel combines them (split-KV decode: DCP's log-sum-exp merge on one GPU).
 #include "common.cuh"
+#include "query.cuh"
 
 namespace hs {
 namespace mla {

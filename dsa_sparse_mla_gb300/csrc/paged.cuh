@@ -3,6 +3,8 @@
 #pragma once
 
 #include "cluster.cuh"
+#include "launch.cuh"
+#include "query.cuh"
 
 namespace hs {
 namespace paged {

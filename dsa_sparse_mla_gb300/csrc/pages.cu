@@ -18,6 +18,7 @@
 // 133 pages 13 us (count 2.5, plan 4.5, moves 8.5 one after the other; 15.6 without launching each before the one before it
 // ends, which costs the host 1.5 us per launch: small forks, bound by the host, are slower with it, 44 against 41 us).
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace hs {
 namespace pages {
