@@ -74,7 +74,9 @@ __device__ __forceinline__ void bulk_s2remote(uint32_t dst, const void* src, uin
 }
 
 // mbarrier.arrive with its default semantics (release at CTA scope) on another CTA's barrier: for handing on what
-// a barrier of this CTA has just shown complete.
+// a barrier of this CTA has just shown complete (here: operands in its own shared memory, fenced for the async proxy by those who
+// wrote them). Released and acquired at cluster scope instead, 64 requests x 4 tokens take 1.98 ms, not 1.14, a chunk of 2,048 tokens
+// 7.5, not 6.4.
 __device__ __forceinline__ void remote_arrive_cta(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -36,9 +36,9 @@
 // 4-11, which rescale O and write the result: thread = row and 256 of O's columns. raw adds a warp that splits scales and the
 // producers (warps 12-19).
 //
-// Measured on a GB300 (events, inputs far larger than L2). copy, 2,048 tokens x 64 heads over 32,768 rows: 5.9 ms, 1,530
-// TFLOP/s, 0.80 of a bf16 matrix product's burst rate and 0.90 of its sustained rate; about 3,170 cycles per tile, of which QK's MMAs take
-// 2,304. raw, 64 requests x 4 tokens x 64 heads over 16-65 thousand rows: 1.10 ms, 1,210 TFLOP/s; about 3,500 cycles per
+// Measured on a GB300 (events, inputs far larger than L2). copy, 2,048 tokens x 64 heads over 32,768 rows: 6.1 to 6.4 ms,
+// 1,420 to 1,490 TFLOP/s, 0.72 to 0.76 of a bf16 matrix product's burst rate and 0.80 to 0.84 of its sustained rate; about 3,170 cycles per tile, of which QK's MMAs take
+// 2,304. raw, 64 requests x 4 tokens x 64 heads over 16-65 thousand rows: 1.15 ms, 1,155 TFLOP/s; about 3,600 cycles per
 // tile, the sum of hand-offs (codes -> producers -> K -> S -> P): no single unit is busy all the time, and
 // more or fewer producer warps, deeper code rings, whole pages as bulk copies and single or double P buffers change it by less
 // than 3 %.

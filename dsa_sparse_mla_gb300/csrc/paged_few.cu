@@ -26,11 +26,11 @@
 // per page tells the softmax warps, which then rescale O^T's columns. A latent value that is NaN or cannot be fp16 is zeroed
 // and its row's rotary values become NaN: rows that see it are NaN, P = 0 times it stays 0.
 //
-// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 527 us, 3,480 GB/s
-// of cache, 0.52 of a plain copy's rate; about 3,700 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
+// Measured on a GB300 (events, inputs far larger than L2): 32 requests x 64 heads over 30-131 thousand rows 546 to 556 us,
+// 3,330 GB/s of cache, 0.50 of a plain copy's rate; about 3,800 cycles per page. The chain fill -> QK -> softmax -> PV of a page's slot sets
 // that pace (two slots); at 4,170 cycles it took 3,150 without the MMAs and 3,800 without the producers' arithmetic. On
 // the way: eight producer warps 5,450 cycles; rows loaded straight into registers 4,600 (4,430 in one batch per
-// page: the loads seem to wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 27 us: about 2 us until
+// page: the loads seem to wait for each other); four hand-overs per page 4,750. 8 requests over 200-2,000 rows 28 us: about 2 us until
 // the shares are known, 5 for Q, 2 to 3 per page, 4 for the partial results (7 with 4-byte stores), the rest launches and the join.
 #include "paged.cuh"
 

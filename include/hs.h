@@ -462,8 +462,9 @@ hs_status hs_kv_offload(const hs_kv_offload_args* a, hs_stream_t stream);
  *   (a, b) -> scale * (a cos theta - b sin theta, a sin theta + b cos theta)
  * (a, b) are values (2i, 2i + 1) of the rotary part (interleaved != 0) or (i, i + rot / 2).
  * inverse != 0 turns by -theta (undoing a rotation; the gradient's direction). Arithmetic is fp32,
- * rounded once to the type; the angle is reduced exactly (whole turns dropped in 64-bit fixed point), so
- * positions up to 2^31 lose nothing. Positions may be negative.
+ * rounded once to the type. Whole turns are dropped exactly (64-bit fixed point); the angle that is left is off by at
+ * most 2^-25 of half a turn (rounded to fp32 once) and 2^-52 of p * inv_freq[i] (the frequency's own 53 bits: next to
+ * nothing at a million positions, for inv_freq = 1 about 2^-24 of a turn at 2^31). Positions may be negative.
  *
  * x and out may be the same tensor (in place). Only the rot values of each head are read and written:
  * the pointers are to the first value of the rotary part of token 0's head 0, the strides (in elements)
@@ -547,6 +548,8 @@ hs_status hs_rope_inv_freq(int32_t rot, double base, int32_t kind, double factor
  *                 count as not there
  *   workspace     hs_paged_mla_workspace_size() bytes of 16-byte aligned device memory, scratch; calls that share
  *                 one must not overlap on the GPU
+ * The same call gives the same bits each time. How a request's work is split, and so its last bits, depends on all of the
+ * batch's lengths.
  * ---------------------------------------------------------------------------------------- */
 typedef struct {
   int32_t T, B, H, causal;

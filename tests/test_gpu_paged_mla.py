@@ -192,7 +192,8 @@ def test_far_rows_pass_32_bits():
     assert flag == 0 and torch.equal(out, want)
 
 
-# Batches by rows per request: few (at most 64), some (at most 256), many (the cached rows are dequantised first).
+# Batches by (token, head) rows per request on average, here with two requests: few (at most 128), some (at most 768), many (the
+# cached rows are dequantised first). Tests that add requests run in another variant; see test_gpu_paged_rule.py.
 SIZES = {"few": [2, 3], "some": [9, 12], "many": [60, 40]}
 
 
