@@ -9,6 +9,7 @@ kernels; there is no fallback. If the library is missing, import succeeds but ev
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 
@@ -19,7 +20,8 @@ __all__ = ["HSError", "lib_path", "load", "hs_abi_version", "hs_check_flag", "hs
            "hs_sparse_mla_fwd", "hs_sparse_mla_workspace_size", "hs_sparse_mla_fwd_static", "hs_hisparse_resolve",
            "hs_hisparse_touch_host", "hs_kv_append", "hs_kv_offload", "hs_rope", "hs_rope_inv_freq", "hs_paged_mla_fwd",
            "hs_paged_mla_workspace_size", "hs_kv_copy_pages", "hs_kv_fork", "hs_kv_free", "hs_kv_compact",
-           "hs_kv_compact_workspace_size", "FLAGS"]
+           "hs_kv_compact_workspace_size", "hs_kv_read", "hs_mla_absorb", "hs_mla_project", "hs_mla_expand", "hs_mla_expanded_fwd",
+           "hs_mla_expanded_workspace_size", "FLAGS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libhs.so")
@@ -97,8 +99,15 @@ def load():
         lib.hs_kv_free.argtypes = [_P, _P]
         lib.hs_kv_compact.argtypes = [_P, _P]
         lib.hs_kv_compact_workspace_size.argtypes = [_i64, ctypes.POINTER(ctypes.c_uint64)]
+        lib.hs_kv_read.argtypes = [_P, _P]
+        lib.hs_mla_absorb.argtypes = [_P, _P]
+        lib.hs_mla_project.argtypes = [_P, _P]
+        lib.hs_mla_expand.argtypes = [_P, _P]
+        lib.hs_mla_expanded_fwd.argtypes = [_P, _P]
+        lib.hs_mla_expanded_workspace_size.argtypes = [_i32, _i32, ctypes.POINTER(ctypes.c_uint64)]
         for f in ("hs_rope", "hs_rope_inv_freq", "hs_paged_mla_fwd", "hs_paged_mla_workspace_size", "hs_kv_copy_pages", "hs_kv_fork",
-                  "hs_kv_free", "hs_kv_compact", "hs_kv_compact_workspace_size"):
+                  "hs_kv_free", "hs_kv_compact", "hs_kv_compact_workspace_size", "hs_kv_read", "hs_mla_absorb", "hs_mla_project",
+                  "hs_mla_expand", "hs_mla_expanded_fwd", "hs_mla_expanded_workspace_size"):
             getattr(lib, f).restype = ctypes.c_int
         for f in ("hs_check_flag", "hs_indexer_scores", "hs_topk", "hs_indexer_topk", "hs_sparse_mla_fwd", "hs_sparse_mla_workspace_size",
                   "hs_sparse_mla_fwd_static", "hs_hisparse_resolve", "hs_hisparse_touch_host", "hs_kv_append", "hs_kv_offload"):
@@ -537,3 +546,119 @@ def hs_kv_compact(block_table, refcount, table_out, refcount_out, src, dst, coun
                                               _int(dst, "dst"), _int(counts, "counts"), pp, cp, sp,
                                               _tensor(workspace, "workspace", torch.uint8), workspace.numel(),
                                               _int(err_flag, "err_flag")), _stream(stream)))
+
+
+class _KvReadArgs(ctypes.Structure):
+    _fields_ = [("B", _i32), ("bt_stride", _i32), ("dtype", _i32), ("kv_pool", _P), ("R", _i64), ("block_table", _P), ("first", _P),
+                ("out_start", _P), ("n", _i64), ("out", _P), ("out_stride", _i64), ("err_flag", _P)]
+
+
+class _MlaHeadsArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("H", _i32), ("Dn", _i32), ("Dv", _i32), ("x", _P), ("x_stride_t", _i64), ("x_stride_h", _i64), ("w", _P),
+                ("out", _P), ("out_stride_t", _i64), ("out_stride_h", _i64), ("err_flag", _P)]
+
+
+class _MlaExpandArgs(ctypes.Structure):
+    _fields_ = [("N", _i32), ("H", _i32), ("width", _i32), ("latent", _P), ("latent_stride", _i64), ("w", _P), ("kv", _P),
+                ("kv_stride", _i64), ("err_flag", _P)]
+
+
+class _MlaExpandedArgs(ctypes.Structure):
+    _fields_ = [("T", _i32), ("B", _i32), ("H", _i32), ("Dn", _i32), ("Dv", _i32), ("causal", _i32), ("q", _P), ("q_stride_t", _i64),
+                ("q_stride_h", _i64), ("kv", _P), ("kv_stride", _i64), ("N", _i64), ("rope", _P), ("rope_stride", _i64),
+                ("req_start", _P), ("kv_start", _P), ("softmax_scale", _f32), ("out", _P), ("lse", _P), ("err_flag", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_uint64)]
+
+
+_pack_kv_read, _pack_mla_heads, _pack_mla_expand, _pack_mla_expanded = (
+    _packer(c) for c in (_KvReadArgs, _MlaHeadsArgs, _MlaExpandArgs, _MlaExpandedArgs))
+
+
+def _strided(t, name, dtype, dims):
+    """Address, shape and strides of a CUDA tensor of this type and number of dimensions whose last one has consecutive values. A
+    dimension of one entry gets the stride that it has in a contiguous tensor (its own says nothing)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != dims:
+        raise HSError(1, "%s must be a %s CUDA tensor of %d dimensions" % (name, dtype, dims))
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise HSError(1, "%s must have consecutive values in its last dimension" % name)
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise HSError(1, "%s is on another device than the current one" % name)
+    if 1 in shape:
+        stride = tuple(math.prod(shape[d + 1:]) if shape[d] == 1 else stride[d] for d in range(dims))
+    return t.data_ptr(), shape, stride
+
+
+def hs_kv_read(kv_pool, block_table, out_start, out, err_flag, first=None, stream=None):
+    """Rows of the paged cache as values: row ``first[r] + i`` of request r (``first`` int32 [B], row 0 on when None) into row
+    ``out_start[r] + i`` of ``out`` (bf16, fp16 or fp32 [n, 576]: 512 latent and 64 rotary values; ``out_start`` int32 [B + 1])."""
+    dtype = out.dtype if isinstance(out, torch.Tensor) else None
+    if dtype not in _ROPE_DTYPES:
+        raise HSError(1, "out must be a bf16, fp16 or fp32 CUDA tensor [n, 576]")
+    op, (n, D), (ot, _) = _strided(out, "out", dtype, 2)
+    (B, pages), (R, row) = block_table.shape, kv_pool.shape
+    if D != 576 or row != 656 or out_start.numel() != B + 1 or (first is not None and first.numel() != B):
+        raise HSError(1, "shape mismatch: kv_pool [R,656], block_table [B,pages], out_start [B+1], first [B], out [n,576]")
+    _check(load().hs_kv_read(_pack_kv_read(B, pages, _ROPE_DTYPES[dtype], _tensor(kv_pool, "kv_pool", torch.uint8), R,
+                                           _int(block_table, "block_table"), 0 if first is None else _int(first, "first"),
+                                           _int(out_start, "out_start"), n, op, ot, _int(err_flag, "err_flag")), _stream(stream)))
+
+
+def _heads_args(x, w, out, err_flag, taken, given):
+    """``taken`` / ``given``: what the last dimensions of x and out have to be, of (Dn, Dv), where the other one follows."""
+    xp, (T, H, Dx), (xt, xh, _) = _strided(x, "x", torch.bfloat16, 3)
+    op, (To, Ho, Do), (ot, oh, _) = _strided(out, "out", torch.bfloat16, 3)
+    wp, (Hw, width, latent), _ = _strided(w, "w", torch.bfloat16, 3)
+    Dn, Dv = (Dx, width - Dx) if given == 512 else (width - Do, Do)
+    if latent != 512 or Hw != H or (To, Ho) != (T, H) or not w.is_contiguous() or (given or Do) != Do or (taken or Dx) != Dx:
+        raise HSError(1, "shape mismatch: x [T,H,%s], w [H,Dn+Dv,512] contiguous, out [T,H,%s]" % (taken or "Dn", given or "Dv"))
+    return _pack_mla_heads(T, H, Dn, Dv, xp, xt, xh, wp, op, ot, oh, _int(err_flag, "err_flag"))
+
+
+def hs_mla_absorb(q, w, out, err_flag, stream=None):
+    """Queries into the latent space: ``out[t, h] = q[t, h] @ w[h, :Dn]``; ``q`` bf16 [T, H, Dn] and ``out`` bf16 [T, H, 512] may be
+    slices of wider heads, ``w`` is the layer's bf16 [H, Dn + Dv, 512]. See include/hs.h."""
+    _check(load().hs_mla_absorb(_heads_args(q, w, out, err_flag, None, 512), _stream(stream)))
+
+
+def hs_mla_project(x, w, out, err_flag, stream=None):
+    """Latent outputs to values: ``out[t, h] = w[h, Dn:] @ x[t, h]``; ``x`` bf16 [T, H, 512], ``out`` bf16 [T, H, Dv], ``w`` as for
+    hs_mla_absorb."""
+    _check(load().hs_mla_project(_heads_args(x, w, out, err_flag, 512, None), _stream(stream)))
+
+
+def hs_mla_expand(latent, w, kv, err_flag, stream=None):
+    """Keys and values of every head from latent rows: ``kv[n, h] = w[h] @ latent[n]``; ``latent`` bf16 [N, 512] (rows may be wider),
+    ``w`` bf16 [H, Dn + Dv, 512], ``kv`` bf16 [N, H, Dn + Dv]."""
+    lp, (N, D), (ls, _) = _strided(latent, "latent", torch.bfloat16, 2)
+    wp, (H, width, latent_dim), _ = _strided(w, "w", torch.bfloat16, 3)
+    kp, shape, (ks, kh, _) = _strided(kv, "kv", torch.bfloat16, 3)
+    if D != 512 or latent_dim != 512 or tuple(shape) != (N, H, width) or (kh != width and H > 1) or not w.is_contiguous():
+        raise HSError(1, "shape mismatch: latent [N,512], w [H,Dn+Dv,512] contiguous, kv [N,H,Dn+Dv] with its heads one after the other")
+    _check(load().hs_mla_expand(_pack_mla_expand(N, H, width, lp, ls, wp, kp, ks, _int(err_flag, "err_flag")), _stream(stream)))
+
+
+def hs_mla_expanded_workspace_size(B: int, Dv: int) -> int:
+    """Bytes of workspace hs_mla_expanded_fwd needs for B requests and Dv values per head on the current device."""
+    n = ctypes.c_uint64(0)
+    _check(load().hs_mla_expanded_workspace_size(int(B), int(Dv), ctypes.byref(n)))
+    return int(n.value)
+
+
+def hs_mla_expanded_fwd(q, kv, rope, req_start, kv_start, softmax_scale: float, out, err_flag, workspace, lse=None, causal: bool = True,
+                        stream=None):
+    """Dense attention over expanded keys and values: ``out`` bf16 [T, H, Dv] (and ``lse`` float32 [T, H] if given) of ``q`` bf16
+    [T, H, Dn + 64] over ``kv`` bf16 [N, H, Dn + Dv] and the shared ``rope`` bf16 [N, 64]. Request r's tokens are ``req_start[r] ..
+    req_start[r + 1] - 1``, its rows ``kv_start[r] .. kv_start[r + 1] - 1`` (int32 [B + 1]), its tokens' own last. See include/hs.h."""
+    qp, (T, H, Dq), (qt, qh, _) = _strided(q, "q", torch.bfloat16, 3)
+    kp, (N, Hk, width), (ks, kh, _) = _strided(kv, "kv", torch.bfloat16, 3)
+    rp, (Nr, D), (rs, _) = _strided(rope, "rope", torch.bfloat16, 2)
+    op, B = _tensor(out, "out", torch.bfloat16), req_start.numel() - 1
+    if out.dim() != 3 or out.shape[:2] != (T, H) or Hk != H or Nr != N or D != 64 or width - out.shape[2] != Dq - 64 \
+            or (kh != width and H > 1) or kv_start.numel() != B + 1 or (lse is not None and lse.shape != (T, H)):
+        raise HSError(1, "shape mismatch: q [T,H,Dn+64], kv [N,H,Dn+Dv] with its heads one after the other, rope [N,64], req_start and "
+                         "kv_start [B+1], out [T,H,Dv], lse [T,H]")
+    _check(load().hs_mla_expanded_fwd(_pack_mla_expanded(
+        T, B, H, Dq - 64, out.shape[2], 1 if causal else 0, qp, qt, qh, kp, ks, N, rp, rs, _int(req_start, "req_start"),
+        _int(kv_start, "kv_start"), softmax_scale, op, 0 if lse is None else _tensor(lse, "lse", torch.float32), _int(err_flag, "err_flag"),
+        _tensor(workspace, "workspace", torch.uint8), workspace.numel()), _stream(stream)))

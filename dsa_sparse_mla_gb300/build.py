@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhs.so")
 SOURCES = ["hs_api.cu", "indexer.cu", "topk.cu", "mla.cu", "mla_static.cu", "resolve.cu", "append.cu", "offload.cu",
-           "rope.cu", "pages.cu", "paged.cu", "paged_few.cu"]
+           "rope.cu", "pages.cu", "paged.cu", "paged_few.cu", "read.cu", "heads.cu", "expanded.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,910 @@
+// expanded.cu — hs_mla_expanded_fwd: attention of each request's new tokens over keys and values of every head (the expanded form of
+// latent attention; the 64 rotary key values are shared by the heads).
+//
+//   logit = scale (q[:Dn] . k[j, h] + q[Dn:] . rope[j]),   out = sum_j softmax(logit)_j v[j, h],   one pass over the rows with a
+//   running reference and sum: P = 2^(logit log2 e - ref), and where a row's maximum passes ref by 2^8 its reference moves and
+//   the accumulator is scaled (so it rarely is).
+//
+// Work is units of (request, head, block of 256 tokens), a unit's cached rows cut into pieces where there are too few units for the
+// SMs. A planning kernel counts units, chooses the pieces and clears a counter; pairs of CTAs take units from the counter, blocks of a
+// head one after the other (they share its keys and values in L2), the longest first.
+//
+// A pair works with two-SM MMAs: each CTA holds the queries, logits, P and output of its 128 tokens and half of every K and V
+// tile (64 of 128 rows of K, half of V's values). Tensor memory: two logit tiles, and with 128 values per head two tiles of P
+// and the output; with 256 values P goes through shared memory instead. In each CTA two warpgroups take the tiles in turn, a
+// thread to a token: it takes its 128 logits into registers at once, which frees the tile for the product after next, so that a
+// tile's softmax has two whole tiles' products (about 2,500 cycles) to hide under. A token's reference passes from one
+// warpgroup to the other through shared memory. The warpgroups also scale and write the output, under the next unit's products.
+//
+// Order of copies and products: K of tile i + 2 before V of tile i, across units (the next unit's K may come before this one's last
+// V, not two units' before). Every role walks the same order on its own.
+//
+// Rows past a request's end are masked as keys and set to zero as values (in shared memory, by a warp that waits for such a tile's copy).
+// A row that a token does not see can still reach its output where P = 0 meets a value that is not finite; where an output is not
+// finite although the token's logits are, the warp computes it again from the rows that the token sees (rescue).
+#include <atomic>
+
+#include "launch.cuh"
+#include "pair.cuh"
+
+namespace hs {
+namespace expanded {
+
+constexpr int kTok = 256, kHalf = 128, kKeys = 128;  // tokens of a block, of a CTA; rows of a tile
+constexpr int kThreads = 384;                        // copies, MMAs, units, tails; 2 x 128 softmax threads
+constexpr int kAhead = 3;                            // K's tiles before V's: QK of tile i + 2 is issued before PV of tile i
+constexpr float kThreshold = 8.0f;                   // log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxReq = 4096;
+constexpr int kPlanThreads = 1024;
+constexpr int kMinPiece = 8;                         // tiles of a piece, at least
+constexpr int kPerPair = 6;                          // pieces of split blocks per pair of CTAs, at most
+
+struct Req {
+  int32_t unit0, q0, m, kv0;   // first unit; first token, tokens; first row
+  int32_t len, nb, np, slot0;  // rows; blocks; pieces per block; first slot of the pieces
+};
+
+struct Unit {
+  int32_t tok, nrows, h, kv0;      // first token, tokens, head, first row of the request
+  int32_t ta, n, see, len;         // first tile, tiles (0: no more units), rows that the first token sees, rows of the request
+  int32_t np, slot, first, pad;    // pieces of the block (1: whole), this piece's slot, the first piece's
+};
+
+struct Params {
+  int32_t T, B, H, causal, clusters, cap;
+  const uint16_t* q;
+  int64_t q_stride_t, q_stride_h;
+  const uint16_t* kv;
+  int64_t kv_stride, N;
+  const uint16_t* rope;
+  int64_t rope_stride;
+  const int32_t* req_start;
+  const int32_t* kv_start;
+  float scale_log2;  // |softmax_scale| log2 e
+  uint32_t flip;     // 0x80000000 where softmax_scale < 0
+  uint16_t* out;
+  float* lse;
+  int32_t* err;
+  int32_t* total;    // [2]: units, the counter
+  Req* req;
+  int32_t* joined;   // [cap][16]: pieces of a block that a warp's rows and columns have seen
+  float* part_lse;   // [cap][2][256]
+  float* part_out;   // [cap][256][Dv]
+};
+
+// ------------------------------------------------------------------------ plan ------------
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int64_t s = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) s += scratch[w];
+  return s;
+}
+// Sum of the values of the threads before this one.
+__device__ __forceinline__ int64_t block_before(int64_t v, int64_t* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  int64_t s = x - v;
+  for (int w = 0; w < warp; ++w) s += scratch[w];
+  return s;
+}
+
+// One CTA. Thread t plans requests 4 t .. 4 t + 3. A piece has at most a quarter of a pair's even share of all tiles (so that the
+// last units to end leave little idle), but kMinPiece at least, and longer where the pieces would not fit their slots.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
+  __shared__ int64_t scratch[32];
+  constexpr int kPer = kMaxReq / kPlanThreads;
+  let_next();
+  int start[kPer], m[kPer], kv0[kPer], len[kPer], nb[kPer], np[kPer];
+  int64_t most[kPer], work = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int r = kPer * threadIdx.x + k;
+    m[k] = start[k] = kv0[k] = len[k] = nb[k] = 0;
+    most[k] = 0;
+    if (r >= p.B) continue;
+    const int64_t a = p.req_start[r], b = p.req_start[r + 1], c = p.kv_start[r], d = p.kv_start[r + 1];
+    if (a < 0 || b < a || b > p.T || (r == 0 && a != 0) || (r == p.B - 1 && b != p.T)) flag_error(p.err, HS_FLAG_BAD_INDEX);
+    if (a < 0 || b <= a || b > p.T) continue;
+    start[k] = (int)a, m[k] = (int)(b - a);
+    nb[k] = (m[k] + kTok - 1) / kTok;
+    if (c < 0 || d < c || d > p.N) {
+      flag_error(p.err, HS_FLAG_BAD_LENGTH);
+    } else {
+      kv0[k] = (int)c, len[k] = (int)(d - c);
+    }
+    most[k] = (len[k] + kKeys - 1) / kKeys;
+    const int64_t least = p.causal ? ((int64_t)len[k] - m[k] + kTok + kKeys - 1) / kKeys : most[k];  // of the first block
+    work += nb[k] * (most[k] + (least < 1 ? 1 : least < most[k] ? least : most[k])) / 2 * p.H;
+  }
+  work = block_sum(work, scratch);
+  int64_t piece = (work / p.clusters + 3) / 4;
+  if (piece < kMinPiece) piece = kMinPiece;
+#pragma unroll 1
+  for (;; piece *= 2) {
+    int64_t slots = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (most[k] > piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
+    if (block_sum(slots, scratch) <= p.cap) break;
+  }
+  int64_t units = 0, slots = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    np[k] = most[k] > piece ? (int)((most[k] + piece - 1) / piece) : 1;
+    units += (int64_t)nb[k] * p.H * np[k];
+    if (np[k] > 1) slots += (int64_t)nb[k] * p.H * np[k];
+  }
+  int64_t unit0 = block_before(units, scratch), slot0 = block_before(slots, scratch);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int r = kPer * threadIdx.x + k;
+    if (r < p.B) p.req[r] = {(int32_t)unit0, start[k], m[k], kv0[k], len[k], nb[k], np[k], (int32_t)slot0};
+    unit0 += (int64_t)nb[k] * p.H * np[k];
+    if (np[k] > 1) slot0 += (int64_t)nb[k] * p.H * np[k];
+  }
+  if (threadIdx.x == kPlanThreads - 1) {
+    p.total[0] = (int32_t)unit0;
+    p.total[1] = 0;
+  }
+  for (int i = threadIdx.x; i < p.cap * 16; i += kPlanThreads) p.joined[i] = 0;
+}
+
+// ------------------------------------------------------------------------ attention -------
+template <int kDn, int kDv>
+struct Shape {
+  static constexpr int kQB = kDn / 64 + 1;                    // blocks of 64 values of a query or key
+  static constexpr bool kWide = kDv > 128;                    // P through shared memory
+  static constexpr int kQBlk = kHalf * 128, kQBytes = kQB * kQBlk;
+  static constexpr int kKBlk = kKeys / 2 * 128, kKBytes = kQB * kKBlk;
+  static constexpr int kVBlk = kKeys * 128, kVBytes = kDv / 128 * kVBlk;
+  static constexpr int kSlot = kKBytes > kVBytes ? kKBytes : kVBytes;
+  static constexpr int kSlots = kWide ? 3 : 7;
+  static constexpr int kPBlk = kHalf * 128, kPBuf = kWide ? 2 * kPBlk : 0;  // blocks of 64 rows of the cache
+  static constexpr int kOffRing = kQBytes, kOffP = kOffRing + kSlots * kSlot, kOffRef = kOffP + 2 * kPBuf;
+  static constexpr int kOffSum = kOffRef + 1024, kOffUnit = kOffSum + 1024, kOffBar = kOffUnit + 2 * (int)sizeof(Unit);
+  static constexpr int kSmem = kOffBar + 512;
+  static constexpr int kColP = 256, kColO = kWide ? 256 : 384;  // tensor-memory columns; logits in 0 .. 255
+  static_assert(kDv % 128 == 0 && kDv <= 256 && kSmem <= 232448 && kSlot % 1024 == 0, "shared and tensor memory");
+};
+
+struct Bars {
+  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_full, o_free, drain;
+  uint64_t tail_full[2], tail_done[2], unit_full[2], unit_empty[2];
+  uint64_t ref[8], sum[8], sum_read[8];  // [warpgroup][quad]
+  uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 512, "barriers");
+
+struct Ring {
+  int slot;
+  uint32_t par;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) slot = 0, par ^= 1u;
+  }
+};
+
+// A role's walk over the units: they arrive in two places of shared memory in turn.
+struct Units {
+  const uint8_t* at;
+  Bars* br;
+  int32_t* err;
+  uint32_t back;  // unit_empty[0] of the CTA that hands units out
+  bool gives;     // whether this thread gives units back for its role
+  // Unit number n (one thread, or every lane of a warp); false after a wait that ran out.
+  __device__ __forceinline__ bool take(uint32_t n, Unit& u) const {
+    if (!mbar_wait_cluster(&br->unit_full[n & 1u], (n >> 1) & 1u, err)) return false;
+    const int4* v = reinterpret_cast<const int4*>(at + (n & 1u) * sizeof(Unit));
+    int4* w = reinterpret_cast<int4*>(&u);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) w[i] = v[i];
+    return true;
+  }
+  __device__ __forceinline__ void give_back(uint32_t n) const {
+    if (gives) remote_arrive_cta(back + 8 * (n & 1u));
+  }
+};
+
+// The order of K and V tiles. step() says what comes next: K of (ku, kt), V of (vu, vt), or the end.
+struct Walk {
+  Unit ku, vu;
+  uint32_t kn, vn;     // numbers of ku and vu
+  int kt, vt;          // the next tile of each
+  int64_t k, v;        // tiles so far
+  bool end;            // no more units
+  enum What { kK, kV, kEnd, kFail };
+  __device__ __forceinline__ bool begin(const Units& us) {
+    kn = vn = 0, kt = vt = 0, k = v = 0;
+    if (!us.take(0, ku)) return false;
+    vu = ku;
+    end = ku.n == 0;
+    return true;
+  }
+  __device__ __forceinline__ What step(const Units& us) {
+#pragma unroll 1
+    for (;;) {
+      if (!end && kt == ku.n && kn == vn) {  // K goes one unit ahead of V at most
+        ++kn, kt = 0;
+        if (!us.take(kn, ku)) return kFail;
+        end = ku.n == 0;
+      }
+      if (!end && kt < ku.n && k - v < kAhead) return kK;
+      if (k == v) return kEnd;  // a unit has one tile at least, so K is at the end
+      if (vt < vu.n) return kV;
+      us.give_back(vn);
+      vu = ku;
+      ++vn, vt = 0;
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// A token's output values col0 .. col0 + kCols - 1 once more, from the rows that it sees alone, where a row of its tiles that it does not
+// see holds a value there that is not finite (P = 0 does not silence it). The whole warp works on one token; rare, so plain: a row
+// at a time, 32 lanes to a product, the reference and sum (inv) as they are.
+template <int kDn, int kDv>
+__device__ __noinline__ bool rescue(const Params& p, const Unit& u, int64_t tok, int see, float me, float inv, int col0, float (&acc)[kDv / 64]) {
+  constexpr int kCols = kDv / 2, kEach = kCols / 32, kQ = kDn / 32;
+  const int lane = threadIdx.x & 31;
+  const int lo = u.ta * kKeys, end = min(lo + u.n * kKeys, u.len), seen = min(see, end);
+  const uint16_t* kv = p.kv + (int64_t)u.kv0 * p.kv_stride + (int64_t)u.h * (kDn + kDv);
+  bool bad = false;
+  for (int j = max(seen, lo); j < end; ++j)
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) bad |= (kv[(int64_t)j * p.kv_stride + kDn + col0 + 32 * e + lane] & 0x7F80u) == 0x7F80u;
+  if (!__any_sync(0xffffffffu, bad)) return false;
+  const uint16_t* qp = p.q + tok * p.q_stride_t + u.h * p.q_stride_h;
+  const uint16_t* rp = p.rope + (int64_t)u.kv0 * p.rope_stride;
+  const float coef = __uint_as_float(__float_as_uint(fmaxf(p.scale_log2, 7.5e-37f)) ^ p.flip);
+  float q[kQ + 2];
+#pragma unroll
+  for (int e = 0; e < kQ + 2; ++e) q[e] = from_bf16(qp[32 * e + lane]);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int j = lo; j < seen; ++j) {
+    const uint16_t* k = kv + (int64_t)j * p.kv_stride;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < kQ; ++e) s = fmaf(q[e], from_bf16(k[32 * e + lane]), s);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) s = fmaf(q[kQ + e], from_bf16(rp[(int64_t)j * p.rope_stride + 32 * e + lane]), s);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    const float w = fast_exp2(fmaf(s, coef, -me)) * inv;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) acc[e] = fmaf(w, from_bf16(k[kDn + col0 + 32 * e + lane]), acc[e]);
+  }
+  return true;
+}
+
+template <int kDn, int kDv>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expanded_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v, const Params p) {
+  using Sh = Shape<kDn, kDv>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // the swizzled blocks need it; the same in both CTAs
+    if (threadIdx.x == 0) flag_error(p.err, HS_FLAG_BAD_STATE);
+    return;
+  }
+  Bars& br = *reinterpret_cast<Bars*>(smem + Sh::kOffBar);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (tid == 0) {
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&br.full[s], 2);
+      mbar_init(&br.empty[s], 1);
+      mbar_init(&br.ref[s], 1);
+      mbar_init(&br.sum[s], 1);
+      mbar_init(&br.sum_read[s], 1);
+    }
+    mbar_init(&br.q_full, 2);
+    mbar_init(&br.q_empty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&br.s_full[b], 1);
+      mbar_init(&br.s_empty[b], 8);
+      mbar_init(&br.p_full[b], 8);
+      mbar_init(&br.pv_done[b], 1);
+      mbar_init(&br.tail_full[b], 1);
+      mbar_init(&br.tail_done[b], 1);
+      mbar_init(&br.unit_full[b], 1);
+      mbar_init(&br.unit_empty[b], 21);  // copies, tails and eight softmax warps of both CTAs, the MMAs
+    }
+    mbar_init(&br.o_full, 1);
+    mbar_init(&br.o_free, 16);
+    mbar_init(&br.drain, 1);
+    mbar_fence_init();
+    prefetch_tensormap(&map_q);
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_r);
+    prefetch_tensormap(&map_v);
+  }
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist
+  if (warp == 0) tc2::alloc(&br.tmem, 512);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = br.tmem;
+  after_previous();  // the plan
+  const Units us = {smem + Sh::kOffUnit, &br, p.err, remote_smem(br.unit_empty, 0), lane == 0};
+
+  if (warp < 4) {
+    // 384 threads start with 168 registers (64,512 in all): 128 keep 96, 256 take 200 (63,488)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp == 0 && lane == 0) {
+      // ================================================================ copies ==================
+      const uint32_t full = remote_smem(br.full, 0), q_full = remote_smem(&br.q_full, 0);
+      Ring ring = {0, 1};
+      uint32_t tails = 0;
+      Walk w;
+      bool ok = w.begin(us);
+#pragma unroll 1
+      while (ok) {
+        const Walk::What what = w.step(us);
+        if (what == Walk::kEnd) break;
+        if (what == Walk::kFail) {
+          ok = false;
+          break;
+        }
+        if (what == Walk::kK && w.kt == 0) {
+          if (!mbar_wait(&br.q_empty, (w.kn & 1u) ^ 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          pair::arrive_expect_tx(q_full, Sh::kQBytes);
+#pragma unroll
+          for (int b = 0; b < Sh::kQB; ++b) pair::load_3d(smem + b * Sh::kQBlk, &map_q, q_full, 64 * b, w.ku.h, w.ku.tok + kHalf * (int)rank);
+        }
+        if (!mbar_wait(&br.empty[ring.slot], ring.par, p.err)) {
+          ok = false;
+          break;
+        }
+        uint8_t* s = smem + Sh::kOffRing + ring.slot * Sh::kSlot;
+        uint32_t bar = full + 8 * (uint32_t)ring.slot;
+        if (what == Walk::kK) {
+          const int y = w.ku.kv0 + (w.ku.ta + w.kt) * kKeys + kKeys / 2 * (int)rank;
+          pair::arrive_expect_tx(bar, Sh::kKBytes);
+#pragma unroll
+          for (int b = 0; b < kDn / 64; ++b) pair::load_3d(s + b * Sh::kKBlk, &map_k, bar, 64 * b, w.ku.h, y);
+          pair::load_2d(s + kDn / 64 * Sh::kKBlk, &map_r, bar, 0, y);
+          ++w.kt, ++w.k;
+        } else {
+          const int tile = w.vu.ta + w.vt, y = w.vu.kv0 + tile * kKeys;
+          if (w.vu.len - tile * kKeys < kKeys) {  // counted on a barrier of this CTA; the tails' warp goes on from there
+            uint64_t* t = &br.tail_full[tails & 1u];
+            if (!mbar_wait(&br.tail_done[tails & 1u], ((tails >> 1) & 1u) ^ 1u, p.err)) {
+              ok = false;
+              break;
+            }
+            ++tails;
+            mbar_arrive_expect_tx(t, Sh::kVBytes);
+            bar = remote_smem(t, rank);
+          } else {
+            pair::arrive_expect_tx(bar, Sh::kVBytes);
+          }
+#pragma unroll
+          for (int b = 0; b < kDv / 128; ++b) pair::load_3d(s + b * Sh::kVBlk, &map_v, bar, kDn + kDv / 2 * (int)rank + 64 * b, w.vu.h, y);
+          ++w.vt, ++w.v;
+        }
+        ring.next(Sh::kSlots);
+      }
+      if (!ok) pair::let_copies_land();
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ================================================================ MMAs ====================
+      constexpr uint32_t id_s = idesc_bf16(kTok, kKeys, 0, 0), id_o = idesc_bf16(kTok, kDv, 0, 1);
+      const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2);
+      const uint64_t kd = smem_desc(smem_u32(smem + Sh::kOffRing), 16, 1024, 2);
+      const uint64_t vd = smem_desc(smem_u32(smem + Sh::kOffRing), Sh::kVBlk, 1024, 2);
+      const uint64_t pd = smem_desc(smem_u32(smem + Sh::kOffP), 16, 1024, 2);
+      Ring ring = {0, 0};
+      Walk w;
+      bool ok = w.begin(us);
+#pragma unroll 1
+      while (ok) {
+        const Walk::What what = w.step(us);
+        if (what == Walk::kEnd) break;
+        if (what == Walk::kFail) break;
+        const uint64_t off = (uint64_t)((ring.slot * Sh::kSlot) >> 4);
+        if (what == Walk::kK) {
+          const uint32_t b = (uint32_t)w.k & 1u;
+          if ((w.kt == 0 && !mbar_wait(&br.q_full, w.kn & 1u, p.err)) ||
+              !mbar_wait(&br.s_empty[b], ((uint32_t)(w.k >> 1) & 1u) ^ 1u, p.err) || !mbar_wait(&br.full[ring.slot], ring.par, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < Sh::kQB; ++k)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc2::ss(tmem + kKeys * b, qd + (uint64_t)((k * Sh::kQBlk + kk * 32) >> 4), kd + off + (uint64_t)((k * Sh::kKBlk + kk * 32) >> 4), id_s,
+                      (k | kk) != 0 ? 1u : 0u);
+          tc2::commit(&br.empty[ring.slot], 0x3);
+          tc2::commit(&br.s_full[b], 0x3);
+          ++w.kt, ++w.k;
+          if (w.kt == w.ku.n) tc2::commit(&br.q_empty, 0x3);
+        } else {
+          const uint32_t b = (uint32_t)w.v & 1u;
+          if ((w.vt == 0 && !mbar_wait(&br.o_free, (w.vn & 1u) ^ 1u, p.err)) || !mbar_wait(&br.full[ring.slot], ring.par, p.err) ||
+              !mbar_wait(&br.p_full[b], (uint32_t)(w.v >> 1) & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk) {
+            const uint64_t vb = vd + off + (uint64_t)((kk * 2048) >> 4);
+            const uint32_t more = (w.vt | kk) != 0 ? 1u : 0u;
+            if (Sh::kWide)
+              tc2::ss(tmem + Sh::kColO, pd + (uint64_t)((b * Sh::kPBuf + (kk / 4) * Sh::kPBlk + (kk % 4) * 32) >> 4), vb, id_o, more);
+            else
+              tc2::ts(tmem + Sh::kColO, tmem + Sh::kColP + 64 * b + 8 * kk, vb, id_o, more);
+          }
+          tc2::commit(&br.empty[ring.slot], 0x3);
+          tc2::commit(&br.pv_done[b], 0x3);
+          ++w.vt, ++w.v;
+          if (w.vt == w.vu.n) tc2::commit(&br.o_full, 0x3);
+        }
+        ring.next(Sh::kSlots);
+      }
+      tc2::commit(&br.drain, 0x1);
+      mbar_wait(&br.drain, 0, p.err);
+    } else if (warp == 2 && rank == 0) {
+      // ================================================================ units ===================
+      const int32_t total = p.total[0];
+      int r0 = 0;
+      uint32_t at[2], bar[2];
+#pragma unroll
+      for (uint32_t c = 0; c < 2; ++c) at[c] = remote_smem(smem + Sh::kOffUnit, c), bar[c] = remote_smem(br.unit_full, c);
+#pragma unroll 1
+      for (uint32_t n = 0;; ++n) {
+        if (!warp_wait(&br.unit_empty[n & 1u], ((n >> 1) & 1u) ^ 1u, p.err, lane)) break;
+        int32_t i = 0;
+        if (lane == 0) i = atomicAdd(&p.total[1], 1);
+        i = __shfl_sync(0xffffffffu, i, 0);
+        Unit u = {};
+        if (i < total) {
+          // its request: the last that starts at or before it (numbers grow, so the search goes on from the last one)
+          for (;;) {
+            const int r = r0 + 1 + lane;
+            const uint32_t le = __ballot_sync(0xffffffffu, r < p.B && p.req[r < p.B ? r : 0].unit0 <= i);
+            r0 += __popc(le);
+            if (le != 0xffffffffu) break;
+          }
+          const Req q = p.req[r0];
+          const int per_head = q.nb * q.np, x = i - q.unit0, rest = x % per_head;
+          const int b = q.nb - 1 - rest / q.np, piece = rest % q.np;
+          u.h = x / per_head;
+          u.tok = q.q0 + b * kTok;
+          u.nrows = q.m - b * kTok < kTok ? q.m - b * kTok : kTok;
+          u.kv0 = q.kv0;
+          u.len = q.len;
+          u.see = p.causal ? q.len - q.m + 1 + b * kTok : q.len;
+          const int64_t last = p.causal ? (int64_t)u.see + u.nrows - 1 : q.len;
+          const int64_t tiles = last > 0 ? (last + kKeys - 1) / kKeys : 0;
+          const int64_t ta = tiles * piece / q.np, tb = tiles * (piece + 1) / q.np;
+          u.ta = (int)ta;
+          u.n = tb > ta ? (int)(tb - ta) : 1;
+          if (tb == ta) u.len = 0;  // a tile of which no row is there
+          u.np = q.np;
+          u.first = q.slot0 + (u.h * q.nb + b) * q.np;
+          u.slot = u.first + piece;
+        }
+        if (lane < 2) {
+          const int4* v = reinterpret_cast<const int4*>(&u);
+          const uint32_t to = at[lane] + (n & 1u) * (uint32_t)sizeof(Unit), on = bar[lane] + 8 * (n & 1u);
+          pair::arrive_expect_tx(on, sizeof(Unit));
+#pragma unroll
+          for (int k = 0; k < 3; ++k) pair::st_async16(to + 16 * k, v[k], on);
+        }
+        __syncwarp();
+        if (i >= total) break;
+      }
+    } else if (warp == 3) {
+      // ================================================================ tails ===================
+      // V tiles that reach past their request's end: rows from there on become zeros, then the tile counts as there.
+      const uint32_t full = remote_smem(br.full, 0);
+      Ring ring = {0, 0};
+      uint32_t tails = 0;
+      Walk w;
+      bool ok = w.begin(us);
+#pragma unroll 1
+      while (ok) {
+        const Walk::What what = w.step(us);  // every lane walks
+        if (what == Walk::kEnd || what == Walk::kFail) break;
+        if (what == Walk::kK) {
+          ++w.kt, ++w.k;
+        } else {
+          const int left = w.vu.len - (w.vu.ta + w.vt) * kKeys;
+          if (left < kKeys) {
+            if (!warp_wait_all(&br.tail_full[tails & 1u], (tails >> 1) & 1u, p.err)) break;
+            uint8_t* s = smem + Sh::kOffRing + ring.slot * Sh::kSlot;
+            const int from = left < 0 ? 0 : left;
+#pragma unroll 1
+            for (int x = 8 * from + lane; x < 8 * kKeys; x += 32)
+#pragma unroll
+              for (int b = 0; b < kDv / 128; ++b) *reinterpret_cast<uint4*>(s + b * Sh::kVBlk + 16 * x) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              remote_arrive_cta(full + 8 * (uint32_t)ring.slot);
+              mbar_arrive(&br.tail_done[tails & 1u]);
+            }
+            ++tails;
+          }
+          ++w.vt, ++w.v;
+        }
+        ring.next(Sh::kSlots);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ================================================================ softmax, output ===========
+    const int quad = warp & 3, g = (warp - 4) >> 2, row = 32 * quad + lane;  // this CTA's token; the tiles whose number has parity g
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t s_empty = remote_smem(br.s_empty, 0), p_full = remote_smem(br.p_full, 0), o_free = remote_smem(&br.o_free, 0);
+    float* refs = reinterpret_cast<float*>(smem + Sh::kOffRef);  // [2][128]
+    float* sums = reinterpret_cast<float*>(smem + Sh::kOffSum);
+    const int mine = 4 * g + quad, other = 4 * (g ^ 1) + quad;  // barriers of the two warps that share these tokens
+    uint32_t said = 0, heard = 0;  // references passed on and taken
+    uint32_t joint = 0;            // units in which this warp had tokens
+    const float coef = fmaxf(p.scale_log2, 7.5e-37f);  // not 0, so that a masked column stays -inf
+    int64_t i = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t n = 0; ok; ++n) {
+      Unit u;
+      ok = __all_sync(0xffffffffu, us.take(n, u));
+      if (!ok || u.n == 0) break;
+      const int have = u.nrows - kHalf * (int)rank;  // tokens of this CTA
+      const bool idle = 32 * quad >= have, there = row < have;
+      int see = p.causal ? u.see + kHalf * (int)rank + row : u.see;
+      see = there ? (see < u.len ? see : u.len) : 0;
+      float ref = -INFINITY, l = 0.f;
+      if (!idle && joint > 0) ok = warp_wait_all(&br.sum_read[other], (joint - 1) & 1u, p.err);
+#pragma unroll 1
+      for (int t = 0; t < u.n && ok; ++t, ++i) {
+        if ((int)(i & 1) != g) continue;
+        const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+        ok = warp_wait_all(&br.s_full[g], ph, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (idle) {
+          __syncwarp();
+          if (lane == 0) remote_arrive_relaxed(s_empty + 8 * (uint32_t)g);
+          // This tile's logits may be there before the warps with tokens have handed on P of the tile before last: without the
+          // wait, this arrival could count for that one.
+          if (i >= 2) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
+          __syncwarp();
+          if (lane == 0) remote_arrive_cta(p_full + 8 * (uint32_t)g);
+          continue;
+        }
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + kKeys * g + 32 * c, v[c]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive_relaxed(s_empty + 8 * (uint32_t)g);
+        const int lim = see - (u.ta + t) * kKeys;  // columns that this token sees
+        if (p.flip) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[c][j] ^= 0x80000000u;
+        }
+        if (!__all_sync(0xffffffffu, lim >= kKeys)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[c][j] = 32 * c + j < lim ? v[c][j] : 0xFF800000u;
+        }
+        float m4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          m4[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+          for (int j = 1; j < 32; ++j) m4[c] = fmaxf(m4[c], __uint_as_float(v[c][j]));
+        }
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        mx = mx == -INFINITY ? mx : mx * coef;
+        const float before = ref;  // this warpgroup's sum refers to it
+        if (t > 0) {               // the other warpgroup's, after the tile before
+          ok = warp_wait_all(&br.ref[other], heard & 1u, p.err);
+          if (!ok) break;
+          ++heard;
+          ref = refs[128 * (g ^ 1) + row];
+        }
+        const float was = ref;  // the accumulator refers to it
+        if (mx > ref + kThreshold) ref = mx;
+        if (t + 1 < u.n) {
+          refs[128 * g + row] = ref;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&br.ref[mine]);
+          ++said;
+        }
+        if (before != ref) l *= fast_exp2(before - ref);
+        const float me = ref == -INFINITY ? 0.f : ref;
+        // P of the tile before last, in this buffer, has been used
+        if (i >= 2) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float a = fast_exp2(fmaf(__uint_as_float(v[c][2 * j]), coef, -me));
+            const float b = fast_exp2(fmaf(__uint_as_float(v[c][2 * j + 1]), coef, -me));
+            s0 += a;
+            s1 += b;
+            v[c][j] = pack_bf16(a, b);
+          }
+          if (Sh::kWide) {
+            uint8_t* blk = smem + Sh::kOffP + g * Sh::kPBuf + (c >> 1) * Sh::kPBlk;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(blk + sw128_offset(row, 64 * (c & 1) + 16 * j)) =
+                  make_uint4(v[c][4 * j], v[c][4 * j + 1], v[c][4 * j + 2], v[c][4 * j + 3]);
+          } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = v[c][j];
+            tmem_st16(lane_base + Sh::kColP + 64 * g + 16 * c, w);
+          }
+        }
+        l += s0 + s1;
+        if (t > 0) {
+          const float al = was == ref ? 1.f : fast_exp2(was - ref);
+          // Rare. A parity tells two tiles apart: the logits of this tile came after PV of the tile three before, whose phase is over.
+          if (__any_sync(0xffffffffu, al != 1.f)) {
+            ok = warp_wait_all(&br.pv_done[g ^ 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kDv / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld32(lane_base + Sh::kColO + 32 * c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * al);
+              tmem_st32(lane_base + Sh::kColO + 32 * c, x);
+            }
+          }
+        }
+        tmem_wait_st();
+        if (Sh::kWide) fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive_cta(p_full + 8 * (uint32_t)g);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------------- the unit's end
+      if (!idle) {
+        // the warpgroups' sums, each with the reference that it refers to; a token's last reference is the larger (it only grows)
+        refs[128 * g + row] = ref;
+        sums[128 * g + row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br.sum[mine]);
+        ok = warp_wait_all(&br.sum[other], joint & 1u, p.err);
+        if (!ok) break;
+        const float ref2 = refs[128 * (g ^ 1) + row], l2 = sums[128 * (g ^ 1) + row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br.sum_read[mine]);
+        ++joint;
+        const float top = fmaxf(ref, ref2);
+        l = (ref == top ? l : l * fast_exp2(ref - top)) + (ref2 == top ? l2 : l2 * fast_exp2(ref2 - top));
+        ref = top;
+      }
+      // A barrier of its own: a parity of pv_done tells two tiles apart, and this warp has not seen the other warpgroup's.
+      ok = warp_wait_all(&br.o_full, n & 1u, p.err);
+      if (!ok) break;
+      tc_fence_after();
+      if (!idle) {
+        const float me = ref == -INFINITY ? 0.f : ref;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float z = l == 0.f ? -INFINITY : (me + log2f(l)) * kLn2;
+        const int64_t tok = (int64_t)u.tok + kHalf * (int)rank + row;
+        constexpr int kCols = kDv / 2;  // of this warpgroup
+        const bool whole = u.np == 1;
+        float* part = p.part_out + ((int64_t)u.slot * kTok + kHalf * (int)rank + row) * kDv + kCols * g;
+        uint16_t* o = p.out + (tok * p.H + u.h) * kDv + kCols * g;
+        bool bad = false;
+#pragma unroll 1
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(lane_base + Sh::kColO + kCols * g + 32 * c, x);
+          tmem_wait_ld();
+          if (l == 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) bad |= !(fabsf(__uint_as_float(x[j])) <= 3.4028235e38f);
+          if (there) {
+            if (whole) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  y[k] = pack_bf16(__uint_as_float(x[8 * j + 2 * k]) * inv, __uint_as_float(x[8 * j + 2 * k + 1]) * inv);
+                *reinterpret_cast<uint4*>(o + 32 * c + 8 * j) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4*>(part + 32 * c + 4 * j) =
+                    make_float4(__uint_as_float(x[4 * j]) * inv, __uint_as_float(x[4 * j + 1]) * inv, __uint_as_float(x[4 * j + 2]) * inv,
+                                __uint_as_float(x[4 * j + 3]) * inv);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive_cta(o_free);
+        for (uint32_t again = __ballot_sync(0xffffffffu, there && bad && l <= 3.4028235e38f); again; again &= again - 1) {
+          const int r = __ffs(again) - 1;
+          float acc[kCols / 32];
+          if (!rescue<kDn, kDv>(p, u, tok - lane + r, __shfl_sync(0xffffffffu, see, r), __shfl_sync(0xffffffffu, me, r),
+                                __shfl_sync(0xffffffffu, inv, r), kCols * g, acc))
+            continue;
+#pragma unroll
+          for (int e = 0; e < kCols / 32; ++e) {
+            if (whole)
+              p.out[((tok - lane + r) * p.H + u.h) * kDv + kCols * g + 32 * e + lane] = (uint16_t)(pack_bf16(acc[e], 0.f) & 0xFFFFu);
+            else
+              (part + (int64_t)(r - lane) * kDv)[32 * e + lane] = acc[e];
+          }
+        }
+        __syncwarp();
+        if (whole) {
+          if (g == 0 && there && p.lse) p.lse[tok * p.H + u.h] = z;
+        } else {
+          const int at = kHalf * (int)rank + row;
+          p.part_lse[((int64_t)u.slot * 2 + g) * kTok + at] = z;
+          __threadfence();
+          __syncwarp();
+          int before = 0;
+          if (lane == 0) before = atomicAdd(&p.joined[(int64_t)u.first * 16 + 8 * (int)rank + mine], 1);
+          before = __shfl_sync(0xffffffffu, before, 0);
+          if (before == u.np - 1) {
+            // The last piece to end joins them all, in their order: eight lanes to a token, kCols / 8 values to a lane.
+            __threadfence();
+            constexpr int kEach = kCols / 8;
+            const int sub = lane & 7;
+#pragma unroll 1
+            for (int r4 = 0; r4 < 32; r4 += 4) {
+              const int rr = 32 * quad + r4 + (lane >> 3);  // of this CTA
+              if (rr >= have) continue;
+              const int rp = kHalf * (int)rank + rr;
+              float top = -INFINITY;
+              for (int k = 0; k < u.np; ++k) {
+                const float y = __ldcg(&p.part_lse[((int64_t)(u.first + k) * 2 + g) * kTok + rp]);
+                top = y > top || y != y ? y : top;  // NaN stays
+              }
+              float acc[kEach], sum = 0.f;
+#pragma unroll
+              for (int j = 0; j < kEach; ++j) acc[j] = 0.f;
+              for (int k = 0; k < u.np; ++k) {
+                const float y = __ldcg(&p.part_lse[((int64_t)(u.first + k) * 2 + g) * kTok + rp]);
+                if (y == -INFINITY) continue;
+                const float wgt = exp2f((y - top) * kLog2e);
+                sum += wgt;
+                const float4* src = reinterpret_cast<const float4*>(p.part_out + ((int64_t)(u.first + k) * kTok + rp) * kDv + kCols * g + kEach * sub);
+#pragma unroll
+                for (int j = 0; j < kEach / 4; ++j) {
+                  const float4 f = __ldcg(src + j);
+                  acc[4 * j] = fmaf(wgt, f.x, acc[4 * j]);
+                  acc[4 * j + 1] = fmaf(wgt, f.y, acc[4 * j + 1]);
+                  acc[4 * j + 2] = fmaf(wgt, f.z, acc[4 * j + 2]);
+                  acc[4 * j + 3] = fmaf(wgt, f.w, acc[4 * j + 3]);
+                }
+              }
+              const float k1 = sum == 0.f ? 0.f : 1.f / sum;
+              const int64_t tk = (int64_t)u.tok + rp;
+              uint16_t* to = p.out + (tk * p.H + u.h) * kDv + kCols * g + kEach * sub;
+#pragma unroll
+              for (int j = 0; j < kEach / 8; ++j) {
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = pack_bf16(acc[8 * j + 2 * k] * k1, acc[8 * j + 2 * k + 1] * k1);
+                *reinterpret_cast<uint4*>(to + 8 * j) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+              if (g == 0 && sub == 0 && p.lse) p.lse[tk * p.H + u.h] = sum == 0.f ? -INFINITY : top + logf(sum);
+            }
+          }
+        }
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) remote_arrive_cta(o_free);
+      }
+      __syncwarp();
+      if (lane == 0) us.give_back(n);
+    }
+  }
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while the other may still signal or read it
+  if (warp == 0) {
+    tc_fence_after();
+    tc2::dealloc(tmem, 512);
+  }
+}
+
+template <int kDn, int kDv>
+static cudaError_t launch(const Params& p, cudaStream_t stream, const char** why) {
+  using Sh = Shape<kDn, kDv>;
+  auto kernel = expanded_kernel<kDn, kDv>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mq, mk, mr, mv;
+  if (!pair::encode_heads(&mq, p.q, kDn + HS_D_ROPE, p.H, p.T, p.q_stride_h, p.q_stride_t, kHalf) ||
+      !pair::encode_heads(&mk, p.kv, kDn + kDv, p.H, p.N, kDn + kDv, p.kv_stride, kKeys / 2) ||
+      !pair::encode_heads(&mv, p.kv, kDn + kDv, p.H, p.N, kDn + kDv, p.kv_stride, kKeys) ||
+      !encode_2d(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.rope, HS_D_ROPE, (uint64_t)p.N, (uint64_t)p.rope_stride * 2, 64, kKeys / 2,
+                 CU_TENSOR_MAP_SWIZZLE_128B)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_next(kernel, dim3(2 * p.clusters), kThreads, Sh::kSmem, stream, mq, mk, mr, mv, p);
+}
+
+// Workspace: totals, requests, joins, log-sum-exps and outputs of pieces.
+static uint64_t up(uint64_t v) { return (v + 127) / 128 * 128; }
+static uint64_t off_req() { return 128; }
+static uint64_t off_joined(int B) { return off_req() + up((uint64_t)B * sizeof(Req)); }
+static uint64_t off_lse(int B, int cap) { return off_joined(B) + up((uint64_t)cap * 16 * 4); }
+static uint64_t off_out(int B, int cap) { return off_lse(B, cap) + up((uint64_t)cap * 2 * kTok * 4); }
+
+}  // namespace expanded
+
+uint64_t mla_expanded_workspace_bytes(int B, int Dv, int sms) {
+  using namespace expanded;
+  const int cap = kPerPair * (sms / 2);
+  return off_out(B, cap) + (uint64_t)cap * kTok * Dv * 4;
+}
+
+cudaError_t launch_mla_expanded(const hs_mla_expanded_args* a, int sms, cudaStream_t stream, const char** why) {
+  using namespace expanded;
+  Params p;
+  p.T = a->T, p.B = a->B, p.H = a->H, p.causal = a->causal, p.clusters = sms / 2, p.cap = kPerPair * (sms / 2);
+  p.q = a->q, p.q_stride_t = a->q_stride_t, p.q_stride_h = a->q_stride_h;
+  p.kv = a->kv, p.kv_stride = a->kv_stride, p.N = a->N;
+  p.rope = a->rope, p.rope_stride = a->rope_stride;
+  p.req_start = a->req_start, p.kv_start = a->kv_start;
+  p.scale_log2 = fabsf(a->softmax_scale) * kLog2e;
+  p.flip = a->softmax_scale < 0.f ? 0x80000000u : 0u;
+  p.out = a->out, p.lse = a->lse, p.err = a->err_flag;
+  uint8_t* w = reinterpret_cast<uint8_t*>(a->workspace);
+  p.total = reinterpret_cast<int32_t*>(w);
+  p.req = reinterpret_cast<Req*>(w + off_req());
+  p.joined = reinterpret_cast<int32_t*>(w + off_joined(a->B));
+  p.part_lse = reinterpret_cast<float*>(w + off_lse(a->B, p.cap));
+  p.part_out = reinterpret_cast<float*>(w + off_out(a->B, p.cap));
+  return a->Dv == 128 ? launch<128, 128>(p, stream, why) : launch<192, 256>(p, stream, why);
+}
+
+}  // namespace hs

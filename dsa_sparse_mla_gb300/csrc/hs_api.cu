@@ -29,6 +29,12 @@ cudaError_t launch_fork(const hs_kv_fork_args* a, cudaStream_t stream);
 cudaError_t launch_free(const hs_kv_free_args* a, cudaStream_t stream);
 cudaError_t launch_compact(const hs_kv_compact_args* a, int sms, cudaStream_t stream);
 uint64_t compact_workspace_bytes(int64_t nblk);
+cudaError_t launch_kv_read(const hs_kv_read_args* a, int sms, cudaStream_t stream);
+cudaError_t launch_mla_absorb(const hs_mla_heads_args* a, int sms, cudaStream_t stream, const char** why);
+cudaError_t launch_mla_project(const hs_mla_heads_args* a, int sms, cudaStream_t stream, const char** why);
+cudaError_t launch_mla_expand(const hs_mla_expand_args* a, int sms, cudaStream_t stream, const char** why);
+cudaError_t launch_mla_expanded(const hs_mla_expanded_args* a, int sms, cudaStream_t stream, const char** why);
+uint64_t mla_expanded_workspace_bytes(int B, int Dv, int sms);
 }  // namespace hs
 
 namespace {
@@ -452,6 +458,120 @@ hs_status hs_kv_compact(const hs_kv_compact_args* a, hs_stream_t stream) {
   hs_status st = check_device(&sms);
   if (st != HS_OK) return st;
   return launched(hs::launch_compact(a, sms, (cudaStream_t)stream), "hs_kv_compact", nullptr);
+}
+
+hs_status hs_kv_read(const hs_kv_read_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->B >= 1 && a->n >= 0, "need B >= 1 and n >= 0 (B=%d, n=%lld)", a->B, (long long)a->n);
+  REQUIRE(a->dtype == HS_BF16 || a->dtype == HS_FP16 || a->dtype == HS_FP32, "dtype must be HS_BF16, HS_FP16 or HS_FP32 (got %d)",
+          a->dtype);
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->n == 0) return ok();
+  REQUIRE(a->kv_pool && a->block_table && a->out_start && a->out, "a required pointer is NULL");
+  REQUIRE(a->R >= 1 && a->bt_stride >= 1, "R and bt_stride must be >= 1");
+  REQUIRE(a->n <= INT32_MAX, "n must be at most 2^31 - 1");
+  REQUIRE(aligned16(a->kv_pool) && aligned16(a->out), "kv_pool and out must be 16-byte aligned");
+  REQUIRE(a->out_stride >= HS_D_QK && a->out_stride % (a->dtype == HS_FP32 ? 4 : 8) == 0,
+          "out_stride must be >= 576 and a multiple of 16 bytes (got %lld)", (long long)a->out_stride);
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  return launched(hs::launch_kv_read(a, sms, (cudaStream_t)stream), "hs_kv_read", nullptr);
+}
+
+// Strides that TMA can step by: positive multiples of 16 bytes, below 2^40 bytes.
+static bool tma_stride(int64_t values) { return values > 0 && values % 8 == 0 && values < ((int64_t)1 << 38); }
+static bool head_dim(int32_t d) { return d == 64 || d == 128 || d == 192 || d == 256; }
+
+static hs_status check_heads(const hs_mla_heads_args* a) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->T >= 0 && a->H >= 1 && a->H <= 1024, "need T >= 0 and H in [1, 1024] (T=%d, H=%d)", a->T, a->H);
+  REQUIRE(head_dim(a->Dn) && head_dim(a->Dv), "Dn and Dv must be 64, 128, 192 or 256 (got %d, %d)", a->Dn, a->Dv);
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->T == 0) return HS_OK;
+  REQUIRE(a->x && a->w && a->out, "a required pointer is NULL");
+  REQUIRE(aligned16(a->x) && aligned16(a->w) && aligned16(a->out), "x, w and out must be 16-byte aligned");
+  REQUIRE(tma_stride(a->x_stride_t) && tma_stride(a->x_stride_h) && tma_stride(a->out_stride_t) && tma_stride(a->out_stride_h),
+          "strides must be positive multiples of 8");
+  return HS_OK;
+}
+
+hs_status hs_mla_absorb(const hs_mla_heads_args* a, hs_stream_t stream) {
+  hs_status st = check_heads(a);
+  if (st != HS_OK) return st;
+  if (a->T == 0) return ok();
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != HS_OK) return st;
+  const char* why = nullptr;
+  return launched(hs::launch_mla_absorb(a, sms, (cudaStream_t)stream, &why), "hs_mla_absorb", why);
+}
+
+hs_status hs_mla_project(const hs_mla_heads_args* a, hs_stream_t stream) {
+  hs_status st = check_heads(a);
+  if (st != HS_OK) return st;
+  if (a->T == 0) return ok();
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != HS_OK) return st;
+  const char* why = nullptr;
+  return launched(hs::launch_mla_project(a, sms, (cudaStream_t)stream, &why), "hs_mla_project", why);
+}
+
+hs_status hs_mla_expand(const hs_mla_expand_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->N >= 0 && a->H >= 1 && a->H <= 1024, "need N >= 0 and H in [1, 1024] (N=%d, H=%d)", a->N, a->H);
+  REQUIRE(a->width >= 64 && a->width <= 512 && a->width % 64 == 0, "width must be a multiple of 64 in [64, 512] (got %d)", a->width);
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->N == 0) return ok();
+  REQUIRE(a->latent && a->w && a->kv, "a required pointer is NULL");
+  REQUIRE(aligned16(a->latent) && aligned16(a->w) && aligned16(a->kv), "latent, w and kv must be 16-byte aligned");
+  REQUIRE(tma_stride(a->latent_stride) && tma_stride(a->kv_stride), "strides must be positive multiples of 8");
+  REQUIRE(a->latent_stride >= HS_D_LATENT && a->kv_stride >= (int64_t)a->H * a->width,
+          "latent_stride must be >= 512 and kv_stride >= H * width");
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  const char* why = nullptr;
+  return launched(hs::launch_mla_expand(a, sms, (cudaStream_t)stream, &why), "hs_mla_expand", why);
+}
+
+hs_status hs_mla_expanded_workspace_size(int32_t B, int32_t Dv, uint64_t* bytes) {
+  REQUIRE(bytes, "bytes is NULL");
+  REQUIRE(B >= 1 && B <= 4096, "B must be in [1, 4096] (got %d)", B);
+  REQUIRE(Dv == 128 || Dv == 256, "Dv must be 128 or 256 (got %d)", Dv);
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  *bytes = hs::mla_expanded_workspace_bytes(B, Dv, sms);
+  return ok();
+}
+
+hs_status hs_mla_expanded_fwd(const hs_mla_expanded_args* a, hs_stream_t stream) {
+  REQUIRE(a, "args is NULL");
+  REQUIRE(a->T >= 0 && a->B >= 1 && a->B <= 4096, "need T >= 0 and B in [1, 4096] (T=%d, B=%d)", a->T, a->B);
+  REQUIRE(a->H >= 1 && a->H <= 1024, "H must be in [1, 1024] (got %d)", a->H);
+  REQUIRE((a->Dn == 128 && a->Dv == 128) || (a->Dn == 192 && a->Dv == 256), "Dn and Dv must be 128 and 128, or 192 and 256 (got %d, %d)",
+          a->Dn, a->Dv);
+  REQUIRE(a->err_flag, "err_flag is NULL");
+  if (a->T == 0) return ok();
+  REQUIRE(a->q && a->kv && a->rope && a->req_start && a->kv_start && a->out && a->workspace, "a required pointer is NULL");
+  REQUIRE(aligned16(a->q) && aligned16(a->kv) && aligned16(a->rope) && aligned16(a->out) && aligned16(a->workspace),
+          "q, kv, rope, out and workspace must be 16-byte aligned");
+  REQUIRE(a->N >= 1 && a->N <= INT32_MAX - 512, "N must be in [1, 2^31 - 513] (got %lld)", (long long)a->N);
+  REQUIRE(tma_stride(a->q_stride_t) && tma_stride(a->q_stride_h) && tma_stride(a->kv_stride) && tma_stride(a->rope_stride),
+          "strides must be positive multiples of 8");
+  REQUIRE(a->kv_stride >= (int64_t)a->H * (a->Dn + a->Dv) && a->rope_stride >= HS_D_ROPE, "kv_stride or rope_stride is too small");
+  REQUIRE((int64_t)a->T * a->H <= INT32_MAX - 1024 * 512, "T * H too large");
+  REQUIRE(isfinite(a->softmax_scale), "softmax_scale is not finite");
+  int sms = 0;
+  hs_status st = check_device(&sms);
+  if (st != HS_OK) return st;
+  const uint64_t need = hs::mla_expanded_workspace_bytes(a->B, a->Dv, sms);
+  REQUIRE(a->workspace_bytes >= need, "workspace holds %llu bytes; these sizes need %llu on this device",
+          (unsigned long long)a->workspace_bytes, (unsigned long long)need);
+  const char* why = nullptr;
+  return launched(hs::launch_mla_expanded(a, sms, (cudaStream_t)stream, &why), "hs_mla_expanded_fwd", why);
 }
 
 }  // extern "C"

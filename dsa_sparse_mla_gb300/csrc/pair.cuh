@@ -1,0 +1,73 @@
+// pair.cuh — device helpers for clusters of two CTAs that work as one (two-SM tensor products): TMA copies and expected bytes
+// counted on a barrier of either CTA, 16-byte stores into either CTA's shared memory that count there, TMA stores.
+#pragma once
+
+#include "cluster.cuh"
+
+namespace hs {
+namespace pair {
+
+// 2-D tiled load into this CTA's shared memory, its bytes counted on a barrier of either CTA of the pair (address from
+// remote_smem). x must be a multiple of 16 bytes.
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Arrives on a barrier of either CTA and has it expect these bytes. Relaxed: the arrival hands on no writes of this thread.
+__device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// 16 bytes into either CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void st_async16(uint32_t dst, int4 v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(dst), "r"(bar),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// 3-D tiled store of one box; what lies outside the tensor is left out. Coordinates are not negative, x a multiple of 16 bytes.
+__device__ __forceinline__ void store_3d(const CUtensorMap* map, const void* src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(smem_u32(src)), "r"(x),
+               "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most kLeft of this thread's store groups still read shared memory.
+template <int kLeft>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// After a wait that ran out: gives copies in flight, which take microseconds, 20 ms to land before the CTA leaves.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 20000000ull) __nanosleep(1000);
+}
+
+// Tensor map of a bf16 [rows][heads][cols] tensor (strides in values) with boxes of box_rows x 64 columns of one head, 128-byte swizzle.
+inline bool encode_heads(CUtensorMap* map, const void* base, uint64_t cols, uint64_t heads, uint64_t rows, int64_t stride_h, int64_t stride_t,
+                         uint32_t box_rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cols, heads, rows};
+  cuuint64_t strides[2] = {(cuuint64_t)stride_h * 2, (cuuint64_t)stride_t * 2};
+  cuuint32_t box[3] = {64, 1, box_rows}, es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace pair
+}  // namespace hs

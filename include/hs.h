@@ -23,6 +23,11 @@
  *   hs_kv_copy_pages, hs_kv_fork, hs_kv_free, hs_kv_compact
  *                       the pages of the cache: copied, shared with a forked request, given back,
  *                       moved together
+ *   hs_kv_read          rows of the cache back as 16- or 32-bit values
+ *   hs_mla_absorb, hs_mla_project, hs_mla_expand
+ *                       between heads and latent vectors: queries into the latent space, latent
+ *                       outputs to values, latent rows to keys and values
+ *   hs_mla_expanded_fwd dense attention over expanded keys and values (prompts)
  *
  * Sources (web pages describing GLM-5.x serving with DSA in vLLM):
  *   [P1] "vLLM v0.32.0 GLM-5.3 サービング: 16基のH200上でのPCP、DCP、およびハイブリッドHiSparse"
@@ -678,6 +683,135 @@ typedef struct {
 
 hs_status hs_kv_compact(const hs_kv_compact_args* a, hs_stream_t stream);
 hs_status hs_kv_compact_workspace_size(int64_t nblk, uint64_t* bytes);
+
+/* ------------------------------------------------------------------------------------------
+ * hs_kv_read — rows of the paged cache read back.
+ *
+ * [P1] 「数字がうまくいく理由」 gives the 656-byte row that hs_kv_append writes and the attention calls
+ * dequantise for themselves; this call gives the values to everything else (the expanded form below, checks of the
+ * quantisation). Row first[r] + i of request r goes to row out_start[r] + i of out, for
+ * 0 <= i < out_start[r + 1] - out_start[r]: 512 latent values code * scale (the product rounded to fp32, then to the type) and the
+ * 64 rotary values as stored, one after the other. Rows of out that belong to no request stay as they are.
+ *
+ *   B              requests (>= 1)
+ *   kv_pool, R     uint8 [R, 656] (16-byte aligned)
+ *   block_table    int32 [B, bt_stride]
+ *   first          int32 [B], or NULL: from row 0
+ *   out_start      int32 [B + 1], ascending, out_start[0] = 0, out_start[B] <= n
+ *   n, out         rows of out; HS_BF16, HS_FP16 or HS_FP32 [n, 576] with out_stride values from row to row (>= 576; address and stride
+ *                  multiples of 16 bytes)
+ *   err_flag       offsets out of order or past n set HS_FLAG_BAD_INDEX, a row outside the table's pages HS_FLAG_BAD_LENGTH, a block outside
+ *                  the pool HS_FLAG_BAD_BLOCK; a row that cannot be read becomes zeros
+ * Asynchronous on `stream`; allocates nothing.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B, bt_stride, dtype;
+  const uint8_t* kv_pool;
+  int64_t R;
+  const int32_t* block_table;
+  const int32_t* first;
+  const int32_t* out_start;
+  int64_t n;
+  void* out;
+  int64_t out_stride;
+  int32_t* err_flag;
+} hs_kv_read_args;
+
+hs_status hs_kv_read(const hs_kv_read_args* a, hs_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The products between latent vectors and heads. [P1] 「再現方法と必要なフラグ」 runs the attention in MQA form: every head's query is
+ * taken into the latent space, so that one cached row serves all heads, and the latent output is taken back. The layer's weight
+ * w bf16 [H, Dn + Dv, 512] (contiguous) makes head h's Dn key values (its first Dn rows) and Dv values (the others) of a
+ * latent vector c:  k = w[h, :Dn] c,  v = w[h, Dn:] c.  Then <q, k> = <q w[h, :Dn], c> and sum_j p_j v_j = w[h, Dn:] sum_j p_j c_j:
+ *
+ *   hs_mla_absorb    out[t, h, :] = x[t, h, :Dn] w[h, :Dn]        bf16 [T, H, Dn]  -> [T, H, 512]   (before hs_paged_mla_fwd)
+ *   hs_mla_project   out[t, h, :] = w[h, Dn:] x[t, h, :512]       bf16 [T, H, 512] -> [T, H, Dv]    (after it)
+ *   hs_mla_expand    kv[n, h, :]  = w[h] latent[n, :]             bf16 [N, 512]    -> [N, H, Dn + Dv]
+ *
+ * Products are summed in fp32 and rounded to bf16 once. Dn and Dv are 64, 128, 192 or 256, 1 <= H <= 1024. x and out have strides (in
+ * values) from token to token and head to head, so that slices of wider heads can be read and written in place (the latent part
+ * of a 576-wide query, say); every pointer is 16-byte aligned and every stride a positive multiple of 8. x and out must not overlap.
+ * err_flag receives HS_FLAG_TIMEOUT only. Asynchronous on `stream`; allocates nothing.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, H, Dn, Dv;
+  const uint16_t* x;
+  int64_t x_stride_t, x_stride_h;
+  const uint16_t* w;
+  uint16_t* out;
+  int64_t out_stride_t, out_stride_h;
+  int32_t* err_flag;
+} hs_mla_heads_args;
+
+hs_status hs_mla_absorb(const hs_mla_heads_args* a, hs_stream_t stream);
+hs_status hs_mla_project(const hs_mla_heads_args* a, hs_stream_t stream);
+
+typedef struct {
+  int32_t N, H, width;     /* width: Dn + Dv, a multiple of 64 up to 512 */
+  const uint16_t* latent;  /* [N, 512], latent_stride values from row to row */
+  int64_t latent_stride;
+  const uint16_t* w;
+  uint16_t* kv;            /* [N, H, width], kv_stride values from row to row (>= H * width) */
+  int64_t kv_stride;
+  int32_t* err_flag;
+} hs_mla_expand_args;
+
+hs_status hs_mla_expand(const hs_mla_expand_args* a, hs_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * hs_mla_expanded_fwd — dense attention of each request's new tokens over expanded keys and values.
+ *
+ * The other form of hs_paged_mla_fwd: (Dn + 64 + Dv) products a head and row instead of 576 + 512, which pays for prompts (their keys
+ * and values, expanded once, serve many tokens); single tokens are better off in the absorbed form. Request r's new
+ * tokens are req_start[r] .. req_start[r + 1] - 1, its rows kv_start[r] .. kv_start[r + 1] - 1, the new tokens' own the last of them.
+ * With m new tokens and n rows its i-th new token sees the first n - m + 1 + i rows (causal != 0; none where that is <= 0) or all n:
+ *   logit_j = softmax_scale * (<q[t,h,:Dn], kv[j,h,:Dn]> + <q[t,h,Dn:], rope[j,:]>)
+ *   out[t,h,:] = sum_j softmax(logit)_j * kv[j,h,Dn:],   lse[t,h] = ln sum_j exp(logit_j)
+ * A token that sees no row gets out = 0, lse = -inf. Rows that a token does not see never reach its output, whatever they hold.
+ *
+ * Compute precision: products of bf16 values and P rounded to bf16, accumulation, maxima and sums fp32, pieces of a split block fp32.
+ *
+ *   T, B, H       new tokens in all, requests (1 <= B <= 4096), heads (1 <= H <= 1024)
+ *   Dn, Dv        128 and 128, or 192 and 256
+ *   q             bf16 [T, H, Dn + 64], the rotary part last, with strides from token to token and head to head
+ *   kv, N         bf16 [N, H, Dn + Dv] (hs_mla_expand), kv_stride values from row to row; N >= 1 rows
+ *   rope          bf16 [N, 64], rope_stride values from row to row (the last values of hs_kv_read's rows)
+ *                 (q, kv and rope 16-byte aligned, strides positive multiples of 8)
+ *   req_start     int32 [B + 1], ascending, req_start[0] = 0, req_start[B] = T
+ *   kv_start      int32 [B + 1], ascending, within [0, N]
+ *   out, lse      bf16 [T, H, Dv] (16-byte aligned);  fp32 [T, H] or NULL
+ *   err_flag      a request's token offsets out of order set HS_FLAG_BAD_INDEX (its outputs are not written), row offsets out of order or
+ *                 past N HS_FLAG_BAD_LENGTH (the request sees no row)
+ *   workspace     hs_mla_expanded_workspace_size() bytes of 16-byte aligned device memory, scratch; calls that share one must not
+ *                 overlap on the GPU
+ * The same call gives the same bits each time. How a block's rows are split, and so its last bits, depends on all of the batch's
+ * lengths. Asynchronous on `stream`; allocates nothing.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, B, H, Dn, Dv, causal;
+  const uint16_t* q;
+  int64_t q_stride_t, q_stride_h;
+  const uint16_t* kv;
+  int64_t kv_stride;
+  int64_t N;
+  const uint16_t* rope;
+  int64_t rope_stride;
+  const int32_t* req_start;
+  const int32_t* kv_start;
+  float softmax_scale;
+  uint16_t* out;
+  float* lse;
+  int32_t* err_flag;
+  void* workspace;
+  uint64_t workspace_bytes;
+} hs_mla_expanded_args;
+
+hs_status hs_mla_expanded_fwd(const hs_mla_expanded_args* a, hs_stream_t stream);
+
+/* Bytes of workspace hs_mla_expanded_fwd needs for B requests and Dv values per head on the current device: about 61 MB
+ * (Dv = 128) or 121 MB (256) for pieces of split blocks. */
+hs_status hs_mla_expanded_workspace_size(int32_t B, int32_t Dv, uint64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,216 @@
+"""hs_kv_read, hs_mla_absorb, hs_mla_project, hs_mla_expand and hs_mla_expanded_fwd against 64-bit references."""
+import math
+
+import pytest
+import torch
+
+import dsa_sparse_mla_gb300 as hs
+import latent_ops as plain
+import plain_ops
+
+pytestmark = pytest.mark.gpu
+
+
+def err():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def gen(seed=0):
+    return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------ the cache read back ----
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("lens,first,wide", [([1], [0], 0), ([64, 0, 1, 63, 65], [0, 0, 3, 2, 64], 8), ([0, 0, 700], [1, 0, 5], 0),
+                                             ([5] * 70, list(range(70)), 64)])
+def test_read(dtype, lens, first, wide):
+    b = plain_ops.make_batch([1] * len(lens), [f + n for f, n in zip(first, lens)], 1)
+    n = sum(lens)
+    out = torch.full((n + 3, 576 + wide), 7.0, dtype=dtype, device="cuda")
+    e = err()
+    hs.hs_kv_read(b["pool"], b["table"], plain.starts(lens).cuda(), out[:, :576], e, first=torch.tensor(first, dtype=torch.int32, device="cuda"))
+    assert hs.hs_check_flag(e) == 0
+    ref = []
+    for r, (f, m) in enumerate(zip(first, lens)):
+        j = torch.arange(f, f + m, device="cuda")
+        ref.append(torch.cat(plain_ops.read_rows(b["pool"][b["table"][r].long()[j // 64] * 64 + j % 64]), 1))
+    ref = torch.cat(ref)
+    step = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 0.0}[dtype]
+    low = 2.0 ** -25 if dtype is torch.float16 else 0.0  # half of fp16's smallest step
+    assert bool(((out[:n, :576].double() - ref).abs() <= ref.abs() * (step + 2.0 ** -24) * (1 + 2.0 ** -8) + low).all())
+    assert bool((out[n:] == 7).all()) and bool((out[:, 576:] == 7).all())
+
+
+def test_read_without_first_and_its_flags():
+    b = plain_ops.make_batch([1, 1], [100, 130], 1)
+    out, e = torch.full((230, 576), 7.0, device="cuda"), err()
+    start = plain.starts([100, 130]).cuda()
+    hs.hs_kv_read(b["pool"], b["table"], start, out, e)
+    assert hs.hs_check_flag(e) == 0 and bool(out.isfinite().all()) and not bool((out == 7).all(1).any())
+    table = b["table"].clone()
+    table[0, 1], table[1, 0] = -1, b["pool"].shape[0] // 64
+    hs.hs_kv_read(b["pool"], table, start, out, e)
+    assert hs.hs_check_flag(e) == hs.FLAGS["BAD_BLOCK"]
+    assert not out[64:164].any() and bool(out[:64].any(1).all()) and bool(out[164:].any(1).all())
+    e = err()
+    far = torch.tensor([64 * table.shape[1] - 50, -1], dtype=torch.int32, device="cuda")
+    hs.hs_kv_read(b["pool"], b["table"], start, out, e, first=far)
+    assert hs.hs_check_flag(e) & hs.FLAGS["BAD_LENGTH"] and not out[50:101].any()
+    for bad in ([0, 120, 100], [0, 100, 231], [3, 100, 230]):
+        e = err()
+        hs.hs_kv_read(b["pool"], b["table"], torch.tensor(bad, dtype=torch.int32, device="cuda"), out, e)
+        assert hs.hs_check_flag(e) & hs.FLAGS["BAD_INDEX"]
+
+
+# ------------------------------------------------------------------ products ---------------
+SIZES = [(1, 1, 64, 64), (3, 2, 128, 128), (129, 3, 192, 256), (255, 1, 256, 64), (257, 5, 64, 192), (600, 2, 128, 256), (1030, 64, 128, 128)]
+
+
+@pytest.mark.parametrize("T,H,Dn,Dv", SIZES)
+def test_absorb(T, H, Dn, Dv):
+    g = gen(T)
+    q, w = plain.rand((T, H, Dn + 64), g).cuda(), plain.weights(H, Dn, Dv, g).cuda()
+    out, e = torch.full((T + 2, H, 576), 7.0, dtype=torch.bfloat16, device="cuda"), err()
+    hs.hs_mla_absorb(q[..., :Dn], w, out[:T, :, :512], e)
+    assert hs.hs_check_flag(e) == 0
+    ref, tol = plain.product(q[..., :Dn], w[:, :Dn], "thd,hdc->thc")
+    assert plain.holds(out[:T, :, :512], ref, tol)
+    assert bool((out[T:] == 7).all()) and bool((out[..., 512:] == 7).all())
+
+
+@pytest.mark.parametrize("T,H,Dn,Dv", SIZES)
+def test_project(T, H, Dn, Dv):
+    g = gen(T + 1)
+    x, w = plain.rand((T, H, 576), g).cuda(), plain.weights(H, Dn, Dv, g).cuda()
+    out, e = torch.full((T + 2, H, Dv + 8), 7.0, dtype=torch.bfloat16, device="cuda"), err()
+    hs.hs_mla_project(x[..., :512], w, out[:T, :, :Dv], e)
+    assert hs.hs_check_flag(e) == 0
+    ref, tol = plain.product(x[..., :512], w[:, Dn:], "thc,hdc->thd")
+    assert plain.holds(out[:T, :, :Dv], ref, tol)
+    assert bool((out[T:] == 7).all()) and bool((out[..., Dv:] == 7).all())
+
+
+@pytest.mark.parametrize("T,H,Dn,Dv", SIZES)
+def test_expand(T, H, Dn, Dv):
+    g = gen(T + 2)
+    c, w = plain.rand((T, 576), g).cuda(), plain.weights(H, Dn, Dv, g).cuda()
+    wide = torch.full((T + 2, H * (Dn + Dv) + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    kv, e = wide[:T, :H * (Dn + Dv)].unflatten(1, (H, Dn + Dv)), err()
+    hs.hs_mla_expand(c[:, :512], w, kv, e)
+    assert hs.hs_check_flag(e) == 0
+    ref, tol = plain.product(c[:, :512], w, "nc,hdc->nhd")
+    assert plain.holds(kv, ref, tol)
+    assert bool((wide[T:] == 7).all()) and bool((wide[:, H * (Dn + Dv):] == 7).all())
+
+
+def test_heads_apart():
+    """Heads first in memory ([H, T, D] storage), and results that equal those of the usual order bit for bit."""
+    g = gen(5)
+    T, H, Dn, Dv = 130, 4, 128, 128
+    q, x, w = plain.rand((H, T, Dn), g).cuda(), plain.rand((H, T, 512), g).cuda(), plain.weights(H, Dn, Dv, g).cuda()
+    a, b = (torch.empty((T, H, 512), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c, d = torch.empty((H, T, Dv), dtype=torch.bfloat16, device="cuda").transpose(0, 1), torch.empty((T, H, Dv), dtype=torch.bfloat16, device="cuda")
+    e = err()
+    hs.hs_mla_absorb(q.transpose(0, 1), w, a, e)
+    hs.hs_mla_absorb(q.transpose(0, 1).contiguous(), w, b, e)
+    hs.hs_mla_project(x.transpose(0, 1), w, c, e)
+    hs.hs_mla_project(x.transpose(0, 1).contiguous(), w, d, e)
+    assert hs.hs_check_flag(e) == 0 and torch.equal(a, b) and torch.equal(c, d)
+
+
+# ------------------------------------------------------------------ attention --------------
+def batch(q_lens, kv_lens, H, Dn, Dv, seed=0, sigma=1.0, spare=0):
+    g = gen(seed)
+    T, N = sum(q_lens), sum(kv_lens) + spare
+    q, kv, rows = plain.rand((T, H, Dn + 64), g, sigma), plain.rand((N, H, Dn + Dv), g), plain.rand((N, 576), g)
+    if spare:
+        kv[-spare:], rows[-spare:] = math.nan, math.nan
+    return dict(q=q.cuda(), kv=kv.cuda(), rope=rows.cuda()[:, 512:], req_start=plain.starts(q_lens).cuda(), kv_start=plain.starts(kv_lens).cuda(),
+                scale=(Dn + 64) ** -0.5)
+
+
+def attend(b, Dv, causal=True, e=None, workspace=None):
+    T, H, _ = b["q"].shape
+    out = torch.full((T, H, Dv), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    e = err() if e is None else e
+    if workspace is None:
+        workspace = torch.full((hs.hs_mla_expanded_workspace_size(b["req_start"].numel() - 1, Dv),), 0xFF, dtype=torch.uint8, device="cuda")
+    hs.hs_mla_expanded_fwd(b["q"], b["kv"], b["rope"], b["req_start"], b["kv_start"], b["scale"], out, e, workspace, lse=lse, causal=causal)
+    assert hs.hs_check_flag(e) == 0
+    return out, lse
+
+
+def check(b, Dn, Dv, causal=True):
+    out, lse = attend(b, Dv, causal)
+    ref, tol, rlse, ltol = plain.attention(b["q"], b["kv"], b["rope"], b["req_start"], b["kv_start"], Dn, b["scale"], causal)
+    assert plain.holds(lse, rlse, ltol)
+    assert plain.holds(out, ref, tol)
+
+
+HEADS = [(128, 128), (192, 256)]
+BATCHES = [([1], [1], 1), ([1], [700], 3), ([5], [3], 2), ([130], [130], 2), ([257], [300], 1), ([0, 3, 0], [9, 128, 0], 2),
+           ([1] * 9, [1, 2, 63, 64, 127, 128, 129, 255, 1000], 5), ([40, 1, 0, 300, 7], [40, 2000, 55, 129, 6], 4), ([600, 513], [600, 900], 2)]
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+@pytest.mark.parametrize("q_lens,kv_lens,H", BATCHES)
+def test_attention(q_lens, kv_lens, H, Dn, Dv):
+    check(batch(q_lens, kv_lens, H, Dn, Dv, spare=200), Dn, Dv)
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_attention_without_mask(Dn, Dv):
+    check(batch([3, 200, 0, 1], [150, 260, 4, 129], 3, Dn, Dv, spare=5), Dn, Dv, causal=False)
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_attention_splits_long_rows(Dn, Dv):
+    check(batch([1, 2, 20], [9000, 5000, 7001], 1, Dn, Dv, spare=3), Dn, Dv)
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_attention_scales_its_output(Dn, Dv):
+    """Logits that grow along the rows move the reference (and scale the output) at most tiles; negative and zero scales."""
+    b = batch([3, 140], [1500, 1000], 2, Dn, Dv, seed=3)
+    ramp = torch.linspace(0, 3, 2500, device="cuda")[:, None, None]
+    b["kv"][..., :Dn] = (b["q"][0, 0, :Dn].float() * ramp + b["kv"][..., :Dn].float()).bfloat16()
+    for scale in (b["scale"], -b["scale"], 0.0):
+        b["scale"] = scale
+        check(b, Dn, Dv)
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_attention_leaves_masked_rows_out(what, Dn, Dv):
+    """Values, keys and rotary keys that are not finite, in rows that some tokens do not see."""
+    for part in ("key", "value", "rope"):
+        b = batch([150, 1, 30], [400, 300, 1800], 2, Dn, Dv, seed=4)
+        rows = torch.tensor([399, 390, 2499, 2490, 2480], device="cuda")  # the last rows of the first and third request
+        if part == "key":
+            b["kv"][rows, :, 5] = what
+        elif part == "value":
+            b["kv"][rows, 1, Dn + 7] = what
+        else:
+            b["rope"][rows, 63] = what
+        out, lse = attend(b, Dv)
+        ref, tol, rlse, ltol = plain.attention(b["q"], b["kv"], b["rope"], b["req_start"], b["kv_start"], Dn, b["scale"])
+        clear = rlse.isfinite() & ref.isfinite().all(-1)  # tokens and heads that see none of them
+        assert int(clear.sum()) > 250
+        assert bool(((out.double() - ref).abs() <= tol)[clear].all()) and bool(((lse.double() - rlse).abs() <= ltol)[clear].all())
+        if what != -math.inf or part == "value":  # a key's -inf may leave its row out
+            bad = ~ref.isfinite()
+            assert bool(out[bad].isfinite().logical_not().all())
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_attention_again_and_again(Dn, Dv):
+    """Many units of few tokens and few tiles, and of few tokens and many, on every pair of CTAs: the same bits each time."""
+    for q_lens, kv_lens, H in (([1, 2, 40] * 30, [1, 130, 300] * 30, 16), ([1] * 20, [4000] * 20, 16), ([300] * 4, [300, 900, 2000, 310], 40)):
+        b = batch(q_lens, kv_lens, H, Dn, Dv, seed=5, spare=130)
+        ref, tol, rlse, ltol = plain.attention(b["q"], b["kv"], b["rope"], b["req_start"], b["kv_start"], Dn, b["scale"])
+        first = attend(b, Dv)
+        assert plain.holds(first[0], ref, tol) and plain.holds(first[1], rlse, ltol)
+        for _ in range(20):
+            again = attend(b, Dv)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
