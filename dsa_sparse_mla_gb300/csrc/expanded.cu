@@ -13,11 +13,12 @@
 // tile (64 of 128 rows of K, half of V's values). Tensor memory: two logit tiles, and with 128 values per head two tiles of P
 // and the output; with 256 values P goes through shared memory instead. In each CTA two warpgroups take the tiles in turn, a
 // thread to a token: it takes its 128 logits into registers at once, which frees the tile for the product after next, so that a
-// tile's softmax has two whole tiles' products (about 2,500 cycles) to hide under. A token's reference passes from one
-// warpgroup to the other through shared memory. The warpgroups also scale and write the output, under the next unit's products.
+// tile's softmax has two whole tiles' products to hide under. A token's reference passes from one warpgroup to the other through
+// shared memory. The warpgroups also scale and write the output, under the next unit's products.
 //
-// Order of copies and products: K of tile i + 2 before V of tile i, across units (the next unit's K may come before this one's last
-// V, not two units' before). Every role walks the same order on its own.
+// Issuing an MMA takes about as long as its execution once a few are under way, and what a warp does between two batches of them
+// (barriers, addresses; its code is cold in the instruction caches, which the softmax fills) takes several hundred cycles. So QK and
+// PV have a warp each, which work in each other's gaps, and K and V a ring of slots and a copying warp each.
 //
 // Rows past a request's end are masked as keys and set to zero as values (in shared memory, by a warp that waits for such a tile's copy).
 // A row that a token does not see can still reach its output where P = 0 meets a value that is not finite; where an output is not
@@ -31,8 +32,7 @@ namespace hs {
 namespace expanded {
 
 constexpr int kTok = 256, kHalf = 128, kKeys = 128;  // tokens of a block, of a CTA; rows of a tile
-constexpr int kThreads = 384;                        // copies, MMAs, units, tails; 2 x 128 softmax threads
-constexpr int kAhead = 3;                            // K's tiles before V's: QK of tile i + 2 is issued before PV of tile i
+constexpr int kThreads = 384;                        // Q and K, QK, PV (units in the other CTA), V; 2 x 128 softmax threads
 constexpr float kThreshold = 8.0f;                   // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -171,19 +171,18 @@ struct Shape {
   static constexpr int kQBlk = kHalf * 128, kQBytes = kQB * kQBlk;
   static constexpr int kKBlk = kKeys / 2 * 128, kKBytes = kQB * kKBlk;
   static constexpr int kVBlk = kKeys * 128, kVBytes = kDv / 128 * kVBlk;
-  static constexpr int kSlot = kKBytes > kVBytes ? kKBytes : kVBytes;
-  static constexpr int kSlots = kWide ? 3 : 7;
-  static constexpr int kPBlk = kHalf * 128, kPBuf = kWide ? 2 * kPBlk : 0;  // blocks of 64 rows of the cache
-  static constexpr int kOffRing = kQBytes, kOffP = kOffRing + kSlots * kSlot, kOffRef = kOffP + 2 * kPBuf;
+  static constexpr int kKSlots = kWide ? 2 : 4, kVSlots = kWide ? 2 : 5;
+  static constexpr int kPBlk = kHalf * 128, kPBytes = kWide ? 2 * kPBlk : 0;  // blocks of 64 cached rows
+  static constexpr int kOffK = kQBytes, kOffV = kOffK + kKSlots * kKBytes, kOffP = kOffV + kVSlots * kVBytes, kOffRef = kOffP + kPBytes;
   static constexpr int kOffSum = kOffRef + 1024, kOffUnit = kOffSum + 1024, kOffBar = kOffUnit + 2 * (int)sizeof(Unit);
   static constexpr int kSmem = kOffBar + 512;
   static constexpr int kColP = 256, kColO = kWide ? 256 : 384;  // tensor-memory columns; logits in 0 .. 255
-  static_assert(kDv % 128 == 0 && kDv <= 256 && kSmem <= 232448 && kSlot % 1024 == 0, "shared and tensor memory");
+  static_assert(kDv % 128 == 0 && kDv <= 256 && kSmem <= 232448, "shared and tensor memory");
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_full, o_free, drain;
-  uint64_t tail_full[2], tail_done[2], unit_full[2], unit_empty[2];
+  uint64_t k_full[4], k_empty[4], v_full[5], v_empty[5], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
+  uint64_t tail_full, unit_full[2], unit_empty[2];
   uint64_t ref[8], sum[8], sum_read[8];  // [warpgroup][quad]
   uint32_t tmem;
 };
@@ -218,43 +217,20 @@ struct Units {
   }
 };
 
-// The order of K and V tiles. step() says what comes next: K of (ku, kt), V of (vu, vt), or the end.
-struct Walk {
-  Unit ku, vu;
-  uint32_t kn, vn;     // numbers of ku and vu
-  int kt, vt;          // the next tile of each
-  int64_t k, v;        // tiles so far
-  bool end;            // no more units
-  enum What { kK, kV, kEnd, kFail };
-  __device__ __forceinline__ bool begin(const Units& us) {
-    kn = vn = 0, kt = vt = 0, k = v = 0;
-    if (!us.take(0, ku)) return false;
-    vu = ku;
-    end = ku.n == 0;
-    return true;
-  }
-  __device__ __forceinline__ What step(const Units& us) {
-#pragma unroll 1
-    for (;;) {
-      if (!end && kt == ku.n && kn == vn) {  // K goes one unit ahead of V at most
-        ++kn, kt = 0;
-        if (!us.take(kn, ku)) return kFail;
-        end = ku.n == 0;
-      }
-      if (!end && kt < ku.n && k - v < kAhead) return kK;
-      if (k == v) return kEnd;  // a unit has one tile at least, so K is at the end
-      if (vt < vu.n) return kV;
-      us.give_back(vn);
-      vu = ku;
-      ++vn, vt = 0;
-    }
-  }
-};
-
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// Whether the phase with this parity is over, without waiting.
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
 // A token's output values col0 .. col0 + kCols - 1 once more, from the rows that it sees alone, where a row of its tiles that it does not
@@ -311,27 +287,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   if (tid == 0) {
     for (int s = 0; s < 8; ++s) {
-      mbar_init(&br.full[s], 2);
-      mbar_init(&br.empty[s], 1);
       mbar_init(&br.ref[s], 1);
       mbar_init(&br.sum[s], 1);
       mbar_init(&br.sum_read[s], 1);
     }
+    for (int s = 0; s < 4; ++s) mbar_init(&br.k_full[s], 2), mbar_init(&br.k_empty[s], 1);
+    for (int s = 0; s < 5; ++s) mbar_init(&br.v_full[s], 2), mbar_init(&br.v_empty[s], 1);
     mbar_init(&br.q_full, 2);
     mbar_init(&br.q_empty, 1);
+    mbar_init(&br.tail_full, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&br.s_full[b], 1);
       mbar_init(&br.s_empty[b], 8);
       mbar_init(&br.p_full[b], 8);
       mbar_init(&br.pv_done[b], 1);
-      mbar_init(&br.tail_full[b], 1);
-      mbar_init(&br.tail_done[b], 1);
+      mbar_init(&br.drain[b], 1);
       mbar_init(&br.unit_full[b], 1);
-      mbar_init(&br.unit_empty[b], 21);  // copies, tails and eight softmax warps of both CTAs, the MMAs
+      mbar_init(&br.unit_empty[b], 22);  // copies of K, copies of V and eight softmax warps of both CTAs, QK, PV
     }
     mbar_init(&br.o_full, 1);
     mbar_init(&br.o_free, 16);
-    mbar_init(&br.drain, 1);
     mbar_fence_init();
     prefetch_tensormap(&map_q);
     prefetch_tensormap(&map_k);
@@ -345,130 +320,122 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = br.tmem;
   after_previous();  // the plan
-  const Units us = {smem + Sh::kOffUnit, &br, p.err, remote_smem(br.unit_empty, 0), lane == 0};
+  const Units us = {smem + Sh::kOffUnit, &br, p.err, remote_smem(br.unit_empty, 1), lane == 0};
 
   if (warp < 4) {
     // 384 threads start with 168 registers (64,512 in all): 128 keep 96, 256 take 200 (63,488)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    if (warp == 0 && lane == 0) {
-      // ================================================================ copies ==================
-      const uint32_t full = remote_smem(br.full, 0), q_full = remote_smem(&br.q_full, 0);
-      Ring ring = {0, 1};
-      uint32_t tails = 0;
-      Walk w;
-      bool ok = w.begin(us);
+    Unit u;
+    if (warp == 0) {
+      // ================================================================ Q and K =================
+      if (lane == 0) {
+        const uint32_t full = remote_smem(br.k_full, 0), q_full = remote_smem(&br.q_full, 0);
+        Ring ring = {0, 1};
+        bool ok = true;
 #pragma unroll 1
-      while (ok) {
-        const Walk::What what = w.step(us);
-        if (what == Walk::kEnd) break;
-        if (what == Walk::kFail) {
-          ok = false;
-          break;
-        }
-        if (what == Walk::kK && w.kt == 0) {
-          if (!mbar_wait(&br.q_empty, (w.kn & 1u) ^ 1u, p.err)) {
-            ok = false;
-            break;
-          }
+        for (uint32_t n = 0; ok; ++n) {
+          ok = us.take(n, u);
+          if (!ok || u.n == 0) break;
+          ok = mbar_wait(&br.q_empty, (n & 1u) ^ 1u, p.err);
+          if (!ok) break;
           pair::arrive_expect_tx(q_full, Sh::kQBytes);
-#pragma unroll
-          for (int b = 0; b < Sh::kQB; ++b) pair::load_3d(smem + b * Sh::kQBlk, &map_q, q_full, 64 * b, w.ku.h, w.ku.tok + kHalf * (int)rank);
-        }
-        if (!mbar_wait(&br.empty[ring.slot], ring.par, p.err)) {
-          ok = false;
-          break;
-        }
-        uint8_t* s = smem + Sh::kOffRing + ring.slot * Sh::kSlot;
-        uint32_t bar = full + 8 * (uint32_t)ring.slot;
-        if (what == Walk::kK) {
-          const int y = w.ku.kv0 + (w.ku.ta + w.kt) * kKeys + kKeys / 2 * (int)rank;
-          pair::arrive_expect_tx(bar, Sh::kKBytes);
-#pragma unroll
-          for (int b = 0; b < kDn / 64; ++b) pair::load_3d(s + b * Sh::kKBlk, &map_k, bar, 64 * b, w.ku.h, y);
-          pair::load_2d(s + kDn / 64 * Sh::kKBlk, &map_r, bar, 0, y);
-          ++w.kt, ++w.k;
-        } else {
-          const int tile = w.vu.ta + w.vt, y = w.vu.kv0 + tile * kKeys;
-          if (w.vu.len - tile * kKeys < kKeys) {  // counted on a barrier of this CTA; the tails' warp goes on from there
-            uint64_t* t = &br.tail_full[tails & 1u];
-            if (!mbar_wait(&br.tail_done[tails & 1u], ((tails >> 1) & 1u) ^ 1u, p.err)) {
-              ok = false;
-              break;
-            }
-            ++tails;
-            mbar_arrive_expect_tx(t, Sh::kVBytes);
-            bar = remote_smem(t, rank);
-          } else {
-            pair::arrive_expect_tx(bar, Sh::kVBytes);
-          }
-#pragma unroll
-          for (int b = 0; b < kDv / 128; ++b) pair::load_3d(s + b * Sh::kVBlk, &map_v, bar, kDn + kDv / 2 * (int)rank + 64 * b, w.vu.h, y);
-          ++w.vt, ++w.v;
-        }
-        ring.next(Sh::kSlots);
-      }
-      if (!ok) pair::let_copies_land();
-    } else if (warp == 1 && lane == 0 && rank == 0) {
-      // ================================================================ MMAs ====================
-      constexpr uint32_t id_s = idesc_bf16(kTok, kKeys, 0, 0), id_o = idesc_bf16(kTok, kDv, 0, 1);
-      const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2);
-      const uint64_t kd = smem_desc(smem_u32(smem + Sh::kOffRing), 16, 1024, 2);
-      const uint64_t vd = smem_desc(smem_u32(smem + Sh::kOffRing), Sh::kVBlk, 1024, 2);
-      const uint64_t pd = smem_desc(smem_u32(smem + Sh::kOffP), 16, 1024, 2);
-      Ring ring = {0, 0};
-      Walk w;
-      bool ok = w.begin(us);
 #pragma unroll 1
-      while (ok) {
-        const Walk::What what = w.step(us);
-        if (what == Walk::kEnd) break;
-        if (what == Walk::kFail) break;
-        const uint64_t off = (uint64_t)((ring.slot * Sh::kSlot) >> 4);
-        if (what == Walk::kK) {
-          const uint32_t b = (uint32_t)w.k & 1u;
-          if ((w.kt == 0 && !mbar_wait(&br.q_full, w.kn & 1u, p.err)) ||
-              !mbar_wait(&br.s_empty[b], ((uint32_t)(w.k >> 1) & 1u) ^ 1u, p.err) || !mbar_wait(&br.full[ring.slot], ring.par, p.err)) {
-            ok = false;
-            break;
+          for (int b = 0; b < Sh::kQB; ++b) pair::load_3d(smem + b * Sh::kQBlk, &map_q, q_full, 64 * b, u.h, u.tok + kHalf * (int)rank);
+          int y = u.kv0 + u.ta * kKeys + kKeys / 2 * (int)rank;
+#pragma unroll 1
+          for (int t = 0; t < u.n; ++t, y += kKeys) {
+            ok = mbar_wait(&br.k_empty[ring.slot], ring.par, p.err);
+            if (!ok) break;
+            uint8_t* s = smem + Sh::kOffK + ring.slot * Sh::kKBytes;
+            const uint32_t bar = full + 8 * (uint32_t)ring.slot;
+            pair::arrive_expect_tx(bar, Sh::kKBytes);
+#pragma unroll 1
+            for (int b = 0; b < kDn / 64; ++b) pair::load_3d(s + b * Sh::kKBlk, &map_k, bar, 64 * b, u.h, y);
+            pair::load_2d(s + kDn / 64 * Sh::kKBlk, &map_r, bar, 0, y);
+            ring.next(Sh::kKSlots);
           }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < Sh::kQB; ++k)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc2::ss(tmem + kKeys * b, qd + (uint64_t)((k * Sh::kQBlk + kk * 32) >> 4), kd + off + (uint64_t)((k * Sh::kKBlk + kk * 32) >> 4), id_s,
-                      (k | kk) != 0 ? 1u : 0u);
-          tc2::commit(&br.empty[ring.slot], 0x3);
-          tc2::commit(&br.s_full[b], 0x3);
-          ++w.kt, ++w.k;
-          if (w.kt == w.ku.n) tc2::commit(&br.q_empty, 0x3);
-        } else {
-          const uint32_t b = (uint32_t)w.v & 1u;
-          if ((w.vt == 0 && !mbar_wait(&br.o_free, (w.vn & 1u) ^ 1u, p.err)) || !mbar_wait(&br.full[ring.slot], ring.par, p.err) ||
-              !mbar_wait(&br.p_full[b], (uint32_t)(w.v >> 1) & 1u, p.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
-            const uint64_t vb = vd + off + (uint64_t)((kk * 2048) >> 4);
-            const uint32_t more = (w.vt | kk) != 0 ? 1u : 0u;
-            if (Sh::kWide)
-              tc2::ss(tmem + Sh::kColO, pd + (uint64_t)((b * Sh::kPBuf + (kk / 4) * Sh::kPBlk + (kk % 4) * 32) >> 4), vb, id_o, more);
-            else
-              tc2::ts(tmem + Sh::kColO, tmem + Sh::kColP + 64 * b + 8 * kk, vb, id_o, more);
-          }
-          tc2::commit(&br.empty[ring.slot], 0x3);
-          tc2::commit(&br.pv_done[b], 0x3);
-          ++w.vt, ++w.v;
-          if (w.vt == w.vu.n) tc2::commit(&br.o_full, 0x3);
+          us.give_back(n);
         }
-        ring.next(Sh::kSlots);
+        if (!ok) pair::let_copies_land();
       }
-      tc2::commit(&br.drain, 0x1);
-      mbar_wait(&br.drain, 0, p.err);
+    } else if (warp == 1 && rank == 0) {
+      // ================================================================ QK ======================
+      constexpr uint32_t id = idesc_bf16(kTok, kKeys, 0, 0);
+      const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2), kd = smem_desc(smem_u32(smem + Sh::kOffK), 16, 1024, 2);
+      Ring ring = {0, 0};
+      uint32_t i = 0;
+      if (lane == 0) {
+        bool ok = true;
+#pragma unroll 1
+        for (uint32_t n = 0; ok; ++n) {
+          ok = us.take(n, u);
+          if (!ok || u.n == 0) break;
+          ok = mbar_wait(&br.q_full, n & 1u, p.err);
+#pragma unroll 1
+          for (int t = 0; t < u.n && ok; ++t, ++i) {
+            const uint32_t b = i & 1u;
+            ok = mbar_wait(&br.k_full[ring.slot], ring.par, p.err) && mbar_wait(&br.s_empty[b], ((i >> 1) & 1u) ^ 1u, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            uint64_t a = qd, k = kd + (uint64_t)((ring.slot * Sh::kKBytes) >> 4);
+#pragma unroll 1
+            for (int blk = 0; blk < Sh::kQB; ++blk, a += Sh::kQBlk >> 4, k += Sh::kKBlk >> 4)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) tc2::ss(tmem + kKeys * b, a + 2 * kk, k + 2 * kk, id, (blk | kk) != 0 ? 1u : 0u);
+            tc2::commit(&br.s_full[b], 0x3);
+            tc2::commit(&br.k_empty[ring.slot], 0x3);
+            ring.next(Sh::kKSlots);
+          }
+          if (!ok) break;
+          tc2::commit(&br.q_empty, 0x3);
+          us.give_back(n);
+        }
+        tc2::commit(&br.drain[0], 0x1);
+        mbar_wait(&br.drain[0], 0, p.err);
+      }
     } else if (warp == 2 && rank == 0) {
+      // ================================================================ PV ======================
+      constexpr uint32_t id = idesc_bf16(kTok, kDv, 0, 1);
+      const uint64_t vd = smem_desc(smem_u32(smem + Sh::kOffV), Sh::kVBlk, 1024, 2), pd = smem_desc(smem_u32(smem + Sh::kOffP), 16, 1024, 2);
+      Ring ring = {0, 0};
+      uint32_t i = 0;
+      if (lane == 0) {
+        bool ok = true;
+#pragma unroll 1
+        for (uint32_t n = 0; ok; ++n) {
+          ok = us.take(n, u);
+          if (!ok || u.n == 0) break;
+          ok = mbar_wait(&br.o_free, (n & 1u) ^ 1u, p.err);
+#pragma unroll 1
+          for (int t = 0; t < u.n && ok; ++t, ++i) {
+            const uint32_t b = i & 1u;
+            ok = mbar_wait(&br.v_full[ring.slot], ring.par, p.err) && mbar_wait(&br.p_full[b], (i >> 1) & 1u, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            uint64_t v = vd + (uint64_t)((ring.slot * Sh::kVBytes) >> 4), w = pd;
+            uint32_t pt = tmem + Sh::kColP + 64 * b;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half, v += 4 * 2048 >> 4, w += Sh::kPBlk >> 4, pt += 32)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t more = (t | half | kk) != 0 ? 1u : 0u;
+                if (Sh::kWide)
+                  tc2::ss(tmem + Sh::kColO, w + 2 * kk, v + (2048 >> 4) * kk, id, more);
+                else
+                  tc2::ts(tmem + Sh::kColO, pt + 8 * kk, v + (2048 >> 4) * kk, id, more);
+              }
+            tc2::commit(&br.pv_done[b], 0x3);
+            tc2::commit(&br.v_empty[ring.slot], 0x3);
+            ring.next(Sh::kVSlots);
+          }
+          if (!ok) break;
+          tc2::commit(&br.o_full, 0x3);
+          us.give_back(n);
+        }
+        tc2::commit(&br.drain[1], 0x1);
+        mbar_wait(&br.drain[1], 0, p.err);
+      }
+    } else if (warp == 2) {
       // ================================================================ units ===================
       const int32_t total = p.total[0];
       int r0 = 0;
@@ -520,41 +487,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (i >= total) break;
       }
     } else if (warp == 3) {
-      // ================================================================ tails ===================
-      // V tiles that reach past their request's end: rows from there on become zeros, then the tile counts as there.
-      const uint32_t full = remote_smem(br.full, 0);
-      Ring ring = {0, 0};
+      // ================================================================ V =======================
+      // A tile that reaches past its request's end is counted on a barrier of this CTA; rows from there on become zeros, then
+      // the tile counts as there.
+      const uint32_t full = remote_smem(br.v_full, 0), tail = remote_smem(&br.tail_full, rank);
+      Ring ring = {0, 1};
       uint32_t tails = 0;
-      Walk w;
-      bool ok = w.begin(us);
+      bool ok = true;
 #pragma unroll 1
-      while (ok) {
-        const Walk::What what = w.step(us);  // every lane walks
-        if (what == Walk::kEnd || what == Walk::kFail) break;
-        if (what == Walk::kK) {
-          ++w.kt, ++w.k;
-        } else {
-          const int left = w.vu.len - (w.vu.ta + w.vt) * kKeys;
+      for (uint32_t n = 0; ok; ++n) {
+        ok = __all_sync(0xffffffffu, us.take(n, u));
+        if (!ok || u.n == 0) break;
+        int y = u.kv0 + u.ta * kKeys, left = u.len - u.ta * kKeys;  // rows of the request from the tile's first on
+#pragma unroll 1
+        for (int t = 0; t < u.n; ++t, y += kKeys, left -= kKeys) {
+          ok = warp_wait(&br.v_empty[ring.slot], ring.par, p.err, lane);
+          if (!ok) break;
+          uint8_t* s = smem + Sh::kOffV + ring.slot * Sh::kVBytes;
+          if (lane == 0) {
+            const uint32_t bar = left < kKeys ? tail : full + 8 * (uint32_t)ring.slot;
+            pair::arrive_expect_tx(bar, Sh::kVBytes);
+#pragma unroll 1
+            for (int b = 0; b < kDv / 128; ++b) pair::load_3d(s + b * Sh::kVBlk, &map_v, bar, kDn + kDv / 2 * (int)rank + 64 * b, u.h, y);
+          }
           if (left < kKeys) {
-            if (!warp_wait_all(&br.tail_full[tails & 1u], (tails >> 1) & 1u, p.err)) break;
-            uint8_t* s = smem + Sh::kOffRing + ring.slot * Sh::kSlot;
-            const int from = left < 0 ? 0 : left;
+            ok = warp_wait(&br.tail_full, tails++ & 1u, p.err, lane);
+            if (!ok) break;
 #pragma unroll 1
-            for (int x = 8 * from + lane; x < 8 * kKeys; x += 32)
+            for (int x = 8 * (left < 0 ? 0 : left) + lane; x < 8 * kKeys; x += 32)
 #pragma unroll
               for (int b = 0; b < kDv / 128; ++b) *reinterpret_cast<uint4*>(s + b * Sh::kVBlk + 16 * x) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-              remote_arrive_cta(full + 8 * (uint32_t)ring.slot);
-              mbar_arrive(&br.tail_done[tails & 1u]);
-            }
-            ++tails;
+            if (lane == 0) remote_arrive_cta(full + 8 * (uint32_t)ring.slot);
           }
-          ++w.vt, ++w.v;
+          ring.next(Sh::kVSlots);
         }
-        ring.next(Sh::kSlots);
+        if (ok) us.give_back(n);
       }
+      if (!ok) pair::let_copies_land();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -565,10 +536,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float* refs = reinterpret_cast<float*>(smem + Sh::kOffRef);  // [2][128]
     float* sums = reinterpret_cast<float*>(smem + Sh::kOffSum);
     const int mine = 4 * g + quad, other = 4 * (g ^ 1) + quad;  // barriers of the two warps that share these tokens
-    uint32_t said = 0, heard = 0;  // references passed on and taken
+    uint32_t heard = 0;            // references taken
     uint32_t joint = 0;            // units in which this warp had tokens
     const float coef = fmaxf(p.scale_log2, 7.5e-37f);  // not 0, so that a masked column stays -inf
-    int64_t i = 0;
+    uint32_t i = 0;                // tiles
     bool ok = true;
 #pragma unroll 1
     for (uint32_t n = 0; ok; ++n) {
@@ -584,20 +555,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = 0; t < u.n && ok; ++t, ++i) {
         if ((int)(i & 1) != g) continue;
-        const uint32_t ph = (uint32_t)(i >> 1) & 1u;
+        const uint32_t ph = (i >> 1) & 1u;
+        if (idle) {
+          ok = warp_wait_all(&br.s_full[g], ph, p.err);
+          if (ok && lane == 0) remote_arrive_relaxed(s_empty + 8 * (uint32_t)g);
+          // This tile's logits may be there before the warps with tokens have handed on P of the tile before last: without the
+          // wait, this arrival could count for that one.
+          if (ok && i >= 2) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
+          __syncwarp();
+          if (ok && lane == 0) remote_arrive_cta(p_full + 8 * (uint32_t)g);
+          continue;
+        }
+        const float before = ref;  // this warpgroup's sum refers to it
+        if (t > 0) {               // the other warpgroup's, after the tile before
+          ok = warp_wait_all(&br.ref[other], heard & 1u, p.err);
+          if (!ok) break;
+          ++heard;
+          ref = refs[128 * (g ^ 1) + row];
+        }
+        const float was = ref;  // the accumulator refers to it
         ok = warp_wait_all(&br.s_full[g], ph, p.err);
         if (!ok) break;
         tc_fence_after();
-        if (idle) {
-          __syncwarp();
-          if (lane == 0) remote_arrive_relaxed(s_empty + 8 * (uint32_t)g);
-          // This tile's logits may be there before the warps with tokens have handed on P of the tile before last: without the
-          // wait, this arrival could count for that one.
-          if (i >= 2) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
-          __syncwarp();
-          if (lane == 0) remote_arrive_cta(p_full + 8 * (uint32_t)g);
-          continue;
-        }
         uint32_t v[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + kKeys * g + 32 * c, v[c]);
@@ -621,33 +600,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float m4[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          m4[c] = __uint_as_float(v[c][0]);
+          m4[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
 #pragma unroll
-          for (int j = 1; j < 32; ++j) m4[c] = fmaxf(m4[c], __uint_as_float(v[c][j]));
+          for (int j = 2; j < 32; j += 2) m4[c] = max3(m4[c], __uint_as_float(v[c][j]), __uint_as_float(v[c][j + 1]));
         }
-        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
         mx = mx == -INFINITY ? mx : mx * coef;
-        const float before = ref;  // this warpgroup's sum refers to it
-        if (t > 0) {               // the other warpgroup's, after the tile before
-          ok = warp_wait_all(&br.ref[other], heard & 1u, p.err);
-          if (!ok) break;
-          ++heard;
-          ref = refs[128 * (g ^ 1) + row];
-        }
-        const float was = ref;  // the accumulator refers to it
         if (mx > ref + kThreshold) ref = mx;
         if (t + 1 < u.n) {
           refs[128 * g + row] = ref;
           __syncwarp();
           if (lane == 0) mbar_arrive(&br.ref[mine]);
-          ++said;
         }
+        // asked early: whether P of the tile before last has been used (with one buffer: of the tile before)
+        bool used = i < 2 || test_wait(&br.pv_done[g], ph ^ 1u);
         if (before != ref) l *= fast_exp2(before - ref);
         const float me = ref == -INFINITY ? 0.f : ref;
-        // P of the tile before last, in this buffer, has been used
-        if (i >= 2) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
-        if (!ok) break;
-        tc_fence_after();
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -659,8 +627,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             s1 += b;
             v[c][j] = pack_bf16(a, b);
           }
+        }
+        l += s0 + s1;
+        if (!__all_sync(0xffffffffu, used)) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
+        if (Sh::kWide && ok && i >= 1) ok = warp_wait_all(&br.pv_done[g ^ 1], ((i - 1) >> 1) & 1u, p.err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
           if (Sh::kWide) {
-            uint8_t* blk = smem + Sh::kOffP + g * Sh::kPBuf + (c >> 1) * Sh::kPBlk;
+            uint8_t* blk = smem + Sh::kOffP + (c >> 1) * Sh::kPBlk;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               *reinterpret_cast<uint4*>(blk + sw128_offset(row, 64 * (c & 1) + 16 * j)) =
@@ -672,12 +648,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_st16(lane_base + Sh::kColP + 64 * g + 16 * c, w);
           }
         }
-        l += s0 + s1;
         if (t > 0) {
           const float al = was == ref ? 1.f : fast_exp2(was - ref);
-          // Rare. A parity tells two tiles apart: the logits of this tile came after PV of the tile three before, whose phase is over.
+          // Rare. (A parity tells two tiles apart: PV of the tile three before came before that of two before, which is over.)
           if (__any_sync(0xffffffffu, al != 1.f)) {
-            ok = warp_wait_all(&br.pv_done[g ^ 1], (uint32_t)((i - 1) >> 1) & 1u, p.err);
+            ok = warp_wait_all(&br.pv_done[g ^ 1], ((i - 1) >> 1) & 1u, p.err);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
