@@ -221,15 +221,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Whether the phase with this parity is over, without waiting.
-__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
@@ -613,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&br.ref[mine]);
         }
         // asked early: whether P of the tile before last has been used (with one buffer: of the tile before)
-        bool used = i < 2 || test_wait(&br.pv_done[g], ph ^ 1u);
+        bool used = i < 2 || pair::test_wait(&br.pv_done[g], ph ^ 1u);
         if (before != ref) l *= fast_exp2(before - ref);
         const float me = ref == -INFINITY ? 0.f : ref;
         float s0 = 0.f, s1 = 0.f;

@@ -7,75 +7,94 @@
 //   absorb   out[t, h, c]   = sum_d q[t, h, d]   W[h, d, c]         reduced over d: W is the MN-major operand
 // so one kernel computes C[m, h, n] = sum_k A[m, h, k] B_h[n, k] and the calls differ in coordinates and in B's major-ness.
 //
-// A pair of CTAs computes a tile of 256 rows and kBN columns with two-SM MMAs: each CTA holds its 128 rows of A, half of the
-// B tile, and its rows of the accumulator (two of them in tensor memory, so that one tile's epilogue runs under the next
-// tile's products). TMA feeds a ring of stages of 64 reduced values; eight epilogue warps round to bf16 once and store whole
-// 128-byte lines by TMA, which also leaves out what is past the tensor's ends. Reduced values beyond K or rows beyond M are read
-// as zeros. Tiles go to the pairs in order, heads (or columns) fastest, so that pairs running at the same time read and
-// write whole rows of A and C.
-#include <atomic>
-
+// A pair of CTAs computes tiles of 256 rows and kBN columns with two-SM MMAs: each CTA holds its 128 rows of A, half of the
+// columns of B, and its rows of the accumulator (two tiles of them in tensor memory, so that one tile's epilogue runs under the next
+// tile's products). All of a head's B (or 256 columns of the expanded width: 128 KB of shared memory per CTA at most) stays while the pair
+// goes on along the rows, so that only A streams through the ring. B comes and goes in chunks of 64 reduced values, with
+// barriers of their own, so that a change of head costs no more than a load's latency. Eight epilogue warps round to bf16 once and
+// store whole 128-byte lines through shared memory. Rows beyond M are read as zeros and not stored.
 #include "pair.cuh"
 
 namespace hs {
 namespace heads {
 
 constexpr int kBM = 256, kHalfM = 128, kBK = 64;
-constexpr int kThreads = 384;                 // producer, MMAs, two idle, eight epilogue warps
-constexpr int kABytes = kHalfM * kBK * 2;     // 16 KB
-constexpr int kEpiWarps = 8, kScratch = 4096; // 32 rows x 128 bytes, two per epilogue warp
-
-template <int kBN>
-struct Shape {
-  static constexpr int kBBytes = kBN / 2 * kBK * 2, kStage = kABytes + kBBytes;
-  static constexpr int kStages = kBN == 256 ? 5 : 6;
-  static constexpr int kOffEpi = kStages * kStage, kOffBar = kOffEpi + kEpiWarps * 2 * kScratch;
-  static constexpr int kSmem = kOffBar + 256;
-  static_assert(kSmem <= 232448 && kStage % 1024 == 0, "shared memory");
-};
+constexpr int kThreads = 384;                 // copies, MMAs, two idle, eight epilogue warps
+constexpr int kSlot = kHalfM * kBK * 2;       // 16 KB of A
+constexpr int kOperands = 12 * kSlot;         // B's chunks, then A's ring: 4 slots at least
+constexpr int kMaxSlots = 11, kMaxChunks = 8;
+constexpr int kEpiWarps = 8, kScratch = 4096; // 32 rows x 128 bytes per epilogue warp
+constexpr int kOffEpi = kOperands, kOffBar = kOffEpi + kEpiWarps * kScratch, kSmem = kOffBar + 512;
+static_assert(kSmem <= 232448, "shared memory");
 
 struct Params {
-  int64_t tiles;
+  int64_t units;
+  uint16_t* c;
+  int64_t c_stride_m, c_stride_h;
   int32_t M, N;            // rows; columns per head
-  int32_t n_tiles, heads;  // column tiles per head
-  int32_t k_steps;
+  int32_t m_tiles, m_unit; // row tiles; of a unit
+  int32_t groups;          // heads, or parts of the expanded width
+  int32_t n_tiles;         // column tiles of a group, one or two: their B stays together
+  int32_t per_head;        // groups per head
+  int32_t k_steps, slots;
+  int32_t a_again;         // A is read by every group
   int32_t b_head, b_row;   // B's rows of head h start at h * b_head + b_row
   int32_t* err;
 };
 
 struct Bars {
-  uint64_t full[6], empty[6], acc_full[2], acc_empty[2], drain;
+  uint64_t a_full[kMaxSlots], a_empty[kMaxSlots], b_full[kMaxChunks], b_empty[kMaxChunks], acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 512, "barriers");
+
+// A pair's items: every so many of the units, a unit being up to m_unit row tiles of one group. Units follow one another with the groups
+// fastest, so that pairs running at the same time read the same rows of A and write whole rows of C.
+struct Run {
+  int64_t unit, step, units;
+  int32_t g, m, end, groups, m_unit, m_tiles;
+  __device__ __forceinline__ explicit Run(const Params& p) {
+    step = gridDim.x >> 1, unit = blockIdx.x >> 1, units = p.units;
+    groups = p.groups, m_unit = p.m_unit, m_tiles = p.m_tiles;
+    start();
+  }
+  __device__ __forceinline__ void start() {
+    const int32_t s = (int32_t)(unit / groups);
+    g = (int32_t)(unit - (int64_t)s * groups);
+    m = s * m_unit;
+    end = min(m + m_unit, m_tiles);
+  }
+  __device__ __forceinline__ bool more() const { return unit < units; }
+  __device__ __forceinline__ bool last() const { return m + 1 == end; }  // of its unit
+  __device__ __forceinline__ void next() {
+    if (++m == end) {
+      unit += step;
+      if (unit < units) start();
+    }
+  }
 };
 
 template <int kBN, bool kMnMajor>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    heads_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                 const __grid_constant__ CUtensorMap map_c, const Params p) {
-  using Sh = Shape<kBN>;
+    heads_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Params p) {
+  constexpr int kChunk = kBN / 2 * kBK * 2;  // of B per CTA
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzled blocks need it; the same in both CTAs
     if (threadIdx.x == 0) flag_error(p.err, HS_FLAG_BAD_STATE);
     return;
   }
-  Bars& br = *reinterpret_cast<Bars*>(smem + Sh::kOffBar);
+  Bars& br = *reinterpret_cast<Bars*>(smem + kOffBar);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  uint8_t* ring_a = smem + p.n_tiles * p.k_steps * kChunk;
   if (tid == 0) {
-    for (int s = 0; s < 6; ++s) {
-      mbar_init(&br.full[s], 2);
-      mbar_init(&br.empty[s], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&br.acc_full[b], 1);
-      mbar_init(&br.acc_empty[b], 2 * kEpiWarps);
-    }
+    for (int s = 0; s < kMaxSlots; ++s) mbar_init(&br.a_full[s], 2), mbar_init(&br.a_empty[s], 1);
+    for (int s = 0; s < kMaxChunks; ++s) mbar_init(&br.b_full[s], 2), mbar_init(&br.b_empty[s], 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&br.acc_full[b], 1), mbar_init(&br.acc_empty[b], 2 * kEpiWarps);
     mbar_init(&br.drain, 1);
     mbar_fence_init();
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
-    prefetch_tensormap(&map_c);
   }
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist
@@ -83,135 +102,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = br.tmem;
-
-  auto place = [&](int64_t tile, int& m0, int& h, int& n0) {
-    const int per_row = p.n_tiles * p.heads;
-    m0 = (int)(tile / per_row) * kBM;
-    const int rest = (int)(tile % per_row);
-    h = rest / p.n_tiles;
-    n0 = rest % p.n_tiles * kBN;
-  };
+  Run run(p);
 
   if (warp == 0) {
     // ================================================================ copies ====================
     if (lane == 0) {
-      const uint32_t full = remote_smem(br.full, 0);
+      const uint32_t a_full = remote_smem(br.a_full, 0), b_full = remote_smem(br.b_full, 0);
+      const uint64_t keep = l2_policy_evict_last(), stream = l2_policy_evict_first();
       int slot = 0;
-      uint32_t par = 1;
+      uint32_t par = 1, groups = 0;
       bool ok = true;
 #pragma unroll 1
-      for (int64_t tile = first; tile < p.tiles && ok; tile += step) {
-        int m0, h, n0;
-        place(tile, m0, h, n0);
+      for (bool first = true; run.more() && ok; first = run.last(), run.next()) {
+        const int h = run.g / p.per_head, n0 = run.g % p.per_head * p.n_tiles * kBN + (int)rank * (kBN / 2);
+        const int rows = h * p.b_head + p.b_row, y = run.m * kBM + kHalfM * (int)rank;
 #pragma unroll 1
-        for (int k = 0; k < p.k_steps; ++k) {
-          if (!mbar_wait(&br.empty[slot], par, p.err)) {
-            ok = false;
-            break;
+        for (int c = 0; c < (first ? p.n_tiles : 1) * p.k_steps; ++c) {  // chunk c: column tile c / k_steps
+          const int nt = c >= p.k_steps ? 1 : 0, k = c - nt * p.k_steps;
+          if (first) {
+            ok = mbar_wait(&br.b_empty[c], (groups & 1u) ^ 1u, p.err);
+            if (!ok) break;
+            uint8_t* d = smem + c * kChunk;
+            const uint32_t bar = b_full + 8 * (uint32_t)c;
+            pair::arrive_expect_tx(bar, kChunk);
+            if (kMnMajor) {  // 64 reduced rows of this CTA's columns, 64 columns to a block
+#pragma unroll 1
+              for (int b = 0; b < kBN / 128; ++b) pair::load_2d(d + b * 8192, &map_b, bar, n0 + nt * kBN + 64 * b, rows + k * kBK, keep);
+            } else {
+              pair::load_2d(d, &map_b, bar, k * kBK, rows + n0 + nt * kBN, keep);
+            }
           }
-          const uint32_t bar = full + 8 * (uint32_t)slot;
-          uint8_t* a = smem + slot * Sh::kStage;
-          pair::arrive_expect_tx(bar, Sh::kStage);
-          pair::load_3d(a, &map_a, bar, k * kBK, h, m0 + kHalfM * (int)rank);
-          if (kMnMajor) {  // 64 reduced rows of this CTA's columns, 64 columns to a block
-#pragma unroll
-            for (int b = 0; b < kBN / 128; ++b)
-              pair::load_2d(a + kABytes + b * 8192, &map_b, bar, n0 + (int)rank * (kBN / 2) + 64 * b, h * p.b_head + p.b_row + k * kBK);
-          } else {
-            pair::load_2d(a + kABytes, &map_b, bar, k * kBK, h * p.b_head + p.b_row + n0 + (int)rank * (kBN / 2));
+          if (nt == 0) {
+            ok = mbar_wait(&br.a_empty[slot], par, p.err);
+            if (!ok) break;
+            const uint32_t bar = a_full + 8 * (uint32_t)slot;
+            pair::arrive_expect_tx(bar, kSlot);
+            pair::load_3d(ring_a + slot * kSlot, &map_a, bar, k * kBK, h, y, p.a_again ? keep : stream);
+            if (++slot == p.slots) slot = 0, par ^= 1u;
           }
-          if (++slot == Sh::kStages) slot = 0, par ^= 1u;
         }
+        if (first) ++groups;
       }
       if (!ok) pair::let_copies_land();
     }
   } else if (warp == 1) {
     // ================================================================ MMAs ======================
+    // Whether the next stage is there is asked before a stage's MMAs, whose issue hides the answer's latency.
     if (lane == 0 && rank == 0) {
       constexpr uint32_t id = idesc_bf16(kBM, kBN, 0, kMnMajor ? 1 : 0);
-      const uint64_t ad = smem_desc(smem_u32(smem), 16, 1024, 2);
-      const uint64_t bd = smem_desc(smem_u32(smem + kABytes), kMnMajor ? 8192 : 16, 1024, 2);
-      int slot = 0;
-      uint32_t par = 0;
-      uint32_t it = 0;
-      bool ok = true;
+      const uint64_t ad = smem_desc(smem_u32(ring_a), 16, 1024, 2);
+      const uint64_t bd = smem_desc(smem_u32(smem), kMnMajor ? 8192 : 16, 1024, 2);
+      int slot0 = 0;
+      uint32_t par0 = 0, it = 0, groups = 0;
+      bool ok = true, there = false;  // there: the next stage of A has been seen
 #pragma unroll 1
-      for (int64_t tile = first; tile < p.tiles && ok; tile += step, ++it) {
-        const uint32_t b = it & 1u, d = tmem + b * 256u;
-        if (!mbar_wait(&br.acc_empty[b], ((it >> 1) & 1u) ^ 1u, p.err)) break;
-        tc_fence_after();
+      for (bool first = true; run.more() && ok; first = run.last(), run.next()) {
+        const bool last = run.last();
+        int slot = slot0;
+        uint32_t par = par0;
 #pragma unroll 1
-        for (int k = 0; k < p.k_steps; ++k) {
-          if (!mbar_wait(&br.full[slot], par, p.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t off = (uint64_t)((slot * Sh::kStage) >> 4);
+        for (int nt = 0, c = 0; nt < p.n_tiles && ok; ++nt, ++it) {
+          const uint32_t b = it & 1u, d = tmem + b * 256u;
+          slot = slot0, par = par0;
+          ok = mbar_wait(&br.acc_empty[b], ((it >> 1) & 1u) ^ 1u, p.err);
+          if (!ok) break;
+#pragma unroll(kMnMajor ? 1 : 8)
+          for (int k = 0; k < (kMnMajor ? p.k_steps : HS_D_LATENT / kBK); ++k, ++c) {
+            if (nt == 0 && !there) ok = mbar_wait(&br.a_full[slot], par, p.err);
+            if (first && ok) ok = mbar_wait(&br.b_full[c], groups & 1u, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = ad + (uint64_t)((slot * kSlot) >> 4), w = bd + (uint64_t)((c * kChunk) >> 4);
+            uint64_t* empty = &br.a_empty[slot];
+            if (++slot == p.slots) slot = 0, par ^= 1u;
+            there = nt + 1 == p.n_tiles || nt == 0 ? pair::test_wait(&br.a_full[slot], par) : false;
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc2::ss(d, ad + off + (uint64_t)((kk * 32) >> 4), bd + off + (uint64_t)((kk * (kMnMajor ? 2048 : 32)) >> 4), id,
-                    (k | kk) != 0 ? 1u : 0u);
-          tc2::commit(&br.empty[slot], 0x3);
-          if (++slot == Sh::kStages) slot = 0, par ^= 1u;
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              tc2::ss(d, a + 2 * kk, w + (kMnMajor ? 128 : 2) * kk, id, (k | kk) != 0 ? 1u : 0u);
+            if (nt + 1 == p.n_tiles) tc2::commit(empty, 0x3);
+            if (last) tc2::commit(&br.b_empty[c], 0x3);
+          }
+          if (ok) tc2::commit(&br.acc_full[b], 0x3);
         }
-        if (ok) tc2::commit(&br.acc_full[b], 0x3);
+        slot0 = slot, par0 = par;
+        if (first) ++groups;
       }
       tc2::commit(&br.drain, 0x1);
       mbar_wait(&br.drain, 0, p.err);
     }
   } else if (warp >= 4) {
     // ================================================================ epilogue ==================
-    // Warp (quad, g): rows 32 quad .. + 31 of this CTA, columns g kBN / 2 .. of the tile, 64 at a time.
+    // Warp (quad, g): rows 32 quad .. + 31 of this CTA, columns g kBN / 2 .. of the tile, 64 at a time. (TMA stores from here
+    // made the copies of A, which go through the same unit, wait for them.)
     const int quad = warp & 3, g = (warp - 4) >> 2;
     const uint32_t at = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(g * (kBN / 2));
     const uint32_t acc_empty = remote_smem(br.acc_empty, 0);
-    uint8_t* scratch = smem + Sh::kOffEpi + (warp - 4) * 2 * kScratch;
-    uint32_t it = 0, n = 0;
+    uint8_t* s = smem + kOffEpi + (warp - 4) * kScratch;
+    const int pl = lane & 7, rl = lane >> 3;
+    uint32_t it = 0;
+    bool ok = true;
 #pragma unroll 1
-    for (int64_t tile = first; tile < p.tiles; tile += step, ++it) {
-      const uint32_t b = it & 1u;
-      if (!warp_wait_all(&br.acc_full[b], (it >> 1) & 1u, p.err)) break;
-      tc_fence_after();
-      int m0, h, n0;
-      place(tile, m0, h, n0);
-      m0 += kHalfM * (int)rank + 32 * quad;
-#pragma unroll
-      for (int c = 0; c < kBN / 128; ++c) {
-        uint32_t v[2][32];
-        tmem_ld32(at + b * 256u + 64 * c, v[0]);
-        tmem_ld32(at + b * 256u + 64 * c + 32, v[1]);
-        tmem_wait_ld();
-        if (c == kBN / 128 - 1) {  // the accumulator has been read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) remote_arrive_relaxed(acc_empty + 8 * b);
-        }
-        const int col = n0 + g * (kBN / 2) + 64 * c;
-        if (m0 >= p.M || col >= p.N) continue;
-        uint8_t* s = scratch + (n++ & 1u) * kScratch;
-        if (lane == 0) pair::store_wait_read<1>();  // the store before the last one has read its scratch
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t w[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int e = 8 * j + 2 * z;
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
-            w[z] = *reinterpret_cast<const uint32_t*>(&b2);
+    for (; run.more() && ok; run.next()) {
+      const int h = run.g / p.per_head, n0 = run.g % p.per_head * p.n_tiles * kBN + g * (kBN / 2);
+      const int row = run.m * kBM + kHalfM * (int)rank + 32 * quad, left = p.M - row;
+      uint16_t* const c0 = p.c + (int64_t)(row + rl) * p.c_stride_m + (int64_t)h * p.c_stride_h + n0 + 8 * pl;
+#pragma unroll 1
+      for (int nt = 0; nt < p.n_tiles; ++nt, ++it) {
+        const uint32_t b = it & 1u;
+        ok = warp_wait_all(&br.acc_full[b], (it >> 1) & 1u, p.err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < kBN / 128; ++c) {
+          uint32_t v[2][32];
+          tmem_ld32(at + b * 256u + 64 * c, v[0]);
+          tmem_ld32(at + b * 256u + 64 * c + 32, v[1]);
+          tmem_wait_ld();
+          if (c == kBN / 128 - 1) {  // the accumulator has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) remote_arrive_relaxed(acc_empty + 8 * b);
           }
-          *reinterpret_cast<uint4*>(s + sw128_offset(lane, 16 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          pair::store_3d(&map_c, s, col, h, m0);
-          pair::store_commit();
+          const int col = nt * kBN + 64 * c;
+          if (left <= 0 || n0 + col >= p.N) continue;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int e = 8 * j + 2 * z;
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
+              w[z] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(s + sw128_offset(lane, 16 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+          uint16_t* to = c0 + col;
+#pragma unroll
+          for (int j = 0; j < 8; ++j, to += 4 * p.c_stride_m) {
+            const uint4 x = *reinterpret_cast<const uint4*>(s + sw128_offset(4 * j + rl, 16 * pl));
+            if (4 * j + rl < left) __stcs(reinterpret_cast<uint4*>(to), x);
+          }
+          __syncwarp();
         }
       }
     }
-    if (lane == 0) pair::store_wait_all();
   }
   __syncthreads();
   cluster_sync();  // no CTA leaves while the other may still signal or read it
@@ -222,13 +257,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int kBN, bool kMnMajor>
-static cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const Params& p, int sms, cudaStream_t stream) {
+static cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, Params p, int sms, cudaStream_t stream) {
   auto kernel = heads_kernel<kBN, kMnMajor>;
-  constexpr int smem = Shape<kBN>::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = p.tiles < sms / 2 ? p.tiles : sms / 2;
-  kernel<<<(int)(2 * pairs), kThreads, smem, stream>>>(ma, mb, mc, p);
+  p.m_tiles = (int)(((int64_t)p.M + kBM - 1) / kBM);
+  p.units = ((int64_t)p.m_tiles + p.m_unit - 1) / p.m_unit * p.groups;
+  const int slots = (kOperands - p.n_tiles * p.k_steps * (kBN / 2 * kBK * 2)) / kSlot;
+  p.slots = slots < kMaxSlots ? slots : kMaxSlots;
+  const int64_t pairs = p.units < sms / 2 ? p.units : sms / 2;
+  kernel<<<(int)(2 * pairs), kThreads, kSmem, stream>>>(ma, mb, p);
   return cudaGetLastError();
 }
 
@@ -245,44 +283,42 @@ constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B;
 cudaError_t launch_mla_expand(const hs_mla_expand_args* a, int sms, cudaStream_t stream, const char** why) {
   using namespace heads;
   const int width = a->H * a->width;
-  CUtensorMap ma, mb, mc;
+  CUtensorMap ma, mb;
   if (!pair::encode_heads(&ma, a->latent, HS_D_LATENT, 1, a->N, HS_D_LATENT, a->latent_stride, kHalfM) ||
-      !encode_2d(&mb, kBf16, a->w, HS_D_LATENT, (uint64_t)width, HS_D_LATENT * 2, kBK, 128, kSw128) ||
-      !pair::encode_heads(&mc, a->kv, width, 1, a->N, width, a->kv_stride, 32))
+      !encode_2d(&mb, kBf16, a->w, HS_D_LATENT, (uint64_t)width, HS_D_LATENT * 2, kBK, 128, kSw128))
     return maps_failed(why);
   Params p = {};
-  p.M = a->N, p.N = width, p.heads = 1, p.n_tiles = (width + 255) / 256, p.k_steps = HS_D_LATENT / kBK, p.err = a->err_flag;
-  p.tiles = ((int64_t)a->N + kBM - 1) / kBM * p.n_tiles;
-  return launch<256, false>(ma, mb, mc, p, sms, stream);
+  p.c = a->kv, p.c_stride_m = a->kv_stride, p.c_stride_h = width;
+  p.M = a->N, p.N = width, p.n_tiles = 1, p.per_head = p.groups = (width + 255) / 256, p.k_steps = HS_D_LATENT / kBK;
+  p.a_again = 1, p.m_unit = 4, p.err = a->err_flag;
+  return launch<256, false>(ma, mb, p, sms, stream);
 }
 
 cudaError_t launch_mla_absorb(const hs_mla_heads_args* a, int sms, cudaStream_t stream, const char** why) {
   using namespace heads;
-  CUtensorMap ma, mb, mc;
+  CUtensorMap ma, mb;
   if (!pair::encode_heads(&ma, a->x, a->Dn, a->H, a->T, a->x_stride_h, a->x_stride_t, kHalfM) ||
-      !encode_2d(&mb, kBf16, a->w, HS_D_LATENT, (uint64_t)a->H * (a->Dn + a->Dv), HS_D_LATENT * 2, 64, kBK, kSw128) ||
-      !pair::encode_heads(&mc, a->out, HS_D_LATENT, a->H, a->T, a->out_stride_h, a->out_stride_t, 32))
+      !encode_2d(&mb, kBf16, a->w, HS_D_LATENT, (uint64_t)a->H * (a->Dn + a->Dv), HS_D_LATENT * 2, 64, kBK, kSw128))
     return maps_failed(why);
   Params p = {};
-  p.M = a->T, p.N = HS_D_LATENT, p.heads = a->H, p.n_tiles = HS_D_LATENT / 256, p.k_steps = a->Dn / kBK, p.err = a->err_flag;
-  p.b_head = a->Dn + a->Dv;
-  p.tiles = ((int64_t)a->T + kBM - 1) / kBM * p.n_tiles * p.heads;
-  return launch<256, true>(ma, mb, mc, p, sms, stream);
+  p.c = a->out, p.c_stride_m = a->out_stride_t, p.c_stride_h = a->out_stride_h;
+  p.M = a->T, p.N = HS_D_LATENT, p.n_tiles = 2, p.per_head = 1, p.groups = a->H, p.k_steps = a->Dn / kBK;
+  p.b_head = a->Dn + a->Dv, p.m_unit = 1, p.err = a->err_flag;
+  return launch<256, true>(ma, mb, p, sms, stream);
 }
 
 cudaError_t launch_mla_project(const hs_mla_heads_args* a, int sms, cudaStream_t stream, const char** why) {
   using namespace heads;
   const int bn = a->Dv > 128 ? 256 : 128;
-  CUtensorMap ma, mb, mc;
+  CUtensorMap ma, mb;
   if (!pair::encode_heads(&ma, a->x, HS_D_LATENT, a->H, a->T, a->x_stride_h, a->x_stride_t, kHalfM) ||
-      !encode_2d(&mb, kBf16, a->w, HS_D_LATENT, (uint64_t)a->H * (a->Dn + a->Dv), HS_D_LATENT * 2, kBK, bn / 2, kSw128) ||
-      !pair::encode_heads(&mc, a->out, a->Dv, a->H, a->T, a->out_stride_h, a->out_stride_t, 32))
+      !encode_2d(&mb, kBf16, a->w, HS_D_LATENT, (uint64_t)a->H * (a->Dn + a->Dv), HS_D_LATENT * 2, kBK, bn / 2, kSw128))
     return maps_failed(why);
   Params p = {};
-  p.M = a->T, p.N = a->Dv, p.heads = a->H, p.n_tiles = 1, p.k_steps = HS_D_LATENT / kBK, p.err = a->err_flag;
-  p.b_head = a->Dn + a->Dv, p.b_row = a->Dn;
-  p.tiles = ((int64_t)a->T + kBM - 1) / kBM * p.heads;
-  return bn == 256 ? launch<256, false>(ma, mb, mc, p, sms, stream) : launch<128, false>(ma, mb, mc, p, sms, stream);
+  p.c = a->out, p.c_stride_m = a->out_stride_t, p.c_stride_h = a->out_stride_h;
+  p.M = a->T, p.N = a->Dv, p.n_tiles = 1, p.per_head = 1, p.groups = a->H, p.k_steps = HS_D_LATENT / kBK;
+  p.b_head = a->Dn + a->Dv, p.b_row = a->Dn, p.m_unit = 1, p.err = a->err_flag;
+  return bn == 256 ? launch<256, false>(ma, mb, p, sms, stream) : launch<128, false>(ma, mb, p, sms, stream);
 }
 
 }  // namespace hs

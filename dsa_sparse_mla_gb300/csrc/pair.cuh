@@ -1,5 +1,5 @@
 // pair.cuh — device helpers for clusters of two CTAs that work as one (two-SM tensor products): TMA copies and expected bytes
-// counted on a barrier of either CTA, 16-byte stores into either CTA's shared memory that count there, TMA stores.
+// counted on a barrier of either CTA, 16-byte stores into either CTA's shared memory that count there.
 #pragma once
 
 #include "cluster.cuh"
@@ -25,6 +25,22 @@ __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, uint3
       : "memory");
 }
 
+// The same under an L2 cache policy.
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4}], [%2], "
+      "%5;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, %5}], "
+      "[%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
 // Arrives on a barrier of either CTA and has it expect these bytes. Relaxed: the arrival hands on no writes of this thread.
 __device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -37,19 +53,15 @@ __device__ __forceinline__ void st_async16(uint32_t dst, int4 v, uint32_t bar) {
                : "memory");
 }
 
-// 3-D tiled store of one box; what lies outside the tensor is left out. Coordinates are not negative, x a multiple of 16 bytes.
-__device__ __forceinline__ void store_3d(const CUtensorMap* map, const void* src, int32_t x, int32_t y, int32_t z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(smem_u32(src)), "r"(x),
-               "r"(y), "r"(z)
+// Whether the phase with this parity is over, without waiting.
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
                : "memory");
+  return ok != 0;
 }
-__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// At most kLeft of this thread's store groups still read shared memory.
-template <int kLeft>
-__device__ __forceinline__ void store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
-}
-__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // After a wait that ran out: gives copies in flight, which take microseconds, 20 ms to land before the CTA leaves.
 __device__ __forceinline__ void let_copies_land() {
