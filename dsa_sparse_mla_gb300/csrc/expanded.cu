@@ -102,33 +102,44 @@ __device__ __forceinline__ int64_t block_before(int64_t v, int64_t* scratch) {
   return s;
 }
 
-// One CTA. Thread t plans requests 4 t .. 4 t + 3. A piece has at most a quarter of a pair's even share of all tiles (so that the
-// last units to end leave little idle), but kMinPiece at least, and longer where the pieces would not fit their slots.
+// Requests in descending order of their longest block, to a quarter of an octave (within one in any order: no result depends on it).
+__device__ __forceinline__ int size_class(int64_t tiles) {
+  return tiles <= 0 ? 127 : 126 - (int)((__float_as_uint((float)tiles) >> 21) - (127u << 2));  // 2^24 tiles at most: classes 27 .. 126
+}
+
+// One CTA. Thread t plans requests 4 t .. 4 t + 3. Long blocks come first, so that the last units to end are short. A block longer
+// than half of a pair's even share of all tiles is split into pieces of at most a quarter of it, but of kMinPiece tiles at least, and
+// longer ones where they would not fit their slots. (Pieces cost: blocks split at a quarter took nine ragged requests from ... us.)
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   __shared__ int64_t scratch[32];
+  __shared__ int32_t classes[128], places[kMaxReq];  // requests of a class, and before it; units of a place
   constexpr int kPer = kMaxReq / kPlanThreads;
   let_next();
-  int start[kPer], m[kPer], kv0[kPer], len[kPer], nb[kPer], np[kPer];
+  int start[kPer], m[kPer], kv0[kPer], len[kPer], nb[kPer], np[kPer], place[kPer];
   int64_t most[kPer], work = 0;
+  if (threadIdx.x < 128) classes[threadIdx.x] = 0;
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = kPer * threadIdx.x + k;
-    m[k] = start[k] = kv0[k] = len[k] = nb[k] = 0;
+    m[k] = start[k] = kv0[k] = len[k] = nb[k] = place[k] = 0;
     most[k] = 0;
     if (r >= p.B) continue;
     const int64_t a = p.req_start[r], b = p.req_start[r + 1], c = p.kv_start[r], d = p.kv_start[r + 1];
     if (a < 0 || b < a || b > p.T || (r == 0 && a != 0) || (r == p.B - 1 && b != p.T)) flag_error(p.err, HS_FLAG_BAD_INDEX);
-    if (a < 0 || b <= a || b > p.T) continue;
-    start[k] = (int)a, m[k] = (int)(b - a);
-    nb[k] = (m[k] + kTok - 1) / kTok;
-    if (c < 0 || d < c || d > p.N) {
-      flag_error(p.err, HS_FLAG_BAD_LENGTH);
-    } else {
-      kv0[k] = (int)c, len[k] = (int)(d - c);
+    if (a >= 0 && b > a && b <= p.T) {
+      start[k] = (int)a, m[k] = (int)(b - a);
+      nb[k] = (m[k] + kTok - 1) / kTok;
+      if (c < 0 || d < c || d > p.N) {
+        flag_error(p.err, HS_FLAG_BAD_LENGTH);
+      } else {
+        kv0[k] = (int)c, len[k] = (int)(d - c);
+      }
+      most[k] = (len[k] + kKeys - 1) / kKeys;
+      const int64_t least = p.causal ? ((int64_t)len[k] - m[k] + kTok + kKeys - 1) / kKeys : most[k];  // of the first block
+      work += nb[k] * (most[k] + (least < 1 ? 1 : least < most[k] ? least : most[k])) / 2 * p.H;
     }
-    most[k] = (len[k] + kKeys - 1) / kKeys;
-    const int64_t least = p.causal ? ((int64_t)len[k] - m[k] + kTok + kKeys - 1) / kKeys : most[k];  // of the first block
-    work += nb[k] * (most[k] + (least < 1 ? 1 : least < most[k] ? least : most[k])) / 2 * p.H;
+    place[k] = atomicAdd(&classes[size_class(nb[k] ? most[k] + 1 : 0)], 1);
   }
   work = block_sum(work, scratch);
   int64_t piece = (work / p.clusters + 3) / 4;
@@ -138,27 +149,57 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     int64_t slots = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
-      if (most[k] > piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
+      if (most[k] > 2 * piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
     if (block_sum(slots, scratch) <= p.cap) break;
   }
-  int64_t units = 0, slots = 0;
+  int64_t slots = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    np[k] = most[k] > piece ? (int)((most[k] + piece - 1) / piece) : 1;
-    units += (int64_t)nb[k] * p.H * np[k];
+    np[k] = most[k] > 2 * piece ? (int)((most[k] + piece - 1) / piece) : 1;
     if (np[k] > 1) slots += (int64_t)nb[k] * p.H * np[k];
   }
-  int64_t unit0 = block_before(units, scratch), slot0 = block_before(slots, scratch);
+  int64_t slot0 = block_before(slots, scratch);
+  if (threadIdx.x == 0) {
+    int before = 0;
+    for (int c = 0; c < 128; ++c) {
+      const int n = classes[c];
+      classes[c] = before;
+      before += n;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (kPer * (int)threadIdx.x + k >= p.B) continue;
+    place[k] += classes[size_class(nb[k] ? most[k] + 1 : 0)];
+    places[place[k]] = nb[k] * p.H * np[k];
+  }
+  __syncthreads();
+  int64_t units = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = kPer * threadIdx.x + k;
-    if (r < p.B) p.req[r] = {(int32_t)unit0, start[k], m[k], kv0[k], len[k], nb[k], np[k], (int32_t)slot0};
-    unit0 += (int64_t)nb[k] * p.H * np[k];
-    if (np[k] > 1) slot0 += (int64_t)nb[k] * p.H * np[k];
+    if (r < p.B) units += places[r];
+  }
+  int64_t unit0 = block_before(units, scratch);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int r = kPer * threadIdx.x + k;
+    if (r >= p.B) continue;
+    const int n = places[r];
+    places[r] = (int32_t)unit0;
+    unit0 += n;
   }
   if (threadIdx.x == kPlanThreads - 1) {
     p.total[0] = (int32_t)unit0;
     p.total[1] = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (kPer * (int)threadIdx.x + k >= p.B) continue;
+    p.req[place[k]] = {places[place[k]], start[k], m[k], kv0[k], len[k], nb[k], np[k], (int32_t)slot0};
+    if (np[k] > 1) slot0 += (int64_t)nb[k] * p.H * np[k];
   }
   for (int i = threadIdx.x; i < p.cap * 16; i += kPlanThreads) p.joined[i] = 0;
 }
@@ -171,9 +212,10 @@ struct Shape {
   static constexpr int kQBlk = kHalf * 128, kQBytes = kQB * kQBlk;
   static constexpr int kKBlk = kKeys / 2 * 128, kKBytes = kQB * kKBlk;
   static constexpr int kVBlk = kKeys * 128, kVBytes = kDv / 128 * kVBlk;
-  static constexpr int kKSlots = kWide ? 2 : 4, kVSlots = kWide ? 2 : 5;
+  static constexpr int kKSlots = kWide ? 2 : 4, kVSlots = kWide ? 2 : 4;
   static constexpr int kPBlk = kHalf * 128, kPBytes = kWide ? 2 * kPBlk : 0;  // blocks of 64 cached rows
-  static constexpr int kOffK = kQBytes, kOffV = kOffK + kKSlots * kKBytes, kOffP = kOffV + kVSlots * kVBytes, kOffRef = kOffP + kPBytes;
+  static constexpr int kOffK = kQBytes, kOffV = kOffK + kKSlots * kKBytes, kOffP = kOffV + kVSlots * kVBytes, kOffRef = kOffP + (kWide ? kPBytes : 8 * 2048);
+  static constexpr int kOffOut = kOffP;                       // 2 KB per softmax warp for the output (wide: in P's place, see the unit's end)
   static constexpr int kOffSum = kOffRef + 1024, kOffUnit = kOffSum + 1024, kOffBar = kOffUnit + 2 * (int)sizeof(Unit);
   static constexpr int kSmem = kOffBar + 512;
   static constexpr int kColP = 256, kColO = kWide ? 256 : 384;  // tensor-memory columns; logits in 0 .. 255
@@ -181,9 +223,9 @@ struct Shape {
 };
 
 struct Bars {
-  uint64_t k_full[4], k_empty[4], v_full[5], v_empty[5], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
   uint64_t tail_full, unit_full[2], unit_empty[2];
-  uint64_t ref[8], sum[8], sum_read[8];  // [warpgroup][quad]
+  uint64_t ref[8], sum[8], over[8];  // [warpgroup][quad]
   uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
@@ -205,7 +247,7 @@ struct Units {
   bool gives;     // whether this thread gives units back for its role
   // Unit number n (one thread, or every lane of a warp); false after a wait that ran out.
   __device__ __forceinline__ bool take(uint32_t n, Unit& u) const {
-    if (!mbar_wait_cluster(&br->unit_full[n & 1u], (n >> 1) & 1u, err)) return false;
+    if (!mbar_wait(&br->unit_full[n & 1u], (n >> 1) & 1u, err)) return false;
     const int4* v = reinterpret_cast<const int4*>(at + (n & 1u) * sizeof(Unit));
     int4* w = reinterpret_cast<int4*>(&u);
 #pragma unroll
@@ -223,6 +265,69 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// Joins the pieces of a block for a warp's tokens and columns, in the pieces' order. Weights first, a lane to a token; then eight
+// lanes to a token, its columns four at a time per lane, the loads of 16 tokens under way at once.
+template <int kDv>
+__device__ __noinline__ void join(const Params& p, const Unit& u, int g, int quad, int rank, int left) {
+  constexpr int kCols = kDv / 2, kGroups = 4;
+  const int lane = threadIdx.x & 31, sub = lane & 7, rows = kHalf * rank + 32 * quad;
+  const float* lse = p.part_lse + ((int64_t)u.first * 2 + g) * kTok + rows;  // [piece][2][256]
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < u.np; ++k) {
+    const float y = __ldcg(lse + (int64_t)k * 2 * kTok + lane);
+    top = y > top || y != y ? y : top;  // NaN stays
+  }
+#pragma unroll 4
+  for (int k = 0; k < u.np; ++k) {
+    const float y = __ldcg(lse + (int64_t)k * 2 * kTok + lane);
+    sum += y == -INFINITY ? 0.f : exp2f((y - top) * kLog2e);
+  }
+  const float scale = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t tok = (int64_t)u.tok + rows;
+  if (g == 0 && p.lse && lane < left) p.lse[(tok + lane) * p.H + u.h] = sum == 0.f ? -INFINITY : top + logf(sum);
+  uint16_t* out = p.out + (tok * p.H + u.h) * kDv + kCols * g;
+  const float* part = p.part_out + ((int64_t)u.first * kTok + rows) * kDv + kCols * g;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 4 * kGroups) {
+    if (r0 >= left) break;
+    float t[kGroups], f[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      t[i] = __shfl_sync(0xffffffffu, top, r0 + 4 * i + (lane >> 3));
+      f[i] = __shfl_sync(0xffffffffu, scale, r0 + 4 * i + (lane >> 3));
+    }
+#pragma unroll 1
+    for (int c = 4 * sub; c < kCols; c += 32) {
+      float4 acc[kGroups];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int k = 0; k < u.np; ++k) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          const int r = r0 + 4 * i + (lane >> 3), rr = r < left ? r : 0;
+          const float y = __ldcg(lse + (int64_t)k * 2 * kTok + rr);
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(part + ((int64_t)k * kTok + rr) * kDv + c));
+          if (y != -INFINITY) {
+            const float w = exp2f((y - t[i]) * kLog2e) * f[i];
+            acc[i].x = fmaf(w, x.x, acc[i].x);
+            acc[i].y = fmaf(w, x.y, acc[i].y);
+            acc[i].z = fmaf(w, x.z, acc[i].z);
+            acc[i].w = fmaf(w, x.w, acc[i].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        const int r = r0 + 4 * i + (lane >> 3);
+        if (r < left)
+          *reinterpret_cast<uint2*>(out + (int64_t)r * p.H * kDv + c) = make_uint2(pack_bf16(acc[i].x, acc[i].y), pack_bf16(acc[i].z, acc[i].w));
+      }
+    }
+  }
+}
 
 // A token's output values col0 .. col0 + kCols - 1 once more, from the rows that it sees alone, where a row of its tiles that it does not
 // see holds a value there that is not finite (P = 0 does not silence it). The whole warp works on one token; rare, so plain: a row
@@ -280,10 +385,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 8; ++s) {
       mbar_init(&br.ref[s], 1);
       mbar_init(&br.sum[s], 1);
-      mbar_init(&br.sum_read[s], 1);
+      mbar_init(&br.over[s], 1);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&br.k_full[s], 2), mbar_init(&br.k_empty[s], 1);
-    for (int s = 0; s < 5; ++s) mbar_init(&br.v_full[s], 2), mbar_init(&br.v_empty[s], 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&br.k_full[s], 2), mbar_init(&br.k_empty[s], 1);
+      mbar_init(&br.v_full[s], 2), mbar_init(&br.v_empty[s], 1);
+    }
     mbar_init(&br.q_full, 2);
     mbar_init(&br.q_empty, 1);
     mbar_init(&br.tail_full, 1);
@@ -327,14 +434,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (uint32_t n = 0; ok; ++n) {
           ok = us.take(n, u);
           if (!ok || u.n == 0) break;
-          ok = mbar_wait(&br.q_empty, (n & 1u) ^ 1u, p.err);
-          if (!ok) break;
-          pair::arrive_expect_tx(q_full, Sh::kQBytes);
-#pragma unroll 1
-          for (int b = 0; b < Sh::kQB; ++b) pair::load_3d(smem + b * Sh::kQBlk, &map_q, q_full, 64 * b, u.h, u.tok + kHalf * (int)rank);
           int y = u.kv0 + u.ta * kKeys + kKeys / 2 * (int)rank;
+          bool asked = false;  // Q: its place is free when the unit before has issued its last QK; until then K goes ahead
 #pragma unroll 1
           for (int t = 0; t < u.n; ++t, y += kKeys) {
+            if (!asked && (t == Sh::kKSlots - 1 || t == u.n - 1 || pair::test_wait(&br.q_empty, (n & 1u) ^ 1u))) {
+              ok = mbar_wait(&br.q_empty, (n & 1u) ^ 1u, p.err);
+              if (!ok) break;
+              pair::arrive_expect_tx(q_full, Sh::kQBytes);
+#pragma unroll 1
+              for (int b = 0; b < Sh::kQB; ++b) pair::load_3d(smem + b * Sh::kQBlk, &map_q, q_full, 64 * b, u.h, u.tok + kHalf * (int)rank);
+              asked = true;
+            }
             ok = mbar_wait(&br.k_empty[ring.slot], ring.par, p.err);
             if (!ok) break;
             uint8_t* s = smem + Sh::kOffK + ring.slot * Sh::kKBytes;
@@ -542,7 +653,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int see = p.causal ? u.see + kHalf * (int)rank + row : u.see;
       see = there ? (see < u.len ? see : u.len) : 0;
       float ref = -INFINITY, l = 0.f;
-      if (!idle && joint > 0) ok = warp_wait_all(&br.sum_read[other], (joint - 1) & 1u, p.err);
+      // the other warp with these tokens has read this one's sums and references, and is done with P's place
+      if (!idle && joint > 0) ok = warp_wait_all(&br.over[other], (joint - 1) & 1u, p.err);
 #pragma unroll 1
       for (int t = 0; t < u.n && ok; ++t, ++i) {
         if ((int)(i & 1) != g) continue;
@@ -674,9 +786,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = warp_wait_all(&br.sum[other], joint & 1u, p.err);
         if (!ok) break;
         const float ref2 = refs[128 * (g ^ 1) + row], l2 = sums[128 * (g ^ 1) + row];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&br.sum_read[mine]);
-        ++joint;
         const float top = fmaxf(ref, ref2);
         l = (ref == top ? l : l * fast_exp2(ref - top)) + (ref2 == top ? l2 : l2 * fast_exp2(ref2 - top));
         ref = top;
@@ -692,8 +801,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int64_t tok = (int64_t)u.tok + kHalf * (int)rank + row;
         constexpr int kCols = kDv / 2;  // of this warpgroup
         const bool whole = u.np == 1;
+        // 32 columns at a time through 2 KB of shared memory, so that a store covers 64 bytes of each of 8 tokens
+        uint8_t* scratch = smem + Sh::kOffOut + (Sh::kWide ? g * Sh::kPBlk + 4096 * quad : 2048 * (warp - 4));
         float* part = p.part_out + ((int64_t)u.slot * kTok + kHalf * (int)rank + row) * kDv + kCols * g;
-        uint16_t* o = p.out + (tok * p.H + u.h) * kDv + kCols * g;
+        const int left = have - 32 * quad;  // tokens of this warp
+        const int64_t pitch = (int64_t)p.H * kDv;
+        uint16_t* o = p.out + ((tok - lane) * p.H + u.h) * kDv + kCols * g;  // the warp's first token
         bool bad = false;
 #pragma unroll 1
         for (int c = 0; c < kCols / 32; ++c) {
@@ -704,30 +817,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = 0u;
           }
+          if (whole) {
+            uint32_t most = 0;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) bad |= !(fabsf(__uint_as_float(x[j])) <= 3.4028235e38f);
-          if (there) {
-            if (whole) {
+            for (int j = 0; j < 16; ++j) {
+              x[j] = pack_bf16(__uint_as_float(x[2 * j]) * inv, __uint_as_float(x[2 * j + 1]) * inv);
+              most = __vmaxu2(most, x[j] & 0x7FFF7FFFu);
+            }
+            bad |= (most & 0xFFFFu) >= 0x7F80u || most >= 0x7F800000u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(scratch + sw64_offset(lane, 16 * j)) = make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = 8 * j + (lane >> 2);
+              const uint4 y = *reinterpret_cast<const uint4*>(scratch + sw64_offset(r, 16 * (lane & 3)));
+              if (r < left) *reinterpret_cast<uint4*>(o + r * pitch + 32 * c + 8 * (lane & 3)) = y;
+            }
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              x[j] = __float_as_uint(__uint_as_float(x[j]) * inv);
+              bad |= !(fabsf(__uint_as_float(x[j])) <= 3.4028235e38f);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 16 columns
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(scratch + sw64_offset(lane, 16 * j)) =
+                    make_uint4(x[16 * h + 4 * j], x[16 * h + 4 * j + 1], x[16 * h + 4 * j + 2], x[16 * h + 4 * j + 3]);
+              __syncwarp();
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                uint32_t y[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  y[k] = pack_bf16(__uint_as_float(x[8 * j + 2 * k]) * inv, __uint_as_float(x[8 * j + 2 * k + 1]) * inv);
-                *reinterpret_cast<uint4*>(o + 32 * c + 8 * j) = make_uint4(y[0], y[1], y[2], y[3]);
+                const int r = 8 * j + (lane >> 2);
+                const uint4 y = *reinterpret_cast<const uint4*>(scratch + sw64_offset(r, 16 * (lane & 3)));
+                if (r < left) *reinterpret_cast<uint4*>(part + (int64_t)(r - lane) * kDv + 32 * c + 16 * h + 4 * (lane & 3)) = y;
               }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<float4*>(part + 32 * c + 4 * j) =
-                    make_float4(__uint_as_float(x[4 * j]) * inv, __uint_as_float(x[4 * j + 1]) * inv, __uint_as_float(x[4 * j + 2]) * inv,
-                                __uint_as_float(x[4 * j + 3]) * inv);
+              __syncwarp();
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) remote_arrive_cta(o_free);
+        if (lane == 0) {
+          remote_arrive_cta(o_free);
+          mbar_arrive(&br.over[mine]);
+        }
+        ++joint;
         for (uint32_t again = __ballot_sync(0xffffffffu, there && bad && l <= 3.4028235e38f); again; again &= again - 1) {
           const int r = __ffs(again) - 1;
           float acc[kCols / 32];
@@ -754,50 +892,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) before = atomicAdd(&p.joined[(int64_t)u.first * 16 + 8 * (int)rank + mine], 1);
           before = __shfl_sync(0xffffffffu, before, 0);
           if (before == u.np - 1) {
-            // The last piece to end joins them all, in their order: eight lanes to a token, kCols / 8 values to a lane.
-            __threadfence();
-            constexpr int kEach = kCols / 8;
-            const int sub = lane & 7;
-#pragma unroll 1
-            for (int r4 = 0; r4 < 32; r4 += 4) {
-              const int rr = 32 * quad + r4 + (lane >> 3);  // of this CTA
-              if (rr >= have) continue;
-              const int rp = kHalf * (int)rank + rr;
-              float top = -INFINITY;
-              for (int k = 0; k < u.np; ++k) {
-                const float y = __ldcg(&p.part_lse[((int64_t)(u.first + k) * 2 + g) * kTok + rp]);
-                top = y > top || y != y ? y : top;  // NaN stays
-              }
-              float acc[kEach], sum = 0.f;
-#pragma unroll
-              for (int j = 0; j < kEach; ++j) acc[j] = 0.f;
-              for (int k = 0; k < u.np; ++k) {
-                const float y = __ldcg(&p.part_lse[((int64_t)(u.first + k) * 2 + g) * kTok + rp]);
-                if (y == -INFINITY) continue;
-                const float wgt = exp2f((y - top) * kLog2e);
-                sum += wgt;
-                const float4* src = reinterpret_cast<const float4*>(p.part_out + ((int64_t)(u.first + k) * kTok + rp) * kDv + kCols * g + kEach * sub);
-#pragma unroll
-                for (int j = 0; j < kEach / 4; ++j) {
-                  const float4 f = __ldcg(src + j);
-                  acc[4 * j] = fmaf(wgt, f.x, acc[4 * j]);
-                  acc[4 * j + 1] = fmaf(wgt, f.y, acc[4 * j + 1]);
-                  acc[4 * j + 2] = fmaf(wgt, f.z, acc[4 * j + 2]);
-                  acc[4 * j + 3] = fmaf(wgt, f.w, acc[4 * j + 3]);
-                }
-              }
-              const float k1 = sum == 0.f ? 0.f : 1.f / sum;
-              const int64_t tk = (int64_t)u.tok + rp;
-              uint16_t* to = p.out + (tk * p.H + u.h) * kDv + kCols * g + kEach * sub;
-#pragma unroll
-              for (int j = 0; j < kEach / 8; ++j) {
-                uint32_t y[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = pack_bf16(acc[8 * j + 2 * k] * k1, acc[8 * j + 2 * k + 1] * k1);
-                *reinterpret_cast<uint4*>(to + 8 * j) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-              if (g == 0 && sub == 0 && p.lse) p.lse[tk * p.H + u.h] = sum == 0.f ? -INFINITY : top + logf(sum);
-            }
+            __threadfence();  // the last piece to end joins them all
+            join<kDv>(p, u, g, quad, (int)rank, left);
           }
         }
       } else {
