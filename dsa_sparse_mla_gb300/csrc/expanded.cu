@@ -651,7 +651,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int have = u.nrows - kHalf * (int)rank;  // tokens of this CTA
       const bool idle = 32 * quad >= have, there = row < have;
       int see = p.causal ? u.see + kHalf * (int)rank + row : u.see;
-      see = there ? (see < u.len ? see : u.len) : 0;
+      // a lane without a token computes what nobody reads; it must not be what makes its warp mask a tile
+      see = there ? min(see, u.len) : INT32_MAX;
       float ref = -INFINITY, l = 0.f;
       // the other warp with these tokens has read this one's sums and references, and is done with P's place
       if (!idle && joint > 0) ok = warp_wait_all(&br.over[other], (joint - 1) & 1u, p.err);
@@ -687,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) remote_arrive_relaxed(s_empty + 8 * (uint32_t)g);
-        const int lim = see - (u.ta + t) * kKeys;  // columns that this token sees
+        const int lim = see - (u.ta + t) * kKeys;  // columns that this token sees: all, or as many
         if (p.flip) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
