@@ -577,16 +577,22 @@ _pack_kv_read, _pack_mla_heads, _pack_mla_expand, _pack_mla_expanded = (
 def _strided(t, name, dtype, dims):
     """Address, shape and strides of a CUDA tensor of this type and number of dimensions whose last one has consecutive values. A
     dimension of one entry gets the stride that it has in a contiguous tensor (its own says nothing)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != dims:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
         raise HSError(1, "%s must be a %s CUDA tensor of %d dimensions" % (name, dtype, dims))
     shape, stride = t.shape, t.stride()
+    if len(shape) != dims:
+        raise HSError(1, "%s must be a %s CUDA tensor of %d dimensions" % (name, dtype, dims))
+    if t.get_device() != _current_device():
+        raise HSError(1, "%s is on another device than the current one" % name)
     if stride[-1] != 1 and shape[-1] > 1:
         raise HSError(1, "%s must have consecutive values in its last dimension" % name)
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise HSError(1, "%s is on another device than the current one" % name)
     if 1 in shape:
         stride = tuple(math.prod(shape[d + 1:]) if shape[d] == 1 else stride[d] for d in range(dims))
     return t.data_ptr(), shape, stride
+
+
+def _current_device():
+    return torch._C._cuda_getDevice()
 
 
 def hs_kv_read(kv_pool, block_table, out_start, out, err_flag, first=None, stream=None):
@@ -604,36 +610,46 @@ def hs_kv_read(kv_pool, block_table, out_start, out, err_flag, first=None, strea
                                            _int(out_start, "out_start"), n, op, ot, _int(err_flag, "err_flag")), _stream(stream)))
 
 
-def _heads_args(x, w, out, err_flag, taken, given):
-    """``taken`` / ``given``: what the last dimensions of x and out have to be, of (Dn, Dv), where the other one follows."""
+def _weight(w):
+    """Address of a layer's weight and its heads and values per head."""
+    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype is not torch.bfloat16 or not w.is_contiguous():
+        raise HSError(1, "w must be a contiguous bf16 CUDA tensor [H, Dn + Dv, 512]")
+    shape = w.shape
+    if len(shape) != 3 or shape[2] != 512:
+        raise HSError(1, "w must be a contiguous bf16 CUDA tensor [H, Dn + Dv, 512]")
+    return w.data_ptr(), shape[0], shape[1]
+
+
+def _heads_args(x, w, out, err_flag, absorb):
     xp, (T, H, Dx), (xt, xh, _) = _strided(x, "x", torch.bfloat16, 3)
     op, (To, Ho, Do), (ot, oh, _) = _strided(out, "out", torch.bfloat16, 3)
-    wp, (Hw, width, latent), _ = _strided(w, "w", torch.bfloat16, 3)
-    Dn, Dv = (Dx, width - Dx) if given == 512 else (width - Do, Do)
-    if latent != 512 or Hw != H or (To, Ho) != (T, H) or not w.is_contiguous() or (given or Do) != Do or (taken or Dx) != Dx:
-        raise HSError(1, "shape mismatch: x [T,H,%s], w [H,Dn+Dv,512] contiguous, out [T,H,%s]" % (taken or "Dn", given or "Dv"))
+    wp, Hw, width = _weight(w)
+    Dn, Dv = (Dx, width - Dx) if absorb else (width - Do, Do)
+    if Hw != H or To != T or Ho != H or (Do if absorb else Dx) != 512:
+        raise HSError(1, "shape mismatch: %s" % ("q [T,H,Dn], w [H,Dn+Dv,512], out [T,H,512]" if absorb else
+                                                 "x [T,H,512], w [H,Dn+Dv,512], out [T,H,Dv]"))
     return _pack_mla_heads(T, H, Dn, Dv, xp, xt, xh, wp, op, ot, oh, _int(err_flag, "err_flag"))
 
 
 def hs_mla_absorb(q, w, out, err_flag, stream=None):
     """Queries into the latent space: ``out[t, h] = q[t, h] @ w[h, :Dn]``; ``q`` bf16 [T, H, Dn] and ``out`` bf16 [T, H, 512] may be
     slices of wider heads, ``w`` is the layer's bf16 [H, Dn + Dv, 512]. See include/hs.h."""
-    _check(load().hs_mla_absorb(_heads_args(q, w, out, err_flag, None, 512), _stream(stream)))
+    _check(load().hs_mla_absorb(_heads_args(q, w, out, err_flag, True), _stream(stream)))
 
 
 def hs_mla_project(x, w, out, err_flag, stream=None):
     """Latent outputs to values: ``out[t, h] = w[h, Dn:] @ x[t, h]``; ``x`` bf16 [T, H, 512], ``out`` bf16 [T, H, Dv], ``w`` as for
     hs_mla_absorb."""
-    _check(load().hs_mla_project(_heads_args(x, w, out, err_flag, 512, None), _stream(stream)))
+    _check(load().hs_mla_project(_heads_args(x, w, out, err_flag, False), _stream(stream)))
 
 
 def hs_mla_expand(latent, w, kv, err_flag, stream=None):
     """Keys and values of every head from latent rows: ``kv[n, h] = w[h] @ latent[n]``; ``latent`` bf16 [N, 512] (rows may be wider),
     ``w`` bf16 [H, Dn + Dv, 512], ``kv`` bf16 [N, H, Dn + Dv]."""
     lp, (N, D), (ls, _) = _strided(latent, "latent", torch.bfloat16, 2)
-    wp, (H, width, latent_dim), _ = _strided(w, "w", torch.bfloat16, 3)
-    kp, shape, (ks, kh, _) = _strided(kv, "kv", torch.bfloat16, 3)
-    if D != 512 or latent_dim != 512 or tuple(shape) != (N, H, width) or (kh != width and H > 1) or not w.is_contiguous():
+    wp, H, width = _weight(w)
+    kp, (Nk, Hk, wk), (ks, kh, _) = _strided(kv, "kv", torch.bfloat16, 3)
+    if D != 512 or Nk != N or Hk != H or wk != width or kh != width:
         raise HSError(1, "shape mismatch: latent [N,512], w [H,Dn+Dv,512] contiguous, kv [N,H,Dn+Dv] with its heads one after the other")
     _check(load().hs_mla_expand(_pack_mla_expand(N, H, width, lp, ls, wp, kp, ks, _int(err_flag, "err_flag")), _stream(stream)))
 
@@ -655,7 +671,7 @@ def hs_mla_expanded_fwd(q, kv, rope, req_start, kv_start, softmax_scale: float, 
     rp, (Nr, D), (rs, _) = _strided(rope, "rope", torch.bfloat16, 2)
     op, B = _tensor(out, "out", torch.bfloat16), req_start.numel() - 1
     if out.dim() != 3 or out.shape[:2] != (T, H) or Hk != H or Nr != N or D != 64 or width - out.shape[2] != Dq - 64 \
-            or (kh != width and H > 1) or kv_start.numel() != B + 1 or (lse is not None and lse.shape != (T, H)):
+            or kh != width or kv_start.numel() != B + 1 or (lse is not None and lse.shape != (T, H)):
         raise HSError(1, "shape mismatch: q [T,H,Dn+64], kv [N,H,Dn+Dv] with its heads one after the other, rope [N,64], req_start and "
                          "kv_start [B+1], out [T,H,Dv], lse [T,H]")
     _check(load().hs_mla_expanded_fwd(_pack_mla_expanded(

@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   __shared__ int32_t classes[128], places[kMaxReq];  // requests of a class, and before it; units of a place
   constexpr int kPer = kMaxReq / kPlanThreads;
   let_next();
+  after_previous();
   int start[kPer], m[kPer], kv0[kPer], len[kPer], nb[kPer], np[kPer], place[kPer];
   int64_t most[kPer], work = 0;
   if (threadIdx.x < 128) classes[threadIdx.x] = 0;
@@ -381,36 +382,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Bars& br = *reinterpret_cast<Bars*>(smem + Sh::kOffBar);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
-  if (tid == 0) {
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(&br.ref[s], 1);
-      mbar_init(&br.sum[s], 1);
-      mbar_init(&br.over[s], 1);
-    }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&br.k_full[s], 2), mbar_init(&br.k_empty[s], 1);
-      mbar_init(&br.v_full[s], 2), mbar_init(&br.v_empty[s], 1);
-    }
+  let_next();
+  if (tid < 8) {
+    mbar_init(&br.ref[tid], 1);
+    mbar_init(&br.sum[tid], 1);
+    mbar_init(&br.over[tid], 1);
+  } else if (tid >= 32 && tid < 36) {
+    mbar_init(&br.k_full[tid - 32], 2);
+    mbar_init(&br.k_empty[tid - 32], 1);
+    mbar_init(&br.v_full[tid - 32], 2);
+    mbar_init(&br.v_empty[tid - 32], 1);
+  } else if (tid >= 64 && tid < 66) {
+    const int b = tid - 64;
+    mbar_init(&br.s_full[b], 1);
+    mbar_init(&br.s_empty[b], 8);
+    mbar_init(&br.p_full[b], 8);
+    mbar_init(&br.pv_done[b], 1);
+    mbar_init(&br.drain[b], 1);
+    mbar_init(&br.unit_full[b], 1);
+    mbar_init(&br.unit_empty[b], 22);  // copies of K, copies of V and eight softmax warps of both CTAs, QK, PV
+  } else if (tid == 96) {
     mbar_init(&br.q_full, 2);
     mbar_init(&br.q_empty, 1);
     mbar_init(&br.tail_full, 1);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&br.s_full[b], 1);
-      mbar_init(&br.s_empty[b], 8);
-      mbar_init(&br.p_full[b], 8);
-      mbar_init(&br.pv_done[b], 1);
-      mbar_init(&br.drain[b], 1);
-      mbar_init(&br.unit_full[b], 1);
-      mbar_init(&br.unit_empty[b], 22);  // copies of K, copies of V and eight softmax warps of both CTAs, QK, PV
-    }
     mbar_init(&br.o_full, 1);
     mbar_init(&br.o_free, 16);
-    mbar_fence_init();
+  } else if (tid == 128) {
     prefetch_tensormap(&map_q);
     prefetch_tensormap(&map_k);
     prefetch_tensormap(&map_r);
     prefetch_tensormap(&map_v);
   }
+  mbar_fence_init();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist
   if (warp == 0) tc2::alloc(&br.tmem, 512);
@@ -918,7 +921,7 @@ template <int kDn, int kDv>
 static cudaError_t launch(const Params& p, cudaStream_t stream, const char** why) {
   using Sh = Shape<kDn, kDv>;
   auto kernel = expanded_kernel<kDn, kDv>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  cudaError_t e = pair::allow_smem(kernel, Sh::kSmem);
   if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mr, mv;
   if (!pair::encode_heads(&mq, p.q, kDn + HS_D_ROPE, p.H, p.T, p.q_stride_h, p.q_stride_t, kHalf) ||
@@ -929,8 +932,7 @@ static cudaError_t launch(const Params& p, cudaStream_t stream, const char** why
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_next(plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
   return launch_next(kernel, dim3(2 * p.clusters), kThreads, Sh::kSmem, stream, mq, mk, mr, mv, p);
 }

@@ -13,6 +13,7 @@
 // goes on along the rows, so that only A streams through the ring. B comes and goes in chunks of 64 reduced values, with
 // barriers of their own, so that a change of head costs no more than a load's latency. Eight epilogue warps round to bf16 once and
 // store whole 128-byte lines through shared memory. Rows beyond M are read as zeros and not stored.
+#include "launch.cuh"
 #include "pair.cuh"
 
 namespace hs {
@@ -87,15 +88,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   uint8_t* ring_a = smem + p.n_tiles * p.k_steps * kChunk;
-  if (tid == 0) {
-    for (int s = 0; s < kMaxSlots; ++s) mbar_init(&br.a_full[s], 2), mbar_init(&br.a_empty[s], 1);
-    for (int s = 0; s < kMaxChunks; ++s) mbar_init(&br.b_full[s], 2), mbar_init(&br.b_empty[s], 1);
-    for (int b = 0; b < 2; ++b) mbar_init(&br.acc_full[b], 1), mbar_init(&br.acc_empty[b], 2 * kEpiWarps);
+  let_next();
+  if (tid < kMaxSlots) {
+    mbar_init(&br.a_full[tid], 2);
+    mbar_init(&br.a_empty[tid], 1);
+  } else if (tid >= 32 && tid < 32 + kMaxChunks) {
+    mbar_init(&br.b_full[tid - 32], 2);
+    mbar_init(&br.b_empty[tid - 32], 1);
+  } else if (tid >= 64 && tid < 66) {
+    mbar_init(&br.acc_full[tid - 64], 1);
+    mbar_init(&br.acc_empty[tid - 64], 2 * kEpiWarps);
+  } else if (tid == 66) {
     mbar_init(&br.drain, 1);
-    mbar_fence_init();
+  } else if (tid == 96) {
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
   }
+  mbar_fence_init();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist
   if (warp == 0) tc2::alloc(&br.tmem, 512);
@@ -103,6 +112,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = br.tmem;
   Run run(p);
+  after_previous();
 
   if (warp == 0) {
     // ================================================================ copies ====================
@@ -119,26 +129,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < (first ? p.n_tiles : 1) * p.k_steps; ++c) {  // chunk c: column tile c / k_steps
           const int nt = c >= p.k_steps ? 1 : 0, k = c - nt * p.k_steps;
+          // The first column tile's chunk of B is needed together with A's stage and counts on its barrier; the second one's on its own.
+          uint32_t bar = b_full + 8 * (uint32_t)c;
+          if (nt == 0) {
+            ok = mbar_wait(&br.a_empty[slot], par, p.err);
+            if (!ok) break;
+            bar = a_full + 8 * (uint32_t)slot;
+            pair::arrive_expect_tx(bar, first ? kSlot + kChunk : kSlot);
+            pair::load_3d(ring_a + slot * kSlot, &map_a, bar, k * kBK, h, y, p.a_again ? keep : stream);
+            if (++slot == p.slots) slot = 0, par ^= 1u;
+          }
           if (first) {
             ok = mbar_wait(&br.b_empty[c], (groups & 1u) ^ 1u, p.err);
             if (!ok) break;
             uint8_t* d = smem + c * kChunk;
-            const uint32_t bar = b_full + 8 * (uint32_t)c;
-            pair::arrive_expect_tx(bar, kChunk);
+            if (nt == 1) pair::arrive_expect_tx(bar, kChunk);
             if (kMnMajor) {  // 64 reduced rows of this CTA's columns, 64 columns to a block
 #pragma unroll 1
               for (int b = 0; b < kBN / 128; ++b) pair::load_2d(d + b * 8192, &map_b, bar, n0 + nt * kBN + 64 * b, rows + k * kBK, keep);
             } else {
               pair::load_2d(d, &map_b, bar, k * kBK, rows + n0 + nt * kBN, keep);
             }
-          }
-          if (nt == 0) {
-            ok = mbar_wait(&br.a_empty[slot], par, p.err);
-            if (!ok) break;
-            const uint32_t bar = a_full + 8 * (uint32_t)slot;
-            pair::arrive_expect_tx(bar, kSlot);
-            pair::load_3d(ring_a + slot * kSlot, &map_a, bar, k * kBK, h, y, p.a_again ? keep : stream);
-            if (++slot == p.slots) slot = 0, par ^= 1u;
           }
         }
         if (first) ++groups;
@@ -169,13 +180,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll(kMnMajor ? 1 : 8)
           for (int k = 0; k < (kMnMajor ? p.k_steps : HS_D_LATENT / kBK); ++k, ++c) {
             if (nt == 0 && !there) ok = mbar_wait(&br.a_full[slot], par, p.err);
-            if (first && ok) ok = mbar_wait(&br.b_full[c], groups & 1u, p.err);
+            if (nt == 1 && first && ok) ok = mbar_wait(&br.b_full[c], groups & 1u, p.err);
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = ad + (uint64_t)((slot * kSlot) >> 4), w = bd + (uint64_t)((c * kChunk) >> 4);
             uint64_t* empty = &br.a_empty[slot];
             if (++slot == p.slots) slot = 0, par ^= 1u;
-            there = nt + 1 == p.n_tiles || nt == 0 ? pair::test_wait(&br.a_full[slot], par) : false;
+            there = pair::test_wait(&br.a_full[slot], par);
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
               tc2::ss(d, a + 2 * kk, w + (kMnMajor ? 128 : 2) * kk, id, (k | kk) != 0 ? 1u : 0u);
@@ -259,15 +270,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <int kBN, bool kMnMajor>
 static cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, Params p, int sms, cudaStream_t stream) {
   auto kernel = heads_kernel<kBN, kMnMajor>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t e = pair::allow_smem(kernel, kSmem);
   if (e != cudaSuccess) return e;
   p.m_tiles = (int)(((int64_t)p.M + kBM - 1) / kBM);
+  // Units of several row tiles reload B less often, but are fewer: at least four for each pair (1,501 rows x 28 groups ... us with units of
+  // four row tiles, ... with one).
+  while (p.m_unit > 1 && (int64_t)p.m_tiles * p.groups < (int64_t)p.m_unit * 4 * (sms / 2)) p.m_unit /= 2;
   p.units = ((int64_t)p.m_tiles + p.m_unit - 1) / p.m_unit * p.groups;
   const int slots = (kOperands - p.n_tiles * p.k_steps * (kBN / 2 * kBK * 2)) / kSlot;
   p.slots = slots < kMaxSlots ? slots : kMaxSlots;
   const int64_t pairs = p.units < sms / 2 ? p.units : sms / 2;
-  kernel<<<(int)(2 * pairs), kThreads, kSmem, stream>>>(ma, mb, p);
-  return cudaGetLastError();
+  return launch_next(kernel, dim3((unsigned)(2 * pairs)), kThreads, kSmem, stream, ma, mb, p);
 }
 
 static cudaError_t maps_failed(const char** why) {

@@ -2,7 +2,9 @@
 //
 // A call's second kernel may be launched while its first still runs (launch_next), so that its blocks stand ready when the first
 // ends: the first lets it (let_next), the second waits for the first's end and its writes before it reads or writes
-// anything (after_previous). The first kernel of a call, and whatever the caller enqueues next, start as usual.
+// anything (after_previous). The first kernel of a call, and whatever the caller enqueues next, start as usual; the calls of read.cu,
+// heads.cu and expanded.cu let a call of theirs that follows start early, too: every one of their blocks waits for what came before,
+// so a kernel's end is still the end of everything before it.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -2,6 +2,8 @@
 // counted on a barrier of either CTA, 16-byte stores into either CTA's shared memory that count there.
 #pragma once
 
+#include <atomic>
+
 #include "cluster.cuh"
 
 namespace hs {
@@ -79,6 +81,29 @@ inline bool encode_heads(CUtensorMap* map, const void* base, uint64_t cols, uint
   cuuint32_t box[3] = {64, 1, box_rows}, es[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Lets a kernel use this much dynamic shared memory; asked once per kernel and device.
+template <typename... P>
+inline cudaError_t allow_smem(void (*kernel)(P...), int bytes) {
+  struct Seen {
+    std::atomic<const void*> kernel[64];
+  };
+  static Seen seen[8];  // kernels of one signature: a few instances of one template
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const void* k = reinterpret_cast<const void*>(kernel);
+  if (dev < 64)
+    for (Seen& s : seen)
+      if (s.kernel[dev].load(std::memory_order_relaxed) == k) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess || dev >= 64) return e;
+  for (Seen& s : seen) {
+    const void* none = nullptr;
+    if (s.kernel[dev].compare_exchange_strong(none, k) || none == k) break;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pair

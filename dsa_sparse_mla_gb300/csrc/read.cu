@@ -6,6 +6,7 @@
 // codes and of results are such that every access of the warp is one run of at least 128 bytes. Bound by HBM: 656 bytes in and 1,152
 // (2,304) out per row.
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace hs {
 namespace read {
@@ -49,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Params p) {
   constexpr int kCodes = 16 / (int)sizeof(T);     // codes each: 4 or 8
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  let_next();
   if (blockIdx.x == 0) {
     for (int r = threadIdx.x; r < p.B; r += kThreads)
       if (p.start[r + 1] < p.start[r] || (r == 0 && p.start[0] != 0) || p.start[r + 1] > p.n) flag_error(p.err, HS_FLAG_BAD_INDEX);
@@ -160,12 +162,8 @@ cudaError_t launch_kv_read(const hs_kv_read_args* a, int sms, cudaStream_t strea
   p.B = a->B, p.bt_stride = a->bt_stride;
   const int64_t want = (a->n + kRows * (kThreads / 32) - 1) / (kRows * (kThreads / 32));
   const int grid = (int)(want < 8 * sms ? want : 8 * sms);
-  if (a->dtype == HS_BF16)
-    read_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
-  else if (a->dtype == HS_FP16)
-    read_kernel<__half><<<grid, kThreads, 0, stream>>>(p);
-  else
-    read_kernel<float><<<grid, kThreads, 0, stream>>>(p);
+  auto kernel = a->dtype == HS_BF16 ? read_kernel<__nv_bfloat16> : a->dtype == HS_FP16 ? read_kernel<__half> : read_kernel<float>;
+  kernel<<<grid, kThreads, 0, stream>>>(p);  // started early, it waits longer than it gains (8 requests in a graph 4.5 us, 5.7 started early)
   return cudaGetLastError();
 }
 
