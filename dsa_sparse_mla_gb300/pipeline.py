@@ -9,20 +9,24 @@ tokens reuse that set in hs_sparse_mla_fwd (shared index sets); ``LongPrefillPas
 chunk of a long prefill through the same three calls. ``DeviceHiSparse`` does the
 same for the mixed-residency decode (hs_hisparse_resolve -> hs_sparse_mla_fwd on physical rows),
 with the older rows in pinned host memory. ``DenseSession`` runs requests that attend densely and may branch
-(hs_rope -> hs_kv_append -> hs_paged_mla_fwd; hs_kv_fork, hs_kv_free and hs_kv_compact between steps).
+(hs_rope -> hs_kv_append -> hs_paged_mla_fwd; hs_kv_fork, hs_kv_free and hs_kv_compact between steps), from per-head queries to
+per-head outputs in either form of latent attention (hs_mla_absorb -> hs_paged_mla_fwd -> hs_mla_project, or hs_kv_read ->
+hs_mla_expand -> hs_mla_expanded_fwd).
 
 Only buffer management lives here; all arithmetic runs in libhs.so.
 """
 from __future__ import annotations
 
 import dataclasses
+import math
 
 import numpy as np
 import torch
 
 from . import (hs_hisparse_resolve, hs_hisparse_touch_host, hs_indexer_scores, hs_indexer_topk, hs_kv_append, hs_kv_compact,
-               hs_kv_compact_workspace_size, hs_kv_fork, hs_kv_free, hs_paged_mla_fwd, hs_paged_mla_workspace_size, hs_rope,
-               hs_rope_inv_freq, hs_sparse_mla_fwd, hs_sparse_mla_workspace_size, hs_topk)
+               hs_kv_compact_workspace_size, hs_kv_fork, hs_kv_free, hs_kv_read, hs_mla_absorb, hs_mla_expand, hs_mla_expanded_fwd,
+               hs_mla_expanded_workspace_size, hs_mla_project, hs_paged_mla_fwd, hs_paged_mla_workspace_size, hs_rope, hs_rope_inv_freq,
+               hs_sparse_mla_fwd, hs_sparse_mla_workspace_size, hs_topk)
 from .inputs import HiSparseWorkload, Workload
 
 
@@ -273,7 +277,7 @@ class DenseSession:
     """Requests that attend densely over the paged latent cache and may branch (several samples of one prompt, beams):
     device state for ``B`` request slots and ``L`` layers, and the calls of a step in their order. ``extend`` gives the new
     tokens their positions and pages, then ``attend`` runs once per layer (hs_rope of queries and keys -> hs_kv_append ->
-    hs_paged_mla_fwd). Between steps ``fork`` makes slots copies of others (pages shared, the partial one copied), ``free``
+    hs_paged_mla_fwd), or ``attend_heads``, which takes and gives per-head values and picks the form of latent attention. Between steps ``fork`` makes slots copies of others (pages shared, the partial one copied), ``free``
     empties slots, and ``compact`` moves the pages in use to the front. Everything runs on the current stream. The attention's
     workspace is made for steps of ``max_tokens`` and grows with the cached rows, or where a step has more tokens."""
 
@@ -296,6 +300,7 @@ class DenseSession:
         self.kv_tokens = 0  # cached rows: shared pages count once per request
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
         self._make_room(max_tokens, 0)
+        self._kept = {}  # attend_heads' buffers by name
         self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
 
     def _make_room(self, tokens: int, cached: int):
@@ -327,6 +332,10 @@ class DenseSession:
         self.positions = (torch.arange(T, dtype=torch.int32, device=self.device)
                           + torch.repeat_interleave(self.seq_len - self.req_start[:-1], new))
         self.seq_len = after
+        # what the expanded form reads: the rows of slots with new tokens
+        read = torch.where(new > 0, after, 0)
+        self.read_start = torch.cat([read.new_zeros(1), read.cumsum(0).int()])
+        self.read_tokens, self.active = int(read.sum()), int((new > 0).sum())
         return T
 
     def attend(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, out: torch.Tensor, lse=None):
@@ -336,6 +345,55 @@ class DenseSession:
         hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=self.pool[layer])
         hs_paged_mla_fwd(q, self.pool[layer], self.table, self.req_start, self.seq_len, self.kv_tokens, self.softmax_scale, out,
                          self.err, self.workspace, lse=lse)
+
+    #: The expanded form from this many new tokens per slot that has any, on average. It expands a slot's rows once, 512 (Dn + Dv)
+    #: products a head and row, and then spends Dn + 64 + Dv on a pair instead of 1,088. Measured, 64 heads, absorbed / expanded in us: (128, 128),
+    #: 8 slots over 8,000 rows x 128 tokens 917 / 1,165, x 192 1,341 / 1,176; one over 32,000 x 128 460 / 662, x 256 827 / 672; (192, 256), 8 over
+    #: 8,000 x 256 1,805 / 2,037, x 384 2,658 / 2,598. (Over short contexts it pays earlier: 16 over 500 x 64 217 / 249, x 128 354 / 278.)
+    EXPAND_FROM = {128: 192, 256: 384}
+    #: Bytes of expanded keys and values at most; steps that would need more stay in the absorbed form.
+    EXPAND_BYTES = 32 << 30
+
+    def _buffer(self, name: str, *shape, dtype=torch.bfloat16):
+        """A buffer that is kept from step to step, made anew with a quarter to spare where it is too small."""
+        n = math.prod(shape)
+        if name not in self._kept or self._kept[name].numel() < n or self._kept[name].dtype != dtype:
+            self._kept[name] = None  # its memory may serve the larger one
+            self._kept[name] = torch.empty(n + n // 4, dtype=dtype, device=self.device)
+        return self._kept[name][:n].view(shape)
+
+    def attend_heads(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
+                     lse=None, form: str | None = None):
+        """Layer ``layer`` of the tokens of the last extend from per-head queries to per-head outputs: ``q`` bf16 [T, H, Dn + 64] (its
+        rotary part, the last 64 values, may be rotated in place) and ``rope`` bf16 [T, 64] (rotated in place), ``latent`` bf16 [T, 512],
+        the layer's weight ``w`` bf16 [H, Dn + Dv, 512], ``out`` bf16 [T, H, Dv]; logits are scaled by (Dn + 64)^-1/2. ``form`` is "absorbed"
+        or "expanded"; None picks it by the new tokens per slot."""
+        (T, H, D), Dn, Dv = q.shape, q.shape[2] - 64, out.shape[2]
+        if form is None:
+            pays = Dv in self.EXPAND_FROM and T >= self.EXPAND_FROM[Dv] * self.active
+            form = "expanded" if pays and 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES else "absorbed"
+        if form not in ("absorbed", "expanded"):
+            raise ValueError("form must be absorbed or expanded")
+        if T == 0:
+            return
+        scale = self.softmax_scale * 24.0 * (Dn + 64) ** -0.5
+        if form == "absorbed":
+            wide, mixed = self._buffer("queries", T, H, 576), self._buffer("mixed", T, H, 512)
+            hs_rope(q[..., Dn:], self.positions, self.inv_freq, out=wide[..., 512:], y=rope[:, None], scale=self.rope_scale)
+        else:
+            hs_rope(q[..., Dn:], self.positions, self.inv_freq, y=rope[:, None], scale=self.rope_scale)
+        hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=self.pool[layer])
+        if form == "absorbed":
+            hs_mla_absorb(q[..., :Dn], w, wide[..., :512], self.err)
+            hs_paged_mla_fwd(wide, self.pool[layer], self.table, self.req_start, self.seq_len, self.kv_tokens, scale, mixed, self.err,
+                             self.workspace, lse=lse)
+            hs_mla_project(mixed, w, out, self.err)
+        else:
+            rows, kv = self._buffer("rows", self.read_tokens, 576), self._buffer("kv", self.read_tokens, H, Dn + Dv)
+            workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.B, Dv), dtype=torch.uint8)
+            hs_kv_read(self.pool[layer], self.table, self.read_start, rows, self.err)
+            hs_mla_expand(rows[:, :512], w, kv, self.err)
+            hs_mla_expanded_fwd(q, kv, rows[:, 512:], self.req_start, self.read_start, scale, out, self.err, workspace, lse=lse)
 
     def fork(self, parent, child):
         parent, child = (torch.as_tensor(x, dtype=torch.int32, device=self.device) for x in (parent, child))
