@@ -31,8 +31,8 @@
 namespace hs {
 namespace expanded {
 
-constexpr int kTok = 256, kHalf = 128, kKeys = 128;  // tokens of a block, of a CTA; rows of a tile
-constexpr int kThreads = 384;                        // Q and K, QK, PV (units in the other CTA), V; 2 x 128 softmax threads
+constexpr int kTok = 256, kHalf = 128, kKeys = 128;  // tokens of a block (at most), of a CTA; rows of a tile
+constexpr int kThreads = 384;                        // Q and K, QK, PV (units in the other CTA), V (and units); 2 x 128 softmax threads
 constexpr float kThreshold = 8.0f;                   // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -52,8 +52,11 @@ struct Unit {
   int32_t np, slot, first, pad;    // pieces of the block (1: whole), this piece's slot, the first piece's
 };
 
+constexpr int kMaxPlaces = 4;
+
 struct Params {
-  int32_t T, B, H, causal, clusters, cap;
+  int32_t T, B, H, causal, cap;
+  int32_t workers, tok;  // pairs of CTAs and 256, or CTAs and 128 tokens of a block
   const uint16_t* q;
   int64_t q_stride_t, q_stride_h;
   const uint16_t* kv;
@@ -75,32 +78,27 @@ struct Params {
 };
 
 // ------------------------------------------------------------------------ plan ------------
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t s = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) s += scratch[w];
-  return s;
-}
-// Sum of the values of the threads before this one.
-__device__ __forceinline__ int64_t block_before(int64_t v, int64_t* scratch) {
+// Sum over the threads before this one, and of all.
+__device__ __forceinline__ int64_t block_before(int64_t v, int64_t* scratch, int64_t* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+  auto scan = [&](int64_t x) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    return x;
+  };
+  const int64_t x = scan(v);
   __syncthreads();
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  int64_t s = x - v;
-  for (int w = 0; w < warp; ++w) s += scratch[w];
-  return s;
+  const int64_t w = scan(scratch[lane]);  // of the warps up to this lane's
+  *all = __shfl_sync(0xffffffffu, w, 31);
+  const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return x - v + (warp > 0 ? before : 0);
 }
+static_assert(kPlanThreads == 32 * 32, "a lane to a warp's sum");
 
 // Requests in descending order of their longest block, to a quarter of an octave (within one in any order: no result depends on it).
 __device__ __forceinline__ int size_class(int64_t tiles) {
@@ -109,7 +107,7 @@ __device__ __forceinline__ int size_class(int64_t tiles) {
 
 // One CTA. Thread t plans requests 4 t .. 4 t + 3. Long blocks come first, so that the last units to end are short. A block longer
 // than half of a pair's even share of all tiles is split into pieces of at most a quarter of it, but of kMinPiece tiles at least, and
-// longer ones where they would not fit their slots. (Pieces cost: blocks split at a quarter took nine ragged requests from ... us.)
+// longer ones where they would not fit their slots.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   __shared__ int64_t scratch[32];
   __shared__ int32_t classes[128], places[kMaxReq];  // requests of a class, and before it; units of a place
@@ -117,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   let_next();
   after_previous();
   int start[kPer], m[kPer], kv0[kPer], len[kPer], nb[kPer], np[kPer], place[kPer];
-  int64_t most[kPer], work = 0;
+  int64_t most[kPer], work = 0, tokens = 0;
   if (threadIdx.x < 128) classes[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
@@ -130,20 +128,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     if (a < 0 || b < a || b > p.T || (r == 0 && a != 0) || (r == p.B - 1 && b != p.T)) flag_error(p.err, HS_FLAG_BAD_INDEX);
     if (a >= 0 && b > a && b <= p.T) {
       start[k] = (int)a, m[k] = (int)(b - a);
-      nb[k] = (m[k] + kTok - 1) / kTok;
+      nb[k] = (m[k] + p.tok - 1) / p.tok;
+      tokens += m[k];
       if (c < 0 || d < c || d > p.N) {
         flag_error(p.err, HS_FLAG_BAD_LENGTH);
       } else {
         kv0[k] = (int)c, len[k] = (int)(d - c);
       }
       most[k] = (len[k] + kKeys - 1) / kKeys;
-      const int64_t least = p.causal ? ((int64_t)len[k] - m[k] + kTok + kKeys - 1) / kKeys : most[k];  // of the first block
+      const int64_t least = p.causal ? ((int64_t)len[k] - m[k] + p.tok + kKeys - 1) / kKeys : most[k];  // of the first block
       work += nb[k] * (most[k] + (least < 1 ? 1 : least < most[k] ? least : most[k])) / 2 * p.H;
     }
     place[k] = atomicAdd(&classes[size_class(nb[k] ? most[k] + 1 : 0)], 1);
   }
-  work = block_sum(work, scratch);
-  int64_t piece = (work / p.clusters + 3) / 4;
+  int64_t all = 0;
+  block_before(tokens, scratch, &all);
+  const bool none = all > p.T;  // requests overlap (offsets out of order, flagged above): no bound on the units would hold
+  block_before(work, scratch, &all);
+  work = all;
+  int64_t piece = (work / p.workers + 3) / 4;
   if (piece < kMinPiece) piece = kMinPiece;
 #pragma unroll 1
   for (;; piece *= 2) {
@@ -151,7 +154,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (most[k] > 2 * piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
-    if (block_sum(slots, scratch) <= p.cap) break;
+    block_before(slots, scratch, &all);
+    if (all <= p.cap) break;
   }
   int64_t slots = 0;
 #pragma unroll
@@ -159,21 +163,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     np[k] = most[k] > 2 * piece ? (int)((most[k] + piece - 1) / piece) : 1;
     if (np[k] > 1) slots += (int64_t)nb[k] * p.H * np[k];
   }
-  int64_t slot0 = block_before(slots, scratch);
-  if (threadIdx.x == 0) {
-    int before = 0;
-    for (int c = 0; c < 128; ++c) {
-      const int n = classes[c];
-      classes[c] = before;
-      before += n;
-    }
-  }
+  int64_t slot0 = block_before(slots, scratch, &all);
+  const int64_t before = block_before(threadIdx.x < 128 ? classes[threadIdx.x] : 0, scratch, &all);
+  if (threadIdx.x < 128) classes[threadIdx.x] = (int)before;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     if (kPer * (int)threadIdx.x + k >= p.B) continue;
     place[k] += classes[size_class(nb[k] ? most[k] + 1 : 0)];
-    places[place[k]] = nb[k] * p.H * np[k];
+    places[place[k]] = none ? 0 : nb[k] * p.H * np[k];
   }
   __syncthreads();
   int64_t units = 0;
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     const int r = kPer * threadIdx.x + k;
     if (r < p.B) units += places[r];
   }
-  int64_t unit0 = block_before(units, scratch);
+  int64_t unit0 = block_before(units, scratch, &all);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = kPer * threadIdx.x + k;
@@ -191,8 +189,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     places[r] = (int32_t)unit0;
     unit0 += n;
   }
-  if (threadIdx.x == kPlanThreads - 1) {
-    p.total[0] = (int32_t)unit0;
+  if (threadIdx.x == 0) {
+    p.total[0] = (int32_t)all;
     p.total[1] = 0;
   }
   __syncthreads();
@@ -206,18 +204,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
 }
 
 // ------------------------------------------------------------------------ attention -------
-template <int kDn, int kDv>
+template <int kDn, int kDv, int kSMs>
 struct Shape {
   static constexpr int kQB = kDn / 64 + 1;                    // blocks of 64 values of a query or key
   static constexpr bool kWide = kDv > 128;                    // P through shared memory
   static constexpr int kQBlk = kHalf * 128, kQBytes = kQB * kQBlk;
-  static constexpr int kKBlk = kKeys / 2 * 128, kKBytes = kQB * kKBlk;
-  static constexpr int kVBlk = kKeys * 128, kVBytes = kDv / 128 * kVBlk;
-  static constexpr int kKSlots = kWide ? 2 : 4, kVSlots = kWide ? 2 : 4;
+  static constexpr int kKRows = kKeys / kSMs, kVCols = kDv / kSMs;  // of a tile, in a CTA
+  static constexpr int kKBlk = kKRows * 128, kKBytes = kQB * kKBlk;
+  static constexpr int kVBlk = kKeys * 128, kVBytes = kVCols / 64 * kVBlk;
+  static constexpr int kKSlots = kWide || kSMs == 1 ? 2 : 4, kVSlots = kKSlots;
+  static constexpr int kPlaces = kSMs == 1 ? 4 : 2;           // units that the roles can be apart
   static constexpr int kPBlk = kHalf * 128, kPBytes = kWide ? 2 * kPBlk : 0;  // blocks of 64 cached rows
   static constexpr int kOffK = kQBytes, kOffV = kOffK + kKSlots * kKBytes, kOffP = kOffV + kVSlots * kVBytes, kOffRef = kOffP + (kWide ? kPBytes : 8 * 2048);
   static constexpr int kOffOut = kOffP;                       // 2 KB per softmax warp for the output (wide: in P's place, see the unit's end)
-  static constexpr int kOffSum = kOffRef + 1024, kOffUnit = kOffSum + 1024, kOffBar = kOffUnit + 2 * (int)sizeof(Unit);
+  static constexpr int kOffSum = kOffRef + 1024, kOffUnit = kOffSum + 1024, kOffBar = kOffUnit + kMaxPlaces * (int)sizeof(Unit);
   static constexpr int kSmem = kOffBar + 512;
   static constexpr int kColP = 256, kColO = kWide ? 256 : 384;  // tensor-memory columns; logits in 0 .. 255
   static_assert(kDv % 128 == 0 && kDv <= 256 && kSmem <= 232448, "shared and tensor memory");
@@ -225,7 +225,7 @@ struct Shape {
 
 struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
-  uint64_t tail_full, unit_full[2], unit_empty[2];
+  uint64_t tail_full, unit_full[kMaxPlaces], unit_empty[kMaxPlaces];
   uint64_t ref[8], sum[8], over[8];  // [warpgroup][quad]
   uint32_t tmem;
 };
@@ -239,7 +239,8 @@ struct Ring {
   }
 };
 
-// A role's walk over the units: they arrive in two places of shared memory in turn.
+// A role's walk over the units: they arrive in kPlaces places of shared memory in turn.
+template <int kPlaces, int kSMs>
 struct Units {
   const uint8_t* at;
   Bars* br;
@@ -248,15 +249,15 @@ struct Units {
   bool gives;     // whether this thread gives units back for its role
   // Unit number n (one thread, or every lane of a warp); false after a wait that ran out.
   __device__ __forceinline__ bool take(uint32_t n, Unit& u) const {
-    if (!mbar_wait(&br->unit_full[n & 1u], (n >> 1) & 1u, err)) return false;
-    const int4* v = reinterpret_cast<const int4*>(at + (n & 1u) * sizeof(Unit));
+    if (!mbar_wait(&br->unit_full[n % kPlaces], (n / kPlaces) & 1u, err)) return false;
+    const int4* v = reinterpret_cast<const int4*>(at + n % kPlaces * sizeof(Unit));
     int4* w = reinterpret_cast<int4*>(&u);
 #pragma unroll
     for (int i = 0; i < 3; ++i) w[i] = v[i];
     return true;
   }
   __device__ __forceinline__ void give_back(uint32_t n) const {
-    if (gives) remote_arrive_cta(back + 8 * (n & 1u));
+    if (gives) pair::Mma<kSMs>::arrive(back + 8 * (n % kPlaces));
   }
 };
 
@@ -369,11 +370,73 @@ __device__ __noinline__ bool rescue(const Params& p, const Unit& u, int64_t tok,
   return true;
 }
 
-template <int kDn, int kDv>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    expanded_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                    const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v, const Params p) {
-  using Sh = Shape<kDn, kDv>;
+// Hands out units: the next one of the plan becomes number n of this pair (CTA).
+template <int kPlaces, int kSMs>
+struct Giver {
+  const Params& p;
+  uint64_t* empty;  // of this CTA
+  uint8_t* units;
+  uint32_t at, full;
+  int r0;           // the last unit's request
+  // The whole warp; false at the end, and after a wait that ran out.
+  __device__ __forceinline__ bool give(uint32_t n, int32_t total, int lane) {
+    if (!warp_wait(&empty[n % kPlaces], ((n / kPlaces) & 1u) ^ 1u, p.err, lane)) return false;
+    int32_t i = 0;
+    if (lane == 0) i = atomicAdd(&p.total[1], 1);
+    i = __shfl_sync(0xffffffffu, i, 0);
+    Unit u = {};
+    if (i < total) {
+      // its request: the last that starts at or before it (numbers grow, so the search goes on from the last one)
+      for (;;) {
+        const int r = r0 + 1 + lane;
+        const uint32_t le = __ballot_sync(0xffffffffu, r < p.B && p.req[r < p.B ? r : 0].unit0 <= i);
+        r0 += __popc(le);
+        if (le != 0xffffffffu) break;
+      }
+      const Req q = p.req[r0];
+      const int per_head = q.nb * q.np, x = i - q.unit0, rest = x % per_head;
+      const int b = q.nb - 1 - rest / q.np, piece = rest % q.np;
+      u.h = x / per_head;
+      u.tok = q.q0 + b * p.tok;
+      u.nrows = min(q.m - b * p.tok, p.tok);
+      u.kv0 = q.kv0;
+      u.len = q.len;
+      u.see = p.causal ? q.len - q.m + 1 + b * p.tok : q.len;
+      const int64_t last = p.causal ? (int64_t)u.see + u.nrows - 1 : q.len;
+      const int64_t tiles = last > 0 ? (last + kKeys - 1) / kKeys : 0;
+      const int64_t ta = tiles * piece / q.np, tb = tiles * (piece + 1) / q.np;
+      u.ta = (int)ta;
+      u.n = tb > ta ? (int)(tb - ta) : 1;
+      if (tb == ta) u.len = 0;  // a tile of which no row is there
+      u.np = q.np;
+      u.first = q.slot0 + (u.h * q.nb + b) * q.np;
+      u.slot = u.first + piece;
+    }
+    if (lane < kSMs) {
+      const int4* v = reinterpret_cast<const int4*>(&u);
+      const uint32_t place = n % kPlaces;
+      if constexpr (kSMs == 2) {
+        const uint32_t on = full + 8 * place;
+        pair::arrive_expect_tx(on, sizeof(Unit));
+#pragma unroll
+        for (int k = 0; k < 3; ++k) pair::st_async16(at + place * (uint32_t)sizeof(Unit) + 16 * k, v[k], on);
+      } else {
+        int4* to = reinterpret_cast<int4*>(units + place * sizeof(Unit));
+#pragma unroll
+        for (int k = 0; k < 3; ++k) to[k] = v[k];
+        pair::Mma<1>::arrive(full + 8 * place);
+      }
+    }
+    __syncwarp();
+    return i < total;
+  }
+};
+
+template <int kDn, int kDv, int kSMs>
+__device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_r, const CUtensorMap& map_v,
+                                       const Params& p) {
+  using Sh = Shape<kDn, kDv, kSMs>;
+  using Mma = pair::Mma<kSMs>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzled blocks need it; the same in both CTAs
     if (threadIdx.x == 0) flag_error(p.err, HS_FLAG_BAD_STATE);
@@ -381,32 +444,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   Bars& br = *reinterpret_cast<Bars*>(smem + Sh::kOffBar);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = kSMs == 2 ? cluster_ctarank() : 0;
   let_next();
   if (tid < 8) {
     mbar_init(&br.ref[tid], 1);
     mbar_init(&br.sum[tid], 1);
     mbar_init(&br.over[tid], 1);
   } else if (tid >= 32 && tid < 36) {
-    mbar_init(&br.k_full[tid - 32], 2);
+    mbar_init(&br.k_full[tid - 32], kSMs);
     mbar_init(&br.k_empty[tid - 32], 1);
-    mbar_init(&br.v_full[tid - 32], 2);
+    mbar_init(&br.v_full[tid - 32], kSMs);
     mbar_init(&br.v_empty[tid - 32], 1);
   } else if (tid >= 64 && tid < 66) {
     const int b = tid - 64;
     mbar_init(&br.s_full[b], 1);
-    mbar_init(&br.s_empty[b], 8);
-    mbar_init(&br.p_full[b], 8);
+    mbar_init(&br.s_empty[b], 4 * kSMs);
+    mbar_init(&br.p_full[b], 4 * kSMs);
     mbar_init(&br.pv_done[b], 1);
     mbar_init(&br.drain[b], 1);
-    mbar_init(&br.unit_full[b], 1);
-    mbar_init(&br.unit_empty[b], 22);  // copies of K, copies of V and eight softmax warps of both CTAs, QK, PV
+  } else if (tid >= 100 && tid < 100 + kMaxPlaces) {
+    mbar_init(&br.unit_full[tid - 100], 1);
+    mbar_init(&br.unit_empty[tid - 100], 10 * kSMs + 2);  // copies of K, copies of V and eight softmax warps of a CTA; QK, PV
   } else if (tid == 96) {
-    mbar_init(&br.q_full, 2);
+    mbar_init(&br.q_full, kSMs);
     mbar_init(&br.q_empty, 1);
     mbar_init(&br.tail_full, 1);
     mbar_init(&br.o_full, 1);
-    mbar_init(&br.o_free, 16);
+    mbar_init(&br.o_free, 8 * kSMs);
   } else if (tid == 128) {
     prefetch_tensormap(&map_q);
     prefetch_tensormap(&map_k);
@@ -415,13 +479,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   mbar_fence_init();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist
-  if (warp == 0) tc2::alloc(&br.tmem, 512);
+  if (kSMs == 2) cluster_sync();  // both CTAs' barriers exist
+  if (warp == 0) Mma::alloc(&br.tmem, 512);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = br.tmem;
   after_previous();  // the plan
-  const Units us = {smem + Sh::kOffUnit, &br, p.err, remote_smem(br.unit_empty, 1), lane == 0};
+  const Units<Sh::kPlaces, kSMs> us = {smem + Sh::kOffUnit, &br, p.err, Mma::at(br.unit_empty, kSMs - 1), lane == 0};
 
   if (warp < 4) {
     // 384 threads start with 168 registers (64,512 in all): 128 keep 96, 256 take 200 (63,488)
@@ -430,33 +494,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ================================================================ Q and K =================
       if (lane == 0) {
-        const uint32_t full = remote_smem(br.k_full, 0), q_full = remote_smem(&br.q_full, 0);
+        const uint32_t full = Mma::at(br.k_full, 0), q_full = Mma::at(&br.q_full, 0);
         Ring ring = {0, 1};
         bool ok = true;
 #pragma unroll 1
         for (uint32_t n = 0; ok; ++n) {
           ok = us.take(n, u);
           if (!ok || u.n == 0) break;
-          int y = u.kv0 + u.ta * kKeys + kKeys / 2 * (int)rank;
+          int y = u.kv0 + u.ta * kKeys + Sh::kKRows * (int)rank;
           bool asked = false;  // Q: its place is free when the unit before has issued its last QK; until then K goes ahead
 #pragma unroll 1
           for (int t = 0; t < u.n; ++t, y += kKeys) {
             if (!asked && (t == Sh::kKSlots - 1 || t == u.n - 1 || pair::test_wait(&br.q_empty, (n & 1u) ^ 1u))) {
               ok = mbar_wait(&br.q_empty, (n & 1u) ^ 1u, p.err);
               if (!ok) break;
-              pair::arrive_expect_tx(q_full, Sh::kQBytes);
+              Mma::expect(q_full, Sh::kQBytes);
 #pragma unroll 1
-              for (int b = 0; b < Sh::kQB; ++b) pair::load_3d(smem + b * Sh::kQBlk, &map_q, q_full, 64 * b, u.h, u.tok + kHalf * (int)rank);
+              for (int b = 0; b < Sh::kQB; ++b) pair::load_3d<kSMs>(smem + b * Sh::kQBlk, &map_q, q_full, 64 * b, u.h, u.tok + kHalf * (int)rank);
               asked = true;
             }
             ok = mbar_wait(&br.k_empty[ring.slot], ring.par, p.err);
             if (!ok) break;
             uint8_t* s = smem + Sh::kOffK + ring.slot * Sh::kKBytes;
             const uint32_t bar = full + 8 * (uint32_t)ring.slot;
-            pair::arrive_expect_tx(bar, Sh::kKBytes);
+            Mma::expect(bar, Sh::kKBytes);
 #pragma unroll 1
-            for (int b = 0; b < kDn / 64; ++b) pair::load_3d(s + b * Sh::kKBlk, &map_k, bar, 64 * b, u.h, y);
-            pair::load_2d(s + kDn / 64 * Sh::kKBlk, &map_r, bar, 0, y);
+            for (int b = 0; b < kDn / 64; ++b) pair::load_3d<kSMs>(s + b * Sh::kKBlk, &map_k, bar, 64 * b, u.h, y);
+            pair::load_2d<kSMs>(s + kDn / 64 * Sh::kKBlk, &map_r, bar, 0, y);
             ring.next(Sh::kKSlots);
           }
           us.give_back(n);
@@ -465,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1 && rank == 0) {
       // ================================================================ QK ======================
-      constexpr uint32_t id = idesc_bf16(kTok, kKeys, 0, 0);
+      constexpr uint32_t id = idesc_bf16(kHalf * kSMs, kKeys, 0, 0);
       const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, 2), kd = smem_desc(smem_u32(smem + Sh::kOffK), 16, 1024, 2);
       Ring ring = {0, 0};
       uint32_t i = 0;
@@ -486,21 +550,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int blk = 0; blk < Sh::kQB; ++blk, a += Sh::kQBlk >> 4, k += Sh::kKBlk >> 4)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) tc2::ss(tmem + kKeys * b, a + 2 * kk, k + 2 * kk, id, (blk | kk) != 0 ? 1u : 0u);
-            tc2::commit(&br.s_full[b], 0x3);
-            tc2::commit(&br.k_empty[ring.slot], 0x3);
+              for (int kk = 0; kk < 4; ++kk) Mma::ss(tmem + kKeys * b, a + 2 * kk, k + 2 * kk, id, (blk | kk) != 0 ? 1u : 0u);
+            Mma::commit(&br.s_full[b]);
+            Mma::commit(&br.k_empty[ring.slot]);
             ring.next(Sh::kKSlots);
           }
           if (!ok) break;
-          tc2::commit(&br.q_empty, 0x3);
+          Mma::commit(&br.q_empty);
           us.give_back(n);
         }
-        tc2::commit(&br.drain[0], 0x1);
+        Mma::commit(&br.drain[0]);
         mbar_wait(&br.drain[0], 0, p.err);
       }
     } else if (warp == 2 && rank == 0) {
       // ================================================================ PV ======================
-      constexpr uint32_t id = idesc_bf16(kTok, kDv, 0, 1);
+      constexpr uint32_t id = idesc_bf16(kHalf * kSMs, kDv, 0, 1);
       const uint64_t vd = smem_desc(smem_u32(smem + Sh::kOffV), Sh::kVBlk, 1024, 2), pd = smem_desc(smem_u32(smem + Sh::kOffP), 16, 1024, 2);
       Ring ring = {0, 0};
       uint32_t i = 0;
@@ -525,77 +589,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int kk = 0; kk < 4; ++kk) {
                 const uint32_t more = (t | half | kk) != 0 ? 1u : 0u;
                 if (Sh::kWide)
-                  tc2::ss(tmem + Sh::kColO, w + 2 * kk, v + (2048 >> 4) * kk, id, more);
+                  Mma::ss(tmem + Sh::kColO, w + 2 * kk, v + (2048 >> 4) * kk, id, more);
                 else
-                  tc2::ts(tmem + Sh::kColO, pt + 8 * kk, v + (2048 >> 4) * kk, id, more);
+                  Mma::ts(tmem + Sh::kColO, pt + 8 * kk, v + (2048 >> 4) * kk, id, more);
               }
-            tc2::commit(&br.pv_done[b], 0x3);
-            tc2::commit(&br.v_empty[ring.slot], 0x3);
+            Mma::commit(&br.pv_done[b]);
+            Mma::commit(&br.v_empty[ring.slot]);
             ring.next(Sh::kVSlots);
           }
           if (!ok) break;
-          tc2::commit(&br.o_full, 0x3);
+          Mma::commit(&br.o_full);
           us.give_back(n);
         }
-        tc2::commit(&br.drain[1], 0x1);
+        Mma::commit(&br.drain[1]);
         mbar_wait(&br.drain[1], 0, p.err);
       }
     } else if (warp == 2) {
       // ================================================================ units ===================
+      Giver<Sh::kPlaces, kSMs> giver = {p, br.unit_empty, smem + Sh::kOffUnit, Mma::at(smem + Sh::kOffUnit, lane & 1), Mma::at(br.unit_full, lane & 1), 0};
       const int32_t total = p.total[0];
-      int r0 = 0;
-      uint32_t at[2], bar[2];
-#pragma unroll
-      for (uint32_t c = 0; c < 2; ++c) at[c] = remote_smem(smem + Sh::kOffUnit, c), bar[c] = remote_smem(br.unit_full, c);
 #pragma unroll 1
-      for (uint32_t n = 0;; ++n) {
-        if (!warp_wait(&br.unit_empty[n & 1u], ((n >> 1) & 1u) ^ 1u, p.err, lane)) break;
-        int32_t i = 0;
-        if (lane == 0) i = atomicAdd(&p.total[1], 1);
-        i = __shfl_sync(0xffffffffu, i, 0);
-        Unit u = {};
-        if (i < total) {
-          // its request: the last that starts at or before it (numbers grow, so the search goes on from the last one)
-          for (;;) {
-            const int r = r0 + 1 + lane;
-            const uint32_t le = __ballot_sync(0xffffffffu, r < p.B && p.req[r < p.B ? r : 0].unit0 <= i);
-            r0 += __popc(le);
-            if (le != 0xffffffffu) break;
-          }
-          const Req q = p.req[r0];
-          const int per_head = q.nb * q.np, x = i - q.unit0, rest = x % per_head;
-          const int b = q.nb - 1 - rest / q.np, piece = rest % q.np;
-          u.h = x / per_head;
-          u.tok = q.q0 + b * kTok;
-          u.nrows = q.m - b * kTok < kTok ? q.m - b * kTok : kTok;
-          u.kv0 = q.kv0;
-          u.len = q.len;
-          u.see = p.causal ? q.len - q.m + 1 + b * kTok : q.len;
-          const int64_t last = p.causal ? (int64_t)u.see + u.nrows - 1 : q.len;
-          const int64_t tiles = last > 0 ? (last + kKeys - 1) / kKeys : 0;
-          const int64_t ta = tiles * piece / q.np, tb = tiles * (piece + 1) / q.np;
-          u.ta = (int)ta;
-          u.n = tb > ta ? (int)(tb - ta) : 1;
-          if (tb == ta) u.len = 0;  // a tile of which no row is there
-          u.np = q.np;
-          u.first = q.slot0 + (u.h * q.nb + b) * q.np;
-          u.slot = u.first + piece;
-        }
-        if (lane < 2) {
-          const int4* v = reinterpret_cast<const int4*>(&u);
-          const uint32_t to = at[lane] + (n & 1u) * (uint32_t)sizeof(Unit), on = bar[lane] + 8 * (n & 1u);
-          pair::arrive_expect_tx(on, sizeof(Unit));
-#pragma unroll
-          for (int k = 0; k < 3; ++k) pair::st_async16(to + 16 * k, v[k], on);
-        }
-        __syncwarp();
-        if (i >= total) break;
+      for (uint32_t n = 0; giver.give(n, total, lane); ++n) {
       }
     } else if (warp == 3) {
       // ================================================================ V =======================
       // A tile that reaches past its request's end is counted on a barrier of this CTA; rows from there on become zeros, then
-      // the tile counts as there.
-      const uint32_t full = remote_smem(br.v_full, 0), tail = remote_smem(&br.tail_full, rank);
+      // the tile counts as there. Without a pair this warp also hands out the units, one ahead.
+      Giver<Sh::kPlaces, kSMs> giver = {p, br.unit_empty, smem + Sh::kOffUnit, Mma::at(smem + Sh::kOffUnit, 0), Mma::at(br.unit_full, 0), 0};
+      const int32_t total = kSMs == 1 ? p.total[0] : 0;
+      bool more = kSMs == 1 && giver.give(0, total, lane);
+      const uint32_t full = Mma::at(br.v_full, 0), tail = Mma::at(&br.tail_full, rank);
       Ring ring = {0, 1};
       uint32_t tails = 0;
       bool ok = true;
@@ -611,9 +634,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint8_t* s = smem + Sh::kOffV + ring.slot * Sh::kVBytes;
           if (lane == 0) {
             const uint32_t bar = left < kKeys ? tail : full + 8 * (uint32_t)ring.slot;
-            pair::arrive_expect_tx(bar, Sh::kVBytes);
+            Mma::expect(bar, Sh::kVBytes);
 #pragma unroll 1
-            for (int b = 0; b < kDv / 128; ++b) pair::load_3d(s + b * Sh::kVBlk, &map_v, bar, kDn + kDv / 2 * (int)rank + 64 * b, u.h, y);
+            for (int b = 0; b < Sh::kVCols / 64; ++b) pair::load_3d<kSMs>(s + b * Sh::kVBlk, &map_v, bar, kDn + Sh::kVCols * (int)rank + 64 * b, u.h, y);
           }
           if (left < kKeys) {
             ok = warp_wait(&br.tail_full, tails++ & 1u, p.err, lane);
@@ -621,12 +644,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int x = 8 * (left < 0 ? 0 : left) + lane; x < 8 * kKeys; x += 32)
 #pragma unroll
-              for (int b = 0; b < kDv / 128; ++b) *reinterpret_cast<uint4*>(s + b * Sh::kVBlk + 16 * x) = make_uint4(0, 0, 0, 0);
+              for (int b = 0; b < Sh::kVCols / 64; ++b) *reinterpret_cast<uint4*>(s + b * Sh::kVBlk + 16 * x) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) remote_arrive_cta(full + 8 * (uint32_t)ring.slot);
+            if (lane == 0) Mma::arrive(full + 8 * (uint32_t)ring.slot);
           }
           ring.next(Sh::kVSlots);
+          if (more && t == (u.n > 1 ? 1 : 0)) more = giver.give(n + 1, total, lane);
         }
         if (ok) us.give_back(n);
       }
@@ -637,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ================================================================ softmax, output ===========
     const int quad = warp & 3, g = (warp - 4) >> 2, row = 32 * quad + lane;  // this CTA's token; the tiles whose number has parity g
     const uint32_t lane_base = tmem + ((uint32_t)(32 * quad) << 16);
-    const uint32_t s_empty = remote_smem(br.s_empty, 0), p_full = remote_smem(br.p_full, 0), o_free = remote_smem(&br.o_free, 0);
+    const uint32_t s_empty = Mma::at(br.s_empty, 0), p_full = Mma::at(br.p_full, 0), o_free = Mma::at(&br.o_free, 0);
     float* refs = reinterpret_cast<float*>(smem + Sh::kOffRef);  // [2][128]
     float* sums = reinterpret_cast<float*>(smem + Sh::kOffSum);
     const int mine = 4 * g + quad, other = 4 * (g ^ 1) + quad;  // barriers of the two warps that share these tokens
@@ -665,12 +689,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t ph = (i >> 1) & 1u;
         if (idle) {
           ok = warp_wait_all(&br.s_full[g], ph, p.err);
-          if (ok && lane == 0) remote_arrive_relaxed(s_empty + 8 * (uint32_t)g);
+          if (ok && lane == 0) Mma::arrive_relaxed(s_empty + 8 * (uint32_t)g);
           // This tile's logits may be there before the warps with tokens have handed on P of the tile before last: without the
           // wait, this arrival could count for that one.
           if (ok && i >= 2) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
           __syncwarp();
-          if (ok && lane == 0) remote_arrive_cta(p_full + 8 * (uint32_t)g);
+          if (ok && lane == 0) Mma::arrive(p_full + 8 * (uint32_t)g);
           continue;
         }
         const float before = ref;  // this warpgroup's sum refers to it
@@ -690,7 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) remote_arrive_relaxed(s_empty + 8 * (uint32_t)g);
+        if (lane == 0) Mma::arrive_relaxed(s_empty + 8 * (uint32_t)g);
         const int lim = see - (u.ta + t) * kKeys;  // columns that this token sees: all, or as many
         if (p.flip) {
 #pragma unroll
@@ -777,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (Sh::kWide) fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) remote_arrive_cta(p_full + 8 * (uint32_t)g);
+        if (lane == 0) Mma::arrive(p_full + 8 * (uint32_t)g);
       }
       if (!ok) break;
       // ---------------------------------------------------------------- the unit's end
@@ -866,7 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          remote_arrive_cta(o_free);
+          Mma::arrive(o_free);
           mbar_arrive(&br.over[mine]);
         }
         ++joint;
@@ -903,38 +927,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) remote_arrive_cta(o_free);
+        if (lane == 0) Mma::arrive(o_free);
       }
       __syncwarp();
       if (lane == 0) us.give_back(n);
     }
   }
   __syncthreads();
-  cluster_sync();  // no CTA leaves while the other may still signal or read it
+  if (kSMs == 2) cluster_sync();  // no CTA leaves while the other may still signal or read it
   if (warp == 0) {
     tc_fence_after();
-    tc2::dealloc(tmem, 512);
+    Mma::dealloc(tmem, 512);
   }
 }
 
 template <int kDn, int kDv>
-static cudaError_t launch(const Params& p, cudaStream_t stream, const char** why) {
-  using Sh = Shape<kDn, kDv>;
-  auto kernel = expanded_kernel<kDn, kDv>;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expanded_pair_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+  attend<kDn, kDv, 2>(map_q, map_k, map_r, map_v, p);
+}
+
+template <int kDn, int kDv>
+__global__ void __launch_bounds__(kThreads, 1)
+    expanded_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+  attend<kDn, kDv, 1>(map_q, map_k, map_r, map_v, p);
+}
+
+template <int kDn, int kDv, int kSMs>
+static cudaError_t launch(Params p, int sms, cudaStream_t stream, const char** why) {
+  using Sh = Shape<kDn, kDv, kSMs>;
+  void (*kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params);
+  if constexpr (kSMs == 2)
+    kernel = expanded_pair_kernel<kDn, kDv>;
+  else
+    kernel = expanded_kernel<kDn, kDv>;
   cudaError_t e = pair::allow_smem(kernel, Sh::kSmem);
   if (e != cudaSuccess) return e;
+  p.workers = sms / kSMs, p.tok = kHalf * kSMs;
   CUtensorMap mq, mk, mr, mv;
   if (!pair::encode_heads(&mq, p.q, kDn + HS_D_ROPE, p.H, p.T, p.q_stride_h, p.q_stride_t, kHalf) ||
-      !pair::encode_heads(&mk, p.kv, kDn + kDv, p.H, p.N, kDn + kDv, p.kv_stride, kKeys / 2) ||
+      !pair::encode_heads(&mk, p.kv, kDn + kDv, p.H, p.N, kDn + kDv, p.kv_stride, Sh::kKRows) ||
       !pair::encode_heads(&mv, p.kv, kDn + kDv, p.H, p.N, kDn + kDv, p.kv_stride, kKeys) ||
-      !encode_2d(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.rope, HS_D_ROPE, (uint64_t)p.N, (uint64_t)p.rope_stride * 2, 64, kKeys / 2,
+      !encode_2d(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.rope, HS_D_ROPE, (uint64_t)p.N, (uint64_t)p.rope_stride * 2, 64, Sh::kKRows,
                  CU_TENSOR_MAP_SWIZZLE_128B)) {
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
   e = launch_next(plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_next(kernel, dim3(2 * p.clusters), kThreads, Sh::kSmem, stream, mq, mk, mr, mv, p);
+  return launch_next(kernel, dim3((unsigned)(p.workers * kSMs)), kThreads, Sh::kSmem, stream, mq, mk, mr, mv, p);
 }
 
 // Workspace: totals, requests, joins, log-sum-exps and outputs of pieces.
@@ -943,6 +986,11 @@ static uint64_t off_req() { return 128; }
 static uint64_t off_joined(int B) { return off_req() + up((uint64_t)B * sizeof(Req)); }
 static uint64_t off_lse(int B, int cap) { return off_joined(B) + up((uint64_t)cap * 16 * 4); }
 static uint64_t off_out(int B, int cap) { return off_lse(B, cap) + up((uint64_t)cap * 2 * kTok * 4); }
+
+// Whether CTAs by themselves are better than pairs: with blocks of at most 128 tokens half of a pair would be idle. Measured (pairs /
+// alone, us, 64 heads, 8 requests over 4,000 rows): 16 tokens each 199 / 186, 128 220 / 195, 129 224 / 252, 256 235 / 259; one token
+// each over 1,000 rows 75 / 62; 16 heads, 64 requests x 33 tokens over 200 rows 77 / 47. (192, 256) has no room for whole tiles.
+static bool few_tokens(int T, int B) { return (int64_t)T <= 128ll * B; }
 
 }  // namespace expanded
 
@@ -955,7 +1003,7 @@ uint64_t mla_expanded_workspace_bytes(int B, int Dv, int sms) {
 cudaError_t launch_mla_expanded(const hs_mla_expanded_args* a, int sms, cudaStream_t stream, const char** why) {
   using namespace expanded;
   Params p;
-  p.T = a->T, p.B = a->B, p.H = a->H, p.causal = a->causal, p.clusters = sms / 2, p.cap = kPerPair * (sms / 2);
+  p.T = a->T, p.B = a->B, p.H = a->H, p.causal = a->causal, p.cap = kPerPair * (sms / 2);
   p.q = a->q, p.q_stride_t = a->q_stride_t, p.q_stride_h = a->q_stride_h;
   p.kv = a->kv, p.kv_stride = a->kv_stride, p.N = a->N;
   p.rope = a->rope, p.rope_stride = a->rope_stride;
@@ -969,7 +1017,8 @@ cudaError_t launch_mla_expanded(const hs_mla_expanded_args* a, int sms, cudaStre
   p.joined = reinterpret_cast<int32_t*>(w + off_joined(a->B));
   p.part_lse = reinterpret_cast<float*>(w + off_lse(a->B, p.cap));
   p.part_out = reinterpret_cast<float*>(w + off_out(a->B, p.cap));
-  return a->Dv == 128 ? launch<128, 128>(p, stream, why) : launch<192, 256>(p, stream, why);
+  if (a->Dv != 128) return launch<192, 256, 2>(p, sms, stream, why);
+  return few_tokens(a->T, a->B) ? launch<128, 128, 1>(p, sms, stream, why) : launch<128, 128, 2>(p, sms, stream, why);
 }
 
 }  // namespace hs

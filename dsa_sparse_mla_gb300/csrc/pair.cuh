@@ -9,22 +9,35 @@
 namespace hs {
 namespace pair {
 
-// 2-D tiled load into this CTA's shared memory, its bytes counted on a barrier of either CTA of the pair (address from
-// remote_smem). x must be a multiple of 16 bytes.
+// Tiled loads into this CTA's shared memory, their bytes counted on a barrier of either CTA of a pair (address from remote_smem), or with
+// kSMs = 1 of this CTA. x must be a multiple of 16 bytes.
+template <int kSMs = 2>
 __device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(bar), "r"(x), "r"(y)
-      : "memory");
+  if constexpr (kSMs == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(map), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
 }
-
+template <int kSMs = 2>
 __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
+  if constexpr (kSMs == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
 // The same under an L2 cache policy.
@@ -64,6 +77,68 @@ __device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
                : "memory");
   return ok != 0;
 }
+
+// One SM by itself or a pair's two: tensor products (a commit arrives on the barrier of every CTA that takes part), and barriers of CTA
+// `rank` by their address. A CTA by itself is not launched as a cluster and takes the forms of its own shared memory throughout.
+template <int kSMs>
+struct Mma {
+  static __device__ __forceinline__ uint32_t at(const void* p, uint32_t rank) {
+    if constexpr (kSMs == 2)
+      return remote_smem(p, rank);
+    else
+      return smem_u32(p);
+  }
+  static __device__ __forceinline__ void arrive(uint32_t bar) {
+    if constexpr (kSMs == 2)
+      remote_arrive_cta(bar);
+    else
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+  }
+  static __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
+    if constexpr (kSMs == 2)
+      remote_arrive_relaxed(bar);
+    else
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+  }
+  static __device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+    if constexpr (kSMs == 2)
+      arrive_expect_tx(bar, bytes);
+    else
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  }
+  static __device__ __forceinline__ void alloc(uint32_t* dst, uint32_t ncols) {
+    if constexpr (kSMs == 2)
+      tc2::alloc(dst, ncols);
+    else
+      tmem_alloc(dst, ncols);
+  }
+  static __device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t ncols) {
+    if constexpr (kSMs == 2)
+      tc2::dealloc(taddr, ncols);
+    else
+      tmem_dealloc(taddr, ncols);
+  }
+  static __device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kSMs == 2)
+      tc2::ss(d, a, b, idesc, accumulate);
+    else
+      mma_bf16_ss(d, a, b, idesc, accumulate);
+  }
+  // A from tensor memory: 16-bit values, two to a column
+  static __device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (kSMs == 2)
+      tc2::ts(d, a, b, idesc, accumulate);
+    else
+      asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b),
+                   "r"(idesc), "r"(accumulate));
+  }
+  static __device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (kSMs == 2)
+      tc2::commit(bar, 0x3);
+    else
+      mma_commit(bar);
+  }
+};
 
 // After a wait that ran out: gives copies in flight, which take microseconds, 20 ms to land before the CTA leaves.
 __device__ __forceinline__ void let_copies_land() {

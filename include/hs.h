@@ -781,8 +781,9 @@ hs_status hs_mla_expand(const hs_mla_expand_args* a, hs_stream_t stream);
  *   req_start     int32 [B + 1], ascending, req_start[0] = 0, req_start[B] = T
  *   kv_start      int32 [B + 1], ascending, within [0, N]
  *   out, lse      bf16 [T, H, Dv] (16-byte aligned);  fp32 [T, H] or NULL
- *   err_flag      a request's token offsets out of order set HS_FLAG_BAD_INDEX (its outputs are not written), row offsets out of order or
- *                 past N HS_FLAG_BAD_LENGTH (the request sees no row)
+ *   err_flag      a request's token offsets out of order set HS_FLAG_BAD_INDEX (its outputs are not written; nobody's where requests
+ *                 overlap so that they have more than T tokens), row offsets out of order or past N HS_FLAG_BAD_LENGTH (the request
+ *                 sees no row)
  *   workspace     hs_mla_expanded_workspace_size() bytes of 16-byte aligned device memory, scratch; calls that share one must not
  *                 overlap on the GPU
  * The same call gives the same bits each time. How a block's rows are split, and so its last bits, depends on all of the batch's

@@ -214,3 +214,103 @@ def test_attention_again_and_again(Dn, Dv):
         for _ in range(20):
             again = attend(b, Dv)
             assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_attention_of_few_and_many_tokens_together(Dn, Dv):
+    """Both sides of the rule between CTAs by themselves and pairs (128 tokens per request on average), with blocks of few tokens in pairs
+    and requests of several blocks in CTAs."""
+    check(batch([1, 700], [300, 900], 2, Dn, Dv, seed=11, spare=9), Dn, Dv)
+    check(batch([2, 400, 1, 0, 3], [300, 500, 1, 7, 4000], 2, Dn, Dv, seed=12, spare=9), Dn, Dv)
+    check(batch([128, 128], [128, 129], 3, Dn, Dv, seed=13), Dn, Dv)
+    check(batch([128, 129], [128, 129], 3, Dn, Dv, seed=13), Dn, Dv)
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_attention_flags(Dn, Dv):
+    """Offsets that are out of order: the flag, the tokens whose results stay those of the good call, those that see nothing, and those
+    that are left alone. Requests of 3, 200 and 4 tokens over 50, 300 and 9 rows."""
+    b = batch([3, 200, 4], [50, 300, 9], 2, Dn, Dv, seed=14)
+    good, _ = attend(b, Dv)
+    T, H, _ = b["q"].shape
+    for key, bad, same, nothing, alone in (
+            ("req_start", [0, 203, 3, 207], [], [], [(0, 207)]),                 # 203 and 204 tokens: more than there are
+            ("req_start", [0, 207, 0, 207], [], [], [(0, 207)]),
+            ("req_start", [0, 3, 203, 206], [(0, 203)], [], [(206, 207)]),       # the last token is nobody's
+            ("req_start", [1, 3, 203, 207], [(3, 207)], [], [(0, 1)]),           # the first one is
+            ("req_start", [0, -1, 203, 207], [(203, 207)], [], [(0, 203)]),
+            ("req_start", [0, 300, 203, 207], [(203, 207)], [], [(0, 203)]),
+            ("kv_start", [0, 50, 350, 400], [(0, 203)], [(203, 207)], []),       # past the 359 rows
+            ("kv_start", [0, -5, 350, 359], [(203, 207)], [(0, 203)], [])):
+        c = dict(b)
+        c[key] = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        out, lse, e = torch.full((T, H, Dv), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T, H), 7.0, device="cuda"), err()
+        ws = torch.empty(hs.hs_mla_expanded_workspace_size(3, Dv), dtype=torch.uint8, device="cuda")
+        hs.hs_mla_expanded_fwd(c["q"], c["kv"], c["rope"], c["req_start"], c["kv_start"], c["scale"], out, e, ws, lse=lse)
+        assert hs.hs_check_flag(e) == hs.FLAGS["BAD_INDEX" if key == "req_start" else "BAD_LENGTH"], bad
+        for lo, hi in same:
+            assert torch.equal(out[lo:hi], good[lo:hi]), bad
+        for lo, hi in nothing:
+            assert not out[lo:hi].any() and bool((lse[lo:hi] == -math.inf).all()), bad
+        for lo, hi in alone:
+            assert bool((out[lo:hi] == 7).all()) and bool((lse[lo:hi] == 7).all()), bad
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_calls_on_other_streams_and_in_graphs(Dn, Dv):
+    """Two calls at once with workspaces of their own, and captured calls replayed on new data: the bits of the plain calls."""
+    bs = [batch(q, k, 4, Dn, Dv, seed=s) for s, (q, k) in enumerate((([1] * 8, [900] * 8), ([300, 40], [700, 2000])))]
+    want = [attend(b, Dv) for b in bs]
+    ws = [torch.empty(hs.hs_mla_expanded_workspace_size(8, Dv), dtype=torch.uint8, device="cuda") for _ in bs]
+    outs = [(torch.empty_like(o), torch.empty_like(l)) for o, l in want]
+    e = err()
+    streams = [torch.cuda.Stream() for _ in bs]
+
+    def call(k, stream=None):
+        b, (o, l) = bs[k], outs[k]
+        hs.hs_mla_expanded_fwd(b["q"], b["kv"], b["rope"], b["req_start"], b["kv_start"], b["scale"], o, e, ws[k], lse=l, stream=stream)
+
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k in (0, 1):
+            call(k, streams[k])
+    torch.cuda.synchronize()
+    for (o, l), (a, b) in zip(outs, want):
+        assert torch.equal(o, a) and torch.equal(l, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0), call(1), call(0)
+    other = batch([1] * 8, [900] * 8, 4, Dn, Dv, seed=77)
+    bs[0]["q"].copy_(other["q"]), bs[0]["kv"].copy_(other["kv"]), bs[0]["rope"].copy_(other["rope"])
+    again = attend(bs[0], Dv)
+    for _ in range(3):
+        outs[0][0].zero_(), outs[1][0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0][0], again[0]) and torch.equal(outs[0][1], again[1]) and torch.equal(outs[1][0], want[1][0])
+    assert hs.hs_check_flag(e) == 0
+
+
+def test_calls_one_after_another_wait_for_each_other():
+    """Each call starts early and reads what the one before it wrote: rows -> keys and values -> attention -> products, many times over."""
+    g = gen(20)
+    H, Dn, Dv, n = 8, 128, 128, 640
+    c, w, q = plain.rand((n, 576), g).cuda(), plain.weights(H, Dn, Dv, g).cuda(), plain.rand((40, H, Dn + 64), g).cuda()
+    start, kv_start = plain.starts([40]).cuda(), plain.starts([n]).cuda()
+    e, ws = err(), torch.empty(hs.hs_mla_expanded_workspace_size(1, Dv), dtype=torch.uint8, device="cuda")
+    kv, out, lat = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((n, H, Dn + Dv), (40, H, Dv), (40, H, 512)))
+
+    def step(k, sync):
+        rows = c * (1.0 + 0.125 * k)
+        for call in (lambda: hs.hs_mla_expand(rows[:, :512], w, kv, e), lambda: hs.hs_mla_expanded_fwd(q, kv, rows[:, 512:], start, kv_start, 0.05, out, e, ws),
+                     lambda: hs.hs_mla_absorb(out, w, lat, e), lambda: hs.hs_mla_project(lat, w, out, e)):
+            call()
+            if sync:
+                torch.cuda.synchronize()
+        return kv.clone(), lat.clone(), out.clone()
+
+    slow = [step(k, True) for k in range(6)]
+    fast = [step(k, False) for k in range(6)]
+    for a, b in zip(slow, fast):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert hs.hs_check_flag(e) == 0
