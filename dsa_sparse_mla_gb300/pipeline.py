@@ -321,8 +321,10 @@ class DenseSession:
         free = (self.refcount <= 0).nonzero()[:, 0][:int(take.sum())].int()
         if int(take.sum()) > free.numel() or int(after.max()) > 64 * self.table.shape[1]:
             raise RuntimeError("the cache has too few pages")
-        cached = int(after.sum())
-        self._make_room(int(new.sum()), cached)
+        # what the expanded form reads: the rows of slots with new tokens
+        read = torch.where(new > 0, after, 0)
+        cached, tokens, self.read_tokens, self.active = torch.stack([after.sum(), new.sum(), read.sum(), (new > 0).sum()]).tolist()
+        self._make_room(tokens, cached)
         self.kv_tokens = cached
         self.table[take] = free
         self.refcount[free.long()] = 1
@@ -332,10 +334,7 @@ class DenseSession:
         self.positions = (torch.arange(T, dtype=torch.int32, device=self.device)
                           + torch.repeat_interleave(self.seq_len - self.req_start[:-1], new))
         self.seq_len = after
-        # what the expanded form reads: the rows of slots with new tokens
-        read = torch.where(new > 0, after, 0)
         self.read_start = torch.cat([read.new_zeros(1), read.cumsum(0).int()])
-        self.read_tokens, self.active = int(read.sum()), int((new > 0).sum())
         return T
 
     def attend(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, out: torch.Tensor, lse=None):

@@ -314,3 +314,65 @@ def test_calls_one_after_another_wait_for_each_other():
     for a, b in zip(slow, fast):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert hs.hs_check_flag(e) == 0
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+def test_attention_with_strides_and_without_lse(Dn, Dv):
+    """Queries that are slices (also with the heads first in memory), rows of keys and values wider than their heads, no lse: the bits of
+    the plain call."""
+    b = batch([70, 1, 260], [200, 65, 400], 3, Dn, Dv, seed=15)
+    want, _ = attend(b, Dv)
+    T, H, D = b["q"].shape
+    N = b["kv"].shape[0]
+    wide = torch.full((T, H, D + 8), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[..., :D] = b["q"]
+    first = torch.empty((H, T, D), dtype=torch.bfloat16, device="cuda")
+    first.copy_(b["q"].transpose(0, 1))
+    rows = torch.full((N, H * (Dn + Dv) + 24), math.nan, dtype=torch.bfloat16, device="cuda")
+    rows[:, :H * (Dn + Dv)] = b["kv"].flatten(1)
+    kv = rows[:, :H * (Dn + Dv)].unflatten(1, (H, Dn + Dv))
+    e, ws = err(), torch.empty(hs.hs_mla_expanded_workspace_size(3, Dv), dtype=torch.uint8, device="cuda")
+    for q in (wide[..., :D], first.transpose(0, 1)):
+        out = torch.empty((T, H, Dv), dtype=torch.bfloat16, device="cuda")
+        hs.hs_mla_expanded_fwd(q, kv, b["rope"].contiguous(), b["req_start"], b["kv_start"], b["scale"], out, e, ws)
+        assert hs.hs_check_flag(e) == 0 and torch.equal(out, want)
+    with pytest.raises(hs.HSError):  # too little workspace
+        hs.hs_mla_expanded_fwd(b["q"], b["kv"], b["rope"], b["req_start"], b["kv_start"], b["scale"], out, e, ws[:-1])
+    with pytest.raises(hs.HSError):  # values of a head not one after the other
+        hs.hs_mla_expanded_fwd(b["q"].transpose(1, 2).contiguous().transpose(1, 2), b["kv"], b["rope"], b["req_start"], b["kv_start"], b["scale"], out, e, ws)
+    assert hs.hs_check_flag(e) == 0
+
+
+def test_rows_past_four_gigabytes():
+    """Keys and values whose bytes need more than 32 bits: the last rows of a large call equal those of a small one."""
+    g = gen(16)
+    N, H, Dn, Dv = 70000, 128, 128, 128
+    latent = torch.empty((N, 576), dtype=torch.bfloat16, device="cuda").normal_()
+    w = plain.weights(H, Dn, Dv, g).cuda()
+    kv, small, e = torch.empty((N, H, 256), dtype=torch.bfloat16, device="cuda"), torch.empty((600, H, 256), dtype=torch.bfloat16, device="cuda"), err()
+    assert 2 * kv.numel() > 1 << 32
+    hs.hs_mla_expand(latent[:, :512], w, kv, e)
+    hs.hs_mla_expand(latent[-600:, :512], w, small, e)
+    assert torch.equal(kv[-600:], small)
+    q = plain.rand((210, H, 192), g).cuda()
+    outs = []
+    for m in (10, 200):  # few tokens and many
+        ws = torch.empty(hs.hs_mla_expanded_workspace_size(2, Dv), dtype=torch.uint8, device="cuda")
+        pair = []
+        for rows, r, starts in ((kv, latent, [0, N - 600, N]), (small, latent[-600:], [0, 0, 600])):
+            out = torch.empty((m, H, Dv), dtype=torch.bfloat16, device="cuda")
+            hs.hs_mla_expanded_fwd(q[:m], rows, r[:, 512:], plain.starts([0, m]).cuda(), torch.tensor(starts, dtype=torch.int32, device="cuda"), 0.07, out, e, ws)
+            pair.append(out)
+        assert torch.equal(*pair)
+    # outputs past 2^32 bytes, both products
+    T = 33000
+    x = torch.empty((T, H, 512), dtype=torch.bfloat16, device="cuda").normal_()
+    assert 2 * x.numel() > 1 << 32
+    out, tail = torch.empty((T, H, Dv), dtype=torch.bfloat16, device="cuda"), torch.empty((300, H, Dv), dtype=torch.bfloat16, device="cuda")
+    hs.hs_mla_project(x, w, out, e)
+    hs.hs_mla_project(x[-300:], w, tail, e)
+    assert torch.equal(out[-300:], tail)
+    hs.hs_mla_absorb(out, w, x, e)
+    back = torch.empty((300, H, 512), dtype=torch.bfloat16, device="cuda")
+    hs.hs_mla_absorb(tail, w, back, e)
+    assert torch.equal(x[-300:], back) and hs.hs_check_flag(e) == 0
