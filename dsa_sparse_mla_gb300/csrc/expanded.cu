@@ -36,8 +36,7 @@ constexpr int kThreads = 384;                        // Q and K, QK, PV (units i
 constexpr float kThreshold = 8.0f;                   // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxReq = 4096;
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanned = 4;                          // requests per thread of the plan
 constexpr int kMinPiece = 8;                         // tiles of a piece, at least
 constexpr int kPerPair = 6;                          // pieces of split blocks per pair of CTAs, at most
 
@@ -79,6 +78,7 @@ struct Params {
 
 // ------------------------------------------------------------------------ plan ------------
 // Sum over the threads before this one, and of all.
+template <int kWarps>
 __device__ __forceinline__ int64_t block_before(int64_t v, int64_t* scratch, int64_t* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto scan = [&](int64_t x) {
@@ -93,25 +93,25 @@ __device__ __forceinline__ int64_t block_before(int64_t v, int64_t* scratch, int
   __syncthreads();
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  const int64_t w = scan(scratch[lane]);  // of the warps up to this lane's
+  const int64_t w = scan(lane < kWarps ? scratch[lane] : 0);  // of the warps up to this lane's
   *all = __shfl_sync(0xffffffffu, w, 31);
   const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   return x - v + (warp > 0 ? before : 0);
 }
-static_assert(kPlanThreads == 32 * 32, "a lane to a warp's sum");
-
 // Requests in descending order of their longest block, to a quarter of an octave (within one in any order: no result depends on it).
 __device__ __forceinline__ int size_class(int64_t tiles) {
   return tiles <= 0 ? 127 : 126 - (int)((__float_as_uint((float)tiles) >> 21) - (127u << 2));  // 2^24 tiles at most: classes 27 .. 126
 }
 
-// One CTA. Thread t plans requests 4 t .. 4 t + 3. Long blocks come first, so that the last units to end are short. A block longer
+// One CTA. Thread t plans requests 4 t .. 4 t + 3 (a call has few, as a rule: 128 threads wait less for each other than 1,024). Long blocks come first, so that the last units to end are short. A block longer
 // than half of a pair's even share of all tiles is split into pieces of at most a quarter of it, but of kMinPiece tiles at least, and
 // longer ones where they would not fit their slots.
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
+  constexpr int kPer = kPlanned, kWarps = kPlanThreads / 32;
+  static_assert(kPlanThreads >= 128 && kWarps <= 32, "a thread to a class, a lane to a warp's sum");
   __shared__ int64_t scratch[32];
-  __shared__ int32_t classes[128], places[kMaxReq];  // requests of a class, and before it; units of a place
-  constexpr int kPer = kMaxReq / kPlanThreads;
+  __shared__ int32_t classes[128], places[kPer * kPlanThreads];  // requests of a class, and before it; units of a place
   let_next();
   after_previous();
   int start[kPer], m[kPer], kv0[kPer], len[kPer], nb[kPer], np[kPer], place[kPer];
@@ -142,9 +142,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     place[k] = atomicAdd(&classes[size_class(nb[k] ? most[k] + 1 : 0)], 1);
   }
   int64_t all = 0;
-  block_before(tokens, scratch, &all);
+  block_before<kWarps>(tokens, scratch, &all);
   const bool none = all > p.T;  // requests overlap (offsets out of order, flagged above): no bound on the units would hold
-  block_before(work, scratch, &all);
+  block_before<kWarps>(work, scratch, &all);
   work = all;
   int64_t piece = (work / p.workers + 3) / 4;
   if (piece < kMinPiece) piece = kMinPiece;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (most[k] > 2 * piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
-    block_before(slots, scratch, &all);
+    block_before<kWarps>(slots, scratch, &all);
     if (all <= p.cap) break;
   }
   int64_t slots = 0;
@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     np[k] = most[k] > 2 * piece ? (int)((most[k] + piece - 1) / piece) : 1;
     if (np[k] > 1) slots += (int64_t)nb[k] * p.H * np[k];
   }
-  int64_t slot0 = block_before(slots, scratch, &all);
-  const int64_t before = block_before(threadIdx.x < 128 ? classes[threadIdx.x] : 0, scratch, &all);
+  int64_t slot0 = block_before<kWarps>(slots, scratch, &all);
+  const int split = (int)all;  // slots in use
+  const int64_t before = block_before<kWarps>(threadIdx.x < 128 ? classes[threadIdx.x] : 0, scratch, &all);
   if (threadIdx.x < 128) classes[threadIdx.x] = (int)before;
   __syncthreads();
 #pragma unroll
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     const int r = kPer * threadIdx.x + k;
     if (r < p.B) units += places[r];
   }
-  int64_t unit0 = block_before(units, scratch, &all);
+  int64_t unit0 = block_before<kWarps>(units, scratch, &all);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = kPer * threadIdx.x + k;
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     p.req[place[k]] = {places[place[k]], start[k], m[k], kv0[k], len[k], nb[k], np[k], (int32_t)slot0};
     if (np[k] > 1) slot0 += (int64_t)nb[k] * p.H * np[k];
   }
-  for (int i = threadIdx.x; i < p.cap * 16; i += kPlanThreads) p.joined[i] = 0;
+  for (int i = threadIdx.x; i < split * 16; i += kPlanThreads) p.joined[i] = 0;
 }
 
 // ------------------------------------------------------------------------ attention -------
@@ -975,7 +976,8 @@ static cudaError_t launch(Params p, int sms, cudaStream_t stream, const char** w
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  e = launch_next(plan_kernel, dim3(1), kPlanThreads, 0, stream, p);
+  // 128 threads plan up to 512 requests, 1,024 threads the others
+  e = p.B <= 128 * kPlanned ? launch_next(plan_kernel<128>, dim3(1), 128, 0, stream, p) : launch_next(plan_kernel<1024>, dim3(1), 1024, 0, stream, p);
   if (e != cudaSuccess) return e;
   return launch_next(kernel, dim3((unsigned)(p.workers * kSMs)), kThreads, Sh::kSmem, stream, mq, mk, mr, mv, p);
 }

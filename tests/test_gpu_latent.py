@@ -376,3 +376,21 @@ def test_rows_past_four_gigabytes():
     back = torch.empty((300, H, 512), dtype=torch.bfloat16, device="cuda")
     hs.hs_mla_absorb(tail, w, back, e)
     assert torch.equal(x[-300:], back) and hs.hs_check_flag(e) == 0
+
+
+def test_attention_of_many_requests():
+    """More requests than the smaller plan takes, up to the most a call may have; most of them small."""
+    g = gen(17)
+    for B in (512, 513, 4096):
+        q_lens = [(1, 0, 2, 1)[r % 4] for r in range(B)]
+        kv_lens = [1 + 37 * r % 150 for r in range(B)]
+        q_lens[-1], kv_lens[-1] = 5, 2000
+        b = batch(q_lens, kv_lens, 1, 128, 128, seed=B)
+        out, lse = attend(b, 128)
+        some = sorted({0, 1, B // 2, B - 2, B - 1} | {int(x) for x in torch.randint(0, B, (40,), generator=g)})
+        for r in some:
+            q, k = sum(q_lens[:r]), sum(kv_lens[:r])
+            one = dict(q=b["q"][q:q + q_lens[r]], kv=b["kv"][k:k + kv_lens[r]], rope=b["rope"][k:k + kv_lens[r]])
+            if q_lens[r]:
+                ref, tol, rlse, ltol = plain.attention(one["q"], one["kv"], one["rope"], plain.starts([q_lens[r]]), plain.starts([kv_lens[r]]), 128, b["scale"])
+                assert plain.holds(out[q:q + q_lens[r]], ref, tol) and plain.holds(lse[q:q + q_lens[r]], rlse, ltol), r
