@@ -29,7 +29,7 @@ cudaError_t launch_fork(const hs_kv_fork_args* a, cudaStream_t stream);
 cudaError_t launch_free(const hs_kv_free_args* a, cudaStream_t stream);
 cudaError_t launch_compact(const hs_kv_compact_args* a, int sms, cudaStream_t stream);
 uint64_t compact_workspace_bytes(int64_t nblk);
-cudaError_t launch_kv_read(const hs_kv_read_args* a, int sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const hs_kv_read_args* a, cudaStream_t stream);
 cudaError_t launch_mla_absorb(const hs_mla_heads_args* a, int sms, cudaStream_t stream, const char** why);
 cudaError_t launch_mla_project(const hs_mla_heads_args* a, int sms, cudaStream_t stream, const char** why);
 cudaError_t launch_mla_expand(const hs_mla_expand_args* a, int sms, cudaStream_t stream, const char** why);
@@ -473,10 +473,9 @@ hs_status hs_kv_read(const hs_kv_read_args* a, hs_stream_t stream) {
   REQUIRE(aligned16(a->kv_pool) && aligned16(a->out), "kv_pool and out must be 16-byte aligned");
   REQUIRE(a->out_stride >= HS_D_QK && a->out_stride % (a->dtype == HS_FP32 ? 4 : 8) == 0,
           "out_stride must be >= 576 and a multiple of 16 bytes (got %lld)", (long long)a->out_stride);
-  int sms = 0;
-  hs_status st = check_device(&sms);
+  hs_status st = check_device(nullptr);
   if (st != HS_OK) return st;
-  return launched(hs::launch_kv_read(a, sms, (cudaStream_t)stream), "hs_kv_read", nullptr);
+  return launched(hs::launch_kv_read(a, (cudaStream_t)stream), "hs_kv_read", nullptr);
 }
 
 // Strides that TMA can step by: positive multiples of 16 bytes, below 2^40 bytes.
