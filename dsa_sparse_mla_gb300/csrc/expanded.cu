@@ -5,20 +5,29 @@
 //   running reference and sum: P = 2^(logit log2 e - ref), and where a row's maximum passes ref by 2^8 its reference moves and
 //   the accumulator is scaled (so it rarely is).
 //
-// Work is units of (request, head, block of 256 tokens), a unit's cached rows cut into pieces where there are too few units for the
-// SMs. A planning kernel counts units, chooses the pieces and clears a counter; pairs of CTAs take units from the counter, blocks of a
-// head one after the other (they share its keys and values in L2), the longest first.
+// Work is units of (request, head, block of tokens), a unit's cached rows cut into pieces where single blocks are long against an even
+// share. A planning kernel counts units, chooses the pieces and clears a counter; workers take units from the counter, blocks of a head
+// one after the other (they share its keys and values in L2), the longest first. A worker is a pair of CTAs with blocks of 256 tokens,
+// or, where requests have few tokens, a CTA by itself with blocks of 128 (few_tokens, below).
 //
 // A pair works with two-SM MMAs: each CTA holds the queries, logits, P and output of its 128 tokens and half of every K and V
 // tile (64 of 128 rows of K, half of V's values). Tensor memory: two logit tiles, and with 128 values per head two tiles of P
 // and the output; with 256 values P goes through shared memory instead. In each CTA two warpgroups take the tiles in turn, a
 // thread to a token: it takes its 128 logits into registers at once, which frees the tile for the product after next, so that a
 // tile's softmax has two whole tiles' products to hide under. A token's reference passes from one warpgroup to the other through
-// shared memory. The warpgroups also scale and write the output, under the next unit's products.
+// shared memory. The warpgroups also scale and write the output, under the next unit's first products.
 //
 // Issuing an MMA takes about as long as its execution once a few are under way, and what a warp does between two batches of them
 // (barriers, addresses; its code is cold in the instruction caches, which the softmax fills) takes several hundred cycles. So QK and
-// PV have a warp each, which work in each other's gaps, and K and V a ring of slots and a copying warp each.
+// PV have a warp each, which work in each other's gaps, and K and V a ring of slots and a copying warp each: 2,048 tokens over 32,768
+// rows x 64 heads 2,720 us with one issuing and one copying warp, 1,606 with two. Tried and not kept: the output written by the warpgroup
+// that took the last tile alone while the other goes on (prompt of 8,192 tokens 870 -> 955 us), or by a fourth warpgroup (the softmax
+// threads have too few registers then: 915).
+//
+// Bound by the tensor cores for prompts and chunks: 2,048 tokens over 32,768 rows 1,420 us in a few calls (1,870 TFLOP/s), 1,560 to 1,690
+// us under the power limit; 8,192 tokens over themselves 815, and 860 to 930. Tiles take 1,440 cycles (1,280 of them MMAs); a unit's end
+// costs about 5,000 (the last tile's softmax, PV and output one after the other). (192, 256): 2,240 cycles for 2,048 of MMAs. Bound by HBM
+// for single tokens over long rows: 8 requests over 8,000 rows 340 us, 6.2 TB/s; over 200 to 2,000 rows 67 us, 4.5 TB/s, by the units' ends.
 //
 // Rows past a request's end are masked as keys and set to zero as values (in shared memory, by a warp that waits for such a tile's copy).
 // A row that a token does not see can still reach its output where P = 0 meets a value that is not finite; where an output is not
@@ -71,7 +80,7 @@ struct Params {
   int32_t* err;
   int32_t* total;    // [2]: units, the counter
   Req* req;
-  int32_t* joined;   // [cap][16]: pieces of a block that a warp's rows and columns have seen
+  int32_t* joined;   // [cap][16]: pieces of a block that are done, for each softmax warp's tokens and columns
   float* part_lse;   // [cap][2][256]
   float* part_out;   // [cap][256][Dv]
 };
