@@ -617,6 +617,8 @@ def _weight(w):
     shape = w.shape
     if len(shape) != 3 or shape[2] != 512:
         raise HSError(1, "w must be a contiguous bf16 CUDA tensor [H, Dn + Dv, 512]")
+    if w.get_device() != _current_device():
+        raise HSError(1, "w is on another device than the current one")
     return w.data_ptr(), shape[0], shape[1]
 
 

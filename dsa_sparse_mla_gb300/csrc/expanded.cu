@@ -112,9 +112,9 @@ __device__ __forceinline__ int size_class(int64_t tiles) {
   return tiles <= 0 ? 127 : 126 - (int)((__float_as_uint((float)tiles) >> 21) - (127u << 2));  // 2^24 tiles at most: classes 27 .. 126
 }
 
-// One CTA. Thread t plans requests 4 t .. 4 t + 3 (a call has few, as a rule: 128 threads wait less for each other than 1,024). Long blocks come first, so that the last units to end are short. A block longer
-// than half of a pair's even share of all tiles is split into pieces of at most a quarter of it, but of kMinPiece tiles at least, and
-// longer ones where they would not fit their slots.
+// One CTA. Thread t plans requests 4 t .. 4 t + 3 (a call has few, as a rule: 128 threads wait less for each other than 1,024). Long
+// blocks come first, so that the last units to end are short. A block longer than half of a worker's even share of all tiles is split
+// into pieces of at most a quarter of it, but of kMinPiece tiles at least, and longer ones where they would not fit their slots.
 template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   constexpr int kPer = kPlanned, kWarps = kPlanThreads / 32;
@@ -1000,7 +1000,9 @@ static uint64_t off_out(int B, int cap) { return off_lse(B, cap) + up((uint64_t)
 
 // Whether CTAs by themselves are better than pairs: with blocks of at most 128 tokens half of a pair would be idle. Measured (pairs /
 // alone, us, 64 heads, 8 requests over 4,000 rows): 16 tokens each 199 / 186, 128 220 / 195, 129 224 / 252, 256 235 / 259; one token
-// each over 1,000 rows 75 / 62; 16 heads, 64 requests x 33 tokens over 200 rows 77 / 47. (192, 256) has no room for whole tiles.
+// each over 1,000 rows 75 / 62; 16 heads, 64 requests x 33 tokens over 200 rows 77 / 47. How the tokens spread over the requests is on the
+// device: all of them in one of 64, 8,192 over themselves, 867 / 918; 1,024 in one of 8 over 8,192 rows 233 / 250. (192, 256) has no room
+// for whole tiles.
 static bool few_tokens(int T, int B) { return (int64_t)T <= 128ll * B; }
 
 }  // namespace expanded

@@ -17,7 +17,8 @@
 // absorb and project are bound by HBM: 16,384 tokens x 64 heads (1.35 GB) 231 to 241 us, 5.6 to 5.8 TB/s; 4,099 x 128 (192, 256) 149
 // us, 5.6 TB/s. expand is bound by its MMAs' issue: 32,768 rows x 64 heads x 256 363 to 390 us, 1,410 to 1,510 TFLOP/s (325 us without copies
 // and stores; a library product of the same sizes takes 316 to 346). Tried and not kept there: B streaming with A (420), two warps issuing
-// 128 columns each (395) or tiles in turn (362: nothing), TMA stores (377 to 383).
+// 128 columns each (395) or tiles in turn (362: nothing), TMA stores (377 to 383), 16 epilogue warps
+// (373; absorb, 256 tokens in a graph, 7.2 -> 8.1).
 #include "launch.cuh"
 #include "pair.cuh"
 
@@ -208,8 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ================================================================ epilogue ==================
-    // Warp (quad, g): rows 32 quad .. + 31 of this CTA, columns g kBN / 2 .. of the tile, 64 at a time. (TMA stores from here
-    // made the copies of A, which go through the same unit, wait for them.)
+    // Warp (quad, g): rows 32 quad .. + 31 of this CTA, columns g kBN / 2 .. of the tile, 64 at a time.
     const int quad = warp & 3, g = (warp - 4) >> 2;
     const uint32_t at = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(g * (kBN / 2));
     const uint32_t acc_empty = remote_smem(br.acc_empty, 0);

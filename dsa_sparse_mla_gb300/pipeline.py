@@ -277,8 +277,9 @@ class DenseSession:
     """Requests that attend densely over the paged latent cache and may branch (several samples of one prompt, beams):
     device state for ``B`` request slots and ``L`` layers, and the calls of a step in their order. ``extend`` gives the new
     tokens their positions and pages, then ``attend`` runs once per layer (hs_rope of queries and keys -> hs_kv_append ->
-    hs_paged_mla_fwd), or ``attend_heads``, which takes and gives per-head values and picks the form of latent attention. Between steps ``fork`` makes slots copies of others (pages shared, the partial one copied), ``free``
-    empties slots, and ``compact`` moves the pages in use to the front. Everything runs on the current stream. The attention's
+    hs_paged_mla_fwd), or ``attend_heads``, which takes and gives per-head values and picks the form of latent attention. Between
+    steps ``fork`` makes slots copies of others (pages shared, the partial one copied), ``free`` empties slots, and ``compact`` moves
+    the pages in use to the front. Everything runs on the current stream. The attention's
     workspace is made for steps of ``max_tokens`` and grows with the cached rows, or where a step has more tokens."""
 
     def __init__(self, B: int, H: int, nblk: int, pages: int, L: int = 1, max_tokens: int = 4096, base: float = 10000.0,
@@ -300,7 +301,7 @@ class DenseSession:
         self.kv_tokens = 0  # cached rows: shared pages count once per request
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
         self._make_room(max_tokens, 0)
-        self._kept = {}  # attend_heads' buffers by name
+        self._kept, self._captured = {}, []  # attend_heads' buffers by name; those that a captured graph uses
         self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
 
     def _make_room(self, tokens: int, cached: int):
@@ -349,30 +350,41 @@ class DenseSession:
     #: products a head and row, and then spends Dn + 64 + Dv on a pair instead of 1,088. Measured, 64 heads, absorbed / expanded in us: (128, 128),
     #: 8 slots over 8,000 rows x 128 tokens 917 / 1,165, x 192 1,341 / 1,176; one over 32,000 x 128 460 / 662, x 256 827 / 672; (192, 256), 8 over
     #: 8,000 x 256 1,805 / 2,037, x 384 2,658 / 2,598. (Over short contexts it pays earlier: 16 over 500 x 64 217 / 249, x 128 354 / 278.)
-    EXPAND_FROM = {128: 192, 256: 384}
+    EXPAND_FROM = {(128, 128): 192, (192, 256): 384}
     #: Bytes of expanded keys and values at most; steps that would need more stay in the absorbed form.
     EXPAND_BYTES = 32 << 30
 
     def _buffer(self, name: str, *shape, dtype=torch.bfloat16):
-        """A buffer that is kept from step to step, made anew with a quarter to spare where it is too small."""
-        n = math.prod(shape)
-        if name not in self._kept or self._kept[name].numel() < n or self._kept[name].dtype != dtype:
-            self._kept[name] = None  # its memory may serve the larger one
-            self._kept[name] = torch.empty(n + n // 4, dtype=dtype, device=self.device)
-        return self._kept[name][:n].view(shape)
+        """A buffer that is kept from step to step, made anew with a quarter to spare where it is too small. One that a captured graph
+        uses stays for as long as the session does."""
+        n, buffer = math.prod(shape), self._kept.get(name)
+        if buffer is None or buffer.numel() < n or buffer.dtype != dtype:
+            if buffer is not None and not torch.cuda.is_current_stream_capturing():
+                buffer.record_stream(torch.cuda.current_stream())  # its memory may serve another tensor once the calls so far are done
+            self._kept[name] = buffer = None
+            self._kept[name] = buffer = torch.empty(n + n // 4, dtype=dtype, device=self.device)
+        if torch.cuda.is_current_stream_capturing() and all(buffer is not x for x in self._captured):
+            self._captured.append(buffer)
+        return buffer[:n].view(shape)
 
     def attend_heads(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
                      lse=None, form: str | None = None):
         """Layer ``layer`` of the tokens of the last extend from per-head queries to per-head outputs: ``q`` bf16 [T, H, Dn + 64] (its
         rotary part, the last 64 values, may be rotated in place) and ``rope`` bf16 [T, 64] (rotated in place), ``latent`` bf16 [T, 512],
         the layer's weight ``w`` bf16 [H, Dn + Dv, 512], ``out`` bf16 [T, H, Dv]; logits are scaled by (Dn + 64)^-1/2. ``form`` is "absorbed"
-        or "expanded"; None picks it by the new tokens per slot."""
+        or "expanded" (heads of 128 and 128, or 192 and 256, alone); None picks it by the new tokens per slot."""
         (T, H, D), Dn, Dv = q.shape, q.shape[2] - 64, out.shape[2]
         if form is None:
-            pays = Dv in self.EXPAND_FROM and T >= self.EXPAND_FROM[Dv] * self.active
+            pays = (Dn, Dv) in self.EXPAND_FROM and T >= self.EXPAND_FROM[Dn, Dv] * self.active
             form = "expanded" if pays and 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES else "absorbed"
         if form not in ("absorbed", "expanded"):
             raise ValueError("form must be absorbed or expanded")
+        if form == "expanded" and (Dn, Dv) not in self.EXPAND_FROM:
+            raise ValueError("the expanded form takes heads of %s" % " or ".join(map(str, self.EXPAND_FROM)))
+        # before anything is turned or written
+        if w.shape != (H, Dn + Dv, 512) or out.shape[:2] != (T, H) or T != self.positions.numel():
+            raise ValueError("shape mismatch: q [T,H,Dn+64], w [H,Dn+Dv,512], out [T,H,Dv] for the %d tokens of the last extend"
+                             % self.positions.numel())
         if T == 0:
             return
         scale = self.softmax_scale * 24.0 * (Dn + 64) ** -0.5

@@ -112,3 +112,51 @@ def test_a_step_in_a_graph():
             out.zero_()
             graph.replay()
             assert torch.equal(out, first[0]) and torch.equal(lse, first[1]) and hs.hs_check_flag(s.err) == 0
+
+
+def test_heads_that_have_one_form_only():
+    """Heads of 192 and 128 values run absorbed, however many tokens; asked for the other form, or with shapes that do not fit, a call
+    changes nothing."""
+    g = torch.Generator().manual_seed(10)
+    H, Dn, Dv = 2, 192, 128
+    s, w = DenseSession(1, H, 16, 16, max_tokens=400), plain.weights(H, Dn, Dv, g).cuda()
+    T = s.extend([400])
+    q, latent, rope = (plain.rand(x, g).cuda() for x in ((T, H, Dn + 64), (T, 512), (T, 64)))
+    held = [x.clone() for x in (q, latent, rope)]
+    out, lse = torch.full((T, H, Dv), 7.0, dtype=torch.bfloat16, device="cuda"), torch.empty((T, H), device="cuda")
+    for bad in (dict(form="expanded"), dict(w=w[:, 64:].contiguous()), dict(q=q[1:]), dict(out=out[:, :1])):
+        args = dict(dict(q=q, latent=latent, rope=rope, w=w, out=out), **bad)
+        with pytest.raises(ValueError):
+            s.attend_heads(0, **args)
+    assert not s.pool.any() and all(torch.equal(a, b) for a, b in zip(held, (q, latent, rope))) and bool((out == 7).all())
+    s.attend_heads(0, q, latent, rope, w, out, lse)
+    assert hs.hs_check_flag(s.err) == 0
+    turned, scale = q.clone(), s.softmax_scale * 24 / math.sqrt(Dn + 64)
+    hs.hs_rope(turned[..., Dn:], s.positions, s.inv_freq, scale=s.rope_scale)
+    ref, tol, rlse, ltol = reference(s, 0, turned, w, Dn, scale)
+    assert plain.holds(out, ref, tol) and plain.holds(lse, rlse, ltol)
+
+
+def test_a_graph_keeps_its_buffers():
+    """Captured, then called with larger heads, for which the buffers are made anew: the graph's replays still have theirs."""
+    g = torch.Generator().manual_seed(11)
+    H, T = 4, 300
+    small, large = (plain.weights(H, Dn, Dv, g).cuda() for Dn, Dv in ((128, 128), (192, 256)))
+    for form in ("absorbed", "expanded"):
+        s = DenseSession(1, 2 * H, 16, 16, max_tokens=T)
+        assert s.extend([T]) == T
+        q, latent, rope = (plain.rand(x, g).cuda() for x in ((T, H, 192), (T, 512), (T, 64)))
+        held, out = [x.clone() for x in (q, latent, rope)], torch.empty((T, H, 128), dtype=torch.bfloat16, device="cuda")
+        s.attend_heads(0, *held, small, out, form=form)
+        first, graph = out.clone(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s.attend_heads(0, *held, small, out, form=form)
+        kept = dict(s._kept)
+        wide = [torch.cat([large] * 2), torch.empty((T, 2 * H, 256), dtype=torch.bfloat16, device="cuda")]
+        s.attend_heads(0, plain.rand((T, 2 * H, 256), g).cuda(), latent.clone(), rope.clone(), *wide, form=form)
+        names = ("queries", "mixed") if form == "absorbed" else ("kv", "expanded")
+        assert all(s._kept[n] is not kept[n] and any(kept[n] is x for x in s._captured) for n in names)
+        for h, x in zip(held, (q, latent, rope)):
+            h.copy_(x)
+        graph.replay()
+        assert torch.equal(out, first) and hs.hs_check_flag(s.err) == 0
