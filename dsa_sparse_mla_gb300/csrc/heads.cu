@@ -11,14 +11,20 @@
 // columns of B, and its rows of the accumulator (two tiles of them in tensor memory, so that one tile's epilogue runs under the next
 // tile's products). All of a head's B (or 256 columns of the expanded width: 128 KB of shared memory per CTA at most) stays while the pair
 // goes on along the rows, so that only A streams through the ring. B comes and goes in chunks of 64 reduced values, with
-// barriers of their own, so that a change of head costs no more than a load's latency. Eight epilogue warps round to bf16 once and
-// store whole 128-byte lines through shared memory. Rows beyond M are read as zeros and not stored.
+// barriers of their own, so that a change of head costs no more than a load's latency. Eight epilogue warps round to bf16 once. Rows beyond
+// M are read as zeros and not stored.
 //
-// absorb and project are bound by HBM: 16,384 tokens x 64 heads (1.35 GB) 231 to 241 us, 5.6 to 5.8 TB/s; 4,099 x 128 (192, 256) 149
-// us, 5.6 TB/s. expand is bound by its MMAs' issue: 32,768 rows x 64 heads x 256 363 to 390 us, 1,410 to 1,510 TFLOP/s (325 us without copies
-// and stores; a library product of the same sizes takes 316 to 346). Tried and not kept there: B streaming with A (420), two warps issuing
-// 128 columns each (395) or tiles in turn (362: nothing), TMA stores (377 to 383), 16 epilogue warps
-// (373; absorb, 256 tokens in a graph, 7.2 -> 8.1).
+// Stores. expand and project, which multiply 512 values for each one that they store, need a deep ring more than anything (copies of A wait behind the
+// stores: expand with 3, 4, 5 slots and lines through shared memory 400, 345, 333 us): a lane stores its row in sectors of 32 bytes straight
+// from registers, and the ring has all of the room (six slots: 319; in pieces of 16 bytes, where a stride leaves nothing else, 423).
+// absorb stores three bytes of four: whole 128-byte lines through shared memory (240 us, in sectors 251; 256 tokens 7.7 and 8.5).
+//
+// absorb and project are bound by HBM: 16,384 tokens x 64 heads (1.35 GB) 231 to 241 us, 5.6 to 5.8 TB/s; 4,099 x 128 (192, 256) 146
+// us, 5.7 TB/s. expand: 32,768 rows x 64 heads x 256 319 to 329 us in a few calls, 327 to 337 in many (1,630 to 1,720 TFLOP/s; one library product of the
+// same sizes 326 to 333, 327 to 338), bound by power: with zeros for inputs it takes 287. What the issuing thread executes between two batches of
+// MMAs is not hidden: a wait in its loop that this case never reaches, eight times unrolled, made it 359 instead of 345 (without copies and
+// stores 278 and 237; 229 are MMAs). Tried and not kept: B streaming with A, two issuing warps, two copying warps, TMA stores,
+// 16 epilogue warps, clusters of four with A multicast to both pairs (36 of them fit: 144 SMs; 336 where pairs took 329).
 #include "launch.cuh"
 #include "pair.cuh"
 
@@ -28,10 +34,10 @@ namespace heads {
 constexpr int kBM = 256, kHalfM = 128, kBK = 64;
 constexpr int kThreads = 384;                 // copies, MMAs, two idle, eight epilogue warps
 constexpr int kSlot = kHalfM * kBK * 2;       // 16 KB of A
-constexpr int kOperands = 12 * kSlot;         // B's chunks, then A's ring: 4 slots at least
+constexpr int kRoom = 14;                     // slots in all: B's chunks, then A's ring, then the epilogue's lines
 constexpr int kMaxSlots = 11, kMaxChunks = 8;
 constexpr int kEpiWarps = 8, kScratch = 4096; // 32 rows x 128 bytes per epilogue warp
-constexpr int kOffEpi = kOperands, kOffBar = kOffEpi + kEpiWarps * kScratch, kSmem = kOffBar + 512;
+constexpr int kOffEpi = kRoom * kSlot - kEpiWarps * kScratch, kOffBar = kRoom * kSlot, kSmem = kOffBar + 512;
 static_assert(kSmem <= 232448, "shared memory");
 
 struct Params {
@@ -46,6 +52,7 @@ struct Params {
   int32_t k_steps, slots;
   int32_t a_again;         // A is read by every group
   int32_t b_head, b_row;   // B's rows of head h start at h * b_head + b_row
+  int32_t sectors;         // C's rows start on 32 bytes
   int32_t* err;
 };
 
@@ -80,6 +87,13 @@ struct Run {
     }
   }
 };
+
+// 16 values, 32 bytes on a 32-byte boundary, in one store.
+__device__ __forceinline__ void store_sector(uint16_t* to, const uint32_t* w) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 template <int kBN, bool kMnMajor>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -164,7 +178,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ================================================================ MMAs ======================
-    // Whether the next stage is there is asked before a stage's MMAs, whose issue hides the answer's latency.
+    // Whether the next stage is there is asked before a stage's MMAs, whose issue hides the answer's latency. The loop has to be small:
+    // only absorb has a second column tile, whose B it waits for.
     if (lane == 0 && rank == 0) {
       constexpr uint32_t id = idesc_bf16(kBM, kBN, 0, kMnMajor ? 1 : 0);
       const uint64_t ad = smem_desc(smem_u32(ring_a), 16, 1024, 2);
@@ -186,7 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll(kMnMajor ? 1 : 8)
           for (int k = 0; k < (kMnMajor ? p.k_steps : HS_D_LATENT / kBK); ++k, ++c) {
             if (nt == 0 && !there) ok = mbar_wait(&br.a_full[slot], par, p.err);
-            if (nt == 1 && first && ok) ok = mbar_wait(&br.b_full[c], groups & 1u, p.err);
+            if (kMnMajor && nt == 1 && first && ok) ok = mbar_wait(&br.b_full[c], groups & 1u, p.err);
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = ad + (uint64_t)((slot * kSlot) >> 4), w = bd + (uint64_t)((c * kChunk) >> 4);
@@ -221,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (; run.more() && ok; run.next()) {
       const int h = run.g / p.per_head, n0 = run.g % p.per_head * p.n_tiles * kBN + g * (kBN / 2);
       const int row = run.m * kBM + kHalfM * (int)rank + 32 * quad, left = p.M - row;
-      uint16_t* const c0 = p.c + (int64_t)(row + rl) * p.c_stride_m + (int64_t)h * p.c_stride_h + n0 + 8 * pl;
+      uint16_t* const c0 = p.c + (int64_t)(row + (kMnMajor ? rl : lane)) * p.c_stride_m + (int64_t)h * p.c_stride_h + n0 + (kMnMajor ? 8 * pl : 0);
 #pragma unroll 1
       for (int nt = 0; nt < p.n_tiles; ++nt, ++it) {
         const uint32_t b = it & 1u;
@@ -241,25 +256,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const int col = nt * kBN + 64 * c;
           if (left <= 0 || n0 + col >= p.N) continue;
+          uint32_t w[32];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const int e = 8 * j + 2 * z;
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
-              w[z] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            *reinterpret_cast<uint4*>(s + sw128_offset(lane, 16 * j)) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 32; ++i) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[i >> 4][2 * (i & 15)]), __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
+            w[i] = *reinterpret_cast<const uint32_t*>(&b2);
           }
-          __syncwarp();
           uint16_t* to = c0 + col;
+          if constexpr (kMnMajor) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j, to += 4 * p.c_stride_m) {
-            const uint4 x = *reinterpret_cast<const uint4*>(s + sw128_offset(4 * j + rl, 16 * pl));
-            if (4 * j + rl < left) __stcs(reinterpret_cast<uint4*>(to), x);
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(s + sw128_offset(lane, 16 * j)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j, to += 4 * p.c_stride_m) {
+              const uint4 x = *reinterpret_cast<const uint4*>(s + sw128_offset(4 * j + rl, 16 * pl));
+              if (4 * j + rl < left) __stcs(reinterpret_cast<uint4*>(to), x);
+            }
+            __syncwarp();
+          } else if (lane < left) {
+            if (p.sectors) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) store_sector(to + 16 * j, w + 8 * j);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) __stcs(reinterpret_cast<uint4*>(to + 8 * j), make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+            }
           }
-          __syncwarp();
         }
       }
     }
@@ -282,7 +305,8 @@ static cudaError_t launch(const CUtensorMap& ma, const CUtensorMap& mb, Params p
   // four row tiles, 15.0 with one).
   while (p.m_unit > 1 && (int64_t)p.m_tiles * p.groups < (int64_t)p.m_unit * 4 * (sms / 2)) p.m_unit /= 2;
   p.units = ((int64_t)p.m_tiles + p.m_unit - 1) / p.m_unit * p.groups;
-  const int slots = (kOperands - p.n_tiles * p.k_steps * (kBN / 2 * kBK * 2)) / kSlot;
+  const int slots = ((kMnMajor ? kOffEpi : kOffBar) - p.n_tiles * p.k_steps * (kBN / 2 * kBK * 2)) / kSlot;  // 6 at least; absorb 4
+  p.sectors = (reinterpret_cast<uintptr_t>(p.c) | (uintptr_t)(p.c_stride_m * 2) | (uintptr_t)(p.c_stride_h * 2)) % 32 == 0;
   p.slots = slots < kMaxSlots ? slots : kMaxSlots;
   const int64_t pairs = p.units < sms / 2 ? p.units : sms / 2;
   return launch_next(kernel, dim3((unsigned)(2 * pairs)), kThreads, kSmem, stream, ma, mb, p);

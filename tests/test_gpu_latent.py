@@ -103,6 +103,28 @@ def test_expand(T, H, Dn, Dv):
     assert bool((wide[T:] == 7).all()) and bool((wide[:, H * (Dn + Dv):] == 7).all())
 
 
+@pytest.mark.parametrize("T,H,Dn,Dv", SIZES)
+def test_where_rows_start(T, H, Dn, Dv):
+    """Results whose rows start on 32 bytes, on 16 bytes only, or on both in turn: within their bounds, the same bits, nothing beside them."""
+    g = gen(T + 3)
+    x, c, w = plain.rand((T, H, 512), g).cuda(), plain.rand((T, 512), g).cuda(), plain.weights(H, Dn, Dv, g).cuda()
+    got = []
+    for shift, pad in ((0, 0), (8, 0), (0, 8), (16, 16)):
+        mem, e = torch.full((T * (H * (Dv + pad)) + shift + 8,), 7.0, dtype=torch.bfloat16, device="cuda"), err()
+        out = mem[shift:][:T * H * (Dv + pad)].view(T, H, Dv + pad)
+        hs.hs_mla_project(x, w, out[..., :Dv], e)
+        width = H * (Dn + Dv)
+        wide = torch.full((T * (width + pad) + shift + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+        kv = wide[shift:][:T * (width + pad)].view(T, width + pad)
+        hs.hs_mla_expand(c, w, kv[:, :width].unflatten(1, (H, Dn + Dv)), e)
+        assert hs.hs_check_flag(e) == 0
+        for m, o, n in ((mem, out, Dv), (wide, kv, width)):
+            assert bool((o[..., n:] == 7).all()) and bool((m[:shift] == 7).all()) and bool((m[shift + o.numel():] == 7).all())
+        got.append((out[..., :Dv].clone(), kv[:, :width].unflatten(1, (H, Dn + Dv)).clone()))
+    assert plain.holds(got[0][0], *plain.product(x, w[:, Dn:], "thc,hdc->thd")) and plain.holds(got[0][1], *plain.product(c, w, "nc,hdc->nhd"))
+    assert all(torch.equal(a, b) for other in got[1:] for a, b in zip(got[0], other))
+
+
 def test_heads_apart():
     """Heads first in memory ([H, T, D] storage), and results that equal those of the usual order bit for bit."""
     g = gen(5)
