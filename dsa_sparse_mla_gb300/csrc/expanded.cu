@@ -24,9 +24,11 @@
 // that took the last tile alone while the other goes on (prompt of 8,192 tokens 870 -> 955 us), or by a fourth warpgroup (the softmax
 // threads have too few registers then: 915).
 //
-// Bound by the tensor cores for prompts and chunks: 2,048 tokens over 32,768 rows 1,420 us in a few calls (1,870 TFLOP/s), 1,560 to 1,690
-// us under the power limit; 8,192 tokens over themselves 815, and 860 to 930. Tiles take 1,440 cycles (1,280 of them MMAs); a unit's end
-// costs about 5,000 (the last tile's softmax, PV and output one after the other). (192, 256): 2,240 cycles for 2,048 of MMAs. Bound by HBM
+// Bound by the tensor cores for prompts and chunks: 2,048 tokens over 32,768 rows 1,380 us in a few calls (1,930 TFLOP/s), 1,515 to 1,590
+// us under the power limit; 8,192 tokens over themselves 785, and 835 to 880. There the softmax counts by the energy of its instructions: with
+// one for two products and one for two sums instead of one each 1,485 -> 1,380, 1,600 -> 1,520, and 845 -> 785, 887 -> 845 (maxima of three
+// by an instruction of their own spilled: 1,420). A unit's end costs about 5,000 cycles (the last tile's softmax, PV and output one
+// after the other), a tile 1,280 of MMAs. (192, 256): 9 ragged requests 340 us, 385. Bound by HBM
 // for single tokens over long rows: 8 requests over 8,000 rows 340 us, 6.2 TB/s; over 200 to 2,000 rows 67 us, 4.5 TB/s, by the units' ends.
 //
 // Rows past a request's end are masked as keys and set to zero as values (in shared memory, by a warp that waits for such a tile's copy).
@@ -274,6 +276,24 @@ struct Units {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two fp32 at once: one instruction where two would be, the same bits.
+__device__ __forceinline__ uint64_t two(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t two(float a, float b) { return two(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ void apart(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 __device__ __forceinline__ float from_bf16(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -757,18 +777,21 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
         bool used = i < 2 || pair::test_wait(&br.pv_done[g], ph ^ 1u);
         if (before != ref) l *= fast_exp2(before - ref);
         const float me = ref == -INFINITY ? 0.f : ref;
-        float s0 = 0.f, s1 = 0.f;
+        uint64_t sum = 0;
+        const uint64_t coef2 = two(coef, coef), me2 = two(-me, -me);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float a = fast_exp2(fmaf(__uint_as_float(v[c][2 * j]), coef, -me));
-            const float b = fast_exp2(fmaf(__uint_as_float(v[c][2 * j + 1]), coef, -me));
-            s0 += a;
-            s1 += b;
+            float a, b;
+            apart(fma2(two(v[c][2 * j], v[c][2 * j + 1]), coef2, me2), a, b);
+            a = fast_exp2(a), b = fast_exp2(b);
+            sum = add2(sum, two(a, b));
             v[c][j] = pack_bf16(a, b);
           }
         }
+        float s0, s1;
+        apart(sum, s0, s1);
         l += s0 + s1;
         if (!__all_sync(0xffffffffu, used)) ok = warp_wait_all(&br.pv_done[g], ph ^ 1u, p.err);
         if (Sh::kWide && ok && i >= 1) ok = warp_wait_all(&br.pv_done[g ^ 1], ((i - 1) >> 1) & 1u, p.err);
