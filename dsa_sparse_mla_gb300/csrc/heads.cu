@@ -14,17 +14,19 @@
 // barriers of their own, so that a change of head costs no more than a load's latency. Eight epilogue warps round to bf16 once. Rows beyond
 // M are read as zeros and not stored.
 //
-// Stores. expand and project, which multiply 512 values for each one that they store, need a deep ring more than anything (copies of A wait behind the
-// stores: expand with 3, 4, 5 slots and lines through shared memory 400, 345, 333 us): a lane stores its row in sectors of 32 bytes straight
-// from registers, and the ring has all of the room (six slots: 319; in pieces of 16 bytes, where a stride leaves nothing else, 423).
-// absorb stores three bytes of four: whole 128-byte lines through shared memory (240 us, in sectors 251; 256 tokens 7.7 and 8.5).
+// Stores. expand and project, which multiply 512 values for each one that they store, need a deep ring more than anything, since copies of
+// A wait behind the stores (expand, lines through shared memory, 3, 4 and 5 slots: 394, 364, 351 us): a lane stores its row in sectors of
+// 32 bytes straight from registers, and the ring has all of the room (six slots: 319; in pieces of 16 bytes, where a stride leaves
+// nothing else, 423). absorb stores three bytes of four: whole 128-byte lines through shared memory (240 us, in sectors 251; 256 tokens
+// 7.7 and 8.5).
 //
-// absorb and project are bound by HBM: 16,384 tokens x 64 heads (1.35 GB) 231 to 241 us, 5.6 to 5.8 TB/s; 4,099 x 128 (192, 256) 146
-// us, 5.7 TB/s. expand: 32,768 rows x 64 heads x 256 319 to 329 us in a few calls, 327 to 337 in many (1,630 to 1,720 TFLOP/s; one library product of the
-// same sizes 326 to 333, 327 to 338), bound by power: with zeros for inputs it takes 287. What the issuing thread executes between two batches of
-// MMAs is not hidden: a wait in its loop that this case never reaches, eight times unrolled, made it 359 instead of 345 (without copies and
-// stores 278 and 237; 229 are MMAs). Tried and not kept: B streaming with A, two issuing warps, two copying warps, TMA stores,
-// 16 epilogue warps, clusters of four with A multicast to both pairs (36 of them fit: 144 SMs; 336 where pairs took 329).
+// absorb and project are bound by HBM: 16,384 tokens x 64 heads (1.35 GB) 231 to 242 us, 5.6 to 5.8 TB/s; 4,099 x 128 (192, 256) 142 to
+// 146, 5.8 TB/s. expand: 32,768 rows x 64 heads x 256 319 to 329 us in a few calls, 327 to 342 in many (1,610 to 1,720 TFLOP/s; one library
+// product of the same sizes 324 to 333, 326 to 338), bound by power: with zeros for inputs it takes 287. What the issuing thread
+// executes between two batches of MMAs is not hidden: a wait in its loop that expand never reaches, eight times unrolled, made it 359
+// instead of 345 (without copies and stores 278 and 237; 229 are MMAs). Tried and not kept: B streaming with A, two issuing warps, two
+// copying warps, TMA stores, 16 epilogue warps, clusters of four with A multicast to both pairs (36 of them fit, 144 SMs: 336 where
+// pairs took 329).
 #include "launch.cuh"
 #include "pair.cuh"
 

@@ -732,6 +732,7 @@ hs_status hs_kv_read(const hs_kv_read_args* a, hs_stream_t stream);
  * Products are summed in fp32 and rounded to bf16 once. Dn and Dv are 64, 128, 192 or 256, 1 <= H <= 1024. x and out have strides (in
  * values) from token to token and head to head, so that slices of wider heads can be read and written in place (the latent part
  * of a 576-wide query, say); every pointer is 16-byte aligned and every stride a positive multiple of 8. x and out must not overlap.
+ * hs_mla_project and hs_mla_expand store fastest where the result's address and strides are multiples of 32 bytes.
  * err_flag receives HS_FLAG_TIMEOUT only. Asynchronous on `stream`; allocates nothing.
  * ---------------------------------------------------------------------------------------- */
 typedef struct {
