@@ -352,7 +352,7 @@ class DenseSession:
     #: 8,000 x 256 1,871 / 1,894, x 384 2,984 / 2,416; one over 32,000 x 384 1,204 / 1,298, x 512 1,628 / 1,319. (Over short contexts it pays
     #: earlier: (128, 128), 16 over 500 x 64 220 / 205, x 128 353 / 223.)
     EXPAND_FROM = {(128, 128): 192, (192, 256): 384}
-    #: Bytes of expanded keys and values at most; steps that would need more stay in the absorbed form.
+    #: Bytes of expanded keys and values at most (their buffer has a quarter to spare); steps that would need more stay in the absorbed form.
     EXPAND_BYTES = 32 << 30
 
     def _buffer(self, name: str, *shape, dtype=torch.bfloat16):
@@ -383,9 +383,12 @@ class DenseSession:
         if form == "expanded" and (Dn, Dv) not in self.EXPAND_FROM:
             raise ValueError("the expanded form takes heads of %s" % " or ".join(map(str, self.EXPAND_FROM)))
         # before anything is turned or written
-        if w.shape != (H, Dn + Dv, 512) or out.shape[:2] != (T, H) or T != self.positions.numel():
-            raise ValueError("shape mismatch: q [T,H,Dn+64], w [H,Dn+Dv,512], out [T,H,Dv] for the %d tokens of the last extend"
-                             % self.positions.numel())
+        if T != self.positions.numel() or (w.shape, out.shape, latent.shape, rope.shape) != ((H, Dn + Dv, 512), (T, H, Dv), (T, 512), (T, 64)) \
+                or (lse is not None and lse.shape != (T, H)) or any(x.dtype is not torch.bfloat16 for x in (q, latent, rope, w, out)):
+            raise ValueError("q [T,H,Dn+64], latent [T,512], rope [T,64], w [H,Dn+Dv,512] and out [T,H,Dv] must be bf16, lse [T,H], for the "
+                             "%d tokens of the last extend" % self.positions.numel())
+        if form == "absorbed" and H > self.H:
+            raise ValueError("the session was made for %d heads" % self.H)
         if T == 0:
             return
         scale = self.softmax_scale * 24.0 * (Dn + 64) ** -0.5
@@ -393,6 +396,8 @@ class DenseSession:
             wide, mixed = self._buffer("queries", T, H, 576), self._buffer("mixed", T, H, 512)
             hs_rope(q[..., Dn:], self.positions, self.inv_freq, out=wide[..., 512:], y=rope[:, None], scale=self.rope_scale)
         else:
+            rows, kv = self._buffer("rows", self.read_tokens, 576), self._buffer("kv", self.read_tokens, H, Dn + Dv)
+            workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.B, Dv), dtype=torch.uint8)
             hs_rope(q[..., Dn:], self.positions, self.inv_freq, y=rope[:, None], scale=self.rope_scale)
         hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=self.pool[layer])
         if form == "absorbed":
@@ -401,8 +406,6 @@ class DenseSession:
                              self.workspace, lse=lse)
             hs_mla_project(mixed, w, out, self.err)
         else:
-            rows, kv = self._buffer("rows", self.read_tokens, 576), self._buffer("kv", self.read_tokens, H, Dn + Dv)
-            workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.B, Dv), dtype=torch.uint8)
             hs_kv_read(self.pool[layer], self.table, self.read_start, rows, self.err)
             hs_mla_expand(rows[:, :512], w, kv, self.err)
             hs_mla_expanded_fwd(q, kv, rows[:, 512:], self.req_start, self.read_start, scale, out, self.err, workspace, lse=lse)

@@ -124,7 +124,9 @@ def test_heads_that_have_one_form_only():
     q, latent, rope = (plain.rand(x, g).cuda() for x in ((T, H, Dn + 64), (T, 512), (T, 64)))
     held = [x.clone() for x in (q, latent, rope)]
     out, lse = torch.full((T, H, Dv), 7.0, dtype=torch.bfloat16, device="cuda"), torch.empty((T, H), device="cuda")
-    for bad in (dict(form="expanded"), dict(w=w[:, 64:].contiguous()), dict(q=q[1:]), dict(out=out[:, :1])):
+    for bad in (dict(form="expanded"), dict(w=w[:, 64:].contiguous()), dict(q=q[1:]), dict(out=out[:, :1]), dict(latent=latent[:, :448]),
+                dict(rope=rope.half()), dict(q=q.float()), dict(lse=lse[1:]),
+                dict(q=torch.cat([q, q], 1), w=torch.cat([w, w]), out=torch.cat([out, out], 1))):
         args = dict(dict(q=q, latent=latent, rope=rope, w=w, out=out), **bad)
         with pytest.raises(ValueError):
             s.attend_heads(0, **args)
