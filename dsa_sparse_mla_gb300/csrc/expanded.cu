@@ -29,7 +29,7 @@
 // one for two products and one for two sums instead of one each 1,485 -> 1,380, 1,600 -> 1,520, and 845 -> 785, 887 -> 845 (maxima of three
 // by an instruction of their own spilled: 1,420). A unit's end costs about 5,000 cycles (the last tile's softmax, PV and output one
 // after the other), a tile 1,280 of MMAs. (192, 256): 9 ragged requests 340 us, 385. Bound by HBM
-// for single tokens over long rows: 8 requests over 8,000 rows 340 us, 6.2 TB/s; over 200 to 2,000 rows 67 us, 4.5 TB/s, by the units' ends.
+// for single tokens over long rows: 8 requests over 8,000 rows 340 us, 6.2 TB/s; over 200 to 2,000 rows 63 us, 4.7 TB/s, by the last units.
 //
 // Rows past a request's end are masked as keys and set to zero as values (in shared memory, by a warp that waits for such a tile's copy).
 // A row that a token does not see can still reach its output where P = 0 meets a value that is not finite; where an output is not
@@ -644,7 +644,8 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
     } else if (warp == 3) {
       // ================================================================ V =======================
       // A tile that reaches past its request's end is counted on a barrier of this CTA; rows from there on become zeros, then
-      // the tile counts as there. Without a pair this warp also hands out the units, one ahead.
+      // the tile counts as there. Without a pair this warp also hands out the units, the next one three tiles before the end (8
+      // requests over 200 to 2,000 rows 62.9 us; at the second tile 67.3, when too many have a long one to come, at the last 67.7).
       Giver<Sh::kPlaces, kSMs> giver = {p, br.unit_empty, smem + Sh::kOffUnit, Mma::at(smem + Sh::kOffUnit, 0), Mma::at(br.unit_full, 0), 0};
       const int32_t total = kSMs == 1 ? p.total[0] : 0;
       bool more = kSMs == 1 && giver.give(0, total, lane);
@@ -680,7 +681,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
             if (lane == 0) Mma::arrive(full + 8 * (uint32_t)ring.slot);
           }
           ring.next(Sh::kVSlots);
-          if (more && t == (u.n > 1 ? 1 : 0)) more = giver.give(n + 1, total, lane);
+          if (more && t == (u.n > 3 ? u.n - 3 : 0)) more = giver.give(n + 1, total, lane);
         }
         if (ok) us.give_back(n);
       }

@@ -191,6 +191,18 @@ def test_attention_splits_long_rows(Dn, Dv):
     check(batch([1, 2, 20], [9000, 5000, 7001], 1, Dn, Dv, spare=3), Dn, Dv)
 
 
+@pytest.mark.parametrize("Dn,Dv,q_lens,kv_lens,H", [(128, 128, [600], [2500], 32), (192, 256, [600], [2500], 32), (128, 128, [60], [2300], 200),
+                                                    (128, 128, [3, 520, 0, 1], [40, 4500, 9, 1], 37)])
+def test_attention_of_more_blocks_than_workers(Dn, Dv, q_lens, kv_lens, H):
+    """Blocks of several tiles for more than one turn of all workers, with some left over; the same bits each time."""
+    b = batch(q_lens, kv_lens, H, Dn, Dv, seed=H)
+    check(b, Dn, Dv)
+    check(b, Dn, Dv, causal=False)
+    first = attend(b, Dv)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(first, attend(b, Dv)))
+
+
 @pytest.mark.parametrize("Dn,Dv", HEADS)
 def test_attention_scales_its_output(Dn, Dv):
     """Logits that grow along the rows move the reference (and scale the output) at most tiles; negative and zero scales."""
