@@ -24,12 +24,14 @@
 // that took the last tile alone while the other goes on (prompt of 8,192 tokens 870 -> 955 us), or by a fourth warpgroup (the softmax
 // threads have too few registers then: 915).
 //
-// Bound by the tensor cores for prompts and chunks: 2,048 tokens over 32,768 rows 1,380 us in a few calls (1,930 TFLOP/s), 1,515 to 1,590
-// us under the power limit; 8,192 tokens over themselves 785, and 835 to 880. There the softmax counts by the energy of its instructions: with
-// one for two products and one for two sums instead of one each 1,485 -> 1,380, 1,600 -> 1,520, and 845 -> 785, 887 -> 845 (maxima of three
-// by an instruction of their own spilled: 1,420). A unit's end costs about 5,000 cycles (the last tile's softmax, PV and output one
-// after the other), a tile 1,280 of MMAs. (192, 256): 9 ragged requests 340 us, 385. Bound by HBM
-// for single tokens over long rows: 8 requests over 8,000 rows 340 us, 6.2 TB/s; over 200 to 2,000 rows 63 us, 4.7 TB/s, by the last units.
+// Bound by the tensor cores for prompts and chunks: 2,048 tokens over 32,768 rows 1,370 to 1,415 us in a few calls (1,880 to 1,940
+// TFLOP/s), 1,510 to 1,590 us under the power limit; 8,192 tokens over themselves 765 to 785, and 820 to 870. There the softmax counts by the
+// energy of its instructions: with one for two products and one for two sums instead of one each 1,485 -> 1,380, 1,600 -> 1,520, and
+// 845 -> 785, 887 -> 845 (maxima of three by an instruction of their own spilled: 1,420). A unit's end costs about 5,000 cycles (the last
+// tile's softmax, PV and output one after the other), a tile 1,280 of MMAs. (192, 256): 9 ragged requests 330 to 337 us, 377. Bound by HBM for
+// single tokens over long rows: 8 requests over 8,000 rows 331 us, 6.3 TB/s; over 200 to 2,000 rows 62 us, 4.8 TB/s, by the last units.
+// (Splitting the blocks of a last turn that is not full: 1,024 tokens over 32,768 rows 861 -> 802 us, but 2,048 over 8,192 366 -> 389 to 418,
+// by the joins.)
 //
 // Rows past a request's end are masked as keys and set to zero as values (in shared memory, by a warp that waits for such a tile's copy).
 // A row that a token does not see can still reach its output where P = 0 meets a value that is not finite; where an output is not
@@ -230,18 +232,18 @@ struct Shape {
   static constexpr int kOffK = kQBytes, kOffV = kOffK + kKSlots * kKBytes, kOffP = kOffV + kVSlots * kVBytes, kOffRef = kOffP + (kWide ? kPBytes : 8 * 2048);
   static constexpr int kOffOut = kOffP;                       // 2 KB per softmax warp for the output (wide: in P's place, see the unit's end)
   static constexpr int kOffSum = kOffRef + 1024, kOffUnit = kOffSum + 1024, kOffBar = kOffUnit + kMaxPlaces * (int)sizeof(Unit);
-  static constexpr int kSmem = kOffBar + 512;
+  static constexpr int kSmem = kOffBar + 640;
   static constexpr int kColP = 256, kColO = kWide ? 256 : 384;  // tensor-memory columns; logits in 0 .. 255
   static_assert(kDv % 128 == 0 && kDv <= 256 && kSmem <= 232448, "shared and tensor memory");
 };
 
 struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
-  uint64_t tail_full, unit_full[kMaxPlaces], unit_empty[kMaxPlaces];
+  uint64_t tail_full, near_end, unit_full[kMaxPlaces], unit_empty[kMaxPlaces];
   uint64_t ref[8], sum[8], over[8];  // [warpgroup][quad]
   uint32_t tmem;
 };
-static_assert(sizeof(Bars) <= 512, "barriers");
+static_assert(sizeof(Bars) <= 640, "barriers");
 
 struct Ring {
   int slot;
@@ -499,6 +501,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
     mbar_init(&br.q_full, kSMs);
     mbar_init(&br.q_empty, 1);
     mbar_init(&br.tail_full, 1);
+    mbar_init(&br.near_end, 1);
     mbar_init(&br.o_full, 1);
     mbar_init(&br.o_free, 8 * kSMs);
   } else if (tid == 128) {
@@ -638,9 +641,11 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
       // ================================================================ units ===================
       Giver<Sh::kPlaces, kSMs> giver = {p, br.unit_empty, smem + Sh::kOffUnit, Mma::at(smem + Sh::kOffUnit, lane & 1), Mma::at(br.unit_full, lane & 1), 0};
       const int32_t total = p.total[0];
+      // the next one when V is five tiles before the end, so that a pair with much left takes none (9 ragged requests 344 us a unit
+      // ahead, 336 so)
 #pragma unroll 1
-      for (uint32_t n = 0; giver.give(n, total, lane); ++n) {
-      }
+      for (uint32_t n = 0; giver.give(n, total, lane); ++n)
+        if (!warp_wait(&br.near_end, n & 1u, p.err, lane)) break;
     } else if (warp == 3) {
       // ================================================================ V =======================
       // A tile that reaches past its request's end is counted on a barrier of this CTA; rows from there on become zeros, then
@@ -682,6 +687,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
           }
           ring.next(Sh::kVSlots);
           if (more && t == (u.n > 3 ? u.n - 3 : 0)) more = giver.give(n + 1, total, lane);
+          if (kSMs == 2 && rank == 1 && lane == 0 && t == (u.n > 5 ? u.n - 5 : 0)) mbar_arrive(&br.near_end);
         }
         if (ok) us.give_back(n);
       }
