@@ -52,6 +52,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPlanned = 4;                          // requests per thread of the plan
 constexpr int kMinPiece = 8;                         // tiles of a piece, at least
 constexpr int kPerPair = 6;                          // pieces of split blocks per pair of CTAs, at most
+constexpr int kTurns = 5, kEnd = 6;                  // turns that splitting may make; tiles' time that a unit's end and its join take
 
 struct Req {
   int32_t unit0, q0, m, kv0;   // first unit; first token, tokens; first row
@@ -117,8 +118,12 @@ __device__ __forceinline__ int size_class(int64_t tiles) {
 }
 
 // One CTA. Thread t plans requests 4 t .. 4 t + 3 (a call has few, as a rule: 128 threads wait less for each other than 1,024). Long
-// blocks come first, so that the last units to end are short. A block longer than half of a worker's even share of all tiles is split
-// into pieces of at most a quarter of it, but of kMinPiece tiles at least, and longer ones where they would not fit their slots.
+// blocks come first, so that the last units to end are short.
+//
+// Pieces: U blocks as long as the longest take ceil(U / workers) turns; cut into j pieces each, w turns where j = w workers / U. The least
+// of w (longest / j + kEnd) decides, for w up to kTurns. (Instead of these, as many pieces as an even share of all tiles has quarters:
+// 256 tokens over 30,000 rows x 16 heads 190 us, 74 so; 300 over 100,000 x 4 heads 341, 104; one token over 60,000 x 16 heads 160, 100, over
+// 8,000 x 64 heads 73, 60.) Pieces are longer where they would not fit their slots.
 template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   constexpr int kPer = kPlanned, kWarps = kPlanThreads / 32;
@@ -128,14 +133,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   let_next();
   after_previous();
   int start[kPer], m[kPer], kv0[kPer], len[kPer], nb[kPer], np[kPer], place[kPer];
-  int64_t most[kPer], work = 0, tokens = 0;
+  int64_t most[kPer], tiles[kPer], tokens = 0;
+  __shared__ int32_t longest, long_blocks;  // tiles of the longest block; blocks of more than half as many
+  __shared__ unsigned long long others;     // tiles of the other blocks
   if (threadIdx.x < 128) classes[threadIdx.x] = 0;
+  if (threadIdx.x == 0) longest = 1, long_blocks = 0, others = 0;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int r = kPer * threadIdx.x + k;
     m[k] = start[k] = kv0[k] = len[k] = nb[k] = place[k] = 0;
-    most[k] = 0;
+    most[k] = tiles[k] = 0;
     if (r >= p.B) continue;
     const int64_t a = p.req_start[r], b = p.req_start[r + 1], c = p.kv_start[r], d = p.kv_start[r + 1];
     if (a < 0 || b < a || b > p.T || (r == 0 && a != 0) || (r == p.B - 1 && b != p.T)) flag_error(p.err, HS_FLAG_BAD_INDEX);
@@ -150,34 +158,52 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
       }
       most[k] = (len[k] + kKeys - 1) / kKeys;
       const int64_t least = p.causal ? ((int64_t)len[k] - m[k] + p.tok + kKeys - 1) / kKeys : most[k];  // of the first block
-      work += nb[k] * (most[k] + (least < 1 ? 1 : least < most[k] ? least : most[k])) / 2 * p.H;
+      tiles[k] = nb[k] * (most[k] + (least < 1 ? 1 : least < most[k] ? least : most[k])) / 2 * p.H;
+      atomicMax(&longest, (int)most[k]);
     }
     place[k] = atomicAdd(&classes[size_class(nb[k] ? most[k] + 1 : 0)], 1);
   }
   int64_t all = 0;
   block_before<kWarps>(tokens, scratch, &all);
   const bool none = all > p.T;  // requests overlap (offsets out of order, flagged above): no bound on the units would hold
-  block_before<kWarps>(work, scratch, &all);
-  work = all;
-  int64_t piece = (work / p.workers + 3) / 4;
-  if (piece < kMinPiece) piece = kMinPiece;
+  const int top = longest;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (nb[k] == 0) continue;
+    if (2 * most[k] > top)
+      atomicAdd(&long_blocks, nb[k] * p.H);
+    else
+      atomicAdd(&others, (unsigned long long)tiles[k]);
+  }
+  __syncthreads();
+  const int blocks = max(1, long_blocks + (int)((others + top - 1) / top));
+  int64_t piece = (int64_t)1 << 32;  // longer than any block
+  int64_t best = (int64_t)((blocks + p.workers - 1) / p.workers) * (top + kEnd);
+  if (2 * blocks <= kTurns * p.workers) {
 #pragma unroll 1
-  for (;; piece *= 2) {
+    for (int w = 1; w <= kTurns; ++w) {
+      const int n = min(w * p.workers / blocks, top / kMinPiece), t = n > 1 ? (top + n - 1) / n : top;
+      if (n > 1 && w * (int64_t)(t + kEnd) < best) best = w * (int64_t)(t + kEnd), piece = t;
+    }
+  }
+  const bool splits = piece < top;
+#pragma unroll 1
+  for (; splits; piece *= 2) {
     int64_t slots = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
-      if (most[k] > 2 * piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
+      if (4 * most[k] > 5 * piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
     block_before<kWarps>(slots, scratch, &all);
     if (all <= p.cap) break;
   }
   int64_t slots = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    np[k] = most[k] > 2 * piece ? (int)((most[k] + piece - 1) / piece) : 1;
+    np[k] = 4 * most[k] > 5 * piece ? (int)((most[k] + piece - 1) / piece) : 1;
     if (np[k] > 1) slots += (int64_t)nb[k] * p.H * np[k];
   }
-  int64_t slot0 = block_before<kWarps>(slots, scratch, &all);
-  const int split = (int)all;  // slots in use
+  int64_t slot0 = splits ? block_before<kWarps>(slots, scratch, &all) : 0;
+  const int split = splits ? (int)all : 0;  // slots in use
   const int64_t before = block_before<kWarps>(threadIdx.x < 128 ? classes[threadIdx.x] : 0, scratch, &all);
   if (threadIdx.x < 128) classes[threadIdx.x] = (int)before;
   __syncthreads();
