@@ -1057,10 +1057,10 @@ static uint64_t off_lse(int B, int cap) { return off_joined(B) + up((uint64_t)ca
 static uint64_t off_out(int B, int cap) { return off_lse(B, cap) + up((uint64_t)cap * 2 * kTok * 4); }
 
 // Whether CTAs by themselves are better than pairs: with blocks of at most 128 tokens half of a pair would be idle. Measured (pairs /
-// alone, us, 64 heads, 8 requests over 4,000 rows): 16 tokens each 199 / 186, 128 220 / 195, 129 224 / 252, 256 235 / 259; one token
-// each over 1,000 rows 75 / 62; 16 heads, 64 requests x 33 tokens over 200 rows 77 / 47. How the tokens spread over the requests is on the
-// device: all of them in one of 64, 8,192 over themselves, 867 / 918; 1,024 in one of 8 over 8,192 rows 233 / 250. (192, 256) has no room
-// for whole tiles.
+// alone, us, 64 heads, 8 requests over 4,000 rows): 16 tokens each 189 / 178, 128 203 / 186, 129 207 / 246, 256 218 / 252; one token
+// each over 1,000 rows 70 / 56, one alone over 4,000 38 / 41; 16 heads, 64 requests x 33 tokens over 200 rows 75 / 44. How the tokens spread
+// over the requests is on the device: all of them in one of 64, 8,192 over themselves, 783 / 879; 1,024 in one of 8 over 8,192 rows
+// 217 / 249. (192, 256) has no room for whole tiles.
 static bool few_tokens(int T, int B) { return (int64_t)T <= 128ll * B; }
 
 }  // namespace expanded

@@ -348,10 +348,10 @@ class DenseSession:
 
     #: The expanded form from this many new tokens per slot that has any, on average. It expands a slot's rows once, 512 (Dn + Dv)
     #: products a head and row, and then spends Dn + 64 + Dv on a pair instead of 1,088. Measured, 64 heads, absorbed / expanded in us: (128, 128),
-    #: 8 slots over 8,000 rows x 128 tokens 900 / 1,043, x 192 1,322 / 1,096; one over 32,000 x 128 457 / 592, x 192 641 / 625; (192, 256), 8 over
-    #: 8,000 x 256 1,871 / 1,894, x 384 2,984 / 2,416; one over 32,000 x 384 1,204 / 1,298, x 512 1,628 / 1,319. (Over short contexts it pays
-    #: earlier: (128, 128), 16 over 500 x 64 220 / 205, x 128 353 / 223.)
-    EXPAND_FROM = {(128, 128): 192, (192, 256): 384}
+    #: 8 slots over 8,000 rows x 128 tokens 901 / 998, x 192 1,313 / 1,029; one over 32,000 x 128 459 / 585, x 192 641 / 530; (192, 256), 8 over
+    #: 8,000 x 192 1,510 / 1,771, x 256 1,812 / 1,790; one over 32,000 x 256 839 / 898, x 384 1,206 / 1,157. (Over short contexts it pays
+    #: earlier: 16 over 500, (128, 128) x 64 217 / 203, (192, 256) x 192 524 / 419.)
+    EXPAND_FROM = {(128, 128): 192, (192, 256): 256}
     #: Bytes of expanded keys and values at most (their buffer has a quarter to spare); steps that would need more stay in the absorbed form.
     EXPAND_BYTES = 32 << 30
 
