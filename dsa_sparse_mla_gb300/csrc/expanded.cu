@@ -5,8 +5,8 @@
 //   running reference and sum: P = 2^(logit log2 e - ref), and where a row's maximum passes ref by 2^8 its reference moves and
 //   the accumulator is scaled (so it rarely is).
 //
-// Work is units of (request, head, block of tokens), a unit's cached rows cut into pieces where single blocks are long against an even
-// share. A planning kernel counts units, chooses the pieces and clears a counter; workers take units from the counter, blocks of a head
+// Work is units of (request, head, block of tokens), a unit's cached rows cut into pieces where there are too few blocks to fill the
+// workers' turns. A planning kernel counts units, chooses the pieces and clears a counter; workers take units from the counter, blocks of a head
 // one after the other (they share its keys and values in L2), the longest first. A worker is a pair of CTAs with blocks of 256 tokens,
 // or, where requests have few tokens, a CTA by itself with blocks of 128 (few_tokens, below).
 //
