@@ -289,7 +289,7 @@ struct Units {
   bool gives;     // whether this thread gives units back for its role
   // Unit number n (one thread, or every lane of a warp); false after a wait that ran out.
   __device__ __forceinline__ bool take(uint32_t n, Unit& u) const {
-    if (!mbar_wait(&br->unit_full[n % kPlaces], (n / kPlaces) & 1u, err)) return false;
+    if (!pair::Mma<kSMs>::wait_writes(&br->unit_full[n % kPlaces], (n / kPlaces) & 1u, err)) return false;
     const int4* v = reinterpret_cast<const int4*>(at + n % kPlaces * sizeof(Unit));
     int4* w = reinterpret_cast<int4*>(&u);
 #pragma unroll
@@ -639,7 +639,12 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
 #pragma unroll 1
           for (int t = 0; t < u.n && ok; ++t, ++i) {
             const uint32_t b = i & 1u;
-            ok = mbar_wait(&br.v_full[ring.slot], ring.par, p.err) && mbar_wait(&br.p_full[b], (i >> 1) & 1u, p.err);
+            // What warps of the other CTA wrote to its shared memory: zeros behind a request's last row, and P where it goes through there.
+            // With a release and an acquire of every memory at cluster scope 9 ragged requests of (192, 256) take 513 us, 331 so; by a warp
+            // of the other CTA that waits for all of its half and hands it on, 343.
+            const bool tail = u.len - (u.ta + t) * kKeys < kKeys;
+            ok = tail ? Mma::wait_writes(&br.v_full[ring.slot], ring.par, p.err) : mbar_wait(&br.v_full[ring.slot], ring.par, p.err);
+            ok = ok && (Sh::kWide ? Mma::wait_writes(&br.p_full[b], (i >> 1) & 1u, p.err) : mbar_wait(&br.p_full[b], (i >> 1) & 1u, p.err));
             if (!ok) break;
             tc_fence_after();
             uint64_t v = vd + (uint64_t)((ring.slot * Sh::kVBytes) >> 4), w = pd;
@@ -711,7 +716,7 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
               for (int b = 0; b < Sh::kVCols / 64; ++b) *reinterpret_cast<uint4*>(s + b * Sh::kVBlk + 16 * x) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) Mma::arrive(full + 8 * (uint32_t)ring.slot);
+            if (lane == 0) Mma::arrive_writes(full + 8 * (uint32_t)ring.slot);
           }
           ring.next(Sh::kVSlots);
           if (more && t == (u.n > 3 ? u.n - 3 : 0)) more = giver.give(n + 1, total, lane);
@@ -869,7 +874,12 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
         if (Sh::kWide) fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) Mma::arrive(p_full + 8 * (uint32_t)g);
+        if (lane == 0) {
+          if (Sh::kWide)
+            Mma::arrive_writes(p_full + 8 * (uint32_t)g);
+          else
+            Mma::arrive(p_full + 8 * (uint32_t)g);
+        }
       }
       if (!ok) break;
       // ---------------------------------------------------------------- the unit's end

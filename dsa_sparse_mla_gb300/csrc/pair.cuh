@@ -61,11 +61,39 @@ __device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// 16 bytes into either CTA's shared memory, counted on a barrier there.
+// 16 bytes into either CTA's shared memory, counted on a barrier there; waited for with Mma::wait_writes.
 __device__ __forceinline__ void st_async16(uint32_t dst, int4 v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(dst), "r"(bar),
                "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
+}
+
+// Release and acquire at cluster scope of shared memory alone (remote_arrive and mbar_wait_cluster do so for every memory, and wait for it).
+__device__ __forceinline__ void fence_release_smem() { asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory"); }
+__device__ __forceinline__ void fence_acquire_smem() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
+
+__device__ __forceinline__ bool try_wait_relaxed(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
+// mbar_wait that sees what another CTA of the cluster wrote to shared memory before its arrival.
+__device__ __forceinline__ bool wait_cluster_smem(uint64_t* bar, uint32_t parity, int32_t* err) {
+  bool ok = try_wait_relaxed(bar, parity);
+  const uint64_t t0 = ok ? 0 : globaltimer();
+  for (uint32_t it = 0; !ok; ++it) {
+    ok = try_wait_relaxed(bar, parity);
+    if (!ok && (it & 63) == 63 && globaltimer() - t0 > kWaitLimitNs) {
+      flag_error(err, HS_FLAG_TIMEOUT);
+      return false;
+    }
+  }
+  fence_acquire_smem();
+  return true;
 }
 
 // Whether the phase with this parity is over, without waiting.
@@ -93,6 +121,23 @@ struct Mma {
       remote_arrive_cta(bar);
     else
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+  }
+  // Hands on this thread's writes of its CTA's shared memory (after __syncwarp its warp's; fenced for the async proxy by those who wrote
+  // them) to a thread of CTA 0 that waits with wait_writes: the other forms here order nothing between two CTAs but tensor memory, reads,
+  // and copies that count on barriers by themselves.
+  static __device__ __forceinline__ void arrive_writes(uint32_t bar) {
+    if constexpr (kSMs == 2) {
+      fence_release_smem();
+      remote_arrive_relaxed(bar);
+    } else {
+      arrive(bar);
+    }
+  }
+  static __device__ __forceinline__ bool wait_writes(uint64_t* bar, uint32_t parity, int32_t* err) {
+    if constexpr (kSMs == 2)
+      return wait_cluster_smem(bar, parity, err);
+    else
+      return mbar_wait(bar, parity, err);
   }
   static __device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
     if constexpr (kSMs == 2)
