@@ -123,7 +123,8 @@ __device__ __forceinline__ int size_class(int64_t tiles) {
 // Pieces: U blocks as long as the longest take ceil(U / workers) turns; cut into j pieces each, w turns where j = w workers / U. The least
 // of w (longest / j + kEnd) decides, for w up to kTurns. (Instead of these, as many pieces as an even share of all tiles has quarters:
 // 256 tokens over 30,000 rows x 16 heads 190 us, 74 so; 300 over 100,000 x 4 heads 341, 104; one token over 60,000 x 16 heads 160, 100, over
-// 8,000 x 64 heads 73, 60.) Pieces are longer where they would not fit their slots.
+// 8,000 x 64 heads 73, 60.) Turns whose pieces do not fit their slots are left out
+// (where their pieces were doubled until they did: 120 requests of one token over 12,800 rows 172 us, 149 so; 67 over 102,400 685, 608).
 template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   constexpr int kPer = kPlanned, kWarps = kPlanThreads / 32;
@@ -177,25 +178,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   }
   __syncthreads();
   const int blocks = max(1, long_blocks + (int)((others + top - 1) / top));
-  int64_t piece = (int64_t)1 << 32;  // longer than any block
-  int64_t best = (int64_t)((blocks + p.workers - 1) / p.workers) * (top + kEnd);
-  if (2 * blocks <= kTurns * p.workers) {
+  constexpr int64_t kWhole = (int64_t)1 << 32;  // longer than any block
+  int64_t piece = kWhole;
+  uint32_t full = 0;  // turns whose pieces have no room
+  while (2 * blocks <= kTurns * p.workers) {
+    int64_t best = (int64_t)((blocks + p.workers - 1) / p.workers) * (top + kEnd);
+    int turns = 0;
 #pragma unroll 1
     for (int w = 1; w <= kTurns; ++w) {
       const int n = min(w * p.workers / blocks, top / kMinPiece), t = n > 1 ? (top + n - 1) / n : top;
-      if (n > 1 && w * (int64_t)(t + kEnd) < best) best = w * (int64_t)(t + kEnd), piece = t;
+      if (n > 1 && !(full >> w & 1u) && w * (int64_t)(t + kEnd) < best) best = w * (int64_t)(t + kEnd), piece = t, turns = w;
     }
-  }
-  const bool splits = piece < top;
-#pragma unroll 1
-  for (; splits; piece *= 2) {
+    if (turns == 0) break;
     int64_t slots = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       if (4 * most[k] > 5 * piece) slots += (int64_t)nb[k] * p.H * ((most[k] + piece - 1) / piece);
     block_before<kWarps>(slots, scratch, &all);
     if (all <= p.cap) break;
+    full |= 1u << turns, piece = kWhole;
   }
+  const bool splits = piece != kWhole;
   int64_t slots = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
