@@ -273,6 +273,32 @@ class DeviceHiSparse:
         self.mla(step, stream)
 
 
+def _check_heads(q, latent, rope, w, out, lse, tokens: int, device):
+    """What the calls of DenseSession.attend_heads ask of its arguments in either form, all of it before any of them turns or writes
+    something: ValueError, or the tensors are as they have to be. Returns (T, H, Dn, Dv)."""
+    (T, H, D), Dn, Dv = q.shape, q.shape[2] - 64, out.shape[2]
+    given = (q, latent, rope, w, out)
+    if T != tokens or (w.shape, out.shape, latent.shape, rope.shape) != ((H, Dn + Dv, 512), (T, H, Dv), (T, 512), (T, 64)) \
+            or (lse is not None and lse.shape != (T, H)) or any(x.dtype is not torch.bfloat16 for x in given):
+        raise ValueError("q [T,H,Dn+64], latent [T,512], rope [T,64], w [H,Dn+Dv,512] and out [T,H,Dv] must be bf16, lse [T,H], for the "
+                         "%d tokens of the last extend" % tokens)
+    if Dn not in (64, 128, 192, 256) or Dv not in (64, 128, 192, 256) or not 1 <= H <= 1024:
+        raise ValueError("Dn and Dv must be 64, 128, 192 or 256 and H in [1, 1024] (got %d, %d, %d)" % (Dn, Dv, H))
+    if lse is not None and lse.dtype is not torch.float32:
+        raise ValueError("lse must be float32")
+    if any(x.device != device for x in given) or (lse is not None and lse.device != device):
+        raise ValueError("tensors must be on the session's device, %s" % device)
+    if not (latent.is_contiguous() and rope.is_contiguous() and w.is_contiguous() and (lse is None or lse.is_contiguous())):
+        raise ValueError("latent, rope, w and lse must be contiguous")
+    for x, name in ((q, "q"), (out, "out")):
+        (a, b, c), (t, h, _) = x.stride(), x.shape
+        if c != 1 or (t > 1 and (a <= 0 or a % 8)) or (h > 1 and (b <= 0 or b % 8)):
+            raise ValueError("%s must have consecutive values in a head, and heads and tokens a multiple of 8 values apart" % name)
+    if any(x.data_ptr() % 16 for x in given):
+        raise ValueError("q, latent, rope, w and out must be 16-byte aligned")
+    return T, H, Dn, Dv
+
+
 class DenseSession:
     """Requests that attend densely over the paged latent cache and may branch (several samples of one prompt, beams):
     device state for ``B`` request slots and ``L`` layers, and the calls of a step in their order. ``extend`` gives the new
@@ -302,6 +328,7 @@ class DenseSession:
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
         self._make_room(max_tokens, 0)
         self._kept, self._captured = {}, []  # attend_heads' buffers by name; those that a captured graph uses
+        self.positions, self.read_tokens, self.active = torch.empty(0, **i32), 0, 0  # of the last extend
         self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
 
     def _make_room(self, tokens: int, cached: int):
@@ -372,25 +399,24 @@ class DenseSession:
                      lse=None, form: str | None = None):
         """Layer ``layer`` of the tokens of the last extend from per-head queries to per-head outputs: ``q`` bf16 [T, H, Dn + 64] (its
         rotary part, the last 64 values, may be rotated in place) and ``rope`` bf16 [T, 64] (rotated in place), ``latent`` bf16 [T, 512],
-        the layer's weight ``w`` bf16 [H, Dn + Dv, 512], ``out`` bf16 [T, H, Dv]; logits are scaled by (Dn + 64)^-1/2. ``form`` is "absorbed"
-        or "expanded" (heads of 128 and 128, or 192 and 256, alone); None picks it by the new tokens per slot."""
-        (T, H, D), Dn, Dv = q.shape, q.shape[2] - 64, out.shape[2]
+        the layer's weight ``w`` bf16 [H, Dn + Dv, 512], ``out`` bf16 [T, H, Dv]; logits are scaled by (Dn + 64)^-1/2. ``q`` and ``out`` may be
+        slices of wider heads. ``form`` is "absorbed" or "expanded" (heads of 128 and 128, or 192 and 256, alone); None picks it by the new
+        tokens per slot. A call that is refused (ValueError, IndexError) has turned and written nothing."""
+        if form not in (None, "absorbed", "expanded"):
+            raise ValueError("form must be absorbed or expanded")
+        pool = self.pool[layer]
+        T, H, Dn, Dv = _check_heads(q, latent, rope, w, out, lse, self.positions.numel(), self.pool.device)
         if form is None:
             pays = (Dn, Dv) in self.EXPAND_FROM and T >= self.EXPAND_FROM[Dn, Dv] * self.active
             form = "expanded" if pays and 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES else "absorbed"
-        if form not in ("absorbed", "expanded"):
-            raise ValueError("form must be absorbed or expanded")
         if form == "expanded" and (Dn, Dv) not in self.EXPAND_FROM:
             raise ValueError("the expanded form takes heads of %s" % " or ".join(map(str, self.EXPAND_FROM)))
-        # before anything is turned or written
-        if T != self.positions.numel() or (w.shape, out.shape, latent.shape, rope.shape) != ((H, Dn + Dv, 512), (T, H, Dv), (T, 512), (T, 64)) \
-                or (lse is not None and lse.shape != (T, H)) or any(x.dtype is not torch.bfloat16 for x in (q, latent, rope, w, out)):
-            raise ValueError("q [T,H,Dn+64], latent [T,512], rope [T,64], w [H,Dn+Dv,512] and out [T,H,Dv] must be bf16, lse [T,H], for the "
-                             "%d tokens of the last extend" % self.positions.numel())
         if form == "absorbed" and H > self.H:
             raise ValueError("the session was made for %d heads" % self.H)
         if T == 0:
             return
+        if torch.cuda.current_device() != self.pool.device.index:
+            raise ValueError("the session's device is not the current one")
         scale = self.softmax_scale * 24.0 * (Dn + 64) ** -0.5
         if form == "absorbed":
             wide, mixed = self._buffer("queries", T, H, 576), self._buffer("mixed", T, H, 512)
@@ -398,17 +424,20 @@ class DenseSession:
         else:
             rows, kv = self._buffer("rows", self.read_tokens, 576), self._buffer("kv", self.read_tokens, H, Dn + Dv)
             workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.B, Dv), dtype=torch.uint8)
+            whole = out if out.is_contiguous() else self._buffer("out", T, H, Dv)
             hs_rope(q[..., Dn:], self.positions, self.inv_freq, y=rope[:, None], scale=self.rope_scale)
-        hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=self.pool[layer])
+        hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=pool)
         if form == "absorbed":
             hs_mla_absorb(q[..., :Dn], w, wide[..., :512], self.err)
-            hs_paged_mla_fwd(wide, self.pool[layer], self.table, self.req_start, self.seq_len, self.kv_tokens, scale, mixed, self.err,
+            hs_paged_mla_fwd(wide, pool, self.table, self.req_start, self.seq_len, self.kv_tokens, scale, mixed, self.err,
                              self.workspace, lse=lse)
             hs_mla_project(mixed, w, out, self.err)
         else:
-            hs_kv_read(self.pool[layer], self.table, self.read_start, rows, self.err)
+            hs_kv_read(pool, self.table, self.read_start, rows, self.err)
             hs_mla_expand(rows[:, :512], w, kv, self.err)
-            hs_mla_expanded_fwd(q, kv, rows[:, 512:], self.req_start, self.read_start, scale, out, self.err, workspace, lse=lse)
+            hs_mla_expanded_fwd(q, kv, rows[:, 512:], self.req_start, self.read_start, scale, whole, self.err, workspace, lse=lse)
+            if whole is not out:
+                out.copy_(whole)
 
     def fork(self, parent, child):
         parent, child = (torch.as_tensor(x, dtype=torch.int32, device=self.device) for x in (parent, child))
