@@ -408,7 +408,8 @@ class DenseSession:
         T, H, Dn, Dv = _check_heads(q, latent, rope, w, out, lse, self.positions.numel(), self.pool.device)
         if form is None:
             pays = (Dn, Dv) in self.EXPAND_FROM and T >= self.EXPAND_FROM[Dn, Dv] * self.active
-            form = "expanded" if pays and 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES else "absorbed"
+            pays = pays and 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES
+            form = "expanded" if pays or (H > self.H and (Dn, Dv) in self.EXPAND_FROM) else "absorbed"
         if form == "expanded" and (Dn, Dv) not in self.EXPAND_FROM:
             raise ValueError("the expanded form takes heads of %s" % " or ".join(map(str, self.EXPAND_FROM)))
         if form == "absorbed" and H > self.H:

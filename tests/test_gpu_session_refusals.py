@@ -51,3 +51,22 @@ def test_results_in_slices_of_wider_rows(form):
         out.fill_(7)
         assert bool((mem == 7).all())
     assert all(torch.equal(got[0], x) for x in got[1:])
+
+
+def test_more_heads_than_the_session_was_made_for():
+    """They run expanded, however few the tokens are, and not at all where that is not their form."""
+    g = torch.Generator().manual_seed(32)
+    for new in ([3, 1], [300, 0]):
+        s, t = DenseSession(2, H - 1, 16, 8, max_tokens=T), sum(new)
+        s.extend(new)
+        for form in ("absorbed", None):
+            for width in (128, 64):
+                a = [plain.rand(x, g).cuda() for x in ((t, H, width + 64), (t, 512), (t, 64))]
+                out = torch.full((t, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+                if form or width == 64:
+                    with pytest.raises(ValueError):
+                        s.attend_heads(0, *a, plain.weights(H, width, 128, g).cuda(), out, form=form)
+                    assert bool((out == 7).all())
+                else:
+                    s.attend_heads(0, *a, plain.weights(H, width, 128, g).cuda(), out, form=form)
+                    assert hs.hs_check_flag(s.err) == 0 and not bool((out == 7).all(-1).any())
