@@ -306,7 +306,9 @@ class DenseSession:
     hs_paged_mla_fwd), or ``attend_heads``, which takes and gives per-head values and picks the form of latent attention. Between
     steps ``fork`` makes slots copies of others (pages shared, the partial one copied), ``free`` empties slots, and ``compact`` moves
     the pages in use to the front. Everything runs on the current stream. The attention's
-    workspace is made for steps of ``max_tokens`` and grows with the cached rows, or where a step has more tokens."""
+    workspace is made for steps of ``max_tokens`` and grows with the cached rows, or where a step has more tokens. A captured ``attend`` or
+    ``attend_heads`` is one of the tokens of the extend before it, whatever has been extended since; all that it reads stays for as long as
+    the session does. Graphs of one session share their buffers: they must not run at the same time."""
 
     def __init__(self, B: int, H: int, nblk: int, pages: int, L: int = 1, max_tokens: int = 4096, base: float = 10000.0,
                  kind: str = "plain", factor: float = 1.0, device="cuda"):
@@ -327,7 +329,7 @@ class DenseSession:
         self.kv_tokens = 0  # cached rows: shared pages count once per request
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
         self._make_room(max_tokens, 0)
-        self._kept, self._captured = {}, []  # attend_heads' buffers by name; those that a captured graph uses
+        self._kept, self._captured = {}, []  # attend_heads' buffers by name; tensors that captured graphs use
         self.positions, self.read_tokens, self.active = torch.empty(0, **i32), 0, 0  # of the last extend
         self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
 
@@ -365,9 +367,15 @@ class DenseSession:
         self.read_start = torch.cat([read.new_zeros(1), read.cumsum(0).int()])
         return T
 
+    def _hold(self, *tensors):
+        """Where a graph is being captured, what it uses stays for as long as the session does."""
+        if torch.cuda.is_current_stream_capturing():
+            self._captured += [x for x in tensors if all(x is not y for y in self._captured)]
+
     def attend(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, out: torch.Tensor, lse=None):
         """Layer ``layer`` of the tokens of the last extend: ``q`` bf16 [T, H, 576] and ``rope`` bf16 [T, 64] are rotated in
         place, ``latent`` bf16 [T, 512] and ``rope`` become cache rows, ``out`` bf16 [T, H, 512] receives the attention."""
+        self._hold(self.positions, self.token_req, self.req_start, self.seq_len, self.workspace)
         hs_rope(q[..., 512:], self.positions, self.inv_freq, y=rope[:, None], scale=self.rope_scale)
         hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=self.pool[layer])
         hs_paged_mla_fwd(q, self.pool[layer], self.table, self.req_start, self.seq_len, self.kv_tokens, self.softmax_scale, out,
@@ -383,16 +391,14 @@ class DenseSession:
     EXPAND_BYTES = 32 << 30
 
     def _buffer(self, name: str, *shape, dtype=torch.bfloat16):
-        """A buffer that is kept from step to step, made anew with a quarter to spare where it is too small. One that a captured graph
-        uses stays for as long as the session does."""
+        """A buffer that is kept from step to step, made anew with a quarter to spare where it is too small."""
         n, buffer = math.prod(shape), self._kept.get(name)
         if buffer is None or buffer.numel() < n or buffer.dtype != dtype:
             if buffer is not None and not torch.cuda.is_current_stream_capturing():
                 buffer.record_stream(torch.cuda.current_stream())  # its memory may serve another tensor once the calls so far are done
             self._kept[name] = buffer = None
             self._kept[name] = buffer = torch.empty(n + n // 4, dtype=dtype, device=self.device)
-        if torch.cuda.is_current_stream_capturing() and all(buffer is not x for x in self._captured):
-            self._captured.append(buffer)
+        self._hold(buffer)
         return buffer[:n].view(shape)
 
     def attend_heads(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
@@ -418,6 +424,7 @@ class DenseSession:
             return
         if torch.cuda.current_device() != self.pool.device.index:
             raise ValueError("the session's device is not the current one")
+        self._hold(self.positions, self.token_req, self.req_start, self.read_start, self.seq_len, self.workspace)
         scale = self.softmax_scale * 24.0 * (Dn + 64) ** -0.5
         if form == "absorbed":
             wide, mixed = self._buffer("queries", T, H, 576), self._buffer("mixed", T, H, 512)
