@@ -365,6 +365,7 @@ class DenseSession:
                           + torch.repeat_interleave(self.seq_len - self.req_start[:-1], new))
         self.seq_len = after
         self.read_start = torch.cat([read.new_zeros(1), read.cumsum(0).int()])
+        self._with_tokens = None
         return T
 
     def _hold(self, *tensors):
@@ -401,6 +402,20 @@ class DenseSession:
         self._hold(buffer)
         return buffer[:n].view(shape)
 
+    def _requests(self):
+        """req_start and read_start of the slots that have new tokens alone: hs_mla_expanded_fwd picks its variant by the tokens per request
+        (a layer's step of 8,192 tokens in one of 64 slots, 64 heads, 991 us with all of them, 900 so; 1,024 over 8,192 rows in one of eight 372, 339)."""
+        if self.active == self.B:
+            return self.req_start, self.read_start
+        if self._with_tokens is not None:
+            return self._with_tokens
+        at = (self.req_start.diff() > 0).cumsum(0).expand(2, -1)  # a slot without tokens writes what the one before it does
+        start = torch.zeros((2, self.active + 1), dtype=torch.int32, device=self.device)
+        start = start.scatter_(1, at, torch.stack([self.req_start[1:], self.read_start[1:]])).unbind()
+        if not torch.cuda.is_current_stream_capturing():  # in a graph it is a part of it
+            self._with_tokens = start
+        return start
+
     def attend_heads(self, layer: int, q: torch.Tensor, latent: torch.Tensor, rope: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
                      lse=None, form: str | None = None):
         """Layer ``layer`` of the tokens of the last extend from per-head queries to per-head outputs: ``q`` bf16 [T, H, Dn + 64] (its
@@ -431,7 +446,9 @@ class DenseSession:
             hs_rope(q[..., Dn:], self.positions, self.inv_freq, out=wide[..., 512:], y=rope[:, None], scale=self.rope_scale)
         else:
             rows, kv = self._buffer("rows", self.read_tokens, 576), self._buffer("kv", self.read_tokens, H, Dn + Dv)
-            workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.B, Dv), dtype=torch.uint8)
+            workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.active, Dv), dtype=torch.uint8)
+            req_start, read_start = self._requests()
+            self._hold(req_start, read_start)
             whole = out if out.is_contiguous() else self._buffer("out", T, H, Dv)
             hs_rope(q[..., Dn:], self.positions, self.inv_freq, y=rope[:, None], scale=self.rope_scale)
         hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=pool)
@@ -443,7 +460,7 @@ class DenseSession:
         else:
             hs_kv_read(pool, self.table, self.read_start, rows, self.err)
             hs_mla_expand(rows[:, :512], w, kv, self.err)
-            hs_mla_expanded_fwd(q, kv, rows[:, 512:], self.req_start, self.read_start, scale, whole, self.err, workspace, lse=lse)
+            hs_mla_expanded_fwd(q, kv, rows[:, 512:], req_start, read_start, scale, whole, self.err, workspace, lse=lse)
             if whole is not out:
                 out.copy_(whole)
 
