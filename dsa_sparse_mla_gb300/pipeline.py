@@ -330,7 +330,7 @@ class DenseSession:
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
         self._make_room(max_tokens, 0)
         self._kept, self._captured = {}, []  # attend_heads' buffers by name; tensors that captured graphs use
-        self.positions, self.read_tokens, self.active = torch.empty(0, **i32), 0, 0  # of the last extend
+        self.positions, self.read_tokens, self.active, self.pairs = torch.empty(0, **i32), 0, 0, 0  # of the last extend
         self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
 
     def _make_room(self, tokens: int, cached: int):
@@ -353,7 +353,9 @@ class DenseSession:
             raise RuntimeError("the cache has too few pages")
         # what the expanded form reads: the rows of slots with new tokens
         read = torch.where(new > 0, after, 0)
-        cached, tokens, self.read_tokens, self.active = torch.stack([after.sum(), new.sum(), read.sum(), (new > 0).sum()]).tolist()
+        # (token, row) pairs that new tokens see, twice
+        pairs = new.long() * (2 * after.long() - new + 1)
+        cached, tokens, self.read_tokens, self.active, self.pairs = torch.stack([after, new, read, new > 0, pairs]).sum(1).tolist()
         self._make_room(tokens, cached)
         self.kv_tokens = cached
         self.table[take] = free
@@ -382,12 +384,8 @@ class DenseSession:
         hs_paged_mla_fwd(q, self.pool[layer], self.table, self.req_start, self.seq_len, self.kv_tokens, self.softmax_scale, out,
                          self.err, self.workspace, lse=lse)
 
-    #: The expanded form from this many new tokens per slot that has any, on average. It expands a slot's rows once, 512 (Dn + Dv)
-    #: products a head and row, and then spends Dn + 64 + Dv on a pair instead of 1,088. Measured, 64 heads, absorbed / expanded in us: (128, 128),
-    #: 8 slots over 8,000 rows x 128 tokens 901 / 998, x 192 1,313 / 1,029; one over 32,000 x 128 459 / 585, x 192 641 / 530; (192, 256), 8 over
-    #: 8,000 x 192 1,510 / 1,771, x 256 1,812 / 1,790; one over 32,000 x 256 839 / 898, x 384 1,206 / 1,157. (Over short contexts it pays
-    #: earlier: 16 over 500, (128, 128) x 64 217 / 203, (192, 256) x 192 524 / 419.)
-    EXPAND_FROM = {(128, 128): 192, (192, 256): 256}
+    #: Heads (Dn, Dv) that the expanded form takes.
+    EXPANDED = ((128, 128), (192, 256))
     #: Bytes of expanded keys and values at most (their buffer has a quarter to spare); steps that would need more stay in the absorbed form.
     EXPAND_BYTES = 32 << 30
 
@@ -402,9 +400,26 @@ class DenseSession:
         self._hold(buffer)
         return buffer[:n].view(shape)
 
+    def _expanded_pays(self, T: int, Dn: int, Dv: int) -> bool:
+        """Whether the last extend's tokens are faster in the expanded form, by what each form does for a head, in products of the absorbed
+        attention: that form makes 1,088 a (token, row) pair and moves 2,176 + Dn + Dv values a token; the other one makes Dn + 64 + Dv a
+        pair, at twice the rate, and Dn + Dv values of every row that is read, worth 650 each (512 products, a store and a load). So a long
+        prompt among single tokens over long contexts stays absorbed: the rows of those are not worth their expansion.
+
+        Fitted to a layer's step of 418 batches (1 to 64 slots, 16 to 512 tokens each over none to 32,000 rows, and prompts among single tokens;
+        16, 64 and 128 heads): in 13 of them the form picked is slower by more than a tenth, by 22 % at most (64 slots x 96 tokens over 300 rows,
+        (192, 256)), mostly where both take the host's 100 us. Absorbed / expanded, us, 64 heads of (128, 128): 8 slots over 8,000 rows x 96
+        tokens 744 / 1,037, x 192 1,333 / 1,084; one over 32,000 x 128 476 / 614, x 192 656 / 561; 16 over 500 x 64 231 / 219; 8,192
+        tokens and 7 slots of one over 60,000 4,154 / 7,757; 1,024 over 16,000 and 32 slots of 4 over 1,000 1,698 / 1,087. (192, 256):
+        8 over 8,000 x 192 1,347 / 1,834, x 512 3,456 / 2,457."""
+        absorbed = 544 * self.pairs + 400 * (2176 + Dn + Dv) * T
+        expanded = (Dn + 64 + Dv) * self.pairs // 4 + 650 * (Dn + Dv) * self.read_tokens
+        return T >= 64 and expanded < absorbed
+
     def _requests(self):
         """req_start and read_start of the slots that have new tokens alone: hs_mla_expanded_fwd picks its variant by the tokens per request
-        (a layer's step of 8,192 tokens in one of 64 slots, 64 heads, 991 us with all of them, 900 so; 1,024 over 8,192 rows in one of eight 372, 339)."""
+        (a layer's step of 8,192 tokens in one of 64 slots, 64 heads, 991 us with all of them, 900 so; 1,024 over 8,192 rows in one of
+        eight 372, 339)."""
         if self.active == self.B:
             return self.req_start, self.read_start
         if self._with_tokens is not None:
@@ -421,18 +436,17 @@ class DenseSession:
         """Layer ``layer`` of the tokens of the last extend from per-head queries to per-head outputs: ``q`` bf16 [T, H, Dn + 64] (its
         rotary part, the last 64 values, may be rotated in place) and ``rope`` bf16 [T, 64] (rotated in place), ``latent`` bf16 [T, 512],
         the layer's weight ``w`` bf16 [H, Dn + Dv, 512], ``out`` bf16 [T, H, Dv]; logits are scaled by (Dn + 64)^-1/2. ``q`` and ``out`` may be
-        slices of wider heads. ``form`` is "absorbed" or "expanded" (heads of 128 and 128, or 192 and 256, alone); None picks it by the new
-        tokens per slot. A call that is refused (ValueError, IndexError) has turned and written nothing."""
+        slices of wider heads. ``form`` is "absorbed" or "expanded" (heads of 128 and 128, or 192 and 256, alone); None picks it by
+        the work of each (_expanded_pays). A call that is refused (ValueError, IndexError) has turned and written nothing."""
         if form not in (None, "absorbed", "expanded"):
             raise ValueError("form must be absorbed or expanded")
         pool = self.pool[layer]
         T, H, Dn, Dv = _check_heads(q, latent, rope, w, out, lse, self.positions.numel(), self.pool.device)
         if form is None:
-            pays = (Dn, Dv) in self.EXPAND_FROM and T >= self.EXPAND_FROM[Dn, Dv] * self.active
-            pays = pays and 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES
-            form = "expanded" if pays or (H > self.H and (Dn, Dv) in self.EXPAND_FROM) else "absorbed"
-        if form == "expanded" and (Dn, Dv) not in self.EXPAND_FROM:
-            raise ValueError("the expanded form takes heads of %s" % " or ".join(map(str, self.EXPAND_FROM)))
+            pays = 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES and self._expanded_pays(T, Dn, Dv)
+            form = "expanded" if (Dn, Dv) in self.EXPANDED and (pays or H > self.H) else "absorbed"
+        if form == "expanded" and (Dn, Dv) not in self.EXPANDED:
+            raise ValueError("the expanded form takes heads of %s" % " or ".join(map(str, self.EXPANDED)))
         if form == "absorbed" and H > self.H:
             raise ValueError("the session was made for %d heads" % self.H)
         if T == 0:

@@ -4,6 +4,7 @@ import torch
 
 import dsa_sparse_mla_gb300 as hs
 import latent_ops as plain
+import test_gpu_session_heads
 from dsa_sparse_mla_gb300.pipeline import DenseSession
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,22 @@ def test_a_prompt_in_one_of_many_slots():
         assert hs.hs_check_flag(s.err) == 0
         units.append(int(s._kept["expanded"][:4].view(torch.int32)))
     assert units[0] == units[1]
+
+
+@pytest.mark.parametrize("over,form", [(4000, "absorbed"), (100, "expanded")])
+def test_prompts_among_single_tokens(over, form):
+    """The form that pays for the whole step: rows that one token alone reads are not worth their expansion."""
+    H, Dn, Dv, new = 2, 128, 128, [300, 0, 300, 1, 1, 1, 1, 0]
+    w, g = plain.weights(H, Dn, Dv, torch.Generator().manual_seed(64)).cuda(), torch.Generator().manual_seed(65)
+    s = DenseSession(8, H, 400, 64, max_tokens=600)
+    for m in ([0] * 3 + [over] * 4 + [9], new):
+        s._kept.clear()
+        T = s.extend(m)
+        q, latent, rope = (plain.rand(x, g).cuda() for x in ((T, H, Dn + 64), (T, 512), (T, 64)))
+        turned, out, lse = q.clone(), torch.full((T, H, Dv), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((T, H), 7.0, device="cuda")
+        hs.hs_rope(turned[..., Dn:], s.positions, s.inv_freq, scale=s.rope_scale)
+        s.attend_heads(0, q, latent, rope, w, out, lse, form=None if m is new else "absorbed")
+        assert hs.hs_check_flag(s.err) == 0
+    assert ("kv" in s._kept) == (form == "expanded")
+    ref, tol, rlse, ltol = test_gpu_session_heads.reference(s, 0, turned, w, Dn, (Dn + 64) ** -0.5)
+    assert plain.holds(out, ref, tol) and plain.holds(lse, rlse, ltol)

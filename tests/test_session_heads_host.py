@@ -1,8 +1,10 @@
 """What DenseSession.attend_heads asks of its arguments before anything is turned or written, without a GPU."""
+import types
+
 import pytest
 import torch
 
-from dsa_sparse_mla_gb300.pipeline import _check_heads
+from dsa_sparse_mla_gb300.pipeline import DenseSession, _check_heads
 
 T, H, Dn, Dv = 5, 2, 128, 192
 CPU = torch.device("cpu")
@@ -53,3 +55,19 @@ BAD = {
 def test_what_is_refused(what):
     with pytest.raises(ValueError):
         _check_heads(**given(**BAD[what]))
+
+
+def pays(new, over, heads):
+    step = types.SimpleNamespace(pairs=sum(m * (2 * n + m + 1) for m, n in zip(new, over)), read_tokens=sum(m + n for m, n in zip(new, over) if m))
+    return DenseSession._expanded_pays(step, sum(new), *heads)
+
+
+@pytest.mark.parametrize("heads", [(128, 128), (192, 256)])
+def test_which_form_pays(heads):
+    """Where the forms' times are far apart (measured, absorbed / expanded)."""
+    assert pays([8192], [0], heads) and pays([128] * 8, [0] * 8, heads) and pays([512] * 16, [500] * 16, heads)  # 272 / 111 us, 8 x 128
+    assert not pays([1] * 64, [2000] * 64, heads) and not pays([32] * 8, [8000] * 8, heads)
+    assert not pays([8192] + [1] * 7, [0] + [60000] * 7, heads)  # 4,154 / 7,757
+    assert not pays([700] * 3 + [1] * 5, [0] * 3 + [4000] * 5, heads)  # 352 / 447, 361 / 715
+    assert pays([2048] + [1] * 63, [2000] + [100] * 63, heads) and pays([1024], [32000], heads)
+    assert pays([192] * 8, [8000] * 8, heads) == (heads == (128, 128))  # 1,333 / 1,084, 1,347 / 1,834
