@@ -331,6 +331,7 @@ class DenseSession:
         self._make_room(max_tokens, 0)
         self._kept, self._captured = {}, []  # attend_heads' buffers by name; tensors that captured graphs use
         self.positions, self.read_tokens, self.active, self.pairs = torch.empty(0, **i32), 0, 0, 0  # of the last extend
+        self._with_tokens, self._room = None, True  # _requests' offsets; whether the expanded form's buffers could be had
         self.compact_workspace = torch.empty(hs_kv_compact_workspace_size(nblk), dtype=torch.uint8, device=device)
 
     def _make_room(self, tokens: int, cached: int):
@@ -367,7 +368,7 @@ class DenseSession:
                           + torch.repeat_interleave(self.seq_len - self.req_start[:-1], new))
         self.seq_len = after
         self.read_start = torch.cat([read.new_zeros(1), read.cumsum(0).int()])
-        self._with_tokens = None
+        self._with_tokens, self._room = None, True
         return T
 
     def _hold(self, *tensors):
@@ -386,19 +387,27 @@ class DenseSession:
 
     #: Heads (Dn, Dv) that the expanded form takes.
     EXPANDED = ((128, 128), (192, 256))
-    #: Bytes of expanded keys and values at most (their buffer has a quarter to spare); steps that would need more stay in the absorbed form.
+    #: Bytes of expanded keys and values at most (their buffer has a quarter to spare); steps that would need more stay in the absorbed form, as do
+    #: those whose buffers cannot be had. A step in the absorbed form gives the rows, keys and values back.
     EXPAND_BYTES = 32 << 30
 
     def _buffer(self, name: str, *shape, dtype=torch.bfloat16):
         """A buffer that is kept from step to step, made anew with a quarter to spare where it is too small."""
         n, buffer = math.prod(shape), self._kept.get(name)
         if buffer is None or buffer.numel() < n or buffer.dtype != dtype:
-            if buffer is not None and not torch.cuda.is_current_stream_capturing():
-                buffer.record_stream(torch.cuda.current_stream())  # its memory may serve another tensor once the calls so far are done
-            self._kept[name] = buffer = None
+            buffer = None
+            self._give_back(name)
+            self._kept[name] = None
             self._kept[name] = buffer = torch.empty(n + n // 4, dtype=dtype, device=self.device)
         self._hold(buffer)
         return buffer[:n].view(shape)
+
+    def _give_back(self, *names):
+        """These buffers' memory may serve other tensors once the calls so far are done. (Not while a graph is captured.)"""
+        for name in names if not torch.cuda.is_current_stream_capturing() else ():
+            buffer = self._kept.pop(name, None)
+            if buffer is not None:
+                buffer.record_stream(torch.cuda.current_stream())
 
     def _expanded_pays(self, T: int, Dn: int, Dv: int) -> bool:
         """Whether the last extend's tokens are faster in the expanded form, by what each form does for a head, in products of the absorbed
@@ -437,13 +446,15 @@ class DenseSession:
         rotary part, the last 64 values, may be rotated in place) and ``rope`` bf16 [T, 64] (rotated in place), ``latent`` bf16 [T, 512],
         the layer's weight ``w`` bf16 [H, Dn + Dv, 512], ``out`` bf16 [T, H, Dv]; logits are scaled by (Dn + 64)^-1/2. ``q`` and ``out`` may be
         slices of wider heads. ``form`` is "absorbed" or "expanded" (heads of 128 and 128, or 192 and 256, alone); None picks it by
-        the work of each (_expanded_pays). A call that is refused (ValueError, IndexError) has turned and written nothing."""
+        the work of each (_expanded_pays). A call that is refused (ValueError, IndexError), or whose buffers cannot be had, has
+        turned and written nothing."""
         if form not in (None, "absorbed", "expanded"):
             raise ValueError("form must be absorbed or expanded")
         pool = self.pool[layer]
         T, H, Dn, Dv = _check_heads(q, latent, rope, w, out, lse, self.positions.numel(), self.pool.device)
+        given = form
         if form is None:
-            pays = 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES and self._expanded_pays(T, Dn, Dv)
+            pays = self._room and 2 * self.read_tokens * H * (Dn + Dv) <= self.EXPAND_BYTES and self._expanded_pays(T, Dn, Dv)
             form = "expanded" if (Dn, Dv) in self.EXPANDED and (pays or H > self.H) else "absorbed"
         if form == "expanded" and (Dn, Dv) not in self.EXPANDED:
             raise ValueError("the expanded form takes heads of %s" % " or ".join(map(str, self.EXPANDED)))
@@ -453,17 +464,25 @@ class DenseSession:
             return
         if torch.cuda.current_device() != self.pool.device.index:
             raise ValueError("the session's device is not the current one")
+        if form == "expanded":
+            try:
+                rows, kv = self._buffer("rows", self.read_tokens, 576), self._buffer("kv", self.read_tokens, H, Dn + Dv)
+                workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.active, Dv), dtype=torch.uint8)
+                whole = out if out.is_contiguous() else self._buffer("out", T, H, Dv)
+            except torch.OutOfMemoryError:
+                if given == "expanded" or H > self.H:
+                    raise
+                form, rows, kv, workspace, self._room = "absorbed", None, None, None, False  # nor is it tried again for the step's other layers
+        if form == "absorbed":
+            self._give_back("rows", "kv")
+            wide, mixed = self._buffer("queries", T, H, 576), self._buffer("mixed", T, H, 512)
         self._hold(self.positions, self.token_req, self.req_start, self.read_start, self.seq_len, self.workspace)
         scale = self.softmax_scale * 24.0 * (Dn + 64) ** -0.5
         if form == "absorbed":
-            wide, mixed = self._buffer("queries", T, H, 576), self._buffer("mixed", T, H, 512)
             hs_rope(q[..., Dn:], self.positions, self.inv_freq, out=wide[..., 512:], y=rope[:, None], scale=self.rope_scale)
         else:
-            rows, kv = self._buffer("rows", self.read_tokens, 576), self._buffer("kv", self.read_tokens, H, Dn + Dv)
-            workspace = self._buffer("expanded", hs_mla_expanded_workspace_size(self.active, Dv), dtype=torch.uint8)
             req_start, read_start = self._requests()
             self._hold(req_start, read_start)
-            whole = out if out.is_contiguous() else self._buffer("out", T, H, Dv)
             hs_rope(q[..., Dn:], self.positions, self.inv_freq, y=rope[:, None], scale=self.rope_scale)
         hs_kv_append(self.token_req, self.positions, self.table, self.err, latent=latent, rope=rope, kv_pool=pool)
         if form == "absorbed":
