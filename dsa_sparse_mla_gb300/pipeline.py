@@ -352,13 +352,11 @@ class DenseSession:
         free = (self.refcount <= 0).nonzero()[:, 0][:int(take.sum())].int()
         if int(take.sum()) > free.numel() or int(after.max()) > 64 * self.table.shape[1]:
             raise RuntimeError("the cache has too few pages")
-        # what the expanded form reads: the rows of slots with new tokens
-        read = torch.where(new > 0, after, 0)
-        # (token, row) pairs that new tokens see, twice
-        pairs = new.long() * (2 * after.long() - new + 1)
-        cached, tokens, self.read_tokens, self.active, self.pairs = torch.stack([after, new, read, new > 0, pairs]).sum(1).tolist()
-        self._make_room(tokens, cached)
-        self.kv_tokens = cached
+        rows, m = torch.stack([after, new]).cpu().numpy().astype(np.int64)  # of every slot
+        self._make_room(int(m.sum()), int(rows.sum()))
+        self.kv_tokens = int(rows.sum())
+        # rows that the expanded form reads, slots with new tokens, and (token, row) pairs that those see, twice
+        self.read_tokens, self.active, self.pairs = int(rows[m > 0].sum()), int((m > 0).sum()), int((m * (2 * rows - m + 1)).sum())
         self.table[take] = free
         self.refcount[free.long()] = 1
         self.token_req = torch.repeat_interleave(torch.arange(self.B, dtype=torch.int32, device=self.device), new)
@@ -367,6 +365,7 @@ class DenseSession:
         self.positions = (torch.arange(T, dtype=torch.int32, device=self.device)
                           + torch.repeat_interleave(self.seq_len - self.req_start[:-1], new))
         self.seq_len = after
+        read = torch.where(new > 0, after, 0)
         self.read_start = torch.cat([read.new_zeros(1), read.cumsum(0).int()])
         self._with_tokens, self._room = None, True
         return T

@@ -68,3 +68,24 @@ def test_keys_and_values_are_given_back():
     s.attend_heads(0, *x, w, out)
     torch.cuda.synchronize()
     assert torch.cuda.memory_allocated() <= before - size and hs.hs_check_flag(s.err) == 0
+
+
+def test_an_extend_without_room_changes_nothing(monkeypatch):
+    """Where the attention's workspace cannot be had, the step before stays the one that attend_heads runs."""
+    s, T = session([500, 300])
+    x, out = inputs(T, 2), [torch.full((T, H, Dv), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    s.attend_heads(0, *x, W.cuda(), out[0])
+    before = {k: v for k, v in vars(s).items() if isinstance(v, (int, bool, torch.Tensor))}
+    held = {k: v.clone() for k, v in before.items() if isinstance(v, torch.Tensor)}
+
+    def no_room(self, tokens, cached):
+        raise torch.OutOfMemoryError("no room")
+
+    with monkeypatch.context() as m:
+        m.setattr(DenseSession, "_make_room", no_room)
+        with pytest.raises(torch.OutOfMemoryError):
+            s.extend([0, 900])
+    assert all(getattr(s, k) is v if isinstance(v, torch.Tensor) else getattr(s, k) == v for k, v in before.items())
+    assert all(torch.equal(getattr(s, k), v) for k, v in held.items())
+    s.attend_heads(0, *inputs(T, 2), W.cuda(), out[1])
+    assert torch.equal(*out) and hs.hs_check_flag(s.err) == 0
