@@ -595,6 +595,18 @@ def _current_device():
     return torch._C._cuda_getDevice()
 
 
+def _here(t, name, dtype):
+    """The address of a contiguous tensor of this type on the current device."""
+    p = _tensor(t, name, dtype)
+    if t.get_device() != _current_device():
+        raise HSError(1, "%s is on another device than the current one" % name)
+    return p
+
+
+def _here_int(t, name):
+    return _here(t, name, torch.int32)
+
+
 def hs_kv_read(kv_pool, block_table, out_start, out, err_flag, first=None, stream=None):
     """Rows of the paged cache as values: row ``first[r] + i`` of request r (``first`` int32 [B], row 0 on when None) into row
     ``out_start[r] + i`` of ``out`` (bf16, fp16 or fp32 [n, 576]: 512 latent and 64 rotary values; ``out_start`` int32 [B + 1])."""
@@ -605,9 +617,9 @@ def hs_kv_read(kv_pool, block_table, out_start, out, err_flag, first=None, strea
     (B, pages), (R, row) = block_table.shape, kv_pool.shape
     if D != 576 or row != 656 or out_start.numel() != B + 1 or (first is not None and first.numel() != B):
         raise HSError(1, "shape mismatch: kv_pool [R,656], block_table [B,pages], out_start [B+1], first [B], out [n,576]")
-    _check(load().hs_kv_read(_pack_kv_read(B, pages, _ROPE_DTYPES[dtype], _tensor(kv_pool, "kv_pool", torch.uint8), R,
-                                           _int(block_table, "block_table"), 0 if first is None else _int(first, "first"),
-                                           _int(out_start, "out_start"), n, op, ot, _int(err_flag, "err_flag")), _stream(stream)))
+    _check(load().hs_kv_read(_pack_kv_read(B, pages, _ROPE_DTYPES[dtype], _here(kv_pool, "kv_pool", torch.uint8), R,
+                                           _here_int(block_table, "block_table"), 0 if first is None else _here_int(first, "first"),
+                                           _here_int(out_start, "out_start"), n, op, ot, _here_int(err_flag, "err_flag")), _stream(stream)))
 
 
 def _weight(w):
@@ -630,7 +642,7 @@ def _heads_args(x, w, out, err_flag, absorb):
     if Hw != H or To != T or Ho != H or (Do if absorb else Dx) != 512:
         raise HSError(1, "shape mismatch: %s" % ("q [T,H,Dn], w [H,Dn+Dv,512], out [T,H,512]" if absorb else
                                                  "x [T,H,512], w [H,Dn+Dv,512], out [T,H,Dv]"))
-    return _pack_mla_heads(T, H, Dn, Dv, xp, xt, xh, wp, op, ot, oh, _int(err_flag, "err_flag"))
+    return _pack_mla_heads(T, H, Dn, Dv, xp, xt, xh, wp, op, ot, oh, _here_int(err_flag, "err_flag"))
 
 
 def hs_mla_absorb(q, w, out, err_flag, stream=None):
@@ -653,7 +665,7 @@ def hs_mla_expand(latent, w, kv, err_flag, stream=None):
     kp, (Nk, Hk, wk), (ks, kh, _) = _strided(kv, "kv", torch.bfloat16, 3)
     if D != 512 or Nk != N or Hk != H or wk != width or kh != width:
         raise HSError(1, "shape mismatch: latent [N,512], w [H,Dn+Dv,512] contiguous, kv [N,H,Dn+Dv] with its heads one after the other")
-    _check(load().hs_mla_expand(_pack_mla_expand(N, H, width, lp, ls, wp, kp, ks, _int(err_flag, "err_flag")), _stream(stream)))
+    _check(load().hs_mla_expand(_pack_mla_expand(N, H, width, lp, ls, wp, kp, ks, _here_int(err_flag, "err_flag")), _stream(stream)))
 
 
 def hs_mla_expanded_workspace_size(B: int, Dv: int) -> int:
@@ -671,12 +683,12 @@ def hs_mla_expanded_fwd(q, kv, rope, req_start, kv_start, softmax_scale: float, 
     qp, (T, H, Dq), (qt, qh, _) = _strided(q, "q", torch.bfloat16, 3)
     kp, (N, Hk, width), (ks, kh, _) = _strided(kv, "kv", torch.bfloat16, 3)
     rp, (Nr, D), (rs, _) = _strided(rope, "rope", torch.bfloat16, 2)
-    op, B = _tensor(out, "out", torch.bfloat16), req_start.numel() - 1
+    op, B = _here(out, "out", torch.bfloat16), req_start.numel() - 1
     if out.dim() != 3 or out.shape[:2] != (T, H) or Hk != H or Nr != N or D != 64 or width - out.shape[2] != Dq - 64 \
             or kh != width or kv_start.numel() != B + 1 or (lse is not None and lse.shape != (T, H)):
         raise HSError(1, "shape mismatch: q [T,H,Dn+64], kv [N,H,Dn+Dv] with its heads one after the other, rope [N,64], req_start and "
                          "kv_start [B+1], out [T,H,Dv], lse [T,H]")
     _check(load().hs_mla_expanded_fwd(_pack_mla_expanded(
-        T, B, H, Dq - 64, out.shape[2], 1 if causal else 0, qp, qt, qh, kp, ks, N, rp, rs, _int(req_start, "req_start"),
-        _int(kv_start, "kv_start"), softmax_scale, op, 0 if lse is None else _tensor(lse, "lse", torch.float32), _int(err_flag, "err_flag"),
-        _tensor(workspace, "workspace", torch.uint8), workspace.numel()), _stream(stream)))
+        T, B, H, Dq - 64, out.shape[2], 1 if causal else 0, qp, qt, qh, kp, ks, N, rp, rs, _here_int(req_start, "req_start"),
+        _here_int(kv_start, "kv_start"), softmax_scale, op, 0 if lse is None else _here(lse, "lse", torch.float32), _here_int(err_flag, "err_flag"),
+        _here(workspace, "workspace", torch.uint8), workspace.numel()), _stream(stream)))
