@@ -25,10 +25,10 @@
 // threads have too few registers then: 915).
 //
 // Bound by the tensor cores for prompts and chunks: 2,048 tokens over 32,768 rows 1,370 to 1,415 us in a few calls (1,880 to 1,940
-// TFLOP/s), 1,510 to 1,590 us under the power limit; 8,192 tokens over themselves 765 to 785, and 820 to 870. There the softmax counts by the
-// energy of its instructions: with one for two products and one for two sums instead of one each 1,485 -> 1,380, 1,600 -> 1,520, and
+// TFLOP/s), 1,590 to 1,627 in long runs, under the power limit; 8,192 tokens over themselves 765 to 785, and 871 to 891. There the softmax
+// counts by the energy of its instructions: with one for two products and one for two sums instead of one each 1,485 -> 1,380, 1,600 -> 1,520, and
 // 845 -> 785, 887 -> 845 (maxima of three by an instruction of their own spilled: 1,420). A unit's end costs about 5,000 cycles (the last
-// tile's softmax, PV and output one after the other), a tile 1,280 of MMAs. (192, 256): 9 ragged requests 330 to 337 us, 377. Bound by HBM for
+// tile's softmax, PV and output one after the other), a tile 1,280 of MMAs. (192, 256): 9 ragged requests 330 to 338 us, 377 to 387. Bound by HBM for
 // single tokens over long rows: 8 requests over 8,000 rows 331 us, 6.3 TB/s; over 200 to 2,000 rows 62 us, 4.8 TB/s, by the last units.
 // (Splitting the blocks of a last turn that is not full: 1,024 tokens over 32,768 rows 861 -> 802 us, but 2,048 over 8,192 366 -> 389 to 418,
 // by the joins.)
@@ -36,8 +36,6 @@
 // Rows past a request's end are masked as keys and set to zero as values (in shared memory, by a warp that waits for such a tile's copy).
 // A row that a token does not see can still reach its output where P = 0 meets a value that is not finite; where an output is not
 // finite although the token's logits are, the warp computes it again from the rows that the token sees (rescue).
-#include <atomic>
-
 #include "launch.cuh"
 #include "pair.cuh"
 
@@ -829,6 +827,9 @@ __device__ __forceinline__ void attend(const CUtensorMap& map_q, const CUtensorM
             float a, b;
             apart(fma2(two(v[c][2 * j], v[c][2 * j + 1]), coef2, me2), a, b);
             a = fast_exp2(a), b = fast_exp2(b);
+            // P has V's type, as the product asks: off by 0.16 % in the root mean square, and so is the output, as much as by its own
+            // rounding (0.23 % in all, 0.17 with 32-bit weights). The sum is of the weights before. P's remainder in a product of its own
+            // would take half as many MMAs again.
             sum = add2(sum, two(a, b));
             v[c][j] = pack_bf16(a, b);
           }
@@ -1073,7 +1074,7 @@ static uint64_t off_out(int B, int cap) { return off_lse(B, cap) + up((uint64_t)
 // alone, us, 64 heads, 8 requests over 4,000 rows): 16 tokens each 189 / 178, 128 203 / 186, 129 207 / 246, 256 218 / 252; one token
 // each over 1,000 rows 70 / 56, one alone over 4,000 38 / 41; 16 heads, 64 requests x 33 tokens over 200 rows 75 / 44. How the tokens spread
 // over the requests is on the device: all of them in one of 64, 8,192 over themselves, 783 / 879; 1,024 in one of 8 over 8,192 rows
-// 217 / 249. (192, 256) has no room for whole tiles.
+// 217 / 249; callers leave out requests without tokens. (192, 256) has no room for whole tiles.
 static bool few_tokens(int T, int B) { return (int64_t)T <= 128ll * B; }
 
 }  // namespace expanded

@@ -9,9 +9,10 @@
 //
 // A pair of CTAs computes tiles of 256 rows and kBN columns with two-SM MMAs: each CTA holds its 128 rows of A, half of the
 // columns of B, and its rows of the accumulator (two tiles of them in tensor memory, so that one tile's epilogue runs under the next
-// tile's products). All of a head's B (or 256 columns of the expanded width: 128 KB of shared memory per CTA at most) stays while the pair
-// goes on along the rows, so that only A streams through the ring. B comes and goes in chunks of 64 reduced values, with
-// barriers of their own, so that a change of head costs no more than a load's latency. Eight epilogue warps round to bf16 once. Rows beyond
+// tile's products). All of a head's B (or 256 columns of the expanded width: 128 KB of shared memory per CTA at most) is there at
+// once. Where every group of columns reads the same A (expand) it stays for up to four row tiles, and only A streams through the ring; absorb
+// and project, whose A differs from head to head, load it again for each tile. B comes and goes in chunks of 64 reduced values, with
+// barriers of their own, so that a change of B costs no more than a load's latency. Eight epilogue warps round to bf16 once. Rows beyond
 // M are read as zeros and not stored.
 //
 // Stores. expand and project, which multiply 512 values for each one that they store, need a deep ring more than anything, since copies of
@@ -21,8 +22,8 @@
 // 7.7 and 8.5).
 //
 // absorb and project are bound by HBM: 16,384 tokens x 64 heads (1.35 GB) 231 to 242 us, 5.6 to 5.8 TB/s; 4,099 x 128 (192, 256) 142 to
-// 146, 5.8 TB/s. expand: 32,768 rows x 64 heads x 256 319 to 329 us in a few calls, 327 to 342 in many (1,610 to 1,720 TFLOP/s; one library
-// product of the same sizes 324 to 333, 326 to 338), bound by power: with zeros for inputs it takes 287. What the issuing thread
+// 146, 5.8 TB/s. expand: 32,768 rows x 64 heads x 256 319 to 329 us in a few calls (1,670 to 1,720 TFLOP/s; one library product of the
+// same sizes 324 to 333) and 365 to 385 in long runs (1,430 to 1,510), bound by power: with zeros for inputs it takes 287. What the issuing thread
 // executes between two batches of MMAs is not hidden: a wait in its loop that expand never reaches, eight times unrolled, made it 359
 // instead of 345 (without copies and stores 278 and 237; 229 are MMAs). Tried and not kept: B streaming with A, two issuing warps, two
 // copying warps, TMA stores, 16 epilogue warps, clusters of four with A multicast to both pairs (36 of them fit, 144 SMs: 336 where

@@ -773,7 +773,8 @@ hs_status hs_mla_expand(const hs_mla_expand_args* a, hs_stream_t stream);
  *
  * Compute precision: products of bf16 values and P rounded to bf16, accumulation, maxima and sums fp32, pieces of a split block fp32.
  *
- *   T, B, H       new tokens in all, requests (1 <= B <= 4096), heads (1 <= H <= 1024)
+ *   T, B, H       new tokens in all, requests (1 <= B <= 4096), heads (1 <= H <= 1024). Blocks of 128 or 256 tokens are picked by T / B:
+ *                 requests without tokens may be there, but are better left out
  *   Dn, Dv        128 and 128, or 192 and 256
  *   q             bf16 [T, H, Dn + 64], the rotary part last, with strides from token to token and head to head
  *   kv, N         bf16 [N, H, Dn + Dv] (hs_mla_expand), kv_stride values from row to row; N >= 1 rows
