@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import latent_ops as plain
-from test_gpu_latent import HEADS, attend, batch
+from test_gpu_latent import HEADS, attend, batch, check
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,11 @@ def test_both_halves_again_and_again(q_lens, kv_lens, H, Dn, Dv):
     assert plain.holds(want[0], ref, tol) and plain.holds(want[1], rlse, ltol)
     for _ in range(100):
         assert all(torch.equal(x, y) for x, y in zip(want, attend(b, Dv)))
+
+
+@pytest.mark.parametrize("Dn,Dv", HEADS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens", [([3, 200, 0], [0, 0, 5]), ([300, 1, 40], [0, 700, 0]), ([7], [1])])
+def test_requests_without_rows(q_lens, kv_lens, causal, Dn, Dv):
+    """At either end of the rows and between others: zeros, and a log-sum-exp of minus infinity."""
+    check(batch(q_lens, kv_lens, 2, Dn, Dv, seed=22), Dn, Dv, causal)

@@ -71,3 +71,30 @@ def test_replayed_on_other_inputs_and_after_more_tokens(form):
     assert not any(x.data_ptr() in used for x in others) and all(getattr(s, n).data_ptr() != x for n, x in zip(names, used))
     for seed in (42, 41, 43):
         assert replay(seed)
+
+
+def test_what_is_given_back_stays_with_the_graph():
+    """Captured without a call before, in a session with idle slots; then an absorbed step gives the keys and values back, and what takes
+    their place has no part in the replays."""
+    w = plain.weights(H, 128, 128, torch.Generator().manual_seed(40)).cuda()
+
+    def session():
+        s = DenseSession(5, H, 40, 20, max_tokens=T)
+        assert s.extend([0] + NEW + [0]) == T
+        return s
+
+    s, want = session(), results("expanded")
+    call(s, "expanded", w, inputs("expanded", 44), *want)
+    s, r, held = session(), results("expanded"), inputs("expanded", 44)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(s, "expanded", w, held, *r)
+    size = s._kept["kv"].numel()
+    tokens = s.extend([1] * 5)
+    call(s, "absorbed", w, inputs("absorbed", 45, tokens), *results("absorbed", tokens))
+    assert "kv" not in s._kept and "rows" not in s._kept
+    others = [torch.full((size,), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for h, x in zip(held, inputs("expanded", 44)):
+        h.copy_(x)
+    graph.replay()
+    assert hs.hs_check_flag(s.err) == 0 and all(torch.equal(a, b) for a, b in zip(r, want)) and all(bool(x.isnan().all()) for x in others)
